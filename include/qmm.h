@@ -61,7 +61,7 @@ typedef enum {
     QMM_ERR_INVALID_ARG = 1, /* shape, parameter, pointer or alignment rule broken */
     QMM_ERR_UNSUPPORTED = 2, /* output dtype not supported */
     QMM_ERR_CUDA = 3,        /* a CUDA call or launch failed */
-    QMM_ERR_INDEX = 4,       /* qmm_rows met an index outside the table */
+    QMM_ERR_INDEX = 4,       /* a kernel met an index outside its table */
     QMM_ERR_TIMEOUT = 5      /* a bounded wait inside a kernel ran out */
 } qmm_status;
 
@@ -329,8 +329,8 @@ const char *qmm_last_error(void);
 
 /*
  * Synchronizes `stream`, then reads and clears the current device's error
- * word: QMM_ERR_INDEX if a qmm_rows index was outside its table,
- * QMM_ERR_TIMEOUT if a bounded wait in a kernel ran out (the kernel then
+ * word: QMM_ERR_INDEX if an index on the device was outside its table
+ * (qmm_rows, qmm_gather_qmm, the paged-attention calls), QMM_ERR_TIMEOUT if a bounded wait in a kernel ran out (the kernel then
  * stops early and its output is incomplete), QMM_ERR_CUDA if the
  * synchronization itself failed, else QMM_OK.
  */
@@ -400,6 +400,145 @@ qmm_status qmm_quantized_matmul_typed(const void *x, qmm_dtype x_dtype, int64_t 
                                       qmm_dtype sb_dtype, int64_t N, int64_t K, int transpose,
                                       int group_size, int bits, void *y, qmm_dtype y_dtype,
                                       qmm_stream_t stream);
+
+/* ------------------------------------------------- paged attention ----
+ * What a decoder layer does between its q/k/v projections and its output
+ * projection when requests share a paged cache of keys and values (the pages
+ * have no counterpart: their runtimes leave attention to their frameworks).
+ * Three calls, made in this order for a step of several requests: the page
+ * plan once a step, then for each layer the rotary append and the attention.
+ * Requests may bring any number of new tokens, none included: single tokens
+ * (decode), a few (drafts to check), a chunk of a prompt, a whole prompt.
+ * Strides count elements and must be multiples of 8; pointers, as everywhere,
+ * are 16-byte aligned.  Nothing is allocated. */
+
+/* A pool of cache pages: key (and value) of head h and row t of page p is the
+ * `head_dim` consecutive elements at k (v) + p * page_stride +
+ * h * head_stride + t * token_stride, so both head-major and token-major
+ * pages fit.  Slot s of the pool is row s mod page_size of page
+ * s / page_size. */
+typedef struct {
+    void *k, *v;          /* device */
+    qmm_dtype dtype;      /* of keys, values, queries and outputs alike */
+    int64_t num_pages;    /* num_pages * page_size below 2^31 */
+    int32_t page_size;    /* rows of a page, 1 to 65536 (16-bit types with heads
+                             of at most 128 are fastest at multiples of 16) */
+    int32_t heads;        /* key and value heads */
+    int32_t head_dim;     /* a multiple of 8, 8 to 256 */
+    int64_t page_stride, head_stride, token_stride;
+} qmm_paged_cache;
+
+/*
+ * qmm_page_plan -- block table, slot map and positions of a step, on the GPU,
+ * from the requests' lengths.
+ *
+ *   past_lens    int32 [requests]  tokens that each request has in the cache
+ *   new_lens     int32 [requests]  tokens that it adds in this step (0: idle)
+ *   free_pages   int32 [free_count]  ids of pages that no request holds, taken
+ *                in order
+ *   next_free    int32 [1], the first entry of free_pages still free; NULL: 0
+ *   block_table  int32 [requests, table_stride], in and out: entry j of a row
+ *                is the page of the request's tokens [j * page_size,
+ *                (j + 1) * page_size).  The entries of past tokens are read;
+ *                those of fresh pages are written; the others stay.
+ *   tokens       room in positions and slots
+ *   starts       int32 [requests + 1]: request b's new tokens are tokens
+ *                starts[b] .. starts[b + 1] - 1 of the step
+ *   seq_lens     int32 [requests]: past + new
+ *   positions    int32 [tokens]: past + i for new token i
+ *   slots        int32 [tokens]: the token's slot in the pool.  Tokens past
+ *                starts[requests] get position 0 and slot -1.
+ *   next_free_out int32 [1]: next_free moved past the pages taken; not the
+ *                same address as next_free
+ *
+ * Pages go to requests in order, and to each in the order of its tokens.
+ * QMM_ERR_INDEX in the device error word: free_pages ran out (entries and
+ * slots are then -1), a length is negative (taken as 0), a request outgrew its
+ * table row or the tokens their room (cut off there), or a page id's slot is
+ * outside [0, 2^31).  requests, free_count, tokens at least 0 and below 2^31;
+ * page_size 1 to 65536; table_stride at least 1.
+ */
+qmm_status qmm_page_plan(const int32_t *past_lens, const int32_t *new_lens, int64_t requests,
+                         const int32_t *free_pages, int64_t free_count, const int32_t *next_free,
+                         int page_size, int32_t *block_table, int64_t table_stride,
+                         int64_t tokens, int32_t *starts, int32_t *seq_lens, int32_t *positions,
+                         int32_t *slots, int32_t *next_free_out, qmm_stream_t stream);
+
+/*
+ * qmm_rope_append -- rotary positions on q and k, and k and v into the cache,
+ * in one pass.
+ *
+ *   q, k, v      [tokens, heads * head_dim] of cache->dtype, tokens q_stride,
+ *                k_stride, v_stride apart (column ranges of one fused
+ *                projection, for instance); q has q_heads heads, k and v have
+ *                cache->heads
+ *   positions    int32 [axes, tokens]: 1 to 4 position axes (time, height and
+ *                width of images and video; text has one, or equal ones)
+ *   sections     HOST array of `axes` counts with sum rotary_dim / 2: the first
+ *                sections[0] frequency pairs turn by axis 0's position, the
+ *                next sections[1] by axis 1's, and so on
+ *   cos_sin      fp32 [max_positions, rotary_dim]: row p has the cosines of
+ *                p's angles for the rotary_dim / 2 frequencies, then the sines
+ *   rotary_dim   first elements of a head that turn, a multiple of 16, at most
+ *                head_dim; the rest passes through
+ *   interleaved  0: pair i is elements (i, i + rotary_dim / 2);
+ *                1: elements (2i, 2i + 1)
+ *   slots        int32 [tokens]: where k and v of a token go; -1: nowhere
+ *   q_out        [tokens, q_heads * head_dim], tokens out_stride apart; may be
+ *                q itself with the same stride
+ *
+ * A pair (x1, x2) becomes (x1 cos - x2 sin, x2 cos + x1 sin) in fp32, rounded
+ * once.  QMM_ERR_INDEX in the device error word: a position outside the table
+ * (the elements that it would turn are written as zeros) or a slot past the
+ * pool (the token is not kept).  Slots that repeat within a call race.
+ */
+qmm_status qmm_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, int64_t tokens, int q_heads,
+                           const int32_t *positions, int axes, const int32_t *sections,
+                           const float *cos_sin, int64_t max_positions, int rotary_dim,
+                           int interleaved, const int32_t *slots, void *q_out,
+                           int64_t out_stride, const qmm_paged_cache *cache, qmm_stream_t stream);
+
+/*
+ * qmm_paged_attention -- softmax(scale * q k^T) v of each request's new tokens
+ * over its pages, its own keys included (append first).
+ *
+ *   q            [tokens, q_heads * head_dim] of cache->dtype, tokens q_stride
+ *                apart; q_heads a multiple of cache->heads: query head h reads
+ *                key head h / (q_heads / cache->heads)
+ *   block_table  int32 [requests, table_stride], starts int32 [requests + 1],
+ *                seq_lens int32 [requests]: as qmm_page_plan writes them.  New
+ *                token i of request b, row starts[b] + i of q, has position
+ *                p = seq_lens[b] - (starts[b + 1] - starts[b]) + i.
+ *   max_new      the most new tokens of any request as the host knows it: it
+ *                chooses between kernels and never changes a result beyond
+ *                rounding
+ *   causal       1: a row sees keys 0 .. p; 0: every key of its request
+ *   window       > 0: of those only keys p - window + 1 and later; 0: all
+ *   out          like q, tokens out_stride apart.  A row that sees no key is
+ *                zero.  Rows of q past starts[requests] stay unwritten.
+ *   lse          fp32 [tokens, q_heads]: log of the sum of exponentials of the
+ *                scaled scores (-infinity where no key is seen), or NULL
+ *   workspace    device memory of at least QMM_ATTENTION_WORKSPACE_BYTES,
+ *                whatever it holds; calls that may overlap on the GPU need
+ *                one each
+ *
+ * A key that a row does not see has no part in the row, whatever its k and v
+ * hold (infinities and NaN, stale rows of a page).  16-bit types: products of
+ * the elements, fp32 scores, sums and statistics, weights rounded once to the
+ * element type for the product with v.  fp32: fp32 throughout.  Results
+ * repeat bit for bit.  Lengths are clamped to the tensors' sizes; a table
+ * entry outside [0, num_pages) that a row needs reads as zero keys and values
+ * and sets QMM_ERR_INDEX in the device error word.
+ */
+#define QMM_ATTENTION_WORKSPACE_BYTES (64 << 20)
+qmm_status qmm_paged_attention(const void *q, int64_t q_stride, int64_t tokens, int q_heads,
+                               const qmm_paged_cache *cache, const int32_t *block_table,
+                               int64_t table_stride, const int32_t *starts,
+                               const int32_t *seq_lens, int64_t requests, int64_t max_new,
+                               float scale, int causal, int64_t window, void *out,
+                               int64_t out_stride, float *lse, void *workspace,
+                               int64_t workspace_bytes, qmm_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@
 #include "qmm.h"
 #include "internal.h"
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -207,6 +208,50 @@ qmm_status matmul_impl(const char *op, const void *x, qmm_dtype x_dtype, int64_t
     e = qmm::launch_mm_f32(x, static_cast<int>(x_dtype), M, pw, transpose != 0,
                            static_cast<float *>(y), s);
   return cuda_status(e, op);
+}
+
+// ----------------------------------------------- paged attention checks ----
+
+bool count31(int64_t n) { return n >= 0 && n <= 0x7FFFFFFF; }
+
+// A cache as the kernels take it, with q_heads query heads over it.
+qmm_status check_cache(const char *op, const qmm_paged_cache *c, int q_heads, qmm::PagedPool *pool) {
+  if (!c) return fail(QMM_ERR_INVALID_ARG, "%s: null cache", op);
+  if (!known_dtype(c->dtype))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: unknown dtype %d", op, static_cast<int>(c->dtype));
+  if (c->head_dim < 8 || c->head_dim > 256 || c->head_dim % 8 != 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: head_dim %d must be a multiple of 8 in [8, 256]", op, c->head_dim);
+  if (c->page_size < 1 || c->page_size > 65536)
+    return fail(QMM_ERR_INVALID_ARG, "%s: page_size %d is not in [1, 65536]", op, c->page_size);
+  if (c->num_pages < 1 || c->num_pages > 0x7FFFFFFF / c->page_size)
+    return fail(QMM_ERR_INVALID_ARG, "%s: num_pages %lld must be positive with num_pages * page_size below 2^31",
+                op, (long long)c->num_pages);
+  if (c->heads < 1 || c->heads > 65536 || q_heads < 1 || q_heads > 65536 || q_heads % c->heads != 0)
+    return fail(QMM_ERR_INVALID_ARG, "%s: q_heads %d must be a positive multiple of the cache's heads %d (at most 65536)",
+                op, q_heads, c->heads);
+  const int64_t strides[3] = {c->page_stride, c->head_stride, c->token_stride};
+  for (int64_t s : strides)
+    if (s < c->head_dim || s % 8 != 0 || s > (int64_t(1) << 36))
+      return fail(QMM_ERR_INVALID_ARG,
+                  "%s: cache strides must be multiples of 8 elements, at least head_dim, at most 2^36 (got %lld)",
+                  op, (long long)s);
+  if (!c->k || !aligned16(c->k) || !c->v || !aligned16(c->v))
+    return fail(QMM_ERR_INVALID_ARG, "%s: the cache's k and v must be non-null and 16-byte aligned", op);
+  *pool = qmm::PagedPool{c->k, c->v, static_cast<int>(c->dtype), c->num_pages, c->page_size, c->heads,
+                         c->head_dim, c->page_stride, c->head_stride, c->token_stride};
+  return QMM_OK;
+}
+
+// `tokens` rows of `width` elements, `stride` apart.
+qmm_status check_rows(const char *op, const char *name, const void *p, int64_t stride, int64_t width,
+                      int64_t tokens) {
+  if (stride < width || stride % 8 != 0 || stride > (int64_t(1) << 32))
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: the stride of %s (%lld) must be a multiple of 8, at least its %lld columns, at most 2^32",
+                op, name, (long long)stride, (long long)width);
+  if (tokens > 0 && (!p || !aligned16(p)))
+    return fail(QMM_ERR_INVALID_ARG, "%s: %s must be a non-null 16-byte aligned pointer", op, name);
+  return QMM_OK;
 }
 
 }  // namespace
@@ -456,6 +501,130 @@ qmm_status qmm_quantized_matmul_typed(const void *x, qmm_dtype x_dtype, int64_t 
                      K, transpose, group_size, bits, y, y_dtype, stream);
 }
 
+// -------------------------------------------------- paged attention ----
+
+qmm_status qmm_page_plan(const int32_t *past_lens, const int32_t *new_lens, int64_t requests,
+                         const int32_t *free_pages, int64_t free_count, const int32_t *next_free,
+                         int page_size, int32_t *block_table, int64_t table_stride,
+                         int64_t tokens, int32_t *starts, int32_t *seq_lens, int32_t *positions,
+                         int32_t *slots, int32_t *next_free_out, qmm_stream_t stream) {
+  const char *op = "qmm_page_plan";
+  if (!count31(requests) || !count31(free_count) || !count31(tokens))
+    return fail(QMM_ERR_INVALID_ARG, "%s: requests, free_count and tokens must be in [0, 2^31)", op);
+  if (page_size < 1 || page_size > 65536)
+    return fail(QMM_ERR_INVALID_ARG, "%s: page_size %d is not in [1, 65536]", op, page_size);
+  if (table_stride < 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: table_stride must be at least 1", op);
+  if (!starts || !aligned16(starts) || !next_free_out || !aligned16(next_free_out))
+    return fail(QMM_ERR_INVALID_ARG, "%s: starts and next_free_out must be non-null and 16-byte aligned", op);
+  if (requests > 0 && (!past_lens || !aligned16(past_lens) || !new_lens || !aligned16(new_lens) ||
+                       !block_table || !aligned16(block_table) || !seq_lens || !aligned16(seq_lens)))
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: past_lens, new_lens, block_table and seq_lens must be non-null and 16-byte aligned", op);
+  if (free_count > 0 && (!free_pages || !aligned16(free_pages)))
+    return fail(QMM_ERR_INVALID_ARG, "%s: free_pages must be non-null and 16-byte aligned", op);
+  if (tokens > 0 && (!positions || !aligned16(positions) || !slots || !aligned16(slots)))
+    return fail(QMM_ERR_INVALID_ARG, "%s: positions and slots must be non-null and 16-byte aligned", op);
+  if (next_free && (!aligned16(next_free) || next_free == next_free_out))
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: next_free must be 16-byte aligned and not the address of next_free_out", op);
+  return cuda_status(qmm::launch_page_plan(past_lens, new_lens, static_cast<int>(requests), free_pages,
+                                           static_cast<int>(free_count), next_free, page_size,
+                                           block_table, table_stride, static_cast<int>(tokens), starts,
+                                           seq_lens, positions, slots, next_free_out,
+                                           reinterpret_cast<cudaStream_t>(stream)),
+                     op);
+}
+
+qmm_status qmm_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, int64_t tokens, int q_heads,
+                           const int32_t *positions, int axes, const int32_t *sections,
+                           const float *cos_sin, int64_t max_positions, int rotary_dim,
+                           int interleaved, const int32_t *slots, void *q_out,
+                           int64_t out_stride, const qmm_paged_cache *cache, qmm_stream_t stream) {
+  const char *op = "qmm_rope_append";
+  qmm::PagedPool pool;
+  qmm_status st;
+  if ((st = check_cache(op, cache, q_heads, &pool)) != QMM_OK) return st;
+  if (!count31(tokens)) return fail(QMM_ERR_INVALID_ARG, "%s: tokens must be in [0, 2^31)", op);
+  if (!count31(max_positions) || max_positions < 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: max_positions must be in [1, 2^31)", op);
+  if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > pool.head_dim)
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: rotary_dim %d must be a positive multiple of 16, at most head_dim %d", op,
+                rotary_dim, pool.head_dim);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1, got %d", op, interleaved);
+  if (axes < 1 || axes > 4 || !sections)
+    return fail(QMM_ERR_INVALID_ARG, "%s: 1 to 4 axes with their sections, got %d", op, axes);
+  int64_t sum = 0;
+  for (int i = 0; i < axes; ++i) {
+    if (sections[i] < 0) return fail(QMM_ERR_INVALID_ARG, "%s: a section is negative", op);
+    sum += sections[i];
+  }
+  if (sum != rotary_dim / 2)
+    return fail(QMM_ERR_INVALID_ARG, "%s: the sections sum to %lld, not rotary_dim / 2 = %d", op,
+                (long long)sum, rotary_dim / 2);
+  const int64_t qw = static_cast<int64_t>(q_heads) * pool.head_dim;
+  const int64_t kw = static_cast<int64_t>(pool.heads) * pool.head_dim;
+  if ((st = check_rows(op, "q", q, q_stride, qw, tokens)) != QMM_OK) return st;
+  if ((st = check_rows(op, "k", k, k_stride, kw, tokens)) != QMM_OK) return st;
+  if ((st = check_rows(op, "v", v, v_stride, kw, tokens)) != QMM_OK) return st;
+  if ((st = check_rows(op, "q_out", q_out, out_stride, qw, tokens)) != QMM_OK) return st;
+  if (q == q_out && q_stride != out_stride)
+    return fail(QMM_ERR_INVALID_ARG, "%s: q_out may be q only with the same stride", op);
+  if (tokens == 0) return QMM_OK;
+  if (!positions || !aligned16(positions) || !slots || !aligned16(slots) || !cos_sin || !aligned16(cos_sin))
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: positions, slots and cos_sin must be non-null and 16-byte aligned", op);
+  return cuda_status(qmm::launch_rope_append(q, q_stride, k, k_stride, v, v_stride,
+                                             static_cast<int>(tokens), q_heads, positions, axes,
+                                             sections, cos_sin, static_cast<int>(max_positions),
+                                             rotary_dim, interleaved != 0, slots, q_out, out_stride,
+                                             pool, reinterpret_cast<cudaStream_t>(stream)),
+                     op);
+}
+
+qmm_status qmm_paged_attention(const void *q, int64_t q_stride, int64_t tokens, int q_heads,
+                               const qmm_paged_cache *cache, const int32_t *block_table,
+                               int64_t table_stride, const int32_t *starts,
+                               const int32_t *seq_lens, int64_t requests, int64_t max_new,
+                               float scale, int causal, int64_t window, void *out,
+                               int64_t out_stride, float *lse, void *workspace,
+                               int64_t workspace_bytes, qmm_stream_t stream) {
+  const char *op = "qmm_paged_attention";
+  qmm::PagedPool pool;
+  qmm_status st;
+  if ((st = check_cache(op, cache, q_heads, &pool)) != QMM_OK) return st;
+  if (!count31(tokens) || !count31(requests) || !count31(max_new) || !count31(window))
+    return fail(QMM_ERR_INVALID_ARG, "%s: tokens, requests, max_new and window must be in [0, 2^31)", op);
+  if (table_stride < 1) return fail(QMM_ERR_INVALID_ARG, "%s: table_stride must be at least 1", op);
+  if (causal != 0 && causal != 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: causal must be 0 or 1, got %d", op, causal);
+  if (!std::isfinite(scale)) return fail(QMM_ERR_INVALID_ARG, "%s: scale is not finite", op);
+  const int64_t width = static_cast<int64_t>(q_heads) * pool.head_dim;
+  if ((st = check_rows(op, "q", q, q_stride, width, tokens)) != QMM_OK) return st;
+  if ((st = check_rows(op, "out", out, out_stride, width, tokens)) != QMM_OK) return st;
+  if (tokens == 0 || requests == 0) return QMM_OK;
+  if (!block_table || !aligned16(block_table) || !starts || !aligned16(starts) || !seq_lens ||
+      !aligned16(seq_lens))
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: block_table, starts and seq_lens must be non-null and 16-byte aligned", op);
+  if (lse && !aligned16(lse)) return fail(QMM_ERR_INVALID_ARG, "%s: lse must be 16-byte aligned", op);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < QMM_ATTENTION_WORKSPACE_BYTES)
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: the workspace must be 16-byte aligned and at least %d bytes, got %lld", op,
+                QMM_ATTENTION_WORKSPACE_BYTES, (long long)workspace_bytes);
+  return cuda_status(qmm::launch_paged_attention(q, q_stride, static_cast<int>(tokens), q_heads, pool,
+                                                 block_table, table_stride, starts, seq_lens,
+                                                 static_cast<int>(requests), max_new, scale,
+                                                 causal != 0, static_cast<int>(window), out,
+                                                 out_stride, lse, workspace,
+                                                 static_cast<size_t>(workspace_bytes),
+                                                 reinterpret_cast<cudaStream_t>(stream)),
+                     op);
+}
+
 qmm_status qmm_get_device_error(qmm_stream_t stream) {
   unsigned bits = 0;
   cudaError_t e = qmm::take_device_error(reinterpret_cast<cudaStream_t>(stream), &bits);
@@ -463,7 +632,7 @@ qmm_status qmm_get_device_error(qmm_stream_t stream) {
   if (bits & qmm::kErrTimeoutBit)
     return fail(QMM_ERR_TIMEOUT, "qmm_get_device_error: a bounded wait inside a kernel ran out");
   if (bits & qmm::kErrIndexBit)
-    return fail(QMM_ERR_INDEX, "qmm_get_device_error: a qmm_rows index was outside its table");
+    return fail(QMM_ERR_INDEX, "qmm_get_device_error: an index on the device was outside its table");
   return QMM_OK;
 }
 

@@ -142,4 +142,37 @@ cudaError_t launch_gemm_static_scratch(const uint16_t *x, int64_t M, const Packe
                                        bool transpose, void *y, bool y_bf16, float *scratch,
                                        cudaStream_t stream, size_t *needed);
 
+// A paged cache (qmm_paged_cache): K and V pools of num_pages pages, strides in
+// elements of `type`.
+struct PagedPool {
+  void *k, *v;
+  int type;
+  int64_t num_pages;
+  int page_size, heads, head_dim;
+  int64_t page_stride, head_stride, token_stride;
+};
+
+// page_plan.cu
+cudaError_t launch_page_plan(const int *past, const int *fresh, int requests, const int *free_pages,
+                             int free_count, const int *next_in, int page, int *table,
+                             int64_t table_stride, int tokens, int *starts, int *seq, int *positions,
+                             int *slots, int *next_out, cudaStream_t stream);
+
+// rope_append.cu
+cudaError_t launch_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                               const void *v, int64_t v_stride, int tokens, int q_heads,
+                               const int *positions, int axes, const int *sections,
+                               const float *cos_sin, int max_positions, int rotary_dim,
+                               bool interleaved, const int *slots, void *q_out, int64_t out_stride,
+                               const PagedPool &pool, cudaStream_t stream);
+
+// paged_attention.cu: the attention kernel(s) for the call's type, head size
+// and lengths.
+cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, int q_heads,
+                                   const PagedPool &pool, const int *table, int64_t table_stride,
+                                   const int *starts, const int *seq, int requests, int64_t max_new,
+                                   float scale, bool causal, int window, void *out,
+                                   int64_t out_stride, float *lse, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
 }  // namespace qmm

@@ -1,0 +1,54 @@
+// qmm_paged_attention: which kernel serves a call.
+#include "paged.cuh"
+
+namespace qmm {
+
+cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, int q_heads,
+                                   const PagedPool &pool, const int *table, int64_t table_stride,
+                                   const int *starts, const int *seq, int requests, int64_t max_new,
+                                   float scale, bool causal, int window, void *out,
+                                   int64_t out_stride, float *lse, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream) {
+  paged::AttnArgs a{};
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = pool.k;
+  a.v = pool.v;
+  a.page_stride = pool.page_stride;
+  a.head_stride = pool.head_stride;
+  a.token_stride = pool.token_stride;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.starts = starts;
+  a.seq = seq;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.lse = lse;
+  a.err = device_error_word();
+  if (!a.err) return cudaErrorInvalidSymbol;
+  a.spin_limit = wait_limit();
+  a.page = pool.page_size;
+  a.num_pages = static_cast<int>(pool.num_pages);
+  a.T = tokens;
+  a.B = requests;
+  a.Hq = q_heads;
+  a.Hkv = pool.heads;
+  a.G = q_heads / pool.heads;
+  a.D = pool.head_dim;
+  const int64_t keys = table_stride < 0x7FFFFFFF / pool.page_size ? table_stride * pool.page_size : 0x7FFFFFFF;
+  a.max_keys = static_cast<int>(keys);
+  a.causal = causal;
+  a.window = window;
+  a.scale_log2 = scale * paged::kLog2e;
+  a.min_rows = 0;
+  a.max_rows = 0x7FFFFFFF;
+  // The workspace: block descriptors first, then the pieces of cut items.
+  constexpr size_t kDescBytes = 64 << 10;
+  a.desc = static_cast<int *>(workspace);
+  a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + kDescBytes);
+  const size_t ws_bytes = workspace_bytes - kDescBytes;
+  (void)max_new;
+  return launch_attention_tiles(a, pool.type, ws_bytes, stream);
+}
+
+}  // namespace qmm

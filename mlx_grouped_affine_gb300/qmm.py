@@ -18,9 +18,26 @@ EXPORTS = ("qmm_quantize", "qmm_dequantize", "qmm_quantized_matmul", "qmm_quanti
            "qmm_gather_qmm", "qmm_gemv_gate_up", "qmm_gemv_silu_gate", "qmm_rows",
            "qmm_last_error", "qmm_get_device_error", "qmm_set_launch_flags", "qmm_set_wait_limit",
            "qmm_promote_types", "qmm_dequantize_typed", "qmm_rows_typed", "qmm_quantize_typed",
-           "qmm_quantized_matmul_typed")
+           "qmm_quantized_matmul_typed", "qmm_page_plan", "qmm_rope_append", "qmm_paged_attention")
+QMM_ATTENTION_WORKSPACE_BYTES = 64 << 20
 
 _lib = None
+
+
+class PagedCache(ctypes.Structure):
+    """qmm_paged_cache: pools of K and V pages (tensors or addresses), strides in
+    elements of page, head and token.  Keeps its tensors alive."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+    def __init__(self, k, v, dtype, num_pages, page_size, heads, head_dim, page_stride,
+                 head_stride, token_stride):
+        super().__init__(_ptr(k), _ptr(v), dtype, num_pages, page_size, heads, head_dim,
+                         page_stride, head_stride, token_stride)
+        self.pools = (k, v)
 
 
 class QmmError(RuntimeError):
@@ -50,7 +67,14 @@ def lib():
         L.qmm_rows_typed.argtypes = [P, P, P, I, I64, I64, P, I64, I, I, P, I, P]
         L.qmm_quantize_typed.argtypes = [P, I, I64, I64, I, I, P, P, P, P]
         L.qmm_quantized_matmul_typed.argtypes = [P, I, I64, P, P, P, I, I64, I64, I, I, I, P, I, P]
-        for f in ("qmm_quantize", "qmm_dequantize", "qmm_quantized_matmul", "qmm_quantized_matmul_noalloc",
+        C, F = ctypes.POINTER(PagedCache), ctypes.c_float
+        L.qmm_page_plan.argtypes = [P, P, I64, P, I64, P, I, P, I64, I64, P, P, P, P, P, P]
+        L.qmm_rope_append.argtypes = [P, I64, P, I64, P, I64, I64, I, P, I, ctypes.POINTER(ctypes.c_int32),
+                                      P, I64, I, I, P, P, I64, C, P]
+        L.qmm_paged_attention.argtypes = [P, I64, I64, I, C, P, I64, P, P, I64, I64, F, I, I64, P,
+                                          I64, P, P, I64, P]
+        for f in ("qmm_page_plan", "qmm_rope_append", "qmm_paged_attention",
+                  "qmm_quantize", "qmm_dequantize", "qmm_quantized_matmul", "qmm_quantized_matmul_noalloc",
                   "qmm_gather_qmm", "qmm_gemv_gate_up", "qmm_gemv_silu_gate", "qmm_rows",
                   "qmm_get_device_error", "qmm_promote_types", "qmm_dequantize_typed",
                   "qmm_rows_typed", "qmm_quantize_typed", "qmm_quantized_matmul_typed"):
@@ -201,3 +225,37 @@ def qmm_quantized_matmul_typed(x, x_dtype, M, w, scales, biases, sb_dtype, N, K,
     _check(lib().qmm_quantized_matmul_typed(_ptr(x), x_dtype, M, _ptr(w), _ptr(scales),
                                             _ptr(biases), sb_dtype, N, K, int(transpose),
                                             group_size, bits, _ptr(y), y_dtype, _stream(stream)))
+
+
+def qmm_page_plan(past_lens, new_lens, requests, free_pages, free_count, next_free, page_size,
+                  block_table, table_stride, tokens, starts, seq_lens, positions, slots,
+                  next_free_out, stream=None):
+    """Block table, slot map and positions of a step from the requests' lengths."""
+    _check(lib().qmm_page_plan(_ptr(past_lens), _ptr(new_lens), requests, _ptr(free_pages),
+                               free_count, _ptr(next_free), page_size, _ptr(block_table),
+                               table_stride, tokens, _ptr(starts), _ptr(seq_lens),
+                               _ptr(positions), _ptr(slots), _ptr(next_free_out),
+                               _stream(stream)))
+
+
+def qmm_rope_append(q, q_stride, k, k_stride, v, v_stride, tokens, q_heads, positions, sections,
+                    cos_sin, max_positions, rotary_dim, interleaved, slots, q_out, out_stride,
+                    cache, stream=None):
+    """Rotary positions on q and k, and k and v into the cache (a PagedCache);
+    sections: the frequency pairs of each position axis, host integers."""
+    axes = len(sections)
+    _check(lib().qmm_rope_append(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, tokens,
+                                 q_heads, _ptr(positions), axes, (ctypes.c_int32 * axes)(*sections),
+                                 _ptr(cos_sin), max_positions, rotary_dim, int(interleaved),
+                                 _ptr(slots), _ptr(q_out), out_stride, cache, _stream(stream)))
+
+
+def qmm_paged_attention(q, q_stride, tokens, q_heads, cache, block_table, table_stride, starts,
+                        seq_lens, requests, max_new, scale, causal, window, out, out_stride, lse,
+                        workspace, workspace_bytes, stream=None):
+    """Attention of each request's new tokens over its pages of a PagedCache; the
+    workspace is at least QMM_ATTENTION_WORKSPACE_BYTES of device memory."""
+    _check(lib().qmm_paged_attention(_ptr(q), q_stride, tokens, q_heads, cache, _ptr(block_table),
+                                     table_stride, _ptr(starts), _ptr(seq_lens), requests, max_new,
+                                     scale, int(causal), window, _ptr(out), out_stride, _ptr(lse),
+                                     _ptr(workspace), workspace_bytes, _stream(stream)))
