@@ -518,5 +518,7 @@ cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
 
 // paged_tiles.cu: every type and head size on the CUDA cores.
 cudaError_t launch_attention_tiles(paged::AttnArgs a, int type, size_t ws_bytes, cudaStream_t stream);
+// paged_decode.cu: 16-bit types, heads of at most 128, few rows per kv head.
+cudaError_t launch_attention_decode(const paged::AttnArgs &a, int type, size_t ws_bytes, cudaStream_t stream);
 
 }  // namespace qmm

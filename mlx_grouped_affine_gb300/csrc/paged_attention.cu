@@ -48,6 +48,7 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
   a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + kDescBytes);
   const size_t ws_bytes = workspace_bytes - kDescBytes;
   (void)max_new;
+  if (pool.type != kTypeF32 && a.D <= 128) return launch_attention_decode(a, pool.type, ws_bytes, stream);
   return launch_attention_tiles(a, pool.type, ws_bytes, stream);
 }
 
