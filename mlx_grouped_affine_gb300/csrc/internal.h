@@ -44,6 +44,10 @@ cudaError_t take_device_error(cudaStream_t stream, unsigned *bits);
 cudaError_t encode_map_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base,
                           uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                           uint32_t box_outer, CUtensorMapSwizzle swizzle);
+// The same for four axes, innermost first; stride_bytes[i] is that of axis i + 1.
+cudaError_t encode_map_4d(CUtensorMap *map, CUtensorMapDataType type, const void *base,
+                          const uint64_t (&dims)[4], const uint64_t (&stride_bytes)[3],
+                          const uint32_t (&box)[4], CUtensorMapSwizzle swizzle);
 int sm_count();
 
 // Raise Kern's dynamic shared memory limit on the current device to at least

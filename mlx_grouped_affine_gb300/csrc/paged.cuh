@@ -155,12 +155,21 @@ __device__ __forceinline__ void cursor_next(const AttnArgs &a, Cursor &c) {
   cursor_item<KT>(a, c);
 }
 
+// x * y / z, in 32 bits where the product fits (a 64-bit division costs several
+// times as much and stands in every block's start).
+__device__ __forceinline__ long long mul_div(long long x, long long y, long long z) {
+  const unsigned long long p = static_cast<unsigned long long>(x) * y;
+  if ((p | z) >> 32 == 0) return static_cast<unsigned>(p) / static_cast<unsigned>(z);
+  return static_cast<long long>(p / static_cast<unsigned long long>(z));
+}
+
 template <int NT>
 struct PlanScratch {
   long long warp_sum[NT / 32];
   long long total;
-  long long found_before;  // tiles before the found element
+  long long found_before, found_tiles;  // tiles before the found request, and its own
   int found;
+  unsigned marks[NT / 32];
   Cursor cursor;
 };
 
@@ -210,13 +219,12 @@ __device__ long long request_tiles(const AttnArgs &a, int base, PlanScratch<NT> 
     if (!big) mine = head_tiles<KT>(a, r, 0, 1) * a.heads;
   }
   // Long requests one after another, their items spread over the block.
-  __shared__ unsigned marks[NT / 32];
   const unsigned m = __ballot_sync(0xffffffffu, big);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) marks[threadIdx.x >> 5] = m;
+  if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = m;
   __syncthreads();
   for (int w = 0; w < NT / 32; ++w) {
-    for (unsigned bits = marks[w]; bits; bits &= bits - 1) {
+    for (unsigned bits = s.marks[w]; bits; bits &= bits - 1) {
       const int owner = 32 * w + __ffs(bits) - 1;
       const Request r = request_of(a, base + owner);
       long long total;
@@ -227,11 +235,102 @@ __device__ long long request_tiles(const AttnArgs &a, int base, PlanScratch<NT> 
   return mine;
 }
 
+// The cut item that block `part` continues, for the joining kernel: request,
+// head, item, the blocks that hold the item's first and last tiles, and the
+// request's first token and count (block
+// p holds tile g when p W / parts <= g, so p = ((g + 1) parts - 1) / W).
+__device__ __forceinline__ void leave_desc(const AttnArgs &a, const Cursor &c, int part, long long t0,
+                                           long long parts, long long W) {
+  int *d = a.desc + 8 * part;
+  if (c.at == 0) {
+    d[0] = -1;
+    return;
+  }
+  const long long g0 = t0 - c.at, g1 = g0 + c.tiles - 1;
+  d[0] = c.b;
+  d[1] = c.h;
+  d[2] = c.qt;
+  d[3] = static_cast<int>(mul_div((g0 + 1) * parts - 1, 1, W));
+  d[4] = static_cast<int>(mul_div((g1 + 1) * parts - 1, 1, W));
+  d[5] = c.r.first;
+  d[6] = c.r.n;
+}
+
+__device__ __forceinline__ long long warp_scan(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// plan_block for at most 32 requests: one a lane, every warp for itself, no
+// barrier (the start of a short call is most of it).
+template <int KT>
+__device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
+  const int lane = threadIdx.x & 31;
+  Request r{0, 0, 0};
+  if (lane < a.B) r = request_of(a, lane);
+  const bool big = items_of(a, r) > kOwnItems;
+  long long one = big ? 0 : head_tiles<KT>(a, r, 0, 1);  // tiles of one head slice
+  for (unsigned bits = __ballot_sync(0xffffffffu, big); bits; bits &= bits - 1) {
+    const int owner = __ffs(bits) - 1;
+    const Request o{__shfl_sync(0xffffffffu, r.first, owner), __shfl_sync(0xffffffffu, r.n, owner),
+                    __shfl_sync(0xffffffffu, r.len, owner)};
+    long long n = head_tiles<KT>(a, o, lane, 32);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) n += __shfl_xor_sync(0xffffffffu, n, x);
+    if (lane == owner) one = n;
+  }
+  const long long mine = one * a.heads, incl = warp_scan(mine);
+  const long long W = __shfl_sync(0xffffffffu, incl, 31);
+  const int parts = static_cast<int>(min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks)));
+  Cursor c;
+  c.left = 0;
+  if (part >= parts) {
+    if (threadIdx.x == 0) a.desc[8 * part] = -1;
+    return c;
+  }
+  const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
+  const int b = __ffs(__ballot_sync(0xffffffffu, t0 < incl && t0 >= incl - mine)) - 1;
+  c.r = Request{__shfl_sync(0xffffffffu, r.first, b), __shfl_sync(0xffffffffu, r.n, b),
+                __shfl_sync(0xffffffffu, r.len, b)};
+  c.b = b;
+  const long long in_request = t0 - __shfl_sync(0xffffffffu, incl - mine, b);
+  const long long per_head = __shfl_sync(0xffffffffu, one, b);
+  c.h = static_cast<int>(mul_div(in_request, 1, per_head));
+  const long long in_head = in_request - c.h * per_head;
+  const int items = items_of(a, c.r);
+  long long before = 0;
+  c.qt = 0;
+  c.at = 0;
+  for (int base = 0; base < items; base += 32) {
+    const int q = base + lane;
+    const long long n = q < items ? item_tiles<KT>(a, c.r, q).tiles : 0;
+    const long long upto = warp_scan(n) + before;
+    const unsigned hit = __ballot_sync(0xffffffffu, in_head < upto && in_head >= upto - n);
+    if (hit) {
+      const int at = __ffs(hit) - 1;
+      c.qt = base + at;
+      c.at = static_cast<int>(in_head - __shfl_sync(0xffffffffu, upto - n, at));
+      break;
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  c.left = static_cast<int>(t1 - t0);
+  cursor_item<KT>(a, c);
+  if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
+  return c;
+}
+
 // The block's place in the line: its cursor and how many tiles it has (0: none).
 // Called by all NT threads of block `part` of `blocks`.  Also leaves in
-// desc[part] the cut item that the block continues, for the joining kernel.
+// desc[part] the cut item that the block continues.
 template <int NT, int KT>
 __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratch<NT> &s) {
+  if (a.B <= 32) return plan_warp<KT>(a, part, blocks);
   // Total, keeping the first chunk's counts.
   long long W = 0, total;
   long long kept = 0;
@@ -241,15 +340,14 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
     block_scan<NT>(mine, s, &total);
     W += total;
   }
-  long long parts = (W + a.min_tiles - 1) / a.min_tiles;
-  if (parts > blocks) parts = blocks;
+  const long long parts = min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks));
   Cursor c;
   c.left = 0;
   if (part >= parts) {
     if (threadIdx.x == 0) a.desc[8 * part] = -1;
     return c;
   }
-  const long long t0 = part * W / parts, t1 = (part + 1) * W / parts;
+  const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
   // The request that holds tile t0.
   long long before = 0;
   __syncthreads();
@@ -260,6 +358,7 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
     if (t0 < incl && t0 >= incl - mine) {
       s.found = base + threadIdx.x;
       s.found_before = incl - mine;
+      s.found_tiles = mine;
     }
     before += total;
     if (before > t0) break;
@@ -272,13 +371,14 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   }
   const long long in_request = t0 - s.found_before;
   const Request r = request_of(a, b);
-  // The head (all heads of a request have the same tiles), then the item.
-  block_scan<NT>(head_tiles<KT>(a, r, threadIdx.x, NT), s, &total);
-  const int h = static_cast<int>(in_request / total);
-  const long long in_head = in_request - h * total;
+  // The head (all head slices of a request have the same tiles), then the item.
+  const long long per_head = mul_div(s.found_tiles, 1, a.heads);
+  const int h = static_cast<int>(mul_div(in_request, 1, per_head));
+  const long long in_head = in_request - h * per_head;
   before = 0;
   const int items = items_of(a, r);
   __syncthreads();
+  if (threadIdx.x == 0) s.cursor.qt = s.cursor.at = 0;
   for (int base = 0; base < items; base += NT) {
     const int q = base + threadIdx.x;
     const long long mine = q < items ? item_tiles<KT>(a, r, q).tiles : 0;
@@ -298,21 +398,7 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   c.at = s.cursor.at;
   c.left = static_cast<int>(t1 - t0);
   cursor_item<KT>(a, c);
-  if (threadIdx.x == 0) {
-    int *d = a.desc + 8 * part;
-    if (c.at == 0) {
-      d[0] = -1;
-    } else {
-      // The blocks that hold the item's first and last tiles: block p holds
-      // tile g when p W / parts <= g, so p = ((g + 1) parts - 1) / W.
-      const long long g0 = t0 - c.at, g1 = g0 + c.tiles - 1;
-      d[0] = c.b;
-      d[1] = c.h;
-      d[2] = c.qt;
-      d[3] = static_cast<int>(((g0 + 1) * parts - 1) / W);
-      d[4] = static_cast<int>(((g1 + 1) * parts - 1) / W);
-    }
-  }
+  if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
   return c;
 }
 
@@ -349,6 +435,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// The page of the pool that holds entry pg of request b's table; num_pages, past
+// the pool's end, where the table holds none of it: its keys then read as zero
+// and the index bit is set.
+__device__ __forceinline__ int page_of(const AttnArgs &a, int b, int pg) {
+  const int id = __ldg(a.table + b * a.table_stride + pg);
+  if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_pages)) return id;
+  atomicOr(a.err, kErrIndexBit);
+  return a.num_pages;
+}
+
+// A box of 64 columns and some rows of a page's head from the pool's tensor map
+// (columns, rows, heads, pages); columns past the head and pages past the pool
+// read as zeros.
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int col, int row, int head,
+                                         int page, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(col), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Element offset of key j of request b's head h, or -1 where the table holds
 // no page of the pool (the key then reads as zero and the index bit is set).
 __device__ __forceinline__ int64_t key_offset(const AttnArgs &a, int b, int h, int j) {
@@ -361,12 +469,12 @@ __device__ __forceinline__ int64_t key_offset(const AttnArgs &a, int b, int h, i
   return id * a.page_stride + row * a.token_stride + h * a.head_stride;
 }
 
-// One output row by one warp, from the keys it sees alone.  The tiled kernels
+// Columns [d0, d1) of an output row by one warp, from the keys it sees alone.  The tiled kernels
 // multiply masked keys by weight zero, which is no longer nothing when such a
 // key's V is not finite; a row that came out non-finite is done again here,
 // where a key that the row does not see is never read.
 template <typename E>
-__device__ __noinline__ void row_alone(const AttnArgs &a, int b, int head, int i) {
+__device__ __noinline__ void row_alone(const AttnArgs &a, int b, int head, int i, int d0, int d1) {
   using T = typename Elem<E>::type;
   const int lane = threadIdx.x & 31;
   const Request r = request_of(a, b);
@@ -409,7 +517,7 @@ __device__ __noinline__ void row_alone(const AttnArgs &a, int b, int head, int i
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int d = 0; d < 8; ++d)
-    if (d < n && lane + 32 * d < a.D) out[lane + 32 * d] = Elem<E>::from_f32(o[d] * inv);
+    if (lane + 32 * d >= d0 && lane + 32 * d < d1) out[lane + 32 * d] = Elem<E>::from_f32(o[d] * inv);
 }
 
 // A piece of a cut item in the workspace: R rows of DP sums, their maxima and
@@ -420,81 +528,149 @@ __device__ __forceinline__ float *slot_of(const AttnArgs &a, int block, int begi
   return a.ws + (2 * static_cast<int64_t>(block) + begins) * (R * (DP + 2));
 }
 
-// Joins the pieces of each cut item, in block order.  Block (c, y) has 16 rows
-// of the item that attention block c continues, when c is the first to
-// continue it.  Bytes: each piece read once; a warp per row, 16 bytes a lane.
+// Joins the pieces of each cut item.  An item in P pieces is continued by
+// P - 1 blocks of the attention kernel, and the P - 1 blocks here of the same
+// numbers share its R x DP sums: the more pieces, the more blocks, so that each
+// reads about R x DP sums whatever P is.  Inside a block up to 16 lanes share a
+// column's pieces (the reads of one are in flight together) and join in lane
+// order: the order of the sums is fixed by P alone.  Joining 6 items of 51
+// pieces took 27 us with a warp per row and takes 3 this way.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinLanes = 16;
+
+// Weights that a block keeps: rows it touches x pieces.
+template <int R>
+constexpr int join_weights(int blocks) { return 2 * R + 3 * blocks; }
+
 template <typename E, int R, int DP>
-__global__ void __launch_bounds__(128) join_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
   using T = typename Elem<E>::type;
+  extern __shared__ float weight[];  // [rows][P]
+  __shared__ float4 sums[kJoinThreads];
+  __shared__ unsigned bad_rows[(R + 31) / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_wait();
-  const int c = blockIdx.x + 1;
-  const int *d = a.desc + 8 * c;
-  const int b = d[0];
-  if (b < 0 || d[3] != c - 1) return;
-  const int h = d[1], qt = d[2], first = d[3], last = d[4];
-  const Request r = request_of(a, b);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int V = (DP + 127) / 128;  // float4s a lane
-  for (int row = blockIdx.y * 16 + warp; row < min(R, (static_cast<int>(blockIdx.y) + 1) * 16); row += 4) {
+  const int4 *d = reinterpret_cast<const int4 *>(a.desc + 8 * (blockIdx.x + 1));
+  const int4 d0 = d[0], d1 = d[1];
+  const int b = d0.x, h = d0.y, qt = d0.z, first = d0.w, last = d1.x;
+  if (b < 0) return;
+  const Request r{d1.y, d1.z, 0};
+  const int P = last - first + 1, me = blockIdx.x - first;
+  constexpr int U = R * DP / 4, UR = DP / 4;  // float4 sums of an item, of a row
+  const int u0 = static_cast<int>(static_cast<unsigned>(me * U) / static_cast<unsigned>(P - 1));
+  const int u1 = static_cast<int>(static_cast<unsigned>((me + 1) * U) / static_cast<unsigned>(P - 1));
+  if (u0 >= u1) return;  // more blocks than sums
+  const int row0 = u0 / UR, rows = (u1 - 1) / UR + 1 - row0;
+  const int lanes = min(P, kJoinLanes), cols = kJoinThreads / lanes;
+  const int tc = tid % cols, j = tid / cols;
+  // The first columns' sums, in flight while the weights are worked out.
+  constexpr int kAhead = 4;
+  float4 early[kAhead];
+  {
+    const int u = min(u0 + tc, u1 - 1), row = u / UR, col = (u - row * UR) * 4;
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int p = j + x * lanes;
+      if (j < lanes && p < P)
+        early[x] = *reinterpret_cast<const float4 *>(slot_of<R, DP>(a, first + p, p == 0) + row * DP + col);
+    }
+  }
+  if (tid < (R + 31) / 32) bad_rows[tid] = 0;
+  // A warp per row: the row's maximum and sum, then each piece's share.
+  for (int x = warp; x < rows; x += kJoinThreads / 32) {
+    int i, head;
+    if (!row_of(a, r, h, qt, row0 + x, &i, &head)) continue;
+    float m = kNegInf, l = 0.f;
+    float l0 = 0.f;  // the sum of the lane's first piece, read beside its maximum
+    for (int p = lane; p < P; p += 32) {
+      const float *s = slot_of<R, DP>(a, first + p, p == 0) + R * DP + row0 + x;
+      const float v = s[0];
+      if (p == lane) l0 = s[R];
+      weight[x * P + p] = v;
+      m = fmaxf(m, v);
+    }
+#pragma unroll
+    for (int y = 16; y; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+    const float base = m == kNegInf ? 0.f : m;
+    for (int p = lane; p < P; p += 32) {
+      const float w = exp2f(weight[x * P + p] - base);
+      l += w * (p == lane ? l0 : slot_of<R, DP>(a, first + p, p == 0)[R * DP + R + row0 + x]);
+      weight[x * P + p] = w;
+    }
+#pragma unroll
+    for (int y = 16; y; y >>= 1) l += __shfl_xor_sync(0xffffffffu, l, y);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int p = lane; p < P; p += 32) weight[x * P + p] *= inv;
+    if (lane == 0 && a.lse && (row0 + x) * UR >= u0)
+      a.lse[(static_cast<int64_t>(r.first) + i) * a.Hq + head] = (m + log2f(l)) * kLn2;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int c0 = u0; c0 < u1; c0 += cols) {
+    const int u = c0 + tc;
+    const int row = u / UR, col = (u - row * UR) * 4;
+    int i = 0, head = 0;
+    const bool live = u < u1 && j < lanes && col < a.D && row_of(a, r, h, qt, row, &i, &head);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      const float *w = weight + (row - row0) * P;
+      if (c0 != u0) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+          const int p = j + x * lanes;
+          if (p < P)
+            early[x] = *reinterpret_cast<const float4 *>(slot_of<R, DP>(a, first + p, p == 0) + row * DP + col);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int p = j + x * lanes;
+        if (p < P) {
+          o.x += w[p] * early[x].x;
+          o.y += w[p] * early[x].y;
+          o.z += w[p] * early[x].z;
+          o.w += w[p] * early[x].w;
+        }
+      }
+#pragma unroll 4
+      for (int p = j + kAhead * lanes; p < P; p += lanes) {
+        const float4 x = *reinterpret_cast<const float4 *>(slot_of<R, DP>(a, first + p, p == 0) + row * DP + col);
+        o.x += w[p] * x.x;
+        o.y += w[p] * x.y;
+        o.z += w[p] * x.z;
+        o.w += w[p] * x.w;
+      }
+    }
+    __syncthreads();
+    sums[tid] = o;
+    __syncthreads();
+    if (live && j == 0) {
+      for (int y = 1; y < lanes; ++y) {
+        const float4 x = sums[y * cols + tid];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+      }
+      T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(r.first) + i) * a.out_stride +
+               static_cast<int64_t>(head) * a.D + col;
+      out[0] = Elem<E>::from_f32(o.x);
+      out[1] = Elem<E>::from_f32(o.y);
+      out[2] = Elem<E>::from_f32(o.z);
+      out[3] = Elem<E>::from_f32(o.w);
+      if (!(isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w)))
+        atomicOr(&bad_rows[row / 32], 1u << (row & 31));
+    }
+  }
+  __syncthreads();
+  for (int x = warp; x < rows; x += kJoinThreads / 32) {
+    const int row = row0 + x;
+    if (!(bad_rows[row / 32] >> (row & 31) & 1u)) continue;
     int i, head;
     if (!row_of(a, r, h, qt, row, &i, &head)) continue;
-    float m = kNegInf;
-    for (int p = first + lane; p <= last; p += 32)
-      m = fmaxf(m, slot_of<R, DP>(a, p, p == first)[R * DP + row]);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const float base = m == kNegInf ? 0.f : m;
-    float l = 0.f;
-    float4 o[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = first; p0 <= last; p0 += 32) {
-      float w = 0.f, wl = 0.f;
-      if (p0 + lane <= last) {
-        const float *s = slot_of<R, DP>(a, p0 + lane, p0 + lane == first) + R * DP + row;
-        w = exp2f(s[0] - base);
-        wl = w * s[R];
-      }
-      const int n = min(32, last - p0 + 1);
-#pragma unroll 4
-      for (int p = 0; p < n; ++p) {
-        const float wp = __shfl_sync(0xffffffffu, w, p);
-        l += __shfl_sync(0xffffffffu, wl, p);
-        const float *s = slot_of<R, DP>(a, p0 + p, p0 + p == first) + row * DP;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (128 * j + 4 * lane < DP) {
-            const float4 x = *reinterpret_cast<const float4 *>(s + 128 * j + 4 * lane);
-            o[j].x += wp * x.x;
-            o[j].y += wp * x.y;
-            o[j].z += wp * x.z;
-            o[j].w += wp * x.w;
-          }
-        }
-      }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(r.first) + i) * a.out_stride +
-             static_cast<int64_t>(head) * a.D;
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int col = 128 * j + 4 * lane;
-      const float y[4] = {o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (col < a.D) {
-          out[col + e] = Elem<E>::from_f32(y[e]);
-          bad |= !isfinite(y[e]);
-        }
-      }
-    }
-    if (lane == 0 && a.lse)
-      a.lse[(static_cast<int64_t>(r.first) + i) * a.Hq + head] = (m + log2f(l)) * kLn2;
-    if (__any_sync(0xffffffffu, bad)) {
-      __syncwarp();
-      row_alone<E>(a, b, head, i);
-    }
+    // This block's columns of the row.
+    const int from = max(u0, row * UR), to = min(u1, (row + 1) * UR);
+    row_alone<E>(a, b, head, i, 4 * (from - row * UR), min(a.D, 4 * (to - row * UR)));
   }
 }
 
@@ -503,8 +679,9 @@ template <typename E, int R, int DP>
 cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks - 1, (R + 15) / 16);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(blocks - 1);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = sizeof(float) * join_weights<R>(blocks);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -514,6 +691,14 @@ cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, join_kernel<E, R, DP>, a);
 }
 
+}  // namespace paged
+
+namespace paged {
+// Maps of the K and V pools with boxes of 64 columns x box_rows rows, 128-byte
+// swizzle.  box_rows is the largest power of two that divides the page size, at
+// most `most`: boxes then never cross a page.
+cudaError_t pool_maps(const AttnArgs &a, int type, int box_rows, CUtensorMap *k, CUtensorMap *v);
+int box_rows(int page, int most);
 }  // namespace paged
 
 // paged_tiles.cu: every type and head size on the CUDA cores.

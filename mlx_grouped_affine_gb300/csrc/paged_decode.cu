@@ -3,43 +3,37 @@
 // A decode step reads every visible key and value once and does 4 G flops a
 // byte-pair, so HBM bounds it: the kernel's work is to keep loads in flight.
 // An item is 16 rows (TQ new tokens x the group's heads: one tensor-core tile
-// of rows), a key tile 64 keys, 16 for each of the block's four warps.  A warp
-// streams its keys through a ring of its own (cp.async, 16 bytes a lane, rows
-// swizzled by 16-byte chunks), so no barrier stands in the stream; the load
-// cursor runs ahead of the compute cursor across item ends, and a key's page
-// is looked up one step before its rows are fetched.  Scores and output are
-// mma.sync m16n8k16 with fp32 accumulators: at these arithmetic intensities
-// its rate is far from the bound.  Each warp has its own running maximum and
-// sum; the four join in shared memory when the item ends.
+// of rows); a key tile is KW keys for each of the block's four warps.  A warp
+// streams its keys through a ring of its own (TMA boxes of a page's rows into
+// 128-byte swizzled shared memory, one mbarrier a stage), so nothing in the
+// stream waits for another warp; the load cursor runs ahead of the compute
+// cursor across item ends.  Page ids are read a window of up to 32 boxes at a
+// time, one a lane, and a window ahead of their use: a table entry costs a trip
+// to L2 or HBM (0.6 to 1.5 us) that would otherwise stand before every step.  KW is 16 keys for heads of 128 and 32 for heads of 64: 8
+// KB a stage, six stages of two blocks an SM in flight.  Scores and output are
+// mma.sync m16n8k16 with fp32 accumulators: at these intensities its rate is
+// far from the bound.  Each warp has its own running maximum and sum; the four
+// join in shared memory when the item ends.
 #include "paged.cuh"
 
 namespace qmm {
 namespace paged {
 namespace {
 
-constexpr int R = 16, KW = 16, kWarps = 4, KT = KW * kWarps, NT = 32 * kWarps;
+constexpr int R = 16, kWarps = 4, NT = 32 * kWarps, ST = 3;
 
 template <int DP>
-__host__ __device__ constexpr int stages() { return DP == 128 ? 3 : 6; }
-template <int DP>
-__host__ __device__ constexpr uint32_t half_bytes() { return KW * DP * 2; }  // K or V of a step
-template <int DP>
-constexpr size_t smem_bytes() {
-  return static_cast<size_t>(kWarps) * stages<DP>() * 2 * half_bytes<DP>() + 2 * R * DP * sizeof(float) +
-         2 * kWarps * R * sizeof(float);
-}
-
-// 16 bytes global -> shared, or zeros.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+struct Tile {
+  static constexpr int KW = 2048 / DP;               // keys of a warp's step
+  static constexpr int KT = KW * kWarps;             // keys of a tile
+  static constexpr uint32_t COLS = KW * 128;         // 64 columns of K or V of a step
+  static constexpr uint32_t HALF = COLS * (DP / 64); // K or V of a step
+  static constexpr uint32_t STAGE = 2 * HALF;
+  static constexpr uint32_t RINGS = kWarps * ST * STAGE;
+  // rings, joined output [2][R][DP], statistics [2][warps][R], barriers
+  static constexpr size_t SMEM = RINGS + 2 * R * DP * 4 + 2 * kWarps * R * 4 + kWarps * ST * 8;
+};
+static_assert(sizeof(PlanScratch<NT>) <= 2 * R * 64 * 4, "the plan's scratch lies in the output's room");
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -70,60 +64,99 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The offset of the key that this lane looks up for the warp's step at the
-// cursor (lanes 0-15 one key each), -1 where no row of the item sees one.
-__device__ __forceinline__ int64_t lane_offset(const AttnArgs &a, const Cursor &c, int warp, int lane) {
-  if (c.left <= 0) return -1;
-  const int key = (c.tile0 + c.at) * KT + warp * KW + (lane & 15);
-  return key >= c.lo && key < c.hi ? key_offset(a, c.b, c.h / a.S, key) : -1;
+// The pages of the warp's next steps of one item: lane l has box l % boxes of
+// step l / boxes (row -1: no key of the item there).
+struct Window {
+  int id, row;
+  int steps, kv;
+};
+template <int DP>
+__device__ __forceinline__ Window next_window(const AttnArgs &a, Cursor &c, int boxes, int box, int warp, int lane) {
+  using X = Tile<DP>;
+  Window w{0, -1, 0, 0};
+  if (c.left <= 0) return w;
+  w.steps = min(min(32 / boxes, c.left), c.tiles - c.at);
+  w.kv = c.h / a.S;
+  const int step = lane / boxes;
+  const int key = (c.tile0 + c.at + step) * X::KT + warp * X::KW + (lane - step * boxes) * box;
+  if (step < w.steps && key + box > c.lo && key < c.hi) {
+    const int pg = key / a.page;
+    w.row = key - pg * a.page;
+    w.id = __ldg(a.table + c.b * a.table_stride + pg);
+  }
+  c.left -= w.steps;
+  c.at += w.steps;
+  if (c.at == c.tiles && c.left > 0) cursor_next<X::KT>(a, c);
+  return w;
 }
 
-// One tile on; to the next item when this one ends.
-__device__ __forceinline__ void cursor_step(const AttnArgs &a, Cursor &c) {
-  --c.left;
-  if (++c.at == c.tiles && c.left > 0) cursor_next<KT>(a, c);
+// Bounded wait of a whole warp; false when it ran out.
+__device__ __forceinline__ bool wait_stage(uint64_t *bar, uint32_t parity, uint32_t limit) {
+  for (uint32_t spin = 0; spin < limit; ++spin)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return false;
 }
 
 template <typename E, int DP>
-__global__ void __launch_bounds__(NT, 2) decode_kernel(AttnArgs a) {
-  constexpr int ST = stages<DP>(), CH = DP / 8, KS = DP / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
-  float *obuf = reinterpret_cast<float *>(smem + kWarps * ST * 2 * half_bytes<DP>());  // [2][R][DP]
-  float *wm = obuf + 2 * R * DP, *wl = wm + kWarps * R;                              // [warps][R]
-  __shared__ PlanScratch<NT> scratch;
-  griddep_launch_dependents();
-  Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, scratch);
-  if (c.left <= 0) return;
+__global__ void __launch_bounds__(NT, 2)
+decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
+              int box) {
+  using X = Tile<DP>;
+  constexpr int KW = X::KW, KT = X::KT, NC = KW / 8, KS = DP / 16;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float *obuf = reinterpret_cast<float *>(smem + X::RINGS);  // [2][R][DP]
+  float *wm = obuf + 2 * R * DP, *wl = wm + kWarps * R;      // [warps][R]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t ring = smem_u32(smem) + warp * ST * 2 * half_bytes<DP>();
-  const uint16_t *gk = static_cast<const uint16_t *>(a.k), *gv = static_cast<const uint16_t *>(a.v);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(wl + kWarps * R) + warp * ST;
+  griddep_launch_dependents();
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < ST; ++s) mbar_init(&bars[s], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, *reinterpret_cast<PlanScratch<NT> *>(obuf));
+  if (c.left <= 0) return;
+  const uint32_t ring = smem_u32(smem) + warp * ST * X::STAGE;
 
-  Cursor ahead = c;  // where the loads are
-  int64_t off = lane_offset(a, ahead, warp, lane);
-  auto issue = [&](int stage) {
-    if (ahead.left > 0) {
-      const uint32_t dst = ring + stage * 2 * half_bytes<DP>();
-#pragma unroll
-      for (int i = 0; i < KW * CH / 32; ++i) {
-        const int id = i * 32 + lane, row = id / CH, ch = id % CH;
-        const int64_t o = __shfl_sync(0xffffffffu, off, row);
-        const bool valid = o >= 0 && ch * 8 < a.D;
-        const int64_t src = valid ? o + ch * 8 : 0;
-        const uint32_t at = row * (DP * 2) + ((ch ^ (row & 7)) << 4);
-        cp_async16(dst + at, gk + src, valid);
-        cp_async16(dst + half_bytes<DP>() + at, gv + src, valid);
-      }
-      cursor_step(a, ahead);
-      off = lane_offset(a, ahead, warp, lane);
+  Cursor ahead = c;  // where the page lookups are
+  const int boxes = KW / box, copies = boxes * (a.D > 64 ? 2 : 1) * 2;
+  Window now = next_window<DP>(a, ahead, boxes, box, warp, lane);
+  Window then{0, -1, 0, 0};
+  int step = 0, fill = 0;  // next step of the window, next stage to load
+  int in_flight = 0;       // stages loaded and not waited for
+  auto issue = [&]() {
+    if (step == now.steps) {
+      now = then;
+      step = 0;
     }
-    cp_commit();
+    if (step == 0) then = next_window<DP>(a, ahead, boxes, box, warp, lane);
+    if (now.steps == 0) return;
+    if (lane == 0) mbar_expect_tx(&bars[fill], copies * box * 128);
+    __syncwarp();
+    for (int x0 = 0; x0 < copies; x0 += 32) {
+      // Copy x: boxes fastest, then the 64-column half, then K or V.
+      const int x = x0 + lane, bx = x % boxes, y = x / boxes;
+      const int id = __shfl_sync(0xffffffffu, now.id, step * boxes + bx);
+      const int row = __shfl_sync(0xffffffffu, now.row, step * boxes + bx);
+      if (x < copies) {
+        // A page past the pool's end reads as zeros.
+        const bool known = static_cast<unsigned>(id) < static_cast<unsigned>(a.num_pages);
+        if (!known && row >= 0) atomicOr(a.err, kErrIndexBit);
+        const int half = a.D > 64 ? y & 1 : 0, v = a.D > 64 ? y >> 1 : y;
+        tma_page(ring + fill * X::STAGE + v * X::HALF + half * X::COLS + bx * box * 128, v ? &vmap : &kmap,
+                 64 * half, max(row, 0), now.kv, known && row >= 0 ? id : a.num_pages, &bars[fill]);
+      }
+    }
+    ++step;
+    ++in_flight;
+    if (++fill == ST) fill = 0;
   };
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s) issue(s);
 
   const int q0 = lane >> 2, qc = (lane & 3) * 2;
-  bool continues = c.at != 0;
+  bool continues = c.at != 0, dead = false;
   int stage = 0;
+  uint32_t phase = 0;
   while (c.left > 0) {
     const int n = min(c.left, c.tiles - c.at);
     const bool whole = c.at == 0 && n == c.tiles;
@@ -164,28 +197,54 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
 
-    for (int t = 0; t < n; ++t) {
-      issue(stage + ST - 1 >= ST ? stage - 1 : stage + ST - 1);
-      cp_wait<ST - 1>();
-      __syncwarp();
-      const uint32_t ks = ring + stage * 2 * half_bytes<DP>(), vs = ks + half_bytes<DP>();
+    // The block's first ST - 1 steps only load.
+#pragma unroll 1
+    for (int t = in_flight == 0 && !dead ? 1 - ST : 0; t < n; ++t) {
+      if (dead) continue;
+      issue();
+      if (t < 0) continue;
+      if (!wait_stage(&bars[stage], phase, a.spin_limit)) {
+        // The block's rows are lost; this warp only keeps the others' barriers.
+        dead = true;
+        if (lane == 0) atomicOr(a.err, kErrTimeoutBit);
+        continue;
+      }
+      --in_flight;
+      const uint32_t ks = ring + stage * X::STAGE, vs = ks + X::HALF;
       const int key0 = (c.tile0 + c.at + t) * KT + warp * KW;
-      float s[2][4] = {};
+      if (key0 < c.lo || key0 + KW > c.hi) {
+        // Rows of the boxes that hold no key of the item: whatever the pages
+        // hold there, their V must weigh nothing.
+        if (lane < KW && (key0 + lane < c.lo || key0 + lane >= c.hi)) {
+#pragma unroll
+          for (int x = 0; x < DP / 8; ++x)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             vs + (x >> 3) * X::COLS + lane * 128 + ((x & 7) << 4)),
+                         "r"(0)
+                         : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
+      float s[NC][4] = {};
       {
         const int row = (lane & 7) + ((lane & 16) >> 1);
 #pragma unroll
         for (int j = 0; j < KS; ++j) {
-          const int ch = 2 * j + ((lane >> 3) & 1);
-          uint32_t b[4];
-          ldmatrix4(ks + row * (DP * 2) + ((ch ^ (row & 7)) << 4), b);
-          mma16816<E>(s[0], qf[j], b[0], b[1]);
-          mma16816<E>(s[1], qf[j], b[2], b[3]);
+          const int ch = 2 * (j & 3) + ((lane >> 3) & 1);
+#pragma unroll
+          for (int x = 0; x < NC / 2; ++x) {
+            uint32_t b[4];
+            ldmatrix4(ks + (j >> 2) * X::COLS + (16 * x + row) * 128 + ((ch ^ (row & 7)) << 4), b);
+            mma16816<E>(s[2 * x], qf[j], b[0], b[1]);
+            mma16816<E>(s[2 * x + 1], qf[j], b[2], b[3]);
+          }
         }
       }
       const bool masked = key0 < deep_lo || key0 + KW > deep_hi;
       float top[2] = {m[0], m[1]};
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < NC; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[x][e] *= a.scale_log2;
@@ -216,28 +275,33 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(AttnArgs a) {
         m[1] = top[1];
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < NC; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s[x][e] = exp2_fast(s[x][e] - base[e >> 1]);
           l[e >> 1] += s[x][e];
         }
       // Weights rounded once to the element type for the product with V.
-      const uint32_t p[4] = {E::pack2(s[0][0], s[0][1]), E::pack2(s[0][2], s[0][3]),
-                             E::pack2(s[1][0], s[1][1]), E::pack2(s[1][2], s[1][3])};
-      {
-        const int row = lane & 15;
+      const int vrow = lane & 15;
+#pragma unroll
+      for (int x = 0; x < NC / 2; ++x) {
+        const uint32_t p[4] = {E::pack2(s[2 * x][0], s[2 * x][1]), E::pack2(s[2 * x][2], s[2 * x][3]),
+                               E::pack2(s[2 * x + 1][0], s[2 * x + 1][1]),
+                               E::pack2(s[2 * x + 1][2], s[2 * x + 1][3])};
 #pragma unroll
         for (int j = 0; j < DP / 16; ++j) {
-          const int ch = 2 * j + (lane >> 4);
+          const int ch = 2 * (j & 3) + (lane >> 4);
           uint32_t b[4];
-          ldmatrix4_t(vs + row * (DP * 2) + ((ch ^ (row & 7)) << 4), b);
+          ldmatrix4_t(vs + (j >> 2) * X::COLS + (16 * x + vrow) * 128 + ((ch ^ (vrow & 7)) << 4), b);
           mma16816<E>(o[2 * j], p, b[0], b[1]);
           mma16816<E>(o[2 * j + 1], p, b[2], b[3]);
         }
       }
       __syncwarp();
-      if (++stage == ST) stage = 0;
+      if (++stage == ST) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
 
     // The four warps' statistics and outputs join.
@@ -271,6 +335,15 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(AttnArgs a) {
         for (int x = 0; x < 2; ++x)
           *reinterpret_cast<float2 *>(ob + (q0 + 8 * x) * DP + 8 * j + qc) = make_float2(o[j][2 * x], o[j][2 * x + 1]);
     }
+    // Eight threads a row from here on: thread tid has columns 4 (tid % 8) + 32 j.
+    const int row = tid >> 3, col = (tid & 7) * 4;
+    float M = kNegInf, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * R + row]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) L += exp2_fast(wm[w * R + row] - (M == kNegInf ? 0.f : M)) * wl[w * R + row];
+    int i = 0, head = 0;
+    const bool live = row_of(a, c.r, c.h, c.qt, row, &i, &head);
     __syncthreads();
     if (warp >= 2) {
 #pragma unroll
@@ -282,55 +355,55 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(AttnArgs a) {
         }
     }
     __syncthreads();
-    constexpr int LPR = DP / 4;  // lanes a row
-#pragma unroll 1
-    for (int x = tid; x < R * LPR; x += NT) {
-      const int row = x / LPR, d = (x % LPR) * 4;
-      float M = kNegInf, L = 0.f;
+    const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+    const int64_t token = static_cast<int64_t>(c.r.first) + i;
+    uint16_t *out = static_cast<uint16_t *>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * a.D;
+    float *piece = slot_of<R, DP>(a, blockIdx.x, !continues);
+    bool bad = false;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * R + row]);
-      const float base = M == kNegInf ? 0.f : M;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) L += exp2_fast(wm[w * R + row] - base) * wl[w * R + row];
+    for (int j = 0; j < DP / 32; ++j) {
+      const int d = col + 32 * j;
       const float4 u = *reinterpret_cast<const float4 *>(obuf + row * DP + d);
       const float4 v = *reinterpret_cast<const float4 *>(obuf + R * DP + row * DP + d);
-      const float4 y = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-      int i = 0, head = 0;
-      const bool live = row_of(a, c.r, c.h, c.qt, row, &i, &head);
-      bool bad = false;
+      const float4 y = make_float4((u.x + v.x) * inv, (u.y + v.y) * inv, (u.z + v.z) * inv, (u.w + v.w) * inv);
       if (!whole) {
-        float *w = slot_of<R, DP>(a, blockIdx.x, !continues);
-        *reinterpret_cast<float4 *>(w + row * DP + d) = y;
-        if (d == 0) {
-          w[R * DP + row] = M;
-          w[R * DP + R + row] = L;
-        }
-      } else if (live) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int64_t token = static_cast<int64_t>(c.r.first) + i;
-        if (d < a.D) {
-          uint16_t *out = static_cast<uint16_t *>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * a.D + d;
-          const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
-          *reinterpret_cast<uint2 *>(out) = make_uint2(E::pack2(z[0], z[1]), E::pack2(z[2], z[3]));
-          bad = !(isfinite(z[0]) && isfinite(z[1]) && isfinite(z[2]) && isfinite(z[3]));
-        }
-        if (d == 0 && a.lse) a.lse[token * a.Hq + head] = (M + log2f(L)) * kLn2;
+        *reinterpret_cast<float4 *>(piece + row * DP + d) = y;
+      } else if (live && d < a.D) {
+        *reinterpret_cast<uint2 *>(out + d) = make_uint2(E::pack2(y.x, y.y), E::pack2(y.z, y.w));
+        bad |= !(isfinite(y.x) && isfinite(y.y) && isfinite(y.z) && isfinite(y.w));
       }
-      const unsigned votes = __ballot_sync(0xffffffffu, bad);
-      if (votes) {
-        __syncwarp();
+    }
+    if (col == 0) {
+      if (!whole) {
+        piece[R * DP + row] = M;
+        piece[R * DP + R + row] = L;
+      } else if (live && a.lse) {
+        a.lse[token * a.Hq + head] = (M + log2f(L)) * kLn2;
+      }
+    }
+    const unsigned votes = __ballot_sync(0xffffffffu, bad);
+    if (votes) {
+      __syncwarp();
 #pragma unroll 1
-        for (int first = 0; first < 32; first += LPR) {
-          const int fi = __shfl_sync(0xffffffffu, i, first), fh = __shfl_sync(0xffffffffu, head, first);
-          if ((votes >> first) & (LPR == 32 ? 0xFFFFFFFFu : (1u << (LPR & 31)) - 1u)) row_alone<E>(a, c.b, fh, fi);
-        }
+      for (int x = 0; x < 32; x += 8) {
+        const int xi = __shfl_sync(0xffffffffu, i, x), xh = __shfl_sync(0xffffffffu, head, x);
+        if (votes >> x & 0xFFu) row_alone<E>(a, c.b, xh, xi, 0, a.D);
       }
     }
     continues = false;
     c.left -= n;
     if (c.left > 0) cursor_next<KT>(a, c);
   }
-  cp_wait<0>();
+  // After a wait that ran out: the copies still in flight, within the default
+  // limit, before the shared memory they write to is given back.
+  while (dead && in_flight > 0) {
+    wait_stage(&bars[stage], phase, kDefaultWaitLimit);
+    --in_flight;
+    if (++stage == ST) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
 }
 
 template <typename E, int DP>
@@ -340,13 +413,17 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.heads = a.Hkv * a.S;
   a.TQ = R / a.Gs;
   a.min_tiles = 2;
-  constexpr size_t smem = smem_bytes<DP>();
-  const cudaError_t e = ensure_smem_limit<decode_kernel<E, DP>>(smem);
+  constexpr size_t smem = Tile<DP>::SMEM;
+  CUtensorMap k, v;
+  const int box = box_rows(a.page, Tile<DP>::KW);
+  cudaError_t e = pool_maps(a, E::kF16 ? kTypeF16 : kTypeBF16, box, &k, &v);
+  if (e != cudaSuccess) return e;
+  e = ensure_smem_limit<decode_kernel<E, DP>>(smem);
   if (e != cudaSuccess) return e;
   int blocks = 2 * sm_count();
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
   if (static_cast<size_t>(blocks) > ws_bytes / per_block) blocks = static_cast<int>(ws_bytes / per_block);
-  decode_kernel<E, DP><<<blocks, NT, smem, stream>>>(a);
+  decode_kernel<E, DP><<<blocks, NT, smem, stream>>>(k, v, a, box);
   const cudaError_t le = cudaGetLastError();
   return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);
 }

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(AttnArgs a) {
         for (int half = 0; half < 2; ++half) {
           const int ht = __shfl_sync(0xffffffffu, t, 16 * half);
           const int hh = __shfl_sync(0xffffffffu, head, 16 * half);
-          if (votes & (0xFFFFu << (16 * half))) row_alone<E>(a, c.b, hh, ht);
+          if (votes & (0xFFFFu << (16 * half))) row_alone<E>(a, c.b, hh, ht, 0, a.D);
         }
       }
     }

@@ -41,6 +41,20 @@ cudaError_t encode_map_2d(CUtensorMap *map, CUtensorMapDataType type, const void
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_map_4d(CUtensorMap *map, CUtensorMapDataType type, const void *base,
+                          const uint64_t (&dims)[4], const uint64_t (&stride_bytes)[3],
+                          const uint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t st[3] = {stride_bytes[0], stride_bytes[1], stride_bytes[2]};
+  const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, type, 4, const_cast<void *>(base), d, st, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // SMs of the current device, asked once per device.
 int sm_count() {
   constexpr int kMaxDevices = 64;

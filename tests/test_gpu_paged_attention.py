@@ -207,3 +207,21 @@ def test_nothing_to_do():
                             True, 0, out, 1024, None, ws, ws.numel() * 4)
     assert (out == 7.0).all()
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
+
+
+@pytest.mark.parametrize("lens", [[(3000, 1), (700, 2)], [(2000, 300)]])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(lens):
+    """One poll a wait: whether a wait runs out depends on timing (a poll may be
+    suspended until the copy lands); either way the kernel drains its copies and
+    returns, and the next call is right."""
+    pool, q, news, heads, scale = setup(lens, 16, 2, 4, 128, "bf16")
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
+    before = qmm.qmm_set_wait_limit(1)
+    try:
+        attend(pool, q, news, heads, scale)
+        torch.cuda.synchronize()
+    finally:
+        qmm.qmm_set_wait_limit(before)
+    assert qmm.qmm_get_device_error() in (qmm.QMM_OK, qmm.QMM_ERR_TIMEOUT)
+    check(pool, q, news, heads, scale)
+    assert qmm.qmm_get_device_error() == qmm.QMM_OK
