@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libqmm.so")
 SOURCES = ("api.cpp", "tensormap.cpp", "dequant.cu", "gemv.cu", "gemv_gather.cu", "gemv_f16.cu",
            "gemm_sm103.cu", "quantize.cu", "mm_f32.cu", "page_plan.cu", "rope_append.cu",
-           "paged_attention.cu", "paged_tiles.cu", "paged_decode.cu")
+           "paged_attention.cu", "paged_tiles.cu", "paged_decode.cu", "paged_prefill.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -19,6 +19,8 @@
 // scores carry scale * log2(e), so the natural-log statistic is
 // lse = (m + log2 l) ln 2.
 #pragma once
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace qmm {
@@ -27,6 +29,7 @@ namespace paged {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
+constexpr int kMaxBlocks = 512;  // of an attention launch: descriptors in the workspace
 
 struct AttnArgs {
   const void *q;
@@ -46,7 +49,8 @@ struct AttnArgs {
   int page, num_pages;
   int T, B, Hq, Hkv, G, D;
   int S, Gs, heads;            // each group of G heads in S slices of Gs; heads = Hkv * S
-  int TQ;                      // new tokens of an item: rows TQ * Gs
+  int TQ;                      // new tokens of an item
+  int TH;                      // new tokens of 128 of its rows (TQ where it has no more)
   int max_keys;                // width * page, at most 2^31 - 1
   int causal, window;          // window 0: none
   float scale_log2;            // scale * log2(e)
@@ -403,13 +407,14 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
 }
 
 // Row r of item (h, qt): its new token in the request and its query head;
-// false for a row past the item's tokens or past the group's heads.
+// false for a row past the item's tokens or past the group's heads.  (An item of
+// 256 rows is two of 128, each with TH tokens of its own.)
 __device__ __forceinline__ bool row_of(const AttnArgs &a, const Request &r, int h, int qt, int row,
                                        int *i, int *head) {
-  const int t = row / a.Gs, g = (h % a.S) * a.Gs + (row - t * a.Gs);
-  *i = qt * a.TQ + t;
+  const int in = row & 127, t = in / a.Gs, g = (h % a.S) * a.Gs + (in - t * a.Gs);
+  *i = qt * a.TQ + (row >> 7) * a.TH + t;
   *head = (h / a.S) * a.G + g;
-  return t < a.TQ && *i < r.n && g < a.G;
+  return t < a.TH && *i < r.n && g < a.G;
 }
 
 // ------------------------------------------------------------ elements ----
@@ -435,25 +440,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// The page of the pool that holds entry pg of request b's table; num_pages, past
-// the pool's end, where the table holds none of it: its keys then read as zero
-// and the index bit is set.
-__device__ __forceinline__ int page_of(const AttnArgs &a, int b, int pg) {
-  const int id = __ldg(a.table + b * a.table_stride + pg);
-  if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_pages)) return id;
-  atomicOr(a.err, kErrIndexBit);
-  return a.num_pages;
-}
-
-// A box of 64 columns and some rows of a page's head from the pool's tensor map
-// (columns, rows, heads, pages); columns past the head and pages past the pool
-// read as zeros.
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int col, int row, int head,
-                                         int page, uint64_t *bar) {
+// A box of a tensor map of four axes: of a pool (columns, rows of a page, heads,
+// pages) or of the queries (columns, heads, tokens, one).  What lies outside the
+// axes reads as zeros; the first coordinate is a multiple of 64.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                        uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(col), "r"(row), "r"(head), "r"(page), "r"(smem_u32(bar))
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -699,11 +694,16 @@ namespace paged {
 // most `most`: boxes then never cross a page.
 cudaError_t pool_maps(const AttnArgs &a, int type, int box_rows, CUtensorMap *k, CUtensorMap *v);
 int box_rows(int page, int most);
+// Map of the queries (columns, heads, tokens) with boxes of 64 x Gs x TH.
+cudaError_t query_map(const AttnArgs &a, int type, CUtensorMap *q);
 }  // namespace paged
 
 // paged_tiles.cu: every type and head size on the CUDA cores.
 cudaError_t launch_attention_tiles(paged::AttnArgs a, int type, size_t ws_bytes, cudaStream_t stream);
 // paged_decode.cu: 16-bit types, heads of at most 128, few rows per kv head.
 cudaError_t launch_attention_decode(const paged::AttnArgs &a, int type, size_t ws_bytes, cudaStream_t stream);
+// paged_prefill.cu: 16-bit types, heads of at most 128, a positive scale, many
+// rows per kv head (tcgen05).
+cudaError_t launch_attention_prefill(const paged::AttnArgs &a, int type, size_t ws_bytes, cudaStream_t stream);
 
 }  // namespace qmm

@@ -23,7 +23,22 @@ cudaError_t pool_maps(const AttnArgs &a, int type, int rows, CUtensorMap *k, CUt
   return e != cudaSuccess ? e : encode_map_4d(v, t, a.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+cudaError_t query_map(const AttnArgs &a, int type, CUtensorMap *q) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(a.D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T), 1};
+  const uint64_t token = static_cast<uint64_t>(a.q_stride) * 2;
+  const uint64_t strides[3] = {static_cast<uint64_t>(a.D) * 2, token, token};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(a.Gs), static_cast<uint32_t>(a.TH), 1};
+  return encode_map_4d(q, type == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 }  // namespace paged
+
+namespace {
+constexpr size_t kDescBytes = 16 << 10;  // 32 bytes for each of up to 512 blocks
+constexpr size_t kFewBytes = 12 << 20;   // region of the kernel of few rows
+constexpr int kFewRows = 64;             // rows a kv head that it takes
+}  // namespace
 
 cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, int q_heads,
                                    const PagedPool &pool, const int *table, int64_t table_stride,
@@ -64,14 +79,34 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
   a.scale_log2 = scale * paged::kLog2e;
   a.min_rows = 0;
   a.max_rows = 0x7FFFFFFF;
-  // The workspace: block descriptors first, then the pieces of cut items.
-  constexpr size_t kDescBytes = 64 << 10;
-  a.desc = static_cast<int *>(workspace);
-  a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + kDescBytes);
-  const size_t ws_bytes = workspace_bytes - kDescBytes;
-  (void)max_new;
-  if (pool.type != kTypeF32 && a.D <= 128) return launch_attention_decode(a, pool.type, ws_bytes, stream);
-  return launch_attention_tiles(a, pool.type, ws_bytes, stream);
+  // The workspace: block descriptors and pieces of cut items, a region for
+  // each of the two kernels that a call may launch.
+  char *ws = static_cast<char *>(workspace);
+  auto region = [&](paged::AttnArgs &x, size_t at) {
+    x.desc = reinterpret_cast<int *>(ws + at);
+    x.ws = reinterpret_cast<float *>(ws + at + kDescBytes);
+  };
+  region(a, 0);
+  if (pool.type == kTypeF32 || a.D > 128)
+    return launch_attention_tiles(a, pool.type, workspace_bytes - kDescBytes, stream);
+  // Few rows a kv head: the kernel of 16-row items, whose cost is the bytes of K
+  // and V; many: the one of 256-row items, whose cost is the tensor pipe's.  The
+  // second takes scores times a positive scale only.
+  const int64_t most_rows = max_new * a.G;
+  if (most_rows <= kFewRows || !(scale > 0.f))
+    return launch_attention_decode(a, pool.type, kFewBytes - kDescBytes, stream);
+  // Requests of both kinds: one kernel after the other, each leaving the
+  // other's requests alone; not when no request can be of the first kind.
+  const bool few = requests > 1 && tokens <= (requests - 1) * max_new + kFewRows / a.G;
+  paged::AttnArgs many = a;
+  region(many, kFewBytes);
+  if (few) {
+    a.max_rows = kFewRows;
+    many.min_rows = kFewRows + 1;
+    const cudaError_t e = launch_attention_decode(a, pool.type, kFewBytes - kDescBytes, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_attention_prefill(many, pool.type, workspace_bytes - kFewBytes - kDescBytes, stream);
 }
 
 }  // namespace qmm

@@ -144,7 +144,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const bool known = static_cast<unsigned>(id) < static_cast<unsigned>(a.num_pages);
         if (!known && row >= 0) atomicOr(a.err, kErrIndexBit);
         const int half = a.D > 64 ? y & 1 : 0, v = a.D > 64 ? y >> 1 : y;
-        tma_page(ring + fill * X::STAGE + v * X::HALF + half * X::COLS + bx * box * 128, v ? &vmap : &kmap,
+        tma_box(ring + fill * X::STAGE + v * X::HALF + half * X::COLS + bx * box * 128, v ? &vmap : &kmap,
                  64 * half, max(row, 0), now.kv, known && row >= 0 ? id : a.num_pages, &bars[fill]);
       }
     }
@@ -411,7 +411,7 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.S = (a.G + R - 1) / R;
   a.Gs = (a.G + a.S - 1) / a.S;
   a.heads = a.Hkv * a.S;
-  a.TQ = R / a.Gs;
+  a.TQ = a.TH = R / a.Gs;
   a.min_tiles = 2;
   constexpr size_t smem = Tile<DP>::SMEM;
   CUtensorMap k, v;
@@ -422,7 +422,7 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int blocks = 2 * sm_count();
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
-  if (static_cast<size_t>(blocks) > ws_bytes / per_block) blocks = static_cast<int>(ws_bytes / per_block);
+  blocks = static_cast<int>(std::min<size_t>(std::min(blocks, kMaxBlocks), ws_bytes / per_block));
   decode_kernel<E, DP><<<blocks, NT, smem, stream>>>(k, v, a, box);
   const cudaError_t le = cudaGetLastError();
   return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);

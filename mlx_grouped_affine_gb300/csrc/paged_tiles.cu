@@ -233,14 +233,14 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.S = (a.G + R - 1) / R;
   a.Gs = (a.G + a.S - 1) / a.S;
   a.heads = a.Hkv * a.S;
-  a.TQ = R / a.Gs;
+  a.TQ = a.TH = R / a.Gs;
   a.min_tiles = 1;
   constexpr size_t smem = smem_bytes<DP>();
   const cudaError_t e = ensure_smem_limit<tiles_kernel<E, DP>>(smem);
   if (e != cudaSuccess) return e;
   int blocks = sm_count() * (DP <= 128 ? 2 : 1);
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
-  if (static_cast<size_t>(blocks) > ws_bytes / per_block) blocks = static_cast<int>(ws_bytes / per_block);
+  blocks = static_cast<int>(std::min<size_t>(std::min(blocks, kMaxBlocks), ws_bytes / per_block));
   tiles_kernel<E, DP><<<blocks, NT, smem, stream>>>(a);
   const cudaError_t le = cudaGetLastError();
   return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);

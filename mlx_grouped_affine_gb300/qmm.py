@@ -100,8 +100,10 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        # The current stream's handle without a Stream object, which costs
+        # several times what the rest of a call's marshalling does.
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
