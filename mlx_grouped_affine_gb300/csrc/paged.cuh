@@ -538,7 +538,7 @@ template <int R>
 constexpr int join_weights(int blocks) { return 2 * R + 3 * blocks; }
 
 template <typename E, int R, int DP>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a) {
   using T = typename Elem<E>::type;
   extern __shared__ float weight[];  // [rows][P]
   __shared__ float4 sums[kJoinThreads];

@@ -99,7 +99,7 @@ __device__ __forceinline__ bool wait_stage(uint64_t *bar, uint32_t parity, uint3
 
 template <typename E, int DP>
 __global__ void __launch_bounds__(NT, 2)
-decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, AttnArgs a,
+decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AttnArgs a,
               int box) {
   using X = Tile<DP>;
   constexpr int KW = X::KW, KT = X::KT, NC = KW / 8, KS = DP / 16;

@@ -3,25 +3,35 @@
 //
 // Per key tile of 128 keys, 256 query rows and heads of D: 4 * 128 * 256 * D
 // flops and 128 * 256 exponentials, against 512 D bytes of K and V: the tensor
-// pipe and the exponentials bound it.  One persistent block per SM; its item is
+// pipe bounds it (2048 cycles a tile at D = 128; the exponentials take 1024 of
+// the special-function units' cycles).  One persistent block per SM; its item is
 // two halves of 128 rows (rows are (token, head of the group) pairs, so every
 // row of an item shares its K and V).  For each half h and key tile j
 //   S_h = Q_h K_j^T     tcgen05.mma, 128 x 128 fp32 in TMEM
-//   P_h = 2^(S_h - m)   a row per thread; 16-bit P over S_h in TMEM
+//   P_h = 2^(S_h - m)   16-bit P over S_h in TMEM
 //   O_h += P_h V_j      tcgen05.mma with P from TMEM, 128 x D fp32 in TMEM
-// and the halves take turns: while one is in its softmax the other has the
-// tensor pipe.  Roles:
-//   warps 0-3, 4-7  softmax and output of half 0, 1 (thread = row = TMEM lane)
-//   warp 8          TMA: Q, and a ring of K and V tiles, a box of a page's rows
-//                   at a time, lanes in parallel
-//   warp 9          issues the MMAs (one lane); owns the TMEM allocation
+// S_h, P_h and O_h of a half follow one another, so the halves take turns:
+// while one is in its softmax the other has the tensor pipe.  One warp issues
+// for both, in turns, which keeps them out of step (with an issuer each they
+// fell into step: both softmaxes, then both products, 5400 cycles a tile).  A
+// half's softmax has two threads a row, 64 columns each: with one thread a row
+// its latency (1600 cycles) stood above what the other half's products hide.
+// Roles:
+//   warps 0-7, 8-15  softmax and output of half 0, 1: warp w has TMEM lanes
+//                    32 (w % 4) on and columns 64 (w / 4 % 2) on of S
+//   warp 16          TMA: Q, and a ring of K and V tiles, a box of a page's rows
+//                    at a time, lanes in parallel
+//   warp 17          issues the MMAs (one lane); owns the TMEM allocation
 // The running maximum moves lazily: P is relative to a row maximum m that is
 // only raised, and O and the row sum rescaled, when a score exceeds it by more
-// than 2^8 (P stays below 256, exact in both types' range; the result is the
+// than 2^8 (P stays below 256, inside both types' range; the result is the
 // same because O and the sum share m).
 //
 // Waits are bounded; one that runs out sets the error word and an abort flag
-// that stops every role, and the block still drains its copies and MMAs.
+// that stops every role, and the block still drains its copies and MMAs.  The
+// two warps of a row meet at a hardware barrier every tile, which is not
+// bounded: a warp that gave up goes on to meet its partner, tile by tile, and
+// does nothing else.
 //
 // Shared tiles are 64-column chunks of 128-byte rows, 128-byte swizzled; K and
 // Q chunks are K-major operands (8-row groups 1024 bytes apart), V chunks
@@ -38,7 +48,8 @@ namespace qmm {
 namespace paged {
 namespace {
 
-constexpr int R = 256, KT = 128, kSoftmaxWarps = 8, NT = 32 * (kSoftmaxWarps + 2);
+constexpr int R = 256, KT = 128, kSoftmaxWarps = 16, NT = 32 * (kSoftmaxWarps + 2);
+constexpr int KC = KT / 2;    // columns of S a softmax thread has
 constexpr float kLazy = 8.f;  // log2 by which scores may exceed the row's reference
 
 template <int DP>
@@ -46,13 +57,21 @@ struct Tile {
   static constexpr uint32_t CHUNK = 128 * 128;          // 128 rows of 64 columns
   static constexpr uint32_t TILE = CHUNK * (DP / 64);   // Q half, K or V tile
   static constexpr int SLOTS = DP == 128 ? 5 : 8;
+  static_assert(SLOTS + 1 <= 16, "a step's barrier is free when its turn comes again");
   static constexpr uint32_t O0 = 256;                   // TMEM: S_0 at 0, S_1 at 128, O_0, O_1
 };
 
+// Barriers of the loads of a step.  A step has one load at least, so no more
+// steps are under way than the ring has slots, and one.
+constexpr int kSteps = 16;
+
 struct Barriers {
-  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_ready[2], o_full[2], o_empty[2], mma_done;
+  uint64_t q_full, q_empty, kv_full[kSteps], kv_empty[8], s_full[2], p_ready[2], o_full[2], o_empty[2], mma_done;
   uint32_t tmem_base;
-  int abort;
+  int abort, redo;
+  Cursor start;                           // the block's
+  Cursor cursor[kSoftmaxWarps / 2];       // of a pair of softmax warps
+  float exchange[kSoftmaxWarps][32];      // between its two warps
 };
 
 template <int DP>
@@ -88,16 +107,20 @@ __device__ __forceinline__ void tc_fence_before() {
 }
 
 // Descriptor of a 128-byte swizzled operand (start, leading and stride byte
-// offsets in units of 16, version 1, swizzle mode 2).  K-major: 8-row groups
-// 1024 bytes apart.  MN-major: atoms 16384 bytes apart along N (a 64-column
-// chunk of 128 keys), 1024 along K.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lead) {
-  uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(lead >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// offsets in units of 16, version 1, swizzle mode 2): its low word holds the
+// start and the leading offset, its high word is the same for all.  K-major:
+// 8-row groups 1024 bytes apart.  MN-major: atoms 16384 bytes apart along N (a
+// 64-column chunk of 128 keys), 1024 along K.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lead) {
+  return (saddr >> 4) | (lead >> 4) << 16;
+}
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+// One lane of the warp, the same at every call; the warp is converged.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
 }
 
 // kind::f16, fp32 accumulator, M = 128; B transposed (MN-major) for V.
@@ -108,19 +131,19 @@ __host__ __device__ constexpr uint32_t idesc() {
 }
 
 template <uint32_t IDESC>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(IDESC), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "n"(IDESC), "r"(acc), "n"(kDescHigh)
       : "memory");
 }
 template <uint32_t IDESC>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(IDESC), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "n"(IDESC), "r"(acc), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
@@ -130,7 +153,7 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 }
 
 
-// 32 columns of this warp's 32 TMEM lanes; no wait.
+// 32 columns of this warp's 32 TMEM lanes into f[O], ..; no wait.
 template <int O, int N>
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&f)[N]) {
   asm volatile(
@@ -158,14 +181,47 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
       "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
-// 16 columns times f, in place.
-__device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
-  float o[16];
+// Two fp32 operations an instruction: (x0, x1) * k + c, and (s0, s1) += (x0, x1).
+__device__ __forceinline__ void fma2(float x0, float x1, float k, float c, float &y0, float &y1) {
+  asm("{\n\t.reg .b64 x, k, c, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 k, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 y, x, k, c;\n\tmov.b64 {%0, %1}, y;\n\t}"
+      : "=f"(y0), "=f"(y1)
+      : "f"(x0), "f"(x1), "f"(k), "f"(c));
+}
+__device__ __forceinline__ void add2(float &s0, float &s1, float x0, float x1) {
+  asm("{\n\t.reg .b64 s, x;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 x, {%2, %3};\n\tadd.rn.f32x2 s, s, x;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(s0), "+f"(s1)
+      : "f"(x0), "f"(x1));
+}
+
+// The two warps of a row meet (64 threads at hardware barrier `id`); whether
+// any of their threads said yes.
+__device__ __forceinline__ bool meet_any(int id, bool yes) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.aligned.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(yes)), "r"(id)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void meet(int id) {
+  asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&o)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]),
         "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
       : "r"(addr));
+}
+// 16 columns times f, in place.
+__device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
+  float o[16];
+  tmem_ld16(addr, o);
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i] *= f;
@@ -221,6 +277,8 @@ __device__ __forceinline__ void piece_done(const AttnArgs &a, Cursor &c, const P
 
 // ----------------------------------------------------------------- roles ----
 
+// Step j of a piece needs V of tile j - 1 and K of tile j (the first only K, the
+// last only V); its loads share a barrier, the ring's slots take them in order.
 template <int DP>
 __device__ void load_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, const CUtensorMap *kmap,
                           const CUtensorMap *vmap, int box, uint8_t *sq, uint8_t *skv, Barriers *bars) {
@@ -228,11 +286,51 @@ __device__ void load_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, 
   const int lane = threadIdx.x & 31;
   volatile int *abort = &bars->abort;
   const int boxes = KT / box;  // 1 to 128 a tile, four a lane at most
-  uint32_t count = 0, q_count = 0;  // tiles and Qs loaded
+  uint32_t slot = 0, round = 0;        // of the ring's next load
+  uint32_t steps = 0, q_count = 0;     // steps and Qs loaded
   bool ok = true;
+  int id[4], row[4], page[4], at[4];   // the next tile's pages; the current tile's
   while (ok && c.left > 0) {
     const Piece p = piece_of(a, c);
     if (p.any.from < p.any.to) {
+      const int kv = c.h / a.S;
+      auto look = [&](int tile) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int bx = lane + 32 * x, key = tile * KT + bx * box;
+          id[x] = 0;
+          row[x] = -KT;  // no key of the item in the box
+          if (bx < boxes && tile < p.any.to && key + box > c.lo && key < c.hi) {
+            const int pg = key / a.page;
+            id[x] = __ldg(a.table + c.b * a.table_stride + pg);
+            // The box that holds the request's end ends with its last key.
+            row[x] = key - pg * a.page - max(0, key + box - c.r.len);
+          }
+        }
+      };
+      // One tile into the ring's next slot; its bytes count on the step's barrier.
+      auto load = [&](const CUtensorMap *map, uint64_t *full) {
+        if (!wait_warp(&bars->kv_empty[slot], (round & 1) ^ 1u, abort, a.err, a.spin_limit)) return false;
+        if (lane == 0) mbar_expect_tx(full, X::TILE);
+        __syncwarp();
+        const uint32_t dst = smem_u32(skv + slot * X::TILE);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int bx = lane + 32 * x;
+          if (bx < boxes) {
+#pragma unroll
+            for (int y = 0; y < DP / 64; ++y)
+              tma_box(dst + y * X::CHUNK + bx * box * 128, map, 64 * y, at[x], kv, page[x], full);
+          }
+        }
+        __syncwarp();
+        if (++slot == X::SLOTS) {
+          slot = 0;
+          ++round;
+        }
+        return true;
+      };
+      look(p.any.from);
       // Q of both halves, once the previous one has been multiplied.
       ok = wait_warp(&bars->q_empty, (q_count & 1) ^ 1u, abort, a.err, a.spin_limit);
       if (!ok) break;
@@ -249,68 +347,43 @@ __device__ void load_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, 
       }
       __syncwarp();
       ++q_count;
-      const int kv = c.h / a.S;
-      int id[4], row[4];
-      auto look = [&](int tile) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int bx = lane + 32 * x, key = tile * KT + bx * box;
-          id[x] = 0;
-          row[x] = -KT;  // no key of the item in the box
-          if (bx < boxes && tile < p.any.to && key + box > c.lo && key < c.hi) {
-            const int pg = key / a.page;
-            id[x] = __ldg(a.table + c.b * a.table_stride + pg);
-            // The box that holds the request's end ends with its last key.
-            row[x] = key - pg * a.page - max(0, key + box - c.r.len);
-          }
-        }
-      };
-      look(p.any.from);
-      for (int j = p.any.from; ok && j < p.any.to; ++j) {
-        int page[4], at[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const bool known = static_cast<unsigned>(id[x]) < static_cast<unsigned>(a.num_pages);
-          if (row[x] > -KT && !known) atomicOr(a.err, kErrIndexBit);
-          // Past the pool's end: reads as zeros.
-          page[x] = row[x] > -KT && known ? id[x] : a.num_pages;
-          at[x] = row[x] > -KT ? row[x] : 0;
-        }
-        look(j + 1);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const uint32_t slot = count % X::SLOTS, round = count / X::SLOTS;
-          ok = wait_warp(&bars->kv_empty[slot], (round & 1) ^ 1u, abort, a.err, a.spin_limit);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&bars->kv_full[slot], X::TILE);
-          __syncwarp();
-          const uint32_t dst = smem_u32(skv + slot * X::TILE);
+      for (int j = p.any.from; ok && j <= p.any.to; ++j, ++steps) {
+        // Two arrivals a step: a load's, or none in its place.
+        uint64_t *full = &bars->kv_full[steps % kSteps];
+        if (j > p.any.from) ok = load(vmap, full);
+        else if (lane == 0) mbar_arrive(full);
+        if (!ok) break;
+        if (j < p.any.to) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int bx = lane + 32 * x;
-            if (bx < boxes) {
-#pragma unroll
-              for (int y = 0; y < DP / 64; ++y)
-                tma_box(dst + y * X::CHUNK + bx * box * 128, v ? vmap : kmap, 64 * y, at[x], kv, page[x],
-                         &bars->kv_full[slot]);
-            }
+            const bool known = static_cast<unsigned>(id[x]) < static_cast<unsigned>(a.num_pages);
+            if (row[x] > -KT && !known) atomicOr(a.err, kErrIndexBit);
+            // Past the pool's end: reads as zeros.
+            page[x] = row[x] > -KT && known ? id[x] : a.num_pages;
+            at[x] = row[x] > -KT ? row[x] : 0;
           }
-          __syncwarp();
-          ++count;
+          look(j + 1);
+          ok = load(kmap, full);
+        } else if (lane == 0) {
+          mbar_arrive(full);
         }
       }
     }
     if (ok) piece_done(a, c, p);
   }
   // Stopped early: the copies in flight land before the block ends (bounded).
+  // A step that had only one of its loads gets the other's arrival.
   if (!ok) {
+    if (lane == 0) mbar_arrive(&bars->kv_full[steps % kSteps]);
+    if (lane == 0) mbar_arrive(&bars->kv_full[steps % kSteps]);
+    __syncwarp();
     if (q_count) {
       for (uint32_t s = 0; s < kDefaultWaitLimit; ++s)
         if (__all_sync(0xffffffffu, mbar_try_wait(&bars->q_full, (q_count - 1) & 1))) break;
     }
-    for (uint32_t n = count > X::SLOTS ? count - X::SLOTS : 0; n < count; ++n) {
+    for (uint32_t n = steps > kSteps - 1 ? steps - (kSteps - 1) : 0; n <= steps; ++n) {
       for (uint32_t s = 0; s < kDefaultWaitLimit; ++s)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->kv_full[n % X::SLOTS], (n / X::SLOTS) & 1))) break;
+        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->kv_full[n % kSteps], (n / kSteps) & 1))) break;
     }
   }
 }
@@ -318,78 +391,67 @@ __device__ void load_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, 
 template <typename E, int DP>
 __device__ void mma_role(const AttnArgs &a, Cursor c, uint8_t *sq, uint8_t *skv, Barriers *bars, uint32_t tmem) {
   using X = Tile<DP>;
-  const int lane = threadIdx.x & 31;
   volatile int *abort = &bars->abort;
-  uint32_t count = 0, q_count = 0;         // K/V tiles and Qs consumed
+  uint32_t steps = 0, q_count = 0, slot = 0;  // as the loads count them
   uint32_t p_count[2] = {0, 0}, o_count[2] = {0, 0};
+  const uint32_t q = desc_low(smem_u32(sq), 16);
+  const uint32_t ring_k = desc_low(smem_u32(skv), 16), ring_v = desc_low(smem_u32(skv), X::CHUNK);
   bool ok = true;
-  auto full = [&](uint32_t n) {
-    return wait_warp(&bars->kv_full[n % X::SLOTS], (n / X::SLOTS) & 1, abort, a.err, a.spin_limit);
-  };
   while (ok && c.left > 0) {
     const Piece p = piece_of(a, c);
     if (p.any.from < p.any.to) {
       ok = wait_warp(&bars->q_full, q_count & 1, abort, a.err, a.spin_limit);
       ++q_count;
-      // Step j: the products of tile j - 1 with V, then of tile j with Q.  Tile j's
-      // K is number count + 2 (j - from) of the ring, its V the next.
-      for (int j = p.any.from; ok && j <= p.any.to; ++j) {
-        const uint32_t kn = count + 2 * (j - p.any.from), vn = kn - 1;
-        if (j < p.any.to) ok = full(kn);
-        if (ok && j > p.any.from) ok = full(vn);
+      for (int j = p.any.from; ok && j <= p.any.to; ++j, ++steps) {
+        ok = wait_warp(&bars->kv_full[steps % kSteps], (steps / kSteps) & 1, abort, a.err, a.spin_limit);
+        if (!ok) break;
+        const bool has_v = j > p.any.from, has_k = j < p.any.to;
+        const uint32_t vs = slot, ks = has_v ? (slot + 1 == X::SLOTS ? 0 : slot + 1) : slot;
+        slot = has_k ? (ks + 1 == X::SLOTS ? 0 : ks + 1) : ks;
+        const uint32_t v = ring_v + vs * (X::TILE >> 4), k = ring_k + ks * (X::TILE >> 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!ok) break;
-          if (j > p.half[h].from && j <= p.half[h].to) {
-            const bool first = j - 1 == p.half[h].from;
-            // The previous piece's output has left O_h.
-            if (first) {
-              ok = wait_warp(&bars->o_empty[h], (o_count[h] & 1) ^ 1u, abort, a.err, a.spin_limit);
-              ++o_count[h];
-            }
-            ok = ok && wait_warp(&bars->p_ready[h], p_count[h] & 1, abort, a.err, a.spin_limit);
-            if (!ok) break;
-            ++p_count[h];
+          const bool pv = j > p.half[h].from && j <= p.half[h].to, qk = j >= p.half[h].from && j < p.half[h].to;
+          const bool first = j - 1 == p.half[h].from;
+          if (pv) {
+            // The previous piece's output has left O_h; P_h is there.
+            if (first && !(ok = wait_warp(&bars->o_empty[h], (o_count[h]++ & 1) ^ 1u, abort, a.err, a.spin_limit)))
+              break;
+            if (!(ok = wait_warp(&bars->p_ready[h], p_count[h]++ & 1, abort, a.err, a.spin_limit))) break;
             tc_fence_after();
-            if (lane == 0) {
-              const uint32_t v = smem_u32(skv + vn % X::SLOTS * X::TILE);
-              const uint32_t o = tmem + X::O0 + h * DP, pa = tmem + 128 * h;
+          }
+          if (elect_one()) {
+            if (pv) {
 #pragma unroll
-              for (int k = 0; k < KT / 16; ++k)
-                mma_ts<idesc<E, DP, true>()>(o, pa + 8 * k, smem_desc(v + 2048 * k, X::CHUNK), !first || k);
+              for (int x = 0; x < KT / 16; ++x)
+                mma_ts<idesc<E, DP, true>()>(tmem + X::O0 + h * DP, tmem + 128 * h + KC * (x >> 2) + 8 * (x & 3),
+                                             v + 128 * x, !first || x);
               if (j == p.half[h].to) mma_commit(&bars->o_full[h]);
             }
-            __syncwarp();
-          }
-          if (j >= p.half[h].from && j < p.half[h].to) {
-            if (lane == 0) {
-              const uint32_t q = smem_u32(sq + h * X::TILE), k = smem_u32(skv + kn % X::SLOTS * X::TILE);
+            if (qk) {
 #pragma unroll
               for (int x = 0; x < DP / 16; ++x) {
-                const uint32_t at = (x >> 2) * X::CHUNK + (x & 3) * 32;
-                mma_ss<idesc<E, KT, false>()>(tmem + 128 * h, smem_desc(q + at, 16), smem_desc(k + at, 16), x != 0);
+                const uint32_t at = (x >> 2) * (X::CHUNK >> 4) + (x & 3) * 2;
+                mma_ss<idesc<E, KT, false>()>(tmem + 128 * h, q + h * (X::TILE >> 4) + at, k + at, x != 0);
               }
               mma_commit(&bars->s_full[h]);
             }
-            __syncwarp();
+            if (h == 1) {
+              if (has_v) mma_commit(&bars->kv_empty[vs]);
+              if (has_k) mma_commit(&bars->kv_empty[ks]);
+              if (j == p.any.to - 1) mma_commit(&bars->q_empty);
+            }
           }
+          __syncwarp();
         }
-        if (!ok) break;
-        if (lane == 0) {
-          if (j > p.any.from) mma_commit(&bars->kv_empty[vn % X::SLOTS]);
-          if (j < p.any.to) mma_commit(&bars->kv_empty[kn % X::SLOTS]);
-          if (j == p.any.to - 1) mma_commit(&bars->q_empty);
-        }
-        __syncwarp();
       }
-      count += 2 * (p.any.to - p.any.from);
     }
     if (ok) piece_done(a, c, p);
   }
   // Every MMA retires before the block frees its TMEM.
-  if (lane == 0) mma_commit(&bars->mma_done);
+  if (elect_one()) mma_commit(&bars->mma_done);
   __syncwarp();
-  for (uint32_t s = 0; s < kDefaultWaitLimit; ++s)
+  for (uint32_t x = 0; x < kDefaultWaitLimit; ++x)
     if (__all_sync(0xffffffffu, mbar_try_wait(&bars->mma_done, 0))) break;
 }
 
@@ -400,160 +462,234 @@ __device__ __forceinline__ uint32_t bits_of(int from, int to, int base) {
   return (hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
 }
 
-template <typename E, int DP>
-__device__ void softmax_role(const AttnArgs &a, Cursor c, int box, Barriers *bars, uint32_t tmem) {
-  using X = Tile<DP>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 2;
-  const int row = threadIdx.x;  // of the item; also half * 128 + TMEM lane
-  const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-  const uint32_t ts = tmem + 128 * h + lanes, to = tmem + X::O0 + h * DP + lanes;
-  volatile int *abort = &bars->abort;
-  uint32_t s_count = 0, o_count = 0;
-  bool continues = c.at != 0;
+// Columns of a row that it does not see become -infinity: the row sees keys
+// [span.lo, span.hi), and its 32 columns are keys key0 + base on; from the box
+// that holds the request's end on, columns are `shift` past their keys.
+__device__ __forceinline__ void hide(float (&s)[32], const Span &span, int key0, int len, int box, int base) {
+  const int tail = len & (box - 1), shift = tail ? box - tail : 0;
+  const int edge = shift ? len - tail - key0 : KT;  // that box's first column
+  const int lo = span.lo - key0, hi = span.hi - key0;
+  uint32_t seen = bits_of(lo, min(hi, edge), base);
+  if (shift) seen |= bits_of(max(lo, edge) + shift, hi + shift, base);
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!(seen >> x & 1u)) s[x] = kNegInf;
+}
+
+__device__ __forceinline__ float chunk_top(const float (&s)[32]) {
+  float t[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int x = 4; x < 32; x += 8)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) t[y] = fmaxf(t[y], x + 4 < 32 ? fmaxf(s[x + y], s[x + 4 + y]) : s[x + y]);
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// Weights 2^(s * scale + base) of 32 columns, rounded once to the element type
+// for the product with V, into 16 columns of TMEM, and their sums before that.
+template <typename E>
+__device__ __forceinline__ void weights(const float (&s)[32], float scale, float base, float (&sums)[2],
+                                        uint32_t addr) {
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    uint32_t pk[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      float e0, e1;
+      fma2(s[16 * y + 2 * x], s[16 * y + 2 * x + 1], scale, base, e0, e1);
+      e0 = exp2_fast(e0);
+      e1 = exp2_fast(e1);
+      add2(sums[0], sums[1], e0, e1);
+      pk[x] = E::pack2(e0, e1);
+    }
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(pk[0]), "r"(pk[1]),
+                 "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(addr + 8 * y)
+                 : "memory");
+  }
+}
+
+// The rows that the block wrote whole, once more where one is not finite.  Called
+// after everything else, when some thread saw such a value, so that the tile
+// loop makes no calls.
+template <typename E>
+__device__ __noinline__ void redo_rows(const AttnArgs &a, Cursor c) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   while (c.left > 0) {
     const Piece p = piece_of(a, c);
-    int i, head;
-    const bool live = row_of(a, c.r, c.h, c.qt, row, &i, &head);
-    const Span span = live ? span_of(a, c.r, i) : Span{0, 0};
-    // Keys that every live row of the warp sees.
-    int deep_lo = live ? span.lo : 0, deep_hi = live ? span.hi : 0x7FFFFFFF;
+    for (int row = warp; p.whole && row < R; row += NT / 32) {
+      int i, head;
+      if (!row_of(a, c.r, c.h, c.qt, row, &i, &head)) continue;
+      const uint16_t *out = static_cast<const uint16_t *>(a.out) +
+                            (static_cast<int64_t>(c.r.first) + i) * a.out_stride + static_cast<int64_t>(head) * a.D;
+      bool bad = false;
+      for (int d = lane; d < a.D; d += 32) bad |= !isfinite(E::to_f32(out[d]));
+      if (__any_sync(0xffffffffu, bad)) row_alone<E>(a, c.b, head, i, 0, a.D);
+    }
+    piece_done(a, c, p);
+  }
+}
+
+template <typename E, int DP>
+__device__ void softmax_role(const AttnArgs &a, int box, Barriers *bars, uint32_t tmem) {
+  using X = Tile<DP>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 3, part = warp >> 2 & 1;
+  const int pair = warp >> 3 << 2 | (warp & 3), meeting = 1 + pair;
+  const int row = 128 * h + 32 * (warp & 3) + lane;  // of the item; its TMEM lane in the half
+  const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const uint32_t ts = tmem + 128 * h + KC * part + lanes;            // its columns of S; P in the first half
+  const uint32_t to = tmem + X::O0 + h * DP + DP / 2 * part + lanes;  // of O
+  volatile int *abort = &bars->abort;
+  // The cursor stays in shared memory between pieces, out of the registers.
+  Cursor *cursor = &bars->cursor[pair];
+  uint32_t s_count = 0, o_count = 0;
+  bool continues = cursor->at != 0, dead = false;
+  while (cursor->left > 0) {
+    int from, to_tile, len;
+    Span span{0, 0};
+    int deep_lo = 0, deep_hi = 0x7FFFFFFF;  // keys that every live row of the warp sees
+    {
+      const Cursor c = *cursor;
+      const Piece p = piece_of(a, c);
+      int i, head;
+      if (row_of(a, c.r, c.h, c.qt, row, &i, &head)) {
+        span = span_of(a, c.r, i);
+        deep_lo = span.lo;
+        deep_hi = span.hi;
+      }
+      from = h ? p.half[1].from : p.half[0].from;
+      to_tile = h ? p.half[1].to : p.half[0].to;
+      len = c.r.len;
+    }
 #pragma unroll
     for (int x = 16; x; x >>= 1) {
       deep_lo = max(deep_lo, __shfl_xor_sync(0xffffffffu, deep_lo, x));
       deep_hi = min(deep_hi, __shfl_xor_sync(0xffffffffu, deep_hi, x));
     }
     float m = kNegInf, l = 0.f;
-    for (int j = p.half[h].from; j < p.half[h].to; ++j) {
-      if (!wait_warp(&bars->s_full[h], s_count & 1, abort, a.err, a.spin_limit)) return;
+    for (int j = from; j < to_tile; ++j) {
+      dead = dead || !wait_warp(&bars->s_full[h], s_count & 1, abort, a.err, a.spin_limit);
       ++s_count;
-      tc_fence_after();
-      float s[KT];
-      tmem_ld32<0>(ts, s);
-      tmem_ld32<32>(ts + 32, s);
-      tmem_ld32<64>(ts + 64, s);
-      tmem_ld32<96>(ts + 96, s);
-      tmem_wait_ld();
-      const int key0 = j * KT;
-      if (key0 < deep_lo || key0 + KT > deep_hi) {
-        // The row's columns: keys [lo, hi); from the box that holds the request's
-        // end on, columns are `shift` past their keys.
-        const int tail = c.r.len % box, shift = tail ? box - tail : 0;
-        const int edge = shift ? c.r.len - tail - key0 : KT;  // that box's first column
-        const int lo = span.lo - key0, hi = span.hi - key0;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t seen = bits_of(lo, min(hi, edge), 32 * w);
-          if (shift) seen |= bits_of(max(lo, edge) + shift, hi + shift, 32 * w);
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (!(seen >> x & 1u)) s[32 * w + x] = kNegInf;
-        }
+      // The columns in two chunks of 32: both are read for the maximum, the first
+      // stays in registers, the second is read again (96 registers a thread).
+      const bool deep = j * KT >= deep_lo && j * KT + KT <= deep_hi;
+      float s[32], top = kNegInf;
+      if (!dead) {
+        tc_fence_after();
+        tmem_ld32<0>(ts + 32, s);
+        tmem_wait_ld();
+        if (!deep) hide(s, span, j * KT, len, box, KC * part + 32);
+        top = chunk_top(s);
+        tmem_ld32<0>(ts, s);
+        tmem_wait_ld();
+        if (!deep) hide(s, span, j * KT, len, box, KC * part);
+        top = fmaxf(top, chunk_top(s)) * a.scale_log2;
       }
-      float top = s[0];
-#pragma unroll
-      for (int x = 1; x < KT; ++x) top = fmaxf(top, s[x]);
-      top *= a.scale_log2;
       // Raise the reference when a score is far above it (and in the first tile).
-      if (__any_sync(0xffffffffu, top > m + kLazy)) {
-        const float up = fmaxf(m, top);
+      if (meet_any(meeting, !dead && top > m + kLazy)) {
+        bars->exchange[warp][lane] = top;
+        meet(meeting);
+        const float up = fmaxf(m, fmaxf(top, bars->exchange[warp ^ 4][lane]));
         const float f = exp2_fast(m - (up == kNegInf ? 0.f : up));
         m = up;
         l *= f;
-        if (j > p.half[h].from) {
+        if (j > from && !dead) {
           // O_h is complete up to the previous tile: S_h was committed after it.
 #pragma unroll 1
-          for (int x = 0; x < DP / 16; ++x) tmem_scale16(to + 16 * x, f);
+          for (int x = 0; x < DP / 32; ++x) tmem_scale16(to + 16 * x, f);
         }
       }
+      if (dead) continue;
       const float base = m == kNegInf ? 0.f : -m;
-      float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float e0 = exp2_fast(fmaf(s[64 * y + 2 * x], a.scale_log2, base));
-          const float e1 = exp2_fast(fmaf(s[64 * y + 2 * x + 1], a.scale_log2, base));
-          sum0 += e0;
-          sum1 += e1;
-          pk[x] = E::pack2(e0, e1);  // rounded once to the element type for the product with V
-        }
-        tmem_st32(ts + 32 * y, pk);
-      }
-      l += sum0 + sum1;
+      float sums[2] = {0.f, 0.f};
+      weights<E>(s, a.scale_log2, base, sums, ts);
+      tmem_ld32<0>(ts + 32, s);
+      tmem_wait_ld();
+      if (!deep) hide(s, span, j * KT, len, box, KC * part + 32);
+      weights<E>(s, a.scale_log2, base, sums, ts + 16);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->p_ready[h]);
+      l += sums[0] + sums[1];
     }
-    // The piece's rows: to the output, or to the workspace when the item is cut.
-    const bool any = p.half[h].from < p.half[h].to;
-    if (any) {
-      if (!wait_warp(&bars->o_full[h], o_count & 1, abort, a.err, a.spin_limit)) return;
+
+    if (from < to_tile) {
+      dead = dead || !wait_warp(&bars->o_full[h], o_count & 1, abort, a.err, a.spin_limit);
       ++o_count;
+      bars->exchange[warp][lane] = l;
+      meet(meeting);
+      l += bars->exchange[warp ^ 4][lane];
+    }
+    if (!dead) {
+      // The row's part: to the output, or to the workspace when the item is cut.
+      const Cursor c = *cursor;
+      const bool any = from < to_tile, whole = c.at == 0 && c.left >= c.tiles;
+      int i, head;
+      const bool live = row_of(a, c.r, c.h, c.qt, row, &i, &head);
+      const float inv = !any ? 0.f : !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const int64_t token = static_cast<int64_t>(c.r.first) + i;
+      float *piece = slot_of<R, DP>(a, blockIdx.x, !continues);
+      if (part == 0) {
+        if (!whole) {
+          piece[R * DP + row] = m;
+          piece[R * DP + R + row] = l;
+        } else if (live && a.lse) {
+          a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
+        }
+      }
+      piece += row * DP + DP / 2 * part;
+      uint16_t *out = static_cast<uint16_t *>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * a.D +
+                      DP / 2 * part;
+      const int cols = a.D - DP / 2 * part;  // of the head from this part on
+      bool bad = false;
       tc_fence_after();
-    }
-    const float inv = !p.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-    const int64_t token = static_cast<int64_t>(c.r.first) + i;
-    uint16_t *out = static_cast<uint16_t *>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * a.D;
-    float *piece = slot_of<R, DP>(a, blockIdx.x, !continues);
-    bool bad = false;
-#pragma unroll
-    for (int x = 0; x < DP / 32; ++x) {
-      float o[32];
-      if (any) {
-        tmem_ld32<0>(to + 32 * x, o);
+#pragma unroll 1
+      for (int x = 0; x < DP / 2; x += 16) {
+        float o[16];
+        tmem_ld16(to + x, o);
         tmem_wait_ld();
-      } else {
 #pragma unroll
-        for (int y = 0; y < 32; ++y) o[y] = 0.f;
-      }
+        for (int y = 0; y < 16; ++y) {
+          o[y] = any ? o[y] * inv : 0.f;  // without a tile O_h holds whatever was there
+          bad |= !isfinite(o[y]);
+        }
+        if (!whole) {
 #pragma unroll
-      for (int y = 0; y < 32; ++y) {
-        o[y] = any ? o[y] * inv : 0.f;
-        bad |= !isfinite(o[y]);
-      }
-      if (!p.whole) {
+          for (int y = 0; y < 16; y += 4)
+            *reinterpret_cast<float4 *>(piece + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+        } else if (live) {
 #pragma unroll
-        for (int y = 0; y < 32; y += 4)
-          *reinterpret_cast<float4 *>(piece + row * DP + 32 * x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
-      } else if (live) {
-#pragma unroll
-        for (int y = 0; y < 32; y += 8)
-          if (32 * x + y < a.D)
-            *reinterpret_cast<uint4 *>(out + 32 * x + y) =
-                make_uint4(E::pack2(o[y], o[y + 1]), E::pack2(o[y + 2], o[y + 3]), E::pack2(o[y + 4], o[y + 5]),
-                           E::pack2(o[y + 6], o[y + 7]));
+          for (int y = 0; y < 16; y += 8)
+            if (x + y < cols)
+              *reinterpret_cast<uint4 *>(out + x + y) =
+                  make_uint4(E::pack2(o[y], o[y + 1]), E::pack2(o[y + 2], o[y + 3]), E::pack2(o[y + 4], o[y + 5]),
+                             E::pack2(o[y + 6], o[y + 7]));
+        }
       }
-    }
-    if (any) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->o_empty[h]);
-    }
-    if (!p.whole) {
-      piece[R * DP + row] = m;
-      piece[R * DP + R + row] = l;
-    } else if (live && a.lse) {
-      a.lse[token * a.Hq + head] = (m + log2f(l)) * kLn2;
-    }
-    unsigned votes = __ballot_sync(0xffffffffu, bad && live && p.whole);
-    if (votes) {
-      __syncwarp();
-      for (; votes; votes &= votes - 1) {
-        const int x = __ffs(votes) - 1;
-        row_alone<E>(a, c.b, __shfl_sync(0xffffffffu, head, x), __shfl_sync(0xffffffffu, i, x), 0, a.D);
+      if (any) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_empty[h]);
       }
+      if (bad && live && whole) bars->redo = 1;
     }
     continues = false;
-    piece_done(a, c, p);
+    // Both warps have read the cursor; one moves it on.
+    meet(meeting);
+    if (part == 0) {
+      Cursor c = *cursor;
+      __syncwarp();
+      piece_done(a, c, piece_of(a, c));
+      if (lane == 0) *cursor = c;
+    }
+    meet(meeting);
   }
 }
 
 template <typename E, int DP>
 __global__ void __launch_bounds__(NT, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-               const __grid_constant__ CUtensorMap vmap, AttnArgs a, int box) {
+               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AttnArgs a, int box) {
   using X = Tile<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sq = smem, *skv = smem + 2 * X::TILE;
@@ -567,18 +703,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < X::SLOTS; ++i) {
-      mbar_init(&bars->kv_full[i], 1);
-      mbar_init(&bars->kv_empty[i], 1);
-    }
+    for (int i = 0; i < kSteps; ++i) mbar_init(&bars->kv_full[i], 2);
+    for (int i = 0; i < X::SLOTS; ++i) mbar_init(&bars->kv_empty[i], 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars->s_full[h], 1);
-      mbar_init(&bars->p_ready[h], 4);
+      mbar_init(&bars->p_ready[h], 8);
       mbar_init(&bars->o_full[h], 1);
-      mbar_init(&bars->o_empty[h], 4);
+      mbar_init(&bars->o_empty[h], 8);
     }
     mbar_init(&bars->mma_done, 1);
-    bars->abort = 0;
+    bars->abort = bars->redo = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   const Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, *reinterpret_cast<PlanScratch<NT> *>(skv));
@@ -595,13 +729,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                  "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  if (threadIdx.x == 0) bars->start = c;
+  if (warp < kSoftmaxWarps && (threadIdx.x & 31) == 0 && !(warp & 4)) bars->cursor[warp >> 3 << 2 | (warp & 3)] = c;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
   if (warp < kSoftmaxWarps) {
-    softmax_role<E, DP>(a, c, box, bars, tmem);
+    softmax_role<E, DP>(a, box, bars, tmem);
   } else {
     if (warp == kSoftmaxWarps) load_role<DP>(a, c, &qmap, &kmap, &vmap, box, sq, skv, bars);
     else if (warp == kSoftmaxWarps + 1) mma_role<E, DP>(a, c, sq, skv, bars, tmem);
@@ -613,6 +749,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
+  if (bars->redo && !bars->abort) redo_rows<E>(a, bars->start);
 }
 
 template <typename E, int DP>

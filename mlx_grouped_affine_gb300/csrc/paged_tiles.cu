@@ -44,7 +44,7 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
 }
 
 template <typename E, int DP>
-__global__ void __launch_bounds__(NT) tiles_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnArgs a) {
   using T = typename Elem<E>::type;
   extern __shared__ __align__(16) float smem[];
   float *Qs = smem;                    // [R][DP + 4]
