@@ -440,18 +440,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// A box of a tensor map of four axes: of a pool (columns, rows of a page, heads,
-// pages) or of the queries (columns, heads, tokens, one).  What lies outside the
-// axes reads as zeros; the first coordinate is a multiple of 64.
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
-                                        uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Element offset of key j of request b's head h, or -1 where the table holds
 // no page of the pool (the key then reads as zero and the index bit is set).
 __device__ __forceinline__ int64_t key_offset(const AttnArgs &a, int b, int h, int j) {
@@ -463,6 +451,97 @@ __device__ __forceinline__ int64_t key_offset(const AttnArgs &a, int b, int h, i
   }
   return id * a.page_stride + row * a.token_stride + h * a.head_stride;
 }
+
+// ------------------------------------------------ K and V to shared memory ----
+// Tiles in shared memory are 64-column chunks of 128-byte rows, whose 16-byte
+// pieces are swizzled by the row: piece x of row r at position x ^ (r % 8).
+//
+// The unit of a copy is a block of 8 keys.  Where the page size is a multiple of
+// 8 a block lies in one page, so that its address is looked up once (one lane a
+// block, long before the copy) and a lane's rows follow by adding the row
+// stride: cp.async at 12 cycles an instruction of a warp, 43 bytes a cycle of one
+// warp and 53 of two.  (A shuffled address for every row: 31 cycles.  TMA boxes
+// of a page's rows: 45 cycles a box and 3.5 a 128-byte row, 20 bytes a cycle at
+// 16-row pages.)  Blocks that the item sees in part, and other page sizes, go row
+// by row.
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// A block as one lane looked it up: `how` 0 no key of the item, 1 one page, 2 row
+// by row; its table entry and its first row in the page.
+struct Block {
+  int how, id, row;
+};
+__device__ __forceinline__ Block look_up(const AttnArgs &a, int b, int key, int lo, int hi) {
+  Block x{0, 0, 0};
+  if (key + 8 <= lo || key >= hi) return x;
+  if (key < lo || key + 8 > hi || a.page % 8 != 0) {
+    x.how = 2;
+    return x;
+  }
+  x.how = 1;
+  const int pg = key / a.page;
+  x.row = key - pg * a.page;
+  x.id = __ldg(a.table + b * a.table_stride + pg);
+  return x;
+}
+
+// Element offset of the block's first row in the pool; -1 none, -2 row by row.
+__device__ __forceinline__ int64_t block_offset(const AttnArgs &a, const Block &x, int kv) {
+  if (x.how != 1) return -static_cast<int64_t>(x.how) + (x.how == 0 ? -1 : 0);
+  if (static_cast<unsigned>(x.id) >= static_cast<unsigned>(a.num_pages)) {
+    atomicOr(a.err, kErrIndexBit);
+    return -1;
+  }
+  return x.id * a.page_stride + x.row * a.token_stride + kv * a.head_stride;
+}
+
+// Where a lane's 16 bytes of a block's rows lie, from the block's place in the
+// first chunk: instruction i covers 32 / (DP / 8) rows.
+template <int DP>
+struct Copier {
+  static constexpr int CH = DP / 8, RPI = 32 / CH, N = 8 / RPI;
+  uint32_t at[N];
+  uint32_t bytes;  // 16, or 0 for columns past the head
+  int first, col;
+  __device__ __forceinline__ Copier(int D, uint32_t chunk) {
+    const int lane = threadIdx.x & 31, ch = lane % CH;
+    first = lane / CH;
+    col = ch * 8;
+    bytes = col < D ? 16u : 0u;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = first + i * RPI;
+      at[i] = (ch >> 3) * chunk + r * 128 + (((ch & 7) ^ r) << 4);
+    }
+  }
+  // One block of one pool; off is the same in all lanes.
+  __device__ __forceinline__ void copy(const AttnArgs &a, const void *pool, int64_t off, uint32_t dst, int b,
+                                       int kv, int key, int lo, int hi) const {
+    const uint16_t *src = static_cast<const uint16_t *>(pool) + col;
+    if (off >= 0) {
+      src += off + first * a.token_stride;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        cp_async16(dst + at[i], src, bytes);
+        src += RPI * a.token_stride;
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const int k = key + first + i * RPI;
+        const int64_t o = off == -2 && k >= lo && k < hi ? key_offset(a, b, kv, k) : -1;
+        uint32_t x = at[0];
+#pragma unroll
+        for (int y = 1; y < N; ++y) x = i == y ? at[y] : x;
+        cp_async16(dst + x, src + (o >= 0 ? o : 0), o >= 0 ? bytes : 0u);
+      }
+    }
+  }
+};
 
 // Columns [d0, d1) of an output row by one warp, from the keys it sees alone.  The tiled kernels
 // multiply masked keys by weight zero, which is no longer nothing when such a
@@ -689,13 +768,11 @@ cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
 }  // namespace paged
 
 namespace paged {
-// Maps of the K and V pools with boxes of 64 columns x box_rows rows, 128-byte
-// swizzle.  box_rows is the largest power of two that divides the page size, at
-// most `most`: boxes then never cross a page.
-cudaError_t pool_maps(const AttnArgs &a, int type, int box_rows, CUtensorMap *k, CUtensorMap *v);
-int box_rows(int page, int most);
 // Map of the queries (columns, heads, tokens) with boxes of 64 x Gs x TH.
 cudaError_t query_map(const AttnArgs &a, int type, CUtensorMap *q);
+// Map of the K pool (columns, rows of a page, heads, pages) with boxes of 64
+// columns x `rows` rows.
+cudaError_t key_map(const AttnArgs &a, int type, int rows, CUtensorMap *k);
 }  // namespace paged
 
 // paged_tiles.cu: every type and head size on the CUDA cores.

@@ -5,22 +5,14 @@ namespace qmm {
 
 namespace paged {
 
-int box_rows(int page, int most) {
-  int r = 1;
-  while (r < most && page % (2 * r) == 0) r *= 2;
-  return r;
-}
-
-cudaError_t pool_maps(const AttnArgs &a, int type, int rows, CUtensorMap *k, CUtensorMap *v) {
-  const CUtensorMapDataType t =
-      type == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+cudaError_t key_map(const AttnArgs &a, int type, int rows, CUtensorMap *k) {
   const uint64_t dims[4] = {static_cast<uint64_t>(a.D), static_cast<uint64_t>(a.page),
                             static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.num_pages)};
   const uint64_t strides[3] = {static_cast<uint64_t>(a.token_stride) * 2, static_cast<uint64_t>(a.head_stride) * 2,
                                static_cast<uint64_t>(a.page_stride) * 2};
   const uint32_t box[4] = {64, static_cast<uint32_t>(rows), 1, 1};
-  const cudaError_t e = encode_map_4d(k, t, a.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-  return e != cudaSuccess ? e : encode_map_4d(v, t, a.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_map_4d(k, type == kTypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       a.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 cudaError_t query_map(const AttnArgs &a, int type, CUtensorMap *q) {

@@ -4,16 +4,16 @@
 // byte-pair, so HBM bounds it: the kernel's work is to keep loads in flight.
 // An item is 16 rows (TQ new tokens x the group's heads: one tensor-core tile
 // of rows); a key tile is KW keys for each of the block's four warps.  A warp
-// streams its keys through a ring of its own (TMA boxes of a page's rows into
-// 128-byte swizzled shared memory, one mbarrier a stage), so nothing in the
+// streams its keys through a ring of its own (cp.async groups), so nothing in the
 // stream waits for another warp; the load cursor runs ahead of the compute
-// cursor across item ends.  Page ids are read a window of up to 32 boxes at a
+// cursor across item ends.  Blocks of 8 keys are looked up a window of 32 at a
 // time, one a lane, and a window ahead of their use: a table entry costs a trip
-// to L2 or HBM (0.6 to 1.5 us) that would otherwise stand before every step.  KW is 16 keys for heads of 128 and 32 for heads of 64: 8
-// KB a stage, six stages of two blocks an SM in flight.  Scores and output are
-// mma.sync m16n8k16 with fp32 accumulators: at these intensities its rate is
-// far from the bound.  Each warp has its own running maximum and sum; the four
-// join in shared memory when the item ends.
+// to L2 or HBM (0.6 to 1.5 us) that would otherwise stand before every step.
+// KW is 16 keys for heads of 128 and 32 for heads of 64: 8 KB a stage, six
+// stages of two blocks an SM in flight.  Scores and output are mma.sync m16n8k16
+// with fp32 accumulators: at these intensities its rate is far from the bound.
+// Each warp has its own running maximum and sum; the four join in shared memory
+// when the item ends.
 #include "paged.cuh"
 
 namespace qmm {
@@ -30,8 +30,8 @@ struct Tile {
   static constexpr uint32_t HALF = COLS * (DP / 64); // K or V of a step
   static constexpr uint32_t STAGE = 2 * HALF;
   static constexpr uint32_t RINGS = kWarps * ST * STAGE;
-  // rings, joined output [2][R][DP], statistics [2][warps][R], barriers
-  static constexpr size_t SMEM = RINGS + 2 * R * DP * 4 + 2 * kWarps * R * 4 + kWarps * ST * 8;
+  // rings, joined output [2][R][DP], statistics [2][warps][R]
+  static constexpr size_t SMEM = RINGS + 2 * R * DP * 4 + 2 * kWarps * R * 4;
 };
 static_assert(sizeof(PlanScratch<NT>) <= 2 * R * 64 * 4, "the plan's scratch lies in the output's room");
 
@@ -64,99 +64,76 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The pages of the warp's next steps of one item: lane l has box l % boxes of
-// step l / boxes (row -1: no key of the item there).
+// The warp's next steps of one item: lane l has looked up block l % BS of step
+// l / BS (BS blocks of 8 keys a step).
 struct Window {
-  int id, row;
-  int steps, kv;
+  Block block;
+  int b, kv, key0, lo, hi;  // key0: the warp's first key in the first step
+  int steps;
 };
 template <int DP>
-__device__ __forceinline__ Window next_window(const AttnArgs &a, Cursor &c, int boxes, int box, int warp, int lane) {
+__device__ __forceinline__ Window next_window(const AttnArgs &a, Cursor &c, int warp, int lane) {
   using X = Tile<DP>;
-  Window w{0, -1, 0, 0};
+  constexpr int BS = X::KW / 8;
+  Window w{};
   if (c.left <= 0) return w;
-  w.steps = min(min(32 / boxes, c.left), c.tiles - c.at);
+  w.steps = min(min(32 / BS, c.left), c.tiles - c.at);
+  w.b = c.b;
   w.kv = c.h / a.S;
-  const int step = lane / boxes;
-  const int key = (c.tile0 + c.at + step) * X::KT + warp * X::KW + (lane - step * boxes) * box;
-  if (step < w.steps && key + box > c.lo && key < c.hi) {
-    const int pg = key / a.page;
-    w.row = key - pg * a.page;
-    w.id = __ldg(a.table + c.b * a.table_stride + pg);
-  }
+  w.key0 = (c.tile0 + c.at) * X::KT + warp * X::KW;
+  w.lo = c.lo;
+  w.hi = c.hi;
+  if (lane / BS < w.steps)
+    w.block = look_up(a, c.b, w.key0 + lane / BS * X::KT + lane % BS * 8, c.lo, c.hi);
   c.left -= w.steps;
   c.at += w.steps;
   if (c.at == c.tiles && c.left > 0) cursor_next<X::KT>(a, c);
   return w;
 }
 
-// Bounded wait of a whole warp; false when it ran out.
-__device__ __forceinline__ bool wait_stage(uint64_t *bar, uint32_t parity, uint32_t limit) {
-  for (uint32_t spin = 0; spin < limit; ++spin)
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return false;
-}
-
 template <typename E, int DP>
-__global__ void __launch_bounds__(NT, 2)
-decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AttnArgs a,
-              int box) {
+__global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ AttnArgs a) {
   using X = Tile<DP>;
-  constexpr int KW = X::KW, KT = X::KT, NC = KW / 8, KS = DP / 16;
+  constexpr int KW = X::KW, KT = X::KT, NC = KW / 8, KS = DP / 16, BS = KW / 8;
   extern __shared__ __align__(1024) uint8_t smem[];
   float *obuf = reinterpret_cast<float *>(smem + X::RINGS);  // [2][R][DP]
   float *wm = obuf + 2 * R * DP, *wl = wm + kWarps * R;      // [warps][R]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(wl + kWarps * R) + warp * ST;
   griddep_launch_dependents();
-  if (lane == 0) {
-#pragma unroll
-    for (int s = 0; s < ST; ++s) mbar_init(&bars[s], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncwarp();
   Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, *reinterpret_cast<PlanScratch<NT> *>(obuf));
   if (c.left <= 0) return;
   const uint32_t ring = smem_u32(smem) + warp * ST * X::STAGE;
+  const Copier<DP> copier(a.D, X::COLS);
 
-  Cursor ahead = c;  // where the page lookups are
-  const int boxes = KW / box, copies = boxes * (a.D > 64 ? 2 : 1) * 2;
-  Window now = next_window<DP>(a, ahead, boxes, box, warp, lane);
-  Window then{0, -1, 0, 0};
+  Cursor ahead = c;  // where the lookups are
+  Window now = next_window<DP>(a, ahead, warp, lane), then{};
+  int64_t off = block_offset(a, now.block, now.kv);
   int step = 0, fill = 0;  // next step of the window, next stage to load
-  int in_flight = 0;       // stages loaded and not waited for
   auto issue = [&]() {
     if (step == now.steps) {
       now = then;
       step = 0;
+      off = block_offset(a, now.block, now.kv);
     }
-    if (step == 0) then = next_window<DP>(a, ahead, boxes, box, warp, lane);
-    if (now.steps == 0) return;
-    if (lane == 0) mbar_expect_tx(&bars[fill], copies * box * 128);
-    __syncwarp();
-    for (int x0 = 0; x0 < copies; x0 += 32) {
-      // Copy x: boxes fastest, then the 64-column half, then K or V.
-      const int x = x0 + lane, bx = x % boxes, y = x / boxes;
-      const int id = __shfl_sync(0xffffffffu, now.id, step * boxes + bx);
-      const int row = __shfl_sync(0xffffffffu, now.row, step * boxes + bx);
-      if (x < copies) {
-        // A page past the pool's end reads as zeros.
-        const bool known = static_cast<unsigned>(id) < static_cast<unsigned>(a.num_pages);
-        if (!known && row >= 0) atomicOr(a.err, kErrIndexBit);
-        const int half = a.D > 64 ? y & 1 : 0, v = a.D > 64 ? y >> 1 : y;
-        tma_box(ring + fill * X::STAGE + v * X::HALF + half * X::COLS + bx * box * 128, v ? &vmap : &kmap,
-                 64 * half, max(row, 0), now.kv, known && row >= 0 ? id : a.num_pages, &bars[fill]);
+    if (step == 0) then = next_window<DP>(a, ahead, warp, lane);
+    if (now.steps > 0) {
+      const uint32_t dst = ring + fill * X::STAGE;
+      const int key0 = now.key0 + step * KT;
+#pragma unroll
+      for (int x = 0; x < BS; ++x) {
+        const int64_t o = __shfl_sync(0xffffffffu, off, step * BS + x);
+        copier.copy(a, a.k, o, dst + 1024 * x, now.b, now.kv, key0 + 8 * x, now.lo, now.hi);
+        copier.copy(a, a.v, o, dst + X::HALF + 1024 * x, now.b, now.kv, key0 + 8 * x, now.lo, now.hi);
       }
+      ++step;
+      if (++fill == ST) fill = 0;
     }
-    ++step;
-    ++in_flight;
-    if (++fill == ST) fill = 0;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   const int q0 = lane >> 2, qc = (lane & 3) * 2;
-  bool continues = c.at != 0, dead = false;
+  bool continues = c.at != 0, fresh = true;
   int stage = 0;
-  uint32_t phase = 0;
   while (c.left > 0) {
     const int n = min(c.left, c.tiles - c.at);
     const bool whole = c.at == 0 && n == c.tiles;
@@ -199,33 +176,13 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 
     // The block's first ST - 1 steps only load.
 #pragma unroll 1
-    for (int t = in_flight == 0 && !dead ? 1 - ST : 0; t < n; ++t) {
-      if (dead) continue;
+    for (int t = fresh ? 1 - ST : 0; t < n; ++t) {
       issue();
       if (t < 0) continue;
-      if (!wait_stage(&bars[stage], phase, a.spin_limit)) {
-        // The block's rows are lost; this warp only keeps the others' barriers.
-        dead = true;
-        if (lane == 0) atomicOr(a.err, kErrTimeoutBit);
-        continue;
-      }
-      --in_flight;
+      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
+      __syncwarp();
       const uint32_t ks = ring + stage * X::STAGE, vs = ks + X::HALF;
       const int key0 = (c.tile0 + c.at + t) * KT + warp * KW;
-      if (key0 < c.lo || key0 + KW > c.hi) {
-        // Rows of the boxes that hold no key of the item: whatever the pages
-        // hold there, their V must weigh nothing.
-        if (lane < KW && (key0 + lane < c.lo || key0 + lane >= c.hi)) {
-#pragma unroll
-          for (int x = 0; x < DP / 8; ++x)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             vs + (x >> 3) * X::COLS + lane * 128 + ((x & 7) << 4)),
-                         "r"(0)
-                         : "memory");
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      }
       float s[NC][4] = {};
       {
         const int row = (lane & 7) + ((lane & 16) >> 1);
@@ -298,11 +255,9 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
       }
       __syncwarp();
-      if (++stage == ST) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      if (++stage == ST) stage = 0;
     }
+    fresh = false;
 
     // The four warps' statistics and outputs join.
 #pragma unroll
@@ -394,16 +349,7 @@ decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     c.left -= n;
     if (c.left > 0) cursor_next<KT>(a, c);
   }
-  // After a wait that ran out: the copies still in flight, within the default
-  // limit, before the shared memory they write to is given back.
-  while (dead && in_flight > 0) {
-    wait_stage(&bars[stage], phase, kDefaultWaitLimit);
-    --in_flight;
-    if (++stage == ST) {
-      stage = 0;
-      phase ^= 1u;
-    }
-  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <typename E, int DP>
@@ -414,16 +360,12 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.TQ = a.TH = R / a.Gs;
   a.min_tiles = 2;
   constexpr size_t smem = Tile<DP>::SMEM;
-  CUtensorMap k, v;
-  const int box = box_rows(a.page, Tile<DP>::KW);
-  cudaError_t e = pool_maps(a, E::kF16 ? kTypeF16 : kTypeBF16, box, &k, &v);
-  if (e != cudaSuccess) return e;
-  e = ensure_smem_limit<decode_kernel<E, DP>>(smem);
+  const cudaError_t e = ensure_smem_limit<decode_kernel<E, DP>>(smem);
   if (e != cudaSuccess) return e;
   int blocks = 2 * sm_count();
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
   blocks = static_cast<int>(std::min<size_t>(std::min(blocks, kMaxBlocks), ws_bytes / per_block));
-  decode_kernel<E, DP><<<blocks, NT, smem, stream>>>(k, v, a, box);
+  decode_kernel<E, DP><<<blocks, NT, smem, stream>>>(a);
   const cudaError_t le = cudaGetLastError();
   return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);
 }

@@ -19,9 +19,15 @@
 // Roles:
 //   warps 0-7, 8-15  softmax and output of half 0, 1: warp w has TMEM lanes
 //                    32 (w % 4) on and columns 64 (w / 4 % 2) on of S
-//   warp 16          TMA: Q, and a ring of K and V tiles, a box of a page's rows
-//                    at a time, lanes in parallel
-//   warp 17          issues the MMAs (one lane); owns the TMEM allocation
+//   warp 16          issues the MMAs (one lane); owns the TMEM allocation
+//   warp 17          Q and K by TMA, K a box of a page's rows at a time
+//   warps 18, 19     V by cp.async
+// K and V share a ring of tiles.  Each way of loading alone is too slow beside
+// the tensor cores' own reads of shared memory: TMA boxes of 16 rows move 20
+// bytes a cycle (3300 cycles for the 64 KB of a tile), and cp.async from three
+// warps, 50 bytes a cycle on an idle SM, 15 here.  V goes the way that can write
+// zeros for single rows (below); a stale row of K only makes scores that are
+// masked.
 // The running maximum moves lazily: P is relative to a row maximum m that is
 // only raised, and O and the row sum rescaled, when a score exceeds it by more
 // than 2^8 (P stays below 256, inside both types' range; the result is the
@@ -37,18 +43,17 @@
 // Q chunks are K-major operands (8-row groups 1024 bytes apart), V chunks
 // MN-major ones (atoms of 64 columns x 8 keys).
 //
-// The last page's rows past the request's end are stale: P is zero there, but
-// zero times a stale infinity is not nothing.  The box that holds the end is
-// therefore loaded shift rows early, so that it ends with the last key: the
-// rows before a page's first read as zero, rows of the page before the box are
-// the request's own.  The box's columns of S move with it, and the mask knows.
+// Rows of a tile that hold no key of the item are written as zeros: P is zero
+// there, but zero times a stale infinity of the last page is not nothing.
 #include "paged.cuh"
 
 namespace qmm {
 namespace paged {
 namespace {
 
-constexpr int R = 256, KT = 128, kSoftmaxWarps = 16, NT = 32 * (kSoftmaxWarps + 2);
+constexpr int R = 256, KT = 128, kSoftmaxWarps = 16, kValueWarps = 2;
+constexpr int NT = 32 * (kSoftmaxWarps + 2 + kValueWarps);
+constexpr uint32_t kDrainPolls = 1u << 14;  // for copies under way after a wait ran out: milliseconds
 constexpr int KC = KT / 2;    // columns of S a softmax thread has
 constexpr float kLazy = 8.f;  // log2 by which scores may exceed the row's reference
 
@@ -277,66 +282,68 @@ __device__ __forceinline__ void piece_done(const AttnArgs &a, Cursor &c, const P
 
 // ----------------------------------------------------------------- roles ----
 
+// A box of the queries' tensor map (columns, heads, tokens, one).  What lies
+// outside reads as zeros; the first coordinate is a multiple of 64.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                        uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// This thread's arrival at the barrier once all its copies so far have landed.
+__device__ __forceinline__ void arrive_landed(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Step j of a piece needs V of tile j - 1 and K of tile j (the first only K, the
-// last only V); its loads share a barrier, the ring's slots take them in order.
+// last only V).  The ring's slots take K and V of a tile in turn: tile j of a
+// piece that begins with load n has K in load n + 2 (j - from), V in the next.  A
+// step's barrier counts an arrival of every thread of the K warp and of the V
+// warps, made when the thread's copies have landed, so that no load waits for
+// another.  (The issuer of the MMAs fences the copies that are generic writes
+// for the tensor cores.)
 template <int DP>
-__device__ void load_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, const CUtensorMap *kmap,
-                          const CUtensorMap *vmap, int box, uint8_t *sq, uint8_t *skv, Barriers *bars) {
+__device__ __forceinline__ bool slot_free(const AttnArgs &a, uint32_t n, Barriers *bars) {
+  using X = Tile<DP>;
+  return wait_warp(&bars->kv_empty[n % X::SLOTS], (n / X::SLOTS & 1) ^ 1u, &bars->abort, a.err, a.spin_limit);
+}
+
+// `box` rows of a TMA box of K; 0: K by cp.async too (pages not of 8 rows).
+template <int DP>
+__device__ void key_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, const CUtensorMap *kmap, int box,
+                         uint8_t *sq, uint8_t *skv, Barriers *bars) {
   using X = Tile<DP>;
   const int lane = threadIdx.x & 31;
-  volatile int *abort = &bars->abort;
-  const int boxes = KT / box;  // 1 to 128 a tile, four a lane at most
-  uint32_t slot = 0, round = 0;        // of the ring's next load
-  uint32_t steps = 0, q_count = 0;     // steps and Qs loaded
+  const Copier<DP> copier(a.D, X::CHUNK);
+  uint32_t load = 0, steps = 0, q_count = 0;
   bool ok = true;
-  int id[4], row[4], page[4], at[4];   // the next tile's pages; the current tile's
   while (ok && c.left > 0) {
     const Piece p = piece_of(a, c);
     if (p.any.from < p.any.to) {
       const int kv = c.h / a.S;
+      // Lane l looks up box (block) l of the next tile.
+      const int rows = box ? box : 8;
+      Block next;
       auto look = [&](int tile) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int bx = lane + 32 * x, key = tile * KT + bx * box;
-          id[x] = 0;
-          row[x] = -KT;  // no key of the item in the box
-          if (bx < boxes && tile < p.any.to && key + box > c.lo && key < c.hi) {
-            const int pg = key / a.page;
-            id[x] = __ldg(a.table + c.b * a.table_stride + pg);
-            // The box that holds the request's end ends with its last key.
-            row[x] = key - pg * a.page - max(0, key + box - c.r.len);
-          }
+        next = Block{0, 0, 0};
+        const int key = tile * KT + rows * lane;
+        if (rows * lane >= KT || tile >= p.any.to) return;
+        if (!box) {
+          next = look_up(a, c.b, key, c.lo, c.hi);
+        } else if (key + rows > c.lo && key < c.hi) {
+          const int pg = key / a.page;
+          next = Block{1, __ldg(a.table + c.b * a.table_stride + pg), key - pg * a.page};
         }
-      };
-      // One tile into the ring's next slot; its bytes count on the step's barrier.
-      auto load = [&](const CUtensorMap *map, uint64_t *full) {
-        if (!wait_warp(&bars->kv_empty[slot], (round & 1) ^ 1u, abort, a.err, a.spin_limit)) return false;
-        if (lane == 0) mbar_expect_tx(full, X::TILE);
-        __syncwarp();
-        const uint32_t dst = smem_u32(skv + slot * X::TILE);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int bx = lane + 32 * x;
-          if (bx < boxes) {
-#pragma unroll
-            for (int y = 0; y < DP / 64; ++y)
-              tma_box(dst + y * X::CHUNK + bx * box * 128, map, 64 * y, at[x], kv, page[x], full);
-          }
-        }
-        __syncwarp();
-        if (++slot == X::SLOTS) {
-          slot = 0;
-          ++round;
-        }
-        return true;
       };
       look(p.any.from);
       // Q of both halves, once the previous one has been multiplied.
-      ok = wait_warp(&bars->q_empty, (q_count & 1) ^ 1u, abort, a.err, a.spin_limit);
+      ok = wait_warp(&bars->q_empty, (q_count & 1) ^ 1u, &bars->abort, a.err, a.spin_limit);
       if (!ok) break;
       if (lane == 0) {
-        const uint32_t rows = a.Gs * a.TH;
-        mbar_expect_tx(&bars->q_full, 2 * (DP / 64) * rows * 128);
+        mbar_expect_tx(&bars->q_full, 2 * (DP / 64) * a.Gs * a.TH * 128);
         const int head = (c.h / a.S) * a.G + (c.h % a.S) * a.Gs;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -347,45 +354,90 @@ __device__ void load_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, 
       }
       __syncwarp();
       ++q_count;
-      for (int j = p.any.from; ok && j <= p.any.to; ++j, ++steps) {
-        // Two arrivals a step: a load's, or none in its place.
-        uint64_t *full = &bars->kv_full[steps % kSteps];
-        if (j > p.any.from) ok = load(vmap, full);
-        else if (lane == 0) mbar_arrive(full);
+      for (int j = p.any.from; ok && j < p.any.to; ++j, ++steps) {
+        uint64_t *bar = &bars->kv_full[steps % kSteps];
+        const Block mine = next;
+        look(j + 1);
+        ok = slot_free<DP>(a, load, bars);
         if (!ok) break;
-        if (j < p.any.to) {
+        const uint32_t dst = smem_u32(skv + load % X::SLOTS * X::TILE);
+        if (box) {
+          // A page past the pool's end, and boxes without a key, read as zeros.
+          const bool known = static_cast<unsigned>(mine.id) < static_cast<unsigned>(a.num_pages);
+          if (mine.how && !known) atomicOr(a.err, kErrIndexBit);
+          if (lane == 0) mbar_expect_tx(bar, X::TILE);
+          __syncwarp();
+          if (lane * box < KT) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const bool known = static_cast<unsigned>(id[x]) < static_cast<unsigned>(a.num_pages);
-            if (row[x] > -KT && !known) atomicOr(a.err, kErrIndexBit);
-            // Past the pool's end: reads as zeros.
-            page[x] = row[x] > -KT && known ? id[x] : a.num_pages;
-            at[x] = row[x] > -KT ? row[x] : 0;
+            for (int x = 0; x < DP / 64; ++x)
+              tma_box(dst + x * X::CHUNK + lane * box * 128, kmap, 64 * x, mine.row, kv,
+                      mine.how && known ? mine.id : a.num_pages, bar);
           }
-          look(j + 1);
-          ok = load(kmap, full);
-        } else if (lane == 0) {
-          mbar_arrive(full);
+          if (lane != 0) mbar_arrive(bar);
+        } else {
+          const int64_t off = block_offset(a, mine, kv);
+#pragma unroll 1
+          for (int x = 0; x < KT / 8; ++x)
+            copier.copy(a, a.k, __shfl_sync(0xffffffffu, off, x), dst + 1024 * x, c.b, kv, j * KT + 8 * x, c.lo, c.hi);
+          arrive_landed(bar);
         }
+        load += 2;
+      }
+      if (ok) mbar_arrive(&bars->kv_full[steps++ % kSteps]);  // no K in the last step
+    }
+    if (ok) piece_done(a, c, p);
+  }
+  // No copy outlives the warp's part.  Stopped early, the barriers of the steps
+  // under way may lack other warps' arrivals: their waits are short.
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!ok) {
+    if (q_count) {
+      for (uint32_t x = 0; x < kDrainPolls; ++x)
+        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->q_full, (q_count - 1) & 1))) break;
+    }
+    for (uint32_t n = steps > X::SLOTS ? steps - X::SLOTS : 0; n < steps; ++n) {
+      for (uint32_t x = 0; x < kDrainPolls; ++x)
+        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->kv_full[n % kSteps], (n / kSteps) & 1))) break;
+    }
+  }
+}
+
+// V: warp w has blocks w, w + 2, .. of a tile's 16 and looks them up a tile ahead.
+template <int DP>
+__device__ void value_role(const AttnArgs &a, Cursor c, int w, uint8_t *skv, Barriers *bars) {
+  using X = Tile<DP>;
+  const int lane = threadIdx.x & 31;
+  const Copier<DP> copier(a.D, X::CHUNK);
+  uint32_t load = 1, steps = 0;
+  bool ok = true;
+  while (ok && c.left > 0) {
+    const Piece p = piece_of(a, c);
+    if (p.any.from < p.any.to) {
+      const int kv = c.h / a.S;
+      Block next;
+      auto look = [&](int tile) {
+        next = Block{0, 0, 0};
+        if (lane < KT / 8 && tile < p.any.to) next = look_up(a, c.b, tile * KT + 8 * lane, c.lo, c.hi);
+      };
+      look(p.any.from);
+      mbar_arrive(&bars->kv_full[steps++ % kSteps]);  // no V in the first step
+      for (int j = p.any.from; ok && j < p.any.to; ++j, ++steps) {
+        uint64_t *bar = &bars->kv_full[steps % kSteps];
+        const int64_t off = block_offset(a, next, kv);
+        look(j + 1);
+        ok = slot_free<DP>(a, load, bars);
+        if (!ok) break;
+        const uint32_t dst = smem_u32(skv + load % X::SLOTS * X::TILE);
+#pragma unroll 2
+        for (int x = w; x < KT / 8; x += kValueWarps)
+          copier.copy(a, a.v, __shfl_sync(0xffffffffu, off, x), dst + 1024 * x, c.b, kv, j * KT + 8 * x, c.lo, c.hi);
+        arrive_landed(bar);
+        load += 2;
       }
     }
     if (ok) piece_done(a, c, p);
   }
-  // Stopped early: the copies in flight land before the block ends (bounded).
-  // A step that had only one of its loads gets the other's arrival.
-  if (!ok) {
-    if (lane == 0) mbar_arrive(&bars->kv_full[steps % kSteps]);
-    if (lane == 0) mbar_arrive(&bars->kv_full[steps % kSteps]);
-    __syncwarp();
-    if (q_count) {
-      for (uint32_t s = 0; s < kDefaultWaitLimit; ++s)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->q_full, (q_count - 1) & 1))) break;
-    }
-    for (uint32_t n = steps > kSteps - 1 ? steps - (kSteps - 1) : 0; n <= steps; ++n) {
-      for (uint32_t s = 0; s < kDefaultWaitLimit; ++s)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->kv_full[n % kSteps], (n / kSteps) & 1))) break;
-    }
-  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the warp's part
 }
 
 template <typename E, int DP>
@@ -405,6 +457,7 @@ __device__ void mma_role(const AttnArgs &a, Cursor c, uint8_t *sq, uint8_t *skv,
       for (int j = p.any.from; ok && j <= p.any.to; ++j, ++steps) {
         ok = wait_warp(&bars->kv_full[steps % kSteps], (steps / kSteps) & 1, abort, a.err, a.spin_limit);
         if (!ok) break;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         const bool has_v = j > p.any.from, has_k = j < p.any.to;
         const uint32_t vs = slot, ks = has_v ? (slot + 1 == X::SLOTS ? 0 : slot + 1) : slot;
         slot = has_k ? (ks + 1 == X::SLOTS ? 0 : ks + 1) : ks;
@@ -428,6 +481,7 @@ __device__ void mma_role(const AttnArgs &a, Cursor c, uint8_t *sq, uint8_t *skv,
                                              v + 128 * x, !first || x);
               if (j == p.half[h].to) mma_commit(&bars->o_full[h]);
             }
+            if (h == 1 && has_v) mma_commit(&bars->kv_empty[vs]);
             if (qk) {
 #pragma unroll
               for (int x = 0; x < DP / 16; ++x) {
@@ -437,7 +491,6 @@ __device__ void mma_role(const AttnArgs &a, Cursor c, uint8_t *sq, uint8_t *skv,
               mma_commit(&bars->s_full[h]);
             }
             if (h == 1) {
-              if (has_v) mma_commit(&bars->kv_empty[vs]);
               if (has_k) mma_commit(&bars->kv_empty[ks]);
               if (j == p.any.to - 1) mma_commit(&bars->q_empty);
             }
@@ -455,22 +508,11 @@ __device__ void mma_role(const AttnArgs &a, Cursor c, uint8_t *sq, uint8_t *skv,
     if (__all_sync(0xffffffffu, mbar_try_wait(&bars->mma_done, 0))) break;
 }
 
-// Bits [from, to) of a word whose bit 0 is column `base`.
-__device__ __forceinline__ uint32_t bits_of(int from, int to, int base) {
-  const int lo = max(from - base, 0), hi = min(to - base, 32);
-  if (lo >= hi) return 0u;
-  return (hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
-}
-
 // Columns of a row that it does not see become -infinity: the row sees keys
-// [span.lo, span.hi), and its 32 columns are keys key0 + base on; from the box
-// that holds the request's end on, columns are `shift` past their keys.
-__device__ __forceinline__ void hide(float (&s)[32], const Span &span, int key0, int len, int box, int base) {
-  const int tail = len & (box - 1), shift = tail ? box - tail : 0;
-  const int edge = shift ? len - tail - key0 : KT;  // that box's first column
-  const int lo = span.lo - key0, hi = span.hi - key0;
-  uint32_t seen = bits_of(lo, min(hi, edge), base);
-  if (shift) seen |= bits_of(max(lo, edge) + shift, hi + shift, base);
+// [span.lo, span.hi), and its 32 columns are keys key0 on.
+__device__ __forceinline__ void hide(float (&s)[32], const Span &span, int key0) {
+  const int lo = max(span.lo - key0, 0), hi = min(span.hi - key0, 32);
+  const uint32_t seen = lo >= hi ? 0u : (hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
 #pragma unroll
   for (int x = 0; x < 32; ++x)
     if (!(seen >> x & 1u)) s[x] = kNegInf;
@@ -530,7 +572,7 @@ __device__ __noinline__ void redo_rows(const AttnArgs &a, Cursor c) {
 }
 
 template <typename E, int DP>
-__device__ void softmax_role(const AttnArgs &a, int box, Barriers *bars, uint32_t tmem) {
+__device__ void softmax_role(const AttnArgs &a, Barriers *bars, uint32_t tmem) {
   using X = Tile<DP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 3, part = warp >> 2 & 1;
   const int pair = warp >> 3 << 2 | (warp & 3), meeting = 1 + pair;
@@ -544,7 +586,7 @@ __device__ void softmax_role(const AttnArgs &a, int box, Barriers *bars, uint32_
   uint32_t s_count = 0, o_count = 0;
   bool continues = cursor->at != 0, dead = false;
   while (cursor->left > 0) {
-    int from, to_tile, len;
+    int from, to_tile;
     Span span{0, 0};
     int deep_lo = 0, deep_hi = 0x7FFFFFFF;  // keys that every live row of the warp sees
     {
@@ -558,7 +600,6 @@ __device__ void softmax_role(const AttnArgs &a, int box, Barriers *bars, uint32_
       }
       from = h ? p.half[1].from : p.half[0].from;
       to_tile = h ? p.half[1].to : p.half[0].to;
-      len = c.r.len;
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) {
@@ -577,11 +618,11 @@ __device__ void softmax_role(const AttnArgs &a, int box, Barriers *bars, uint32_
         tc_fence_after();
         tmem_ld32<0>(ts + 32, s);
         tmem_wait_ld();
-        if (!deep) hide(s, span, j * KT, len, box, KC * part + 32);
+        if (!deep) hide(s, span, j * KT + KC * part + 32);
         top = chunk_top(s);
         tmem_ld32<0>(ts, s);
         tmem_wait_ld();
-        if (!deep) hide(s, span, j * KT, len, box, KC * part);
+        if (!deep) hide(s, span, j * KT + KC * part);
         top = fmaxf(top, chunk_top(s)) * a.scale_log2;
       }
       // Raise the reference when a score is far above it (and in the first tile).
@@ -604,7 +645,7 @@ __device__ void softmax_role(const AttnArgs &a, int box, Barriers *bars, uint32_
       weights<E>(s, a.scale_log2, base, sums, ts);
       tmem_ld32<0>(ts + 32, s);
       tmem_wait_ld();
-      if (!deep) hide(s, span, j * KT, len, box, KC * part + 32);
+      if (!deep) hide(s, span, j * KT + KC * part + 32);
       weights<E>(s, a.scale_log2, base, sums, ts + 16);
       tmem_wait_st();
       tc_fence_before();
@@ -689,7 +730,7 @@ __device__ void softmax_role(const AttnArgs &a, int box, Barriers *bars, uint32_
 template <typename E, int DP>
 __global__ void __launch_bounds__(NT, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ AttnArgs a, int box) {
+               const __grid_constant__ AttnArgs a, int box) {
   using X = Tile<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sq = smem, *skv = smem + 2 * X::TILE;
@@ -699,11 +740,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&qmap) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+    if (box) asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < kSteps; ++i) mbar_init(&bars->kv_full[i], 2);
+    for (int i = 0; i < kSteps; ++i) mbar_init(&bars->kv_full[i], 32 * (1 + kValueWarps));
     for (int i = 0; i < X::SLOTS; ++i) mbar_init(&bars->kv_empty[i], 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(&bars->s_full[h], 1);
@@ -723,7 +763,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
       *reinterpret_cast<uint4 *>(sq + x) = make_uint4(0, 0, 0, 0);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  if (warp == kSoftmaxWarps + 1) {
+  if (warp == kSoftmaxWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&bars->tmem_base)),
                  "r"(512u));
@@ -736,16 +776,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp < kSoftmaxWarps) {
-    softmax_role<E, DP>(a, box, bars, tmem);
-  } else {
-    if (warp == kSoftmaxWarps) load_role<DP>(a, c, &qmap, &kmap, &vmap, box, sq, skv, bars);
-    else if (warp == kSoftmaxWarps + 1) mma_role<E, DP>(a, c, sq, skv, bars, tmem);
-  }
+  if (warp < kSoftmaxWarps) softmax_role<E, DP>(a, bars, tmem);
+  else if (warp == kSoftmaxWarps) mma_role<E, DP>(a, c, sq, skv, bars, tmem);
+  else if (warp == kSoftmaxWarps + 1) key_role<DP>(a, c, &qmap, &kmap, box, sq, skv, bars);
+  else value_role<DP>(a, c, warp - kSoftmaxWarps - 2, skv, bars);
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kSoftmaxWarps + 1) {
+  if (warp == kSoftmaxWarps) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
@@ -760,11 +798,14 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.TH = 128 / a.Gs;
   a.TQ = 2 * a.TH;
   a.min_tiles = 1;
-  const int box = box_rows(a.page, KT);
+  // Rows of a TMA box of K: the largest power of two that divides the page.
+  int box = 0;
+  if (a.page % 8 == 0)
+    for (box = 8; box < KT && a.page % (2 * box) == 0;) box *= 2;
   const int type = E::kF16 ? kTypeF16 : kTypeBF16;
-  CUtensorMap q, k, v;
-  cudaError_t e = pool_maps(a, type, box, &k, &v);
-  if (e == cudaSuccess) e = query_map(a, type, &q);
+  CUtensorMap q, k;
+  cudaError_t e = query_map(a, type, &q);
+  if (e == cudaSuccess) e = box ? key_map(a, type, box, &k) : (k = q, cudaSuccess);
   if (e != cudaSuccess) return e;
   constexpr size_t smem = smem_bytes<DP>();
   e = ensure_smem_limit<prefill_kernel<E, DP>>(smem);
@@ -772,7 +813,7 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   int blocks = sm_count();
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
   blocks = static_cast<int>(std::min<size_t>(std::min(blocks, kMaxBlocks), ws_bytes / per_block));
-  prefill_kernel<E, DP><<<blocks, NT, smem, stream>>>(q, k, v, a, box);
+  prefill_kernel<E, DP><<<blocks, NT, smem, stream>>>(q, k, a, box);
   const cudaError_t le = cudaGetLastError();
   return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);
 }
