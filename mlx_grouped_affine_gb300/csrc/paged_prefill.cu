@@ -238,6 +238,14 @@ __device__ __forceinline__ void tmem_scale16(uint32_t addr, float f) {
       : "memory");
 }
 
+// 32 bytes to global memory, 32-byte aligned.
+__device__ __forceinline__ void store32(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                        uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+               "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+
 // ---------------------------------------------------------------- pieces ----
 
 // Key tiles of a piece [t0, t1) that half h's rows see; from == to: none.
@@ -440,6 +448,7 @@ __device__ void value_role(const AttnArgs &a, Cursor c, int w, uint8_t *skv, Bar
   asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the warp's part
 }
 
+// By one thread: a vote of the warp after every wait would cost as much again.
 template <typename E, int DP>
 __device__ void mma_role(const AttnArgs &a, Cursor c, uint8_t *sq, uint8_t *skv, Barriers *bars, uint32_t tmem) {
   using X = Tile<DP>;
@@ -610,8 +619,6 @@ __device__ void softmax_role(const AttnArgs &a, Barriers *bars, uint32_t tmem) {
     for (int j = from; j < to_tile; ++j) {
       dead = dead || !wait_warp(&bars->s_full[h], s_count & 1, abort, a.err, a.spin_limit);
       ++s_count;
-      // The columns in two chunks of 32: both are read for the maximum, the first
-      // stays in registers, the second is read again (96 registers a thread).
       const bool deep = j * KT >= deep_lo && j * KT + KT <= deep_hi;
       float s[32], top = kNegInf;
       if (!dead) {
@@ -682,6 +689,9 @@ __device__ void softmax_role(const AttnArgs &a, Barriers *bars, uint32_t tmem) {
       uint16_t *out = static_cast<uint16_t *>(a.out) + token * a.out_stride + static_cast<int64_t>(head) * a.D +
                       DP / 2 * part;
       const int cols = a.D - DP / 2 * part;  // of the head from this part on
+      // A row's stores are whole 32-byte sectors where rows and heads allow it: a
+      // warp's store touches 32 rows, and each is a trip of its own.
+      const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | a.out_stride * 2 | a.D * 2) & 31) == 0;
       bool bad = false;
       tc_fence_after();
 #pragma unroll 1
@@ -696,15 +706,20 @@ __device__ void softmax_role(const AttnArgs &a, Barriers *bars, uint32_t tmem) {
         }
         if (!whole) {
 #pragma unroll
-          for (int y = 0; y < 16; y += 4)
-            *reinterpret_cast<float4 *>(piece + x + y) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
-        } else if (live) {
-#pragma unroll
           for (int y = 0; y < 16; y += 8)
-            if (x + y < cols)
-              *reinterpret_cast<uint4 *>(out + x + y) =
-                  make_uint4(E::pack2(o[y], o[y + 1]), E::pack2(o[y + 2], o[y + 3]), E::pack2(o[y + 4], o[y + 5]),
-                             E::pack2(o[y + 6], o[y + 7]));
+            store32(piece + x + y, __float_as_uint(o[y]), __float_as_uint(o[y + 1]), __float_as_uint(o[y + 2]),
+                    __float_as_uint(o[y + 3]), __float_as_uint(o[y + 4]), __float_as_uint(o[y + 5]),
+                    __float_as_uint(o[y + 6]), __float_as_uint(o[y + 7]));
+        } else if (live) {
+          uint32_t u[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) u[y] = E::pack2(o[2 * y], o[2 * y + 1]);
+          if (wide) {
+            if (x < cols) store32(out + x, u[0], u[1], u[2], u[3], u[4], u[5], u[6], u[7]);
+          } else {
+            if (x < cols) *reinterpret_cast<uint4 *>(out + x) = make_uint4(u[0], u[1], u[2], u[3]);
+            if (x + 8 < cols) *reinterpret_cast<uint4 *>(out + x + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+          }
         }
       }
       if (any) {
