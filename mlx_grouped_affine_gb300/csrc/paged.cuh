@@ -6,10 +6,11 @@
 // shares every K and V tile it reads.  An item is (request, kv head, TQ
 // consecutive new tokens): it walks the key tiles (KT keys each) that any of
 // its rows may see.  (A group of more heads than a tile has rows is cut into
-// S slices of Gs heads, each walked as a kv head of its own.)  All items' key tiles, in order, form one line of W tiles;
-// block c of `parts` takes tiles [c W / parts, (c + 1) W / parts).  Every
-// block therefore does the same work whatever the requests' lengths are, and
-// at most parts - 1 items are cut.  A cut item's pieces leave their running
+// S slices of Gs heads, each walked as a kv head of its own.)  All items' key tiles, in order, form one line; an item
+// counts item_cost units for its start and end, then one for each tile, W in
+// all, and block c of `parts` takes units [c W / parts, (c + 1) W / parts).
+// Every block therefore does the same work whatever the requests' lengths are,
+// and at most parts - 1 items are cut.  A cut item's pieces leave their running
 // maximum, sum and unnormalised output in the workspace, and a second kernel
 // joins them in block order (so results repeat bit for bit).
 //
@@ -55,7 +56,8 @@ struct AttnArgs {
   int causal, window;          // window 0: none
   float scale_log2;            // scale * log2(e)
   int min_rows, max_rows;      // requests of another row count are left to the other kernel
-  int min_tiles;               // least key tiles worth a block of their own
+  int min_tiles;               // least units worth a block of their own
+  int item_cost;               // units of an item beside its tiles
 };
 
 // A request as the kernels use it: lengths clamped so that nothing that the
@@ -126,7 +128,7 @@ struct Cursor {
   int lo, hi;         // keys of the item
   int tile0, tiles;   // key tiles of the item
   int at;             // next tile of the item, from 0
-  int left;           // tiles left for the block
+  int left;           // units left for the block
 };
 
 template <int KT>
@@ -138,8 +140,9 @@ __device__ __forceinline__ void cursor_item(const AttnArgs &a, Cursor &c) {
   c.tiles = t.tiles;
 }
 
-// On to the next item (only when tiles are left for the block, so one exists;
-// the bound on b stops a block whose lengths changed under it).
+// On to the next item, whose start takes item_cost units (only when units are
+// left for the block, so one exists; the bound on b stops a block whose lengths
+// changed under it).
 template <int KT>
 __device__ __forceinline__ void cursor_next(const AttnArgs &a, Cursor &c) {
   c.at = 0;
@@ -157,6 +160,16 @@ __device__ __forceinline__ void cursor_next(const AttnArgs &a, Cursor &c) {
     }
   }
   cursor_item<KT>(a, c);
+  c.left = max(c.left - a.item_cost, 0);
+}
+
+// The cursor's item from its unit u on, with `left` units from there.
+template <int KT>
+__device__ __forceinline__ void cursor_start(const AttnArgs &a, Cursor &c, int u, long long left) {
+  cursor_item<KT>(a, c);
+  const int skip = max(a.item_cost - u, 0);
+  c.at = max(u - a.item_cost, 0);
+  c.left = static_cast<int>(max(left - skip, 0ll));
 }
 
 // x * y / z, in 32 bits where the product fits (a 64-bit division costs several
@@ -200,12 +213,12 @@ __device__ __forceinline__ long long block_scan(long long v, PlanScratch<NT> &s,
   return before + v;
 }
 
-// Tiles of one head slice of request r: every step-th item from `from` on.
+// Units of one head slice of request r: every step-th item from `from` on.
 template <int KT>
 __device__ __forceinline__ long long head_tiles(const AttnArgs &a, const Request &r, int from, int step) {
   long long n = 0;
   const int items = items_of(a, r);
-  for (int q = from; q < items; q += step) n += item_tiles<KT>(a, r, q).tiles;
+  for (int q = from; q < items; q += step) n += item_tiles<KT>(a, r, q).tiles + a.item_cost;
   return n;
 }
 
@@ -242,15 +255,15 @@ __device__ long long request_tiles(const AttnArgs &a, int base, PlanScratch<NT> 
 // The cut item that block `part` continues, for the joining kernel: request,
 // head, item, the blocks that hold the item's first and last tiles, and the
 // request's first token and count (block
-// p holds tile g when p W / parts <= g, so p = ((g + 1) parts - 1) / W).
+// p holds unit g when p W / parts <= g, so p = ((g + 1) parts - 1) / W).
 __device__ __forceinline__ void leave_desc(const AttnArgs &a, const Cursor &c, int part, long long t0,
                                            long long parts, long long W) {
   int *d = a.desc + 8 * part;
-  if (c.at == 0) {
+  if (c.at == 0 || c.left == 0) {
     d[0] = -1;
     return;
   }
-  const long long g0 = t0 - c.at, g1 = g0 + c.tiles - 1;
+  const long long g0 = t0 - c.at, g1 = g0 + c.tiles - 1;  // units of its first and last tiles
   d[0] = c.b;
   d[1] = c.h;
   d[2] = c.qt;
@@ -312,7 +325,7 @@ __device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
   c.at = 0;
   for (int base = 0; base < items; base += 32) {
     const int q = base + lane;
-    const long long n = q < items ? item_tiles<KT>(a, c.r, q).tiles : 0;
+    const long long n = q < items ? item_tiles<KT>(a, c.r, q).tiles + a.item_cost : 0;
     const long long upto = warp_scan(n) + before;
     const unsigned hit = __ballot_sync(0xffffffffu, in_head < upto && in_head >= upto - n);
     if (hit) {
@@ -323,8 +336,7 @@ __device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
     }
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
-  c.left = static_cast<int>(t1 - t0);
-  cursor_item<KT>(a, c);
+  cursor_start<KT>(a, c, c.at, t1 - t0);
   if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
   return c;
 }
@@ -385,7 +397,7 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   if (threadIdx.x == 0) s.cursor.qt = s.cursor.at = 0;
   for (int base = 0; base < items; base += NT) {
     const int q = base + threadIdx.x;
-    const long long mine = q < items ? item_tiles<KT>(a, r, q).tiles : 0;
+    const long long mine = q < items ? item_tiles<KT>(a, r, q).tiles + a.item_cost : 0;
     const long long incl = block_scan<NT>(mine, s, &total) + before;
     if (in_head < incl && in_head >= incl - mine) {
       s.cursor.qt = q;
@@ -399,9 +411,7 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   c.b = b;
   c.h = h;
   c.qt = s.cursor.qt;
-  c.at = s.cursor.at;
-  c.left = static_cast<int>(t1 - t0);
-  cursor_item<KT>(a, c);
+  cursor_start<KT>(a, c, s.cursor.at, t1 - t0);
   if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
   return c;
 }
@@ -462,8 +472,8 @@ __device__ __forceinline__ int64_t key_offset(const AttnArgs &a, int b, int h, i
 // stride: cp.async at 12 cycles an instruction of a warp, 43 bytes a cycle of one
 // warp and 53 of two.  (A shuffled address for every row: 31 cycles.  TMA boxes
 // of a page's rows: 45 cycles a box and 3.5 a 128-byte row, 20 bytes a cycle at
-// 16-row pages.)  Blocks that the item sees in part, and other page sizes, go row
-// by row.
+// 16-row pages.)  Rows that hold no key of the item are written as zeros.  At
+// other page sizes every row is looked up when it is copied.
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -478,20 +488,19 @@ struct Block {
 __device__ __forceinline__ Block look_up(const AttnArgs &a, int b, int key, int lo, int hi) {
   Block x{0, 0, 0};
   if (key + 8 <= lo || key >= hi) return x;
-  if (key < lo || key + 8 > hi || a.page % 8 != 0) {
-    x.how = 2;
-    return x;
+  x.how = 2;
+  if (a.page % 8 == 0) {
+    x.how = 1;
+    const int pg = key / a.page;
+    x.row = key - pg * a.page;
+    x.id = __ldg(a.table + b * a.table_stride + pg);
   }
-  x.how = 1;
-  const int pg = key / a.page;
-  x.row = key - pg * a.page;
-  x.id = __ldg(a.table + b * a.table_stride + pg);
   return x;
 }
 
 // Element offset of the block's first row in the pool; -1 none, -2 row by row.
 __device__ __forceinline__ int64_t block_offset(const AttnArgs &a, const Block &x, int kv) {
-  if (x.how != 1) return -static_cast<int64_t>(x.how) + (x.how == 0 ? -1 : 0);
+  if (x.how != 1) return x.how == 0 ? -1 : -2;
   if (static_cast<unsigned>(x.id) >= static_cast<unsigned>(a.num_pages)) {
     atomicOr(a.err, kErrIndexBit);
     return -1;
@@ -522,22 +531,30 @@ struct Copier {
   __device__ __forceinline__ void copy(const AttnArgs &a, const void *pool, int64_t off, uint32_t dst, int b,
                                        int kv, int key, int lo, int hi) const {
     const uint16_t *src = static_cast<const uint16_t *>(pool) + col;
-    if (off >= 0) {
+    if (off >= 0 && key >= lo && key + 8 <= hi) {
       src += off + first * a.token_stride;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         cp_async16(dst + at[i], src, bytes);
         src += RPI * a.token_stride;
       }
+    } else if (off >= -1) {  // rows [lo, hi) of the block's keys, or none
+      src += max(off, int64_t(0)) + first * a.token_stride;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int k = key + first + i * RPI;
+        cp_async16(dst + at[i], src, off >= 0 && k >= lo && k < hi ? bytes : 0u);
+        src += RPI * a.token_stride;
+      }
     } else {
 #pragma unroll 1
       for (int i = 0; i < N; ++i) {
         const int k = key + first + i * RPI;
-        const int64_t o = off == -2 && k >= lo && k < hi ? key_offset(a, b, kv, k) : -1;
+        const int64_t o = k >= lo && k < hi ? key_offset(a, b, kv, k) : -1;
         uint32_t x = at[0];
 #pragma unroll
         for (int y = 1; y < N; ++y) x = i == y ? at[y] : x;
-        cp_async16(dst + x, src + (o >= 0 ? o : 0), o >= 0 ? bytes : 0u);
+        cp_async16(dst + x, src + max(o, int64_t(0)), o >= 0 ? bytes : 0u);
       }
     }
   }

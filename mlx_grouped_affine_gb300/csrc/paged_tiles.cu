@@ -235,6 +235,7 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.heads = a.Hkv * a.S;
   a.TQ = a.TH = R / a.Gs;
   a.min_tiles = 1;
+  a.item_cost = 1;
   constexpr size_t smem = smem_bytes<DP>();
   const cudaError_t e = ensure_smem_limit<tiles_kernel<E, DP>>(smem);
   if (e != cudaSuccess) return e;
