@@ -12,7 +12,8 @@
 // Every block therefore does the same work whatever the requests' lengths are,
 // and at most parts - 1 items are cut.  A cut item's pieces leave their running
 // maximum, sum and unnormalised output in the workspace, and a second kernel
-// joins them in block order (so results repeat bit for bit).
+// joins them in block order (so results repeat bit for bit).  It works out the
+// blocks' places itself, while the first kernel still runs.
 //
 // Softmax over a line of keys in pieces: with m = max s, l = sum 2^(s - m) and
 // o = sum 2^(s - m) v over each piece, pieces a and b join as
@@ -30,7 +31,6 @@ namespace paged {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
-constexpr int kMaxBlocks = 512;  // of an attention launch: descriptors in the workspace
 
 struct AttnArgs {
   const void *q;
@@ -44,7 +44,6 @@ struct AttnArgs {
   int64_t out_stride;
   float *lse;                  // [T, Hq] or null
   float *ws;                   // partial rows of cut items
-  int *desc;                   // [blocks][8]: the cut item each block continues
   unsigned *err;
   uint32_t spin_limit;
   int page, num_pages;
@@ -252,25 +251,17 @@ __device__ long long request_tiles(const AttnArgs &a, int base, PlanScratch<NT> 
   return mine;
 }
 
-// The cut item that block `part` continues, for the joining kernel: request,
-// head, item, the blocks that hold the item's first and last tiles, and the
-// request's first token and count (block
-// p holds unit g when p W / parts <= g, so p = ((g + 1) parts - 1) / W).
-__device__ __forceinline__ void leave_desc(const AttnArgs &a, const Cursor &c, int part, long long t0,
-                                           long long parts, long long W) {
-  int *d = a.desc + 8 * part;
-  if (c.at == 0 || c.left == 0) {
-    d[0] = -1;
-    return;
-  }
-  const long long g0 = t0 - c.at, g1 = g0 + c.tiles - 1;  // units of its first and last tiles
-  d[0] = c.b;
-  d[1] = c.h;
-  d[2] = c.qt;
-  d[3] = static_cast<int>(mul_div((g0 + 1) * parts - 1, 1, W));
-  d[4] = static_cast<int>(mul_div((g1 + 1) * parts - 1, 1, W));
-  d[5] = c.r.first;
-  d[6] = c.r.n;
+// A block's place in the line, and the blocks that hold the first and the last
+// tile of the item it begins in (block p holds unit g when p W / parts <= g, so
+// p = ((g + 1) parts - 1) / W).
+struct Place {
+  Cursor c;
+  int first, last;
+};
+__device__ __forceinline__ void place_cut(Place &p, long long t0, long long parts, long long W) {
+  const long long g0 = t0 - p.c.at, g1 = g0 + p.c.tiles - 1;  // units of its first and last tiles
+  p.first = static_cast<int>(mul_div((g0 + 1) * parts - 1, 1, W));
+  p.last = static_cast<int>(mul_div((g1 + 1) * parts - 1, 1, W));
 }
 
 __device__ __forceinline__ long long warp_scan(long long v) {
@@ -286,7 +277,7 @@ __device__ __forceinline__ long long warp_scan(long long v) {
 // plan_block for at most 32 requests: one a lane, every warp for itself, no
 // barrier (the start of a short call is most of it).
 template <int KT>
-__device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
+__device__ Place plan_warp(const AttnArgs &a, int part, int blocks) {
   const int lane = threadIdx.x & 31;
   Request r{0, 0, 0};
   if (lane < a.B) r = request_of(a, lane);
@@ -304,12 +295,10 @@ __device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
   const long long mine = one * a.heads, incl = warp_scan(mine);
   const long long W = __shfl_sync(0xffffffffu, incl, 31);
   const int parts = static_cast<int>(min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks)));
-  Cursor c;
+  Place place;
+  Cursor &c = place.c;
   c.left = 0;
-  if (part >= parts) {
-    if (threadIdx.x == 0) a.desc[8 * part] = -1;
-    return c;
-  }
+  if (part >= parts) return place;
   const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
   const int b = __ffs(__ballot_sync(0xffffffffu, t0 < incl && t0 >= incl - mine)) - 1;
   c.r = Request{__shfl_sync(0xffffffffu, r.first, b), __shfl_sync(0xffffffffu, r.n, b),
@@ -337,15 +326,14 @@ __device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
   cursor_start<KT>(a, c, c.at, t1 - t0);
-  if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
-  return c;
+  place_cut(place, t0, parts, W);
+  return place;
 }
 
-// The block's place in the line: its cursor and how many tiles it has (0: none).
-// Called by all NT threads of block `part` of `blocks`.  Also leaves in
-// desc[part] the cut item that the block continues.
+// The place of block `part` of `blocks` (no units left: none).  Called by all NT
+// threads of a block.
 template <int NT, int KT>
-__device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratch<NT> &s) {
+__device__ Place plan_block(const AttnArgs &a, int part, int blocks, PlanScratch<NT> &s) {
   if (a.B <= 32) return plan_warp<KT>(a, part, blocks);
   // Total, keeping the first chunk's counts.
   long long W = 0, total;
@@ -357,12 +345,10 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
     W += total;
   }
   const long long parts = min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks));
-  Cursor c;
+  Place place;
+  Cursor &c = place.c;
   c.left = 0;
-  if (part >= parts) {
-    if (threadIdx.x == 0) a.desc[8 * part] = -1;
-    return c;
-  }
+  if (part >= parts) return place;
   const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
   // The request that holds tile t0.
   long long before = 0;
@@ -381,10 +367,7 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   }
   __syncthreads();
   const int b = s.found;
-  if (b < 0) {  // only if the lengths changed while the kernel ran
-    if (threadIdx.x == 0) a.desc[8 * part] = -1;
-    return c;
-  }
+  if (b < 0) return place;  // only if the lengths changed while the kernel ran
   const long long in_request = t0 - s.found_before;
   const Request r = request_of(a, b);
   // The head (all head slices of a request have the same tiles), then the item.
@@ -412,8 +395,8 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   c.h = h;
   c.qt = s.cursor.qt;
   cursor_start<KT>(a, c, s.cursor.at, t1 - t0);
-  if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
-  return c;
+  place_cut(place, t0, parts, W);
+  return place;
 }
 
 // Row r of item (h, qt): its new token in the request and its query head;
@@ -633,20 +616,21 @@ constexpr int kJoinLanes = 16;
 template <int R>
 constexpr int join_weights(int blocks) { return 2 * R + 3 * blocks; }
 
-template <typename E, int R, int DP>
+template <typename E, int R, int DP, int KT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a) {
   using T = typename Elem<E>::type;
   extern __shared__ float weight[];  // [rows][P]
   __shared__ float4 sums[kJoinThreads];
   __shared__ unsigned bad_rows[(R + 31) / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  griddep_wait();
-  const int4 *d = reinterpret_cast<const int4 *>(a.desc + 8 * (blockIdx.x + 1));
-  const int4 d0 = d[0], d1 = d[1];
-  const int b = d0.x, h = d0.y, qt = d0.z, first = d0.w, last = d1.x;
-  if (b < 0) return;
-  const Request r{d1.y, d1.z, 0};
+  __shared__ PlanScratch<kJoinThreads> scratch;
+  // The item that attention block blockIdx.x + 1 continues; gridDim.x + 1 blocks.
+  const Place place = plan_block<kJoinThreads, KT>(a, blockIdx.x + 1, gridDim.x + 1, scratch);
+  if (place.c.left <= 0 || place.c.at == 0) return;
+  const int b = place.c.b, h = place.c.h, qt = place.c.qt, first = place.first, last = place.last;
+  const Request r = place.c.r;
   const int P = last - first + 1, me = blockIdx.x - first;
+  griddep_wait();
   constexpr int U = R * DP / 4, UR = DP / 4;  // float4 sums of an item, of a row
   const int u0 = static_cast<int>(static_cast<unsigned>(me * U) / static_cast<unsigned>(P - 1));
   const int u1 = static_cast<int>(static_cast<unsigned>((me + 1) * U) / static_cast<unsigned>(P - 1));
@@ -766,7 +750,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 // After the attention kernel on the same stream; starts early and waits.
-template <typename E, int R, int DP>
+template <typename E, int R, int DP, int KT>
 cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -779,7 +763,7 @@ cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<E, R, DP>, a);
+  return cudaLaunchKernelEx(&cfg, join_kernel<E, R, DP, KT>, a);
 }
 
 }  // namespace paged

@@ -6,8 +6,10 @@
 // pairs are (i, i + r/2) or (2i, 2i + 1); axis(i) follows from the sections.
 //
 // Nothing is read twice but the table's row, so bytes bound it: q, k, v read
-// once, q, K, V written once, 16 bytes a lane.  A thread has eight pairs of a
-// token for HPT heads: their cosines and sines stay in registers.
+// once, q, K, V written once, 16 bytes a lane.  A thread has one place in a token
+// (eight pairs of a head, or eight elements that pass through) and walks a few
+// tokens with it: where its elements come from and go to is worked out once, a
+// token costs it a few adds.
 #include "paged.cuh"
 
 namespace qmm {
@@ -31,9 +33,7 @@ struct RopeArgs {
 };
 
 template <typename E>
-struct Vec8;  // eight elements in their own type
-template <typename E>
-struct Vec8 {
+struct Vec8 {  // eight elements in their own type
   uint4 w;
   __device__ __forceinline__ void load(const uint16_t *p) { w = *reinterpret_cast<const uint4 *>(p); }
   __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = w; }
@@ -82,161 +82,134 @@ __device__ __forceinline__ int64_t slot_offset(const RopeArgs &a, int t) {
   return pg * a.page_stride + (slot - pg * a.page) * a.token_stride;
 }
 
-template <typename E, int HPT, bool INTERLEAVED>
-__global__ void __launch_bounds__(256) rope_append_kernel(RopeArgs a, int tokens_per_block, int units) {
-  using T = typename Elem<E>::type;
+// The cosines and sines of pairs i0 .. i0 + 7 for token t; a bit for each pair
+// whose position is outside the table.  `axis` is the first pair's.  Where the
+// axis changes among the eight, the next axis's row is read whole too and its
+// pairs replace the first's.
+__device__ __forceinline__ unsigned angles(const RopeArgs &a, int t, int i0, int axis, float (&c)[8],
+                                           float (&s)[8]) {
   const int half = a.r / 2;
-  const int turns = a.r / 16, keeps = (a.D - a.r) / 8, copies = a.D / 8;
-  const int groups = (a.Hq + a.Hk + HPT - 1) / HPT;
-  const int t0 = blockIdx.x * tokens_per_block;
-  const int here = min(tokens_per_block, a.T - t0);
-  for (int x = threadIdx.x; x < here * units; x += blockDim.x) {
-    const int t = t0 + x / units;
-    int u = x % units;
-    const int64_t row = t;
-    if (u < groups * turns) {
-      // Eight pairs of HPT heads of q or k.
-      const int h0 = u / turns * HPT, i0 = u % turns * 8;
-      Vec8<E> lo[HPT], hi[HPT];
+  auto row = [&](int x, float (&cx)[8], float (&sx)[8]) {
+    const int pos = __ldg(a.positions + static_cast<int64_t>(x) * a.T + t);
+    const bool ok = static_cast<unsigned>(pos) < static_cast<unsigned>(a.max_pos);
+    const float *p = a.table + static_cast<int64_t>(ok ? pos : 0) * a.r + i0;
 #pragma unroll
-      for (int j = 0; j < HPT; ++j) {
-        const int h = h0 + j;
-        if (h >= a.Hq + a.Hk) continue;
-        const T *p = h < a.Hq ? static_cast<const T *>(a.q) + row * a.q_stride + static_cast<int64_t>(h) * a.D
-                              : static_cast<const T *>(a.k) + row * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.D;
-        lo[j].load(p + (INTERLEAVED ? 2 * i0 : i0));
-        hi[j].load(p + (INTERLEAVED ? 2 * i0 + 8 : half + i0));
-      }
-      float c[8], s[8];
-      bool known = true;
-      int axis = 0;
-      while (axis < a.axes - 1 && i0 >= a.end[axis]) ++axis;
-      if (axis == a.axes - 1 || i0 + 8 <= a.end[axis]) {
-        // The eight pairs share an axis.
-        const int pos = __ldg(a.positions + static_cast<int64_t>(axis) * a.T + t);
-        known = static_cast<unsigned>(pos) < static_cast<unsigned>(a.max_pos);
-        const float *p = a.table + static_cast<int64_t>(known ? pos : 0) * a.r + i0;
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 cv = __ldg(reinterpret_cast<const float4 *>(p + e));
-          const float4 sv = __ldg(reinterpret_cast<const float4 *>(p + half + e));
-          c[e] = cv.x; c[e + 1] = cv.y; c[e + 2] = cv.z; c[e + 3] = cv.w;
-          s[e] = sv.x; s[e + 1] = sv.y; s[e + 2] = sv.z; s[e + 3] = sv.w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          while (axis < a.axes - 1 && i0 + e >= a.end[axis]) ++axis;
-          const int pos = __ldg(a.positions + static_cast<int64_t>(axis) * a.T + t);
-          const bool ok = static_cast<unsigned>(pos) < static_cast<unsigned>(a.max_pos);
-          known &= ok;
-          const float *p = a.table + static_cast<int64_t>(ok ? pos : 0) * a.r + i0 + e;
-          c[e] = __ldg(p);
-          s[e] = __ldg(p + half);
-        }
-      }
-      if (!known) {
-        atomicOr(a.err, kErrIndexBit);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = s[e] = 0.f;
-      }
-      const int64_t slot = h0 + HPT > a.Hq ? slot_offset(a, t) : -1;
-#pragma unroll
-      for (int j = 0; j < HPT; ++j) {
-        const int h = h0 + j;
-        if (h >= a.Hq + a.Hk) continue;
-        float x0[8], x1[8];
-        lo[j].get(x0);
-        hi[j].get(x1);
-        if (INTERLEAVED) {
-          // pairs (x[2e], x[2e + 1]) of the sixteen consecutive elements
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float u0 = x0[2 * e], u1 = x0[2 * e + 1], w0 = x1[2 * e], w1 = x1[2 * e + 1];
-            x0[2 * e] = u0 * c[e] - u1 * s[e];
-            x0[2 * e + 1] = u1 * c[e] + u0 * s[e];
-            x1[2 * e] = w0 * c[4 + e] - w1 * s[4 + e];
-            x1[2 * e + 1] = w1 * c[4 + e] + w0 * s[4 + e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float u0 = x0[e], u1 = x1[e];
-            x0[e] = u0 * c[e] - u1 * s[e];
-            x1[e] = u1 * c[e] + u0 * s[e];
-          }
-        }
-        if (!known) {  // a zero row, whatever q and k hold
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x0[e] = x1[e] = 0.f;
-        }
-        lo[j].set(x0);
-        hi[j].set(x1);
-        T *p;
-        if (h < a.Hq) {
-          p = static_cast<T *>(a.q_out) + row * a.out_stride + static_cast<int64_t>(h) * a.D;
-        } else {
-          if (slot < 0) continue;
-          p = static_cast<T *>(a.k_cache) + slot + (h - a.Hq) * a.head_stride;
-        }
-        lo[j].store(p + (INTERLEAVED ? 2 * i0 : i0));
-        hi[j].store(p + (INTERLEAVED ? 2 * i0 + 8 : half + i0));
-      }
-      continue;
+    for (int e = 0; e < 8; e += 4) {
+      const float4 cv = __ldg(reinterpret_cast<const float4 *>(p + e));
+      const float4 sv = __ldg(reinterpret_cast<const float4 *>(p + half + e));
+      cx[e] = cv.x; cx[e + 1] = cv.y; cx[e + 2] = cv.z; cx[e + 3] = cv.w;
+      sx[e] = sv.x; sx[e + 1] = sv.y; sx[e + 2] = sv.z; sx[e + 3] = sv.w;
     }
-    u -= groups * turns;
-    if (u < groups * keeps) {
-      // Eight elements past the rotated ones, of HPT heads of q or k.
-      const int h0 = u / keeps * HPT, d = a.r + u % keeps * 8;
-      Vec8<E> w[HPT];
+    return ok ? 0u : 0xFFu;
+  };
+  unsigned outside = row(axis, c, s);
+#pragma unroll 1
+  for (int x = axis; x < a.axes - 1 && a.end[x] < i0 + 8; ++x) {
+    const int from = a.end[x] - i0;  // the next axis's pairs
+    float cx[8], sx[8];
+    const unsigned bad = row(x + 1, cx, sx);
 #pragma unroll
-      for (int j = 0; j < HPT; ++j) {
-        const int h = h0 + j;
-        if (h >= a.Hq + a.Hk) continue;
-        w[j].load(h < a.Hq ? static_cast<const T *>(a.q) + row * a.q_stride + static_cast<int64_t>(h) * a.D + d
-                           : static_cast<const T *>(a.k) + row * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.D + d);
+    for (int e = 1; e < 8; ++e) {
+      if (e >= from) {
+        c[e] = cx[e];
+        s[e] = sx[e];
       }
-      const int64_t slot = h0 + HPT > a.Hq ? slot_offset(a, t) : -1;
-#pragma unroll
-      for (int j = 0; j < HPT; ++j) {
-        const int h = h0 + j;
-        if (h < a.Hq)
-          w[j].store(static_cast<T *>(a.q_out) + row * a.out_stride + static_cast<int64_t>(h) * a.D + d);
-        else if (h < a.Hq + a.Hk && slot >= 0)
-          w[j].store(static_cast<T *>(a.k_cache) + slot + (h - a.Hq) * a.head_stride + d);
-      }
-      continue;
     }
-    u -= groups * keeps;
-    // Eight elements of HPT heads of v.
-    const int h0 = u / copies * HPT, d = u % copies * 8;
-    Vec8<E> w[HPT];
+    const unsigned mine = 0xFFu << from;
+    outside = (outside & ~mine) | (bad & mine);
+  }
+  return outside;
+}
+
+// Measured on 8192 tokens of 40 heads of 128, three axes: 64 threads and at most
+// 64 registers (16 blocks an SM) 40 us, 128 threads 42, 48 registers (spills) 54.
+constexpr int kThreads = 64;
+
+template <typename E, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 16) rope_append_kernel(const __grid_constant__ RopeArgs a, int units,
+                                                               int tokens) {
+  using T = typename Elem<E>::type;
+  const int half = a.r / 2, turns = a.r / 16, keeps = (a.D - a.r) / 8, copies = a.D / 8, heads = a.Hq + a.Hk;
+  int u = blockIdx.x * kThreads + threadIdx.x;
+  if (u >= units) return;
+  // The thread's place: a turn (i0, its first pair), a copy of q or k past the
+  // turned elements, or a copy of v.
+  const bool turn = u < heads * turns;
+  int h, d0, d1, i0 = 0;  // head, and the first elements of its two (one) vectors
+  bool v = false;
+  if (turn) {
+    h = u / turns;
+    i0 = (u - h * turns) * 8;
+    d0 = INTERLEAVED ? 2 * i0 : i0;
+    d1 = INTERLEAVED ? 2 * i0 + 8 : half + i0;
+  } else if ((u -= heads * turns) < heads * keeps) {
+    h = u / keeps;
+    d0 = d1 = a.r + (u - h * keeps) * 8;
+  } else {
+    u -= heads * keeps;
+    h = u / copies;
+    d0 = d1 = (u - h * copies) * 8;
+    v = true;
+  }
+  const bool query = !v && h < a.Hq;
+  if (!v && !query) h -= a.Hq;
+  const T *src = static_cast<const T *>(v ? a.v : query ? a.q : a.k) + static_cast<int64_t>(h) * a.D;
+  const int64_t src_stride = v ? a.v_stride : query ? a.q_stride : a.k_stride;
+  T *dst = query ? static_cast<T *>(a.q_out) + static_cast<int64_t>(h) * a.D
+                 : static_cast<T *>(v ? a.v_cache : a.k_cache) + h * a.head_stride;
+  int axis = 0;
+  while (axis < a.axes - 1 && i0 >= a.end[axis]) ++axis;
+  const int t0 = blockIdx.y * tokens, t1 = min(a.T, t0 + tokens);
+#pragma unroll 1
+  for (int t = t0; t < t1; ++t) {
+    const T *from = src + t * src_stride;
+    Vec8<E> lo, hi;
+    lo.load(from + d0);
+    if (turn) hi.load(from + d1);
+    int64_t to = t * a.out_stride;
+    if (!query) to = slot_offset(a, t);
+    if (turn) {
+      float c[8], s[8], x0[8], x1[8];
+      const unsigned outside = angles(a, t, i0, axis, c, s);
+      if (outside) atomicOr(a.err, kErrIndexBit);
+      lo.get(x0);
+      hi.get(x1);
+      // Pair e is (y0, y1) of the two vectors, or consecutive elements of them.
 #pragma unroll
-    for (int j = 0; j < HPT; ++j)
-      if (h0 + j < a.Hk)
-        w[j].load(static_cast<const T *>(a.v) + row * a.v_stride + static_cast<int64_t>(h0 + j) * a.D + d);
-    const int64_t slot = slot_offset(a, t);
-    if (slot < 0) continue;
-#pragma unroll
-    for (int j = 0; j < HPT; ++j)
-      if (h0 + j < a.Hk) w[j].store(static_cast<T *>(a.v_cache) + slot + (h0 + j) * a.head_stride + d);
+      for (int e = 0; e < 8; ++e) {
+        float &y0 = INTERLEAVED ? (e < 4 ? x0[2 * e] : x1[2 * e - 8]) : x0[e];
+        float &y1 = INTERLEAVED ? (e < 4 ? x0[2 * e + 1] : x1[2 * e - 7]) : x1[e];
+        const float z0 = y0, z1 = y1;
+        y0 = z0 * c[e] - z1 * s[e];
+        y1 = z1 * c[e] + z0 * s[e];
+        if (outside >> e & 1u) y0 = y1 = 0.f;  // whatever q and k hold
+      }
+      lo.set(x0);
+      hi.set(x1);
+    }
+    if (to < 0) continue;
+    lo.store(dst + to + d0);
+    if (turn) hi.store(dst + to + d1);
   }
 }
 
-template <typename E, int HPT, bool INTERLEAVED>
+template <typename E, bool INTERLEAVED>
 cudaError_t launch_t(const RopeArgs &a, cudaStream_t stream) {
-  const int groups = (a.Hq + a.Hk + HPT - 1) / HPT;
-  const int units = groups * (a.r / 16 + (a.D - a.r) / 8) + (a.Hk + HPT - 1) / HPT * (a.D / 8);
-  int per_block = 256 / units;
-  if (per_block < 1) per_block = 1;
-  const int64_t blocks = (static_cast<int64_t>(a.T) + per_block - 1) / per_block;
-  rope_append_kernel<E, HPT, INTERLEAVED><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, per_block, units);
+  const int heads = a.Hq + a.Hk;
+  const int units = heads * (a.r / 16 + (a.D - a.r) / 8) + a.Hk * (a.D / 8);
+  const unsigned columns = (units + kThreads - 1) / kThreads;
+  // Tokens of a thread: up to 8, as long as the SMs have eight blocks each.
+  int tokens = static_cast<int>(static_cast<int64_t>(a.T) * columns / (8 * sm_count()));
+  tokens = tokens < 1 ? 1 : tokens > 8 ? 8 : tokens;
+  while ((a.T + tokens - 1) / tokens > 65535) tokens *= 2;
+  const dim3 grid(columns, static_cast<unsigned>((static_cast<int64_t>(a.T) + tokens - 1) / tokens));
+  rope_append_kernel<E, INTERLEAVED><<<grid, kThreads, 0, stream>>>(a, units, tokens);
   return cudaGetLastError();
 }
 
 template <typename E>
 cudaError_t launch_e(const RopeArgs &a, bool interleaved, cudaStream_t stream) {
-  return interleaved ? launch_t<E, 2, true>(a, stream) : launch_t<E, 2, false>(a, stream);
+  return interleaved ? launch_t<E, true>(a, stream) : launch_t<E, false>(a, stream);
 }
 
 }  // namespace
