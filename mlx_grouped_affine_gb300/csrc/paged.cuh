@@ -12,8 +12,7 @@
 // Every block therefore does the same work whatever the requests' lengths are,
 // and at most parts - 1 items are cut.  A cut item's pieces leave their running
 // maximum, sum and unnormalised output in the workspace, and a second kernel
-// joins them in block order (so results repeat bit for bit).  It works out the
-// blocks' places itself, while the first kernel still runs.
+// joins them in block order (so results repeat bit for bit).
 //
 // Softmax over a line of keys in pieces: with m = max s, l = sum 2^(s - m) and
 // o = sum 2^(s - m) v over each piece, pieces a and b join as
@@ -31,6 +30,7 @@ namespace paged {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -INFINITY;
+constexpr int kMaxBlocks = 512;  // of an attention launch: descriptors in the workspace
 
 struct AttnArgs {
   const void *q;
@@ -44,6 +44,7 @@ struct AttnArgs {
   int64_t out_stride;
   float *lse;                  // [T, Hq] or null
   float *ws;                   // partial rows of cut items
+  int *desc;                   // [blocks][8]: the cut item each block continues
   unsigned *err;
   uint32_t spin_limit;
   int page, num_pages;
@@ -251,17 +252,25 @@ __device__ long long request_tiles(const AttnArgs &a, int base, PlanScratch<NT> 
   return mine;
 }
 
-// A block's place in the line, and the blocks that hold the first and the last
-// tile of the item it begins in (block p holds unit g when p W / parts <= g, so
-// p = ((g + 1) parts - 1) / W).
-struct Place {
-  Cursor c;
-  int first, last;
-};
-__device__ __forceinline__ void place_cut(Place &p, long long t0, long long parts, long long W) {
-  const long long g0 = t0 - p.c.at, g1 = g0 + p.c.tiles - 1;  // units of its first and last tiles
-  p.first = static_cast<int>(mul_div((g0 + 1) * parts - 1, 1, W));
-  p.last = static_cast<int>(mul_div((g1 + 1) * parts - 1, 1, W));
+// The cut item that block `part` continues, for the joining kernel: request,
+// head, item, the blocks that hold the item's first and last tiles, and the
+// request's first token and count (block
+// p holds unit g when p W / parts <= g, so p = ((g + 1) parts - 1) / W).
+__device__ __forceinline__ void leave_desc(const AttnArgs &a, const Cursor &c, int part, long long t0,
+                                           long long parts, long long W) {
+  int *d = a.desc + 8 * part;
+  if (c.at == 0 || c.left == 0) {
+    d[0] = -1;
+    return;
+  }
+  const long long g0 = t0 - c.at, g1 = g0 + c.tiles - 1;  // units of its first and last tiles
+  d[0] = c.b;
+  d[1] = c.h;
+  d[2] = c.qt;
+  d[3] = static_cast<int>(mul_div((g0 + 1) * parts - 1, 1, W));
+  d[4] = static_cast<int>(mul_div((g1 + 1) * parts - 1, 1, W));
+  d[5] = c.r.first;
+  d[6] = c.r.n;
 }
 
 __device__ __forceinline__ long long warp_scan(long long v) {
@@ -277,7 +286,7 @@ __device__ __forceinline__ long long warp_scan(long long v) {
 // plan_block for at most 32 requests: one a lane, every warp for itself, no
 // barrier (the start of a short call is most of it).
 template <int KT>
-__device__ Place plan_warp(const AttnArgs &a, int part, int blocks) {
+__device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
   const int lane = threadIdx.x & 31;
   Request r{0, 0, 0};
   if (lane < a.B) r = request_of(a, lane);
@@ -295,10 +304,12 @@ __device__ Place plan_warp(const AttnArgs &a, int part, int blocks) {
   const long long mine = one * a.heads, incl = warp_scan(mine);
   const long long W = __shfl_sync(0xffffffffu, incl, 31);
   const int parts = static_cast<int>(min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks)));
-  Place place;
-  Cursor &c = place.c;
+  Cursor c;
   c.left = 0;
-  if (part >= parts) return place;
+  if (part >= parts) {
+    if (threadIdx.x == 0) a.desc[8 * part] = -1;
+    return c;
+  }
   const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
   const int b = __ffs(__ballot_sync(0xffffffffu, t0 < incl && t0 >= incl - mine)) - 1;
   c.r = Request{__shfl_sync(0xffffffffu, r.first, b), __shfl_sync(0xffffffffu, r.n, b),
@@ -326,14 +337,15 @@ __device__ Place plan_warp(const AttnArgs &a, int part, int blocks) {
     before = __shfl_sync(0xffffffffu, upto, 31);
   }
   cursor_start<KT>(a, c, c.at, t1 - t0);
-  place_cut(place, t0, parts, W);
-  return place;
+  if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
+  return c;
 }
 
-// The place of block `part` of `blocks` (no units left: none).  Called by all NT
-// threads of a block.
+// The block's place in the line: its cursor and how many tiles it has (0: none).
+// Called by all NT threads of block `part` of `blocks`.  Also leaves in
+// desc[part] the cut item that the block continues.
 template <int NT, int KT>
-__device__ Place plan_block(const AttnArgs &a, int part, int blocks, PlanScratch<NT> &s) {
+__device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratch<NT> &s) {
   if (a.B <= 32) return plan_warp<KT>(a, part, blocks);
   // Total, keeping the first chunk's counts.
   long long W = 0, total;
@@ -345,10 +357,12 @@ __device__ Place plan_block(const AttnArgs &a, int part, int blocks, PlanScratch
     W += total;
   }
   const long long parts = min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks));
-  Place place;
-  Cursor &c = place.c;
+  Cursor c;
   c.left = 0;
-  if (part >= parts) return place;
+  if (part >= parts) {
+    if (threadIdx.x == 0) a.desc[8 * part] = -1;
+    return c;
+  }
   const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
   // The request that holds tile t0.
   long long before = 0;
@@ -367,7 +381,10 @@ __device__ Place plan_block(const AttnArgs &a, int part, int blocks, PlanScratch
   }
   __syncthreads();
   const int b = s.found;
-  if (b < 0) return place;  // only if the lengths changed while the kernel ran
+  if (b < 0) {  // only if the lengths changed while the kernel ran
+    if (threadIdx.x == 0) a.desc[8 * part] = -1;
+    return c;
+  }
   const long long in_request = t0 - s.found_before;
   const Request r = request_of(a, b);
   // The head (all head slices of a request have the same tiles), then the item.
@@ -395,8 +412,8 @@ __device__ Place plan_block(const AttnArgs &a, int part, int blocks, PlanScratch
   c.h = h;
   c.qt = s.cursor.qt;
   cursor_start<KT>(a, c, s.cursor.at, t1 - t0);
-  place_cut(place, t0, parts, W);
-  return place;
+  if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
+  return c;
 }
 
 // Row r of item (h, qt): its new token in the request and its query head;
@@ -602,13 +619,14 @@ __device__ __forceinline__ float *slot_of(const AttnArgs &a, int block, int begi
   return a.ws + (2 * static_cast<int64_t>(block) + begins) * (R * (DP + 2));
 }
 
-// Joins the pieces of each cut item.  An item in P pieces is continued by
-// P - 1 blocks of the attention kernel, and the P - 1 blocks here of the same
-// numbers share its R x DP sums: the more pieces, the more blocks, so that each
-// reads about R x DP sums whatever P is.  Inside a block up to 16 lanes share a
-// column's pieces (the reads of one are in flight together) and join in lane
-// order: the order of the sums is fixed by P alone.  Joining 6 items of 51
-// pieces took 27 us with a warp per row and takes 3 this way.
+// Joins the pieces of each cut item.  An item in P pieces is continued by P - 1
+// blocks of the attention kernel, and the blocks here of the same numbers, R / 64
+// of each (one at least), share its R x DP sums: whatever P and R are, a block
+// reads about 64 x DP of them.  While it has few, up to 16 lanes share a column's
+// pieces (their reads are in flight together) and join in lane order; else a
+// thread has whole columns, four at a time.  The order of the sums is fixed by P
+// alone.  (6 items of 51 pieces took 27 us with a warp per row; 64 items of 256
+// rows in two or three pieces took 46 us with a block for all of an item's rows.)
 constexpr int kJoinThreads = 512;
 constexpr int kJoinLanes = 16;
 
@@ -616,27 +634,27 @@ constexpr int kJoinLanes = 16;
 template <int R>
 constexpr int join_weights(int blocks) { return 2 * R + 3 * blocks; }
 
-template <typename E, int R, int DP, int KT>
+template <typename E, int R, int DP>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a) {
   using T = typename Elem<E>::type;
   extern __shared__ float weight[];  // [rows][P]
   __shared__ float4 sums[kJoinThreads];
   __shared__ unsigned bad_rows[(R + 31) / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ PlanScratch<kJoinThreads> scratch;
-  // The item that attention block blockIdx.x + 1 continues; gridDim.x + 1 blocks.
-  const Place place = plan_block<kJoinThreads, KT>(a, blockIdx.x + 1, gridDim.x + 1, scratch);
-  if (place.c.left <= 0 || place.c.at == 0) return;
-  const int b = place.c.b, h = place.c.h, qt = place.c.qt, first = place.first, last = place.last;
-  const Request r = place.c.r;
-  const int P = last - first + 1, me = blockIdx.x - first;
   griddep_wait();
+  const int4 *d = reinterpret_cast<const int4 *>(a.desc + 8 * (blockIdx.x + 1));
+  const int4 d0 = d[0], d1 = d[1];
+  const int b = d0.x, h = d0.y, qt = d0.z, first = d0.w, last = d1.x;
+  if (b < 0) return;
+  const Request r{d1.y, d1.z, 0};
+  const int P = last - first + 1;
+  const int me = (blockIdx.x - first) * gridDim.y + blockIdx.y, all = (P - 1) * gridDim.y;
   constexpr int U = R * DP / 4, UR = DP / 4;  // float4 sums of an item, of a row
-  const int u0 = static_cast<int>(static_cast<unsigned>(me * U) / static_cast<unsigned>(P - 1));
-  const int u1 = static_cast<int>(static_cast<unsigned>((me + 1) * U) / static_cast<unsigned>(P - 1));
+  const int u0 = static_cast<int>(static_cast<unsigned>(me * U) / static_cast<unsigned>(all));
+  const int u1 = static_cast<int>(static_cast<unsigned>((me + 1) * U) / static_cast<unsigned>(all));
   if (u0 >= u1) return;  // more blocks than sums
   const int row0 = u0 / UR, rows = (u1 - 1) / UR + 1 - row0;
-  const int lanes = min(P, kJoinLanes), cols = kJoinThreads / lanes;
+  const int lanes = max(1, min(min(P, kJoinLanes), kJoinThreads / (u1 - u0))), cols = kJoinThreads / lanes;
   const int tc = tid % cols, j = tid / cols;
   // The first columns' sums, in flight while the weights are worked out.
   constexpr int kAhead = 4;
@@ -646,7 +664,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
       const int p = j + x * lanes;
-      if (j < lanes && p < P)
+      if (lanes > 1 && j < lanes && p < P)
         early[x] = *reinterpret_cast<const float4 *>(slot_of<R, DP>(a, first + p, p == 0) + row * DP + col);
     }
   }
@@ -680,12 +698,51 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       a.lse[(static_cast<int64_t>(r.first) + i) * a.Hq + head] = (m + log2f(l)) * kLn2;
   }
   __syncthreads();
+  auto write = [&](int row, int col, const float4 &o) {
+    int i, head;
+    if (col >= a.D || !row_of(a, r, h, qt, row, &i, &head)) return;
+    T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(r.first) + i) * a.out_stride +
+             static_cast<int64_t>(head) * a.D + col;
+    out[0] = Elem<E>::from_f32(o.x);
+    out[1] = Elem<E>::from_f32(o.y);
+    out[2] = Elem<E>::from_f32(o.z);
+    out[3] = Elem<E>::from_f32(o.w);
+    if (!(isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w)))
+      atomicOr(&bad_rows[row / 32], 1u << (row & 31));
+  };
+  if (lanes == 1) {
+    constexpr int kCols = 4;
+    for (int c0 = u0 + tid; c0 < u1; c0 += kCols * kJoinThreads) {
+      float4 o[kCols];
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < P; ++p) {
+        const float *s = slot_of<R, DP>(a, first + p, p == 0);
+        float4 v[kCols];
+#pragma unroll
+        for (int x = 0; x < kCols; ++x)
+          v[x] = *reinterpret_cast<const float4 *>(s + 4 * min(c0 + x * kJoinThreads, u1 - 1));
+#pragma unroll
+        for (int x = 0; x < kCols; ++x) {
+          const float w = weight[(min(c0 + x * kJoinThreads, u1 - 1) / UR - row0) * P + p];
+          o[x].x += w * v[x].x;
+          o[x].y += w * v[x].y;
+          o[x].z += w * v[x].z;
+          o[x].w += w * v[x].w;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) {
+        const int u = c0 + x * kJoinThreads;
+        if (u < u1) write(u / UR, u % UR * 4, o[x]);
+      }
+    }
+  }
 #pragma unroll 1
-  for (int c0 = u0; c0 < u1; c0 += cols) {
+  for (int c0 = u0; lanes > 1 && c0 < u1; c0 += cols) {
     const int u = c0 + tc;
     const int row = u / UR, col = (u - row * UR) * 4;
-    int i = 0, head = 0;
-    const bool live = u < u1 && j < lanes && col < a.D && row_of(a, r, h, qt, row, &i, &head);
+    const bool live = u < u1 && j < lanes;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
       const float *w = weight + (row - row0) * P;
@@ -727,14 +784,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         o.z += x.z;
         o.w += x.w;
       }
-      T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(r.first) + i) * a.out_stride +
-               static_cast<int64_t>(head) * a.D + col;
-      out[0] = Elem<E>::from_f32(o.x);
-      out[1] = Elem<E>::from_f32(o.y);
-      out[2] = Elem<E>::from_f32(o.z);
-      out[3] = Elem<E>::from_f32(o.w);
-      if (!(isfinite(o.x) && isfinite(o.y) && isfinite(o.z) && isfinite(o.w)))
-        atomicOr(&bad_rows[row / 32], 1u << (row & 31));
+      write(row, col, o);
     }
   }
   __syncthreads();
@@ -750,11 +800,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 // After the attention kernel on the same stream; starts early and waits.
-template <typename E, int R, int DP, int KT>
+template <typename E, int R, int DP>
 cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
   if (blocks < 2) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks - 1);
+  cfg.gridDim = dim3(blocks - 1, R > 64 ? R / 64 : 1);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = sizeof(float) * join_weights<R>(blocks);
   cfg.stream = stream;
@@ -763,7 +813,7 @@ cudaError_t launch_join(const AttnArgs &a, int blocks, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<E, R, DP, KT>, a);
+  return cudaLaunchKernelEx(&cfg, join_kernel<E, R, DP>, a);
 }
 
 }  // namespace paged

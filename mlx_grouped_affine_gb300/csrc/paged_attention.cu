@@ -27,6 +27,7 @@ cudaError_t query_map(const AttnArgs &a, int type, CUtensorMap *q) {
 }  // namespace paged
 
 namespace {
+constexpr size_t kDescBytes = 16 << 10;  // 32 bytes for each of up to 512 blocks
 constexpr size_t kFewBytes = 12 << 20;   // region of the kernel of few rows
 constexpr int kFewRows = 64;             // rows a kv head that it takes
 }  // namespace
@@ -70,29 +71,34 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
   a.scale_log2 = scale * paged::kLog2e;
   a.min_rows = 0;
   a.max_rows = 0x7FFFFFFF;
-  // The workspace: pieces of cut items, a region for each of the two kernels that
-  // a call may launch.
-  a.ws = static_cast<float *>(workspace);
+  // The workspace: block descriptors and pieces of cut items, a region for
+  // each of the two kernels that a call may launch.
+  char *ws = static_cast<char *>(workspace);
+  auto region = [&](paged::AttnArgs &x, size_t at) {
+    x.desc = reinterpret_cast<int *>(ws + at);
+    x.ws = reinterpret_cast<float *>(ws + at + kDescBytes);
+  };
+  region(a, 0);
   if (pool.type == kTypeF32 || a.D > 128)
-    return launch_attention_tiles(a, pool.type, workspace_bytes, stream);
+    return launch_attention_tiles(a, pool.type, workspace_bytes - kDescBytes, stream);
   // Few rows a kv head: the kernel of 16-row items, whose cost is the bytes of K
   // and V; many: the one of 256-row items, whose cost is the tensor pipe's.  The
   // second takes scores times a positive scale only.
   const int64_t most_rows = max_new * a.G;
   if (most_rows <= kFewRows || !(scale > 0.f))
-    return launch_attention_decode(a, pool.type, kFewBytes, stream);
+    return launch_attention_decode(a, pool.type, kFewBytes - kDescBytes, stream);
   // Requests of both kinds: one kernel after the other, each leaving the
   // other's requests alone; not when no request can be of the first kind.
   const bool few = requests > 1 && tokens <= (requests - 1) * max_new + kFewRows / a.G;
   paged::AttnArgs many = a;
-  many.ws += kFewBytes / sizeof(float);
+  region(many, kFewBytes);
   if (few) {
     a.max_rows = kFewRows;
     many.min_rows = kFewRows + 1;
-    const cudaError_t e = launch_attention_decode(a, pool.type, kFewBytes, stream);
+    const cudaError_t e = launch_attention_decode(a, pool.type, kFewBytes - kDescBytes, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_attention_prefill(many, pool.type, workspace_bytes - kFewBytes, stream);
+  return launch_attention_prefill(many, pool.type, workspace_bytes - kFewBytes - kDescBytes, stream);
 }
 
 }  // namespace qmm

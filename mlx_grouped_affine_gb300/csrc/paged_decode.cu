@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ A
   float *wm = obuf + 2 * R * DP, *wl = wm + kWarps * R;      // [warps][R]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_launch_dependents();
-  Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, *reinterpret_cast<PlanScratch<NT> *>(obuf)).c;
+  Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, *reinterpret_cast<PlanScratch<NT> *>(obuf));
   if (c.left <= 0) return;
   const uint32_t ring = smem_u32(smem) + warp * ST * X::STAGE;
   const Copier<DP> copier(a.D, X::COLS);
@@ -365,10 +365,10 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int blocks = 2 * sm_count();
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
-  blocks = static_cast<int>(std::min<size_t>(blocks, ws_bytes / per_block));
+  blocks = static_cast<int>(std::min<size_t>(std::min(blocks, kMaxBlocks), ws_bytes / per_block));
   decode_kernel<E, DP><<<blocks, NT, smem, stream>>>(a);
   const cudaError_t le = cudaGetLastError();
-  return le != cudaSuccess ? le : launch_join<E, R, DP, Tile<DP>::KT>(a, blocks, stream);
+  return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);
 }
 
 template <typename E>

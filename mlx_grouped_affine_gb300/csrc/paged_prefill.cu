@@ -770,7 +770,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     bars->abort = bars->redo = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, *reinterpret_cast<PlanScratch<NT> *>(skv)).c;
+  const Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, *reinterpret_cast<PlanScratch<NT> *>(skv));
   if (c.left <= 0) return;
   if (a.Gs * a.TH < 128) {
     // Rows of Q that no load writes: zeros, so that they multiply as such.
@@ -828,10 +828,10 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int blocks = sm_count();
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
-  blocks = static_cast<int>(std::min<size_t>(blocks, ws_bytes / per_block));
+  blocks = static_cast<int>(std::min<size_t>(std::min(blocks, kMaxBlocks), ws_bytes / per_block));
   prefill_kernel<E, DP><<<blocks, NT, smem, stream>>>(q, k, a, box);
   const cudaError_t le = cudaGetLastError();
-  return le != cudaSuccess ? le : launch_join<E, R, DP, KT>(a, blocks, stream);
+  return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);
 }
 
 template <typename E>

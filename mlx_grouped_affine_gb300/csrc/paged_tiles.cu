@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
   int64_t *off = reinterpret_cast<int64_t *>(Ps + KT * (R + 4));
   __shared__ PlanScratch<NT> scratch;
   griddep_launch_dependents();
-  Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, scratch).c;
+  Cursor c = plan_block<NT, KT>(a, blockIdx.x, gridDim.x, scratch);
   const int tid = threadIdx.x, rg = tid >> 4, kt = tid & 15, lane = tid & 31;
   constexpr int VEC = DP / 8, NJ = DP / 64;
   bool continues = c.at != 0;
@@ -241,10 +241,10 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   int blocks = sm_count() * (DP <= 128 ? 2 : 1);
   const size_t per_block = 2 * sizeof(float) * R * (DP + 2);
-  blocks = static_cast<int>(std::min<size_t>(blocks, ws_bytes / per_block));
+  blocks = static_cast<int>(std::min<size_t>(std::min(blocks, kMaxBlocks), ws_bytes / per_block));
   tiles_kernel<E, DP><<<blocks, NT, smem, stream>>>(a);
   const cudaError_t le = cudaGetLastError();
-  return le != cudaSuccess ? le : launch_join<E, R, DP, KT>(a, blocks, stream);
+  return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);
 }
 
 template <typename E>
