@@ -9,6 +9,11 @@ torch = pytest.importorskip("torch")
 from mlx_grouped_affine_gb300 import qmm  # noqa: E402
 from paged_util import i32, pages  # noqa: E402
 
+@pytest.fixture(autouse=True)
+def clear_what_earlier_calls_left():
+    """The device error word holds what any earlier call reported until it is read."""
+    qmm.qmm_get_device_error()
+
 
 def plan(past, new, page, free, first=None, width=None, extra=0, room=None, seed=0):
     """The call on a table whose held entries are distinct ids, and the loop's result."""

@@ -11,6 +11,12 @@ torch = pytest.importorskip("torch")
 from mlx_grouped_affine_gb300 import qmm  # noqa: E402
 from paged_util import Pool, attend, check, i32, queries, workspace  # noqa: E402
 
+@pytest.fixture(autouse=True)
+def clear_what_earlier_calls_left():
+    """The device error word holds what any earlier call reported until it is read."""
+    qmm.qmm_get_device_error()
+
+
 # (past, new) of each request.
 DECODE = [(0, 1), (1, 1), (37, 1), (300, 1), (64, 1)]
 DRAFTS = [(0, 3), (129, 5), (700, 2), (15, 1), (50, 0)]

@@ -9,6 +9,11 @@ torch = pytest.importorskip("torch")
 from mlx_grouped_affine_gb300 import qmm  # noqa: E402
 from paged_util import TYPES, i32  # noqa: E402
 
+@pytest.fixture(autouse=True)
+def clear_what_earlier_calls_left():
+    """The device error word holds what any earlier call reported until it is read."""
+    qmm.qmm_get_device_error()
+
 
 def run(t, hq, hk, d, r, sections, dtype, page=16, layout="hnd", interleaved=False, in_place=False,
         positions=None, slots=None, rows=500, seed=0, pad=0):
