@@ -421,8 +421,8 @@ typedef struct {
     void *k, *v;          /* device */
     qmm_dtype dtype;      /* of keys, values, queries and outputs alike */
     int64_t num_pages;    /* num_pages * page_size below 2^31 */
-    int32_t page_size;    /* rows of a page, 1 to 65536 (16-bit types with heads
-                             of at most 128 are fastest at multiples of 16) */
+    int32_t page_size;    /* rows of a page, 1 to 65536; multiples of 8 are
+                             faster (a block of 8 keys is looked up once) */
     int32_t heads;        /* key and value heads */
     int32_t head_dim;     /* a multiple of 8, 8 to 256 */
     int64_t page_stride, head_stride, token_stride;

@@ -813,7 +813,7 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.TH = 128 / a.Gs;
   a.TQ = 2 * a.TH;
   a.min_tiles = 1;
-  a.item_cost = 3;
+  a.item_cost = 3;  // its first products and its output, in key tiles
   // Rows of a TMA box of K: the largest power of two that divides the page.
   int box = 0;
   if (a.page % 8 == 0)

@@ -2,6 +2,7 @@
 lengths from none to thousands, pages that end inside key tiles, masks that
 leave rows empty, non-finite keys and values where no row looks."""
 import math
+import random
 
 import pytest
 
@@ -69,6 +70,26 @@ def test_pages(dtype, page):
 def test_key_counts_around_tiles(dtype, keys):
     check(*setup([(keys - 1, 1)], 16, 1, 8, 128, dtype), what="decode")
     check(*setup([(0, keys)], 16, 1, 8, 128, dtype), what="prompt")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("requests,past,new", [
+    (32, 100, 3), (33, 100, 3), (33, 40, 90), (129, 60, 2), (700, 30, 2), (1400, 9, 2), (40, 20, 300)])
+def test_many_requests(dtype, requests, past, new):
+    """More requests than a warp's lanes or a block's threads plan at once; some idle, some long."""
+    rng = random.Random(requests + past + new)
+    lens = [(rng.randint(0, past), rng.choice([0, 1, 1, rng.randint(0, new)])) for _ in range(requests)]
+    lens[requests // 2] = (past, new)
+    lens[-1] = (past // 2, new)
+    check(*setup(lens, 16, 1, 4, 64, dtype), what="%d requests" % requests)
+
+
+@pytest.mark.parametrize("kv,group", [(1, 17), (2, 33), (1, 128), (1, 130), (1, 200)])
+@pytest.mark.parametrize("lens", [[(30, 1), (5, 1)], [(90, 40), (0, 3)]])
+def test_wide_groups(kv, group, lens):
+    """Groups of more heads than an item has rows are walked in slices."""
+    for dtype in ("bf16", "f32"):
+        check(*setup(lens, 16, kv, group, 64, dtype), what="group %d" % group)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
