@@ -43,6 +43,14 @@ __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
   *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// c += (a0 b0, a1 b1): two fp32 multiply-adds an instruction.
+__device__ __forceinline__ void fma_pair(float2 &c, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(c.x), "+f"(c.y)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 template <typename E, int DP>
 __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnArgs a) {
   using T = typename Elem<E>::type;
@@ -74,7 +82,8 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
       store8(Qs + row * (DP + 4) + d, q);
     }
     Span span[4];
-    float m[4], l[4], o[4][NJ][4];
+    float m[4], l[4];
+    float2 o[4][NJ][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       int t, head;
@@ -85,7 +94,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+        for (int e = 0; e < 2; ++e) o[i][j][e] = make_float2(0.f, 0.f);
     }
     for (int tile = c.tile0 + c.at; tile < c.tile0 + c.at + n; ++tile) {
       const int key0 = tile * KT;
@@ -105,7 +114,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
         store8(Vs + key * DP + d, v);
       }
       __syncthreads();
-      float s[4][4] = {};
+      float2 s2[4][4] = {};  // sums of even and odd columns
 #pragma unroll 2
       for (int d = 0; d < DP; d += 4) {
         float4 q[4], k[4];
@@ -118,12 +127,15 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            s[i][j] = fmaf(q[i].x, k[j].x, s[i][j]);
-            s[i][j] = fmaf(q[i].y, k[j].y, s[i][j]);
-            s[i][j] = fmaf(q[i].z, k[j].z, s[i][j]);
-            s[i][j] = fmaf(q[i].w, k[j].w, s[i][j]);
+            fma_pair(s2[i][j], q[i].x, q[i].y, k[j].x, k[j].y);
+            fma_pair(s2[i][j], q[i].z, q[i].w, k[j].z, k[j].w);
           }
       }
+      float s[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
       float4 p[4];  // the thread's four keys, four rows each
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[i][j][e] *= f;
+          for (int e = 0; e < 2; ++e) o[i][j][e] = make_float2(o[i][j][e].x * f, o[i][j][e].y * f);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -165,10 +177,8 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
           const float4 v = *reinterpret_cast<const float4 *>(Vs + key * DP + 64 * j + 4 * kt);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            o[i][j][0] = fmaf(wi[i], v.x, o[i][j][0]);
-            o[i][j][1] = fmaf(wi[i], v.y, o[i][j][1]);
-            o[i][j][2] = fmaf(wi[i], v.z, o[i][j][2]);
-            o[i][j][3] = fmaf(wi[i], v.w, o[i][j][3]);
+            fma_pair(o[i][j][0], wi[i], wi[i], v.x, v.y);
+            fma_pair(o[i][j][1], wi[i], wi[i], v.z, v.w);
           }
         }
       }
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
           *reinterpret_cast<float4 *>(w + row * DP + 64 * j + 4 * kt) =
-              make_float4(o[i][j][0], o[i][j][1], o[i][j][2], o[i][j][3]);
+              make_float4(o[i][j][0].x, o[i][j][0].y, o[i][j][1].x, o[i][j][1].y);
         if (kt == 0) {
           w[R * DP + row] = m[i];
           w[R * DP + R + row] = l[i];
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
           for (int e = 0; e < 4; ++e) {
             const int d = 64 * j + 4 * kt + e;
             if (d < a.D) {
-              const float y = o[i][j][e] * inv;
+              const float y = (e & 1 ? o[i][j][e >> 1].y : o[i][j][e >> 1].x) * inv;
               out[d] = Elem<E>::from_f32(y);
               bad |= !isfinite(y);
             }
