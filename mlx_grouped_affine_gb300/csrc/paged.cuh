@@ -6,9 +6,10 @@
 // shares every K and V tile it reads.  An item is (request, kv head, TQ
 // consecutive new tokens): it walks the key tiles (KT keys each) that any of
 // its rows may see.  (A group of more heads than a tile has rows is cut into
-// S slices of Gs heads, each walked as a kv head of its own.)  All items' key tiles, in order, form one line; an item
-// counts item_cost units for its start and end, then one for each tile, W in
-// all, and block c of `parts` takes units [c W / parts, (c + 1) W / parts).
+// S slices of Gs heads, each walked as a kv head of its own.)  All items' key
+// tiles, in order, form one line; an item counts item_cost units for its start
+// and end, then one for each tile, W in all, and block c of `parts` takes units
+// [c W / parts, (c + 1) W / parts).
 // Every block therefore does the same work whatever the requests' lengths are,
 // and at most parts - 1 items are cut.  A cut item's pieces leave their running
 // maximum, sum and unnormalised output in the workspace, and a second kernel
@@ -56,7 +57,6 @@ struct AttnArgs {
   int causal, window;          // window 0: none
   float scale_log2;            // scale * log2(e)
   int min_rows, max_rows;      // requests of another row count are left to the other kernel
-  int min_tiles;               // least units worth a block of their own
   int item_cost;               // units of an item beside its tiles
 };
 
@@ -273,80 +273,11 @@ __device__ __forceinline__ void leave_desc(const AttnArgs &a, const Cursor &c, i
   d[6] = c.r.n;
 }
 
-__device__ __forceinline__ long long warp_scan(long long v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-
-// plan_block for at most 32 requests: one a lane, every warp for itself, no
-// barrier (the start of a short call is most of it).
-template <int KT>
-__device__ Cursor plan_warp(const AttnArgs &a, int part, int blocks) {
-  const int lane = threadIdx.x & 31;
-  Request r{0, 0, 0};
-  if (lane < a.B) r = request_of(a, lane);
-  const bool big = items_of(a, r) > kOwnItems;
-  long long one = big ? 0 : head_tiles<KT>(a, r, 0, 1);  // tiles of one head slice
-  for (unsigned bits = __ballot_sync(0xffffffffu, big); bits; bits &= bits - 1) {
-    const int owner = __ffs(bits) - 1;
-    const Request o{__shfl_sync(0xffffffffu, r.first, owner), __shfl_sync(0xffffffffu, r.n, owner),
-                    __shfl_sync(0xffffffffu, r.len, owner)};
-    long long n = head_tiles<KT>(a, o, lane, 32);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) n += __shfl_xor_sync(0xffffffffu, n, x);
-    if (lane == owner) one = n;
-  }
-  const long long mine = one * a.heads, incl = warp_scan(mine);
-  const long long W = __shfl_sync(0xffffffffu, incl, 31);
-  const int parts = static_cast<int>(min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks)));
-  Cursor c;
-  c.left = 0;
-  if (part >= parts) {
-    if (threadIdx.x == 0) a.desc[8 * part] = -1;
-    return c;
-  }
-  const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
-  const int b = __ffs(__ballot_sync(0xffffffffu, t0 < incl && t0 >= incl - mine)) - 1;
-  c.r = Request{__shfl_sync(0xffffffffu, r.first, b), __shfl_sync(0xffffffffu, r.n, b),
-                __shfl_sync(0xffffffffu, r.len, b)};
-  c.b = b;
-  const long long in_request = t0 - __shfl_sync(0xffffffffu, incl - mine, b);
-  const long long per_head = __shfl_sync(0xffffffffu, one, b);
-  c.h = static_cast<int>(mul_div(in_request, 1, per_head));
-  const long long in_head = in_request - c.h * per_head;
-  const int items = items_of(a, c.r);
-  long long before = 0;
-  c.qt = 0;
-  c.at = 0;
-  for (int base = 0; base < items; base += 32) {
-    const int q = base + lane;
-    const long long n = q < items ? item_tiles<KT>(a, c.r, q).tiles + a.item_cost : 0;
-    const long long upto = warp_scan(n) + before;
-    const unsigned hit = __ballot_sync(0xffffffffu, in_head < upto && in_head >= upto - n);
-    if (hit) {
-      const int at = __ffs(hit) - 1;
-      c.qt = base + at;
-      c.at = static_cast<int>(in_head - __shfl_sync(0xffffffffu, upto - n, at));
-      break;
-    }
-    before = __shfl_sync(0xffffffffu, upto, 31);
-  }
-  cursor_start<KT>(a, c, c.at, t1 - t0);
-  if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
-  return c;
-}
-
 // The block's place in the line: its cursor and how many tiles it has (0: none).
 // Called by all NT threads of block `part` of `blocks`.  Also leaves in
 // desc[part] the cut item that the block continues.
 template <int NT, int KT>
 __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratch<NT> &s) {
-  if (a.B <= 32) return plan_warp<KT>(a, part, blocks);
   // Total, keeping the first chunk's counts.
   long long W = 0, total;
   long long kept = 0;
@@ -356,7 +287,7 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
     block_scan<NT>(mine, s, &total);
     W += total;
   }
-  const long long parts = min((W + a.min_tiles - 1) / a.min_tiles, static_cast<long long>(blocks));
+  const long long parts = min(W, static_cast<long long>(blocks));
   Cursor c;
   c.left = 0;
   if (part >= parts) {

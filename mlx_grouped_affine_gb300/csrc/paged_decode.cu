@@ -358,7 +358,6 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.Gs = (a.G + a.S - 1) / a.S;
   a.heads = a.Hkv * a.S;
   a.TQ = a.TH = R / a.Gs;
-  a.min_tiles = 2;
   a.item_cost = 6;  // an item's queries, the join of its warps and its output, in key tiles
   constexpr size_t smem = Tile<DP>::SMEM;
   const cudaError_t e = ensure_smem_limit<decode_kernel<E, DP>>(smem);

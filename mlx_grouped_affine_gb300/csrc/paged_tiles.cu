@@ -244,7 +244,6 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.Gs = (a.G + a.S - 1) / a.S;
   a.heads = a.Hkv * a.S;
   a.TQ = a.TH = R / a.Gs;
-  a.min_tiles = 1;
   a.item_cost = 1;
   constexpr size_t smem = smem_bytes<DP>();
   const cudaError_t e = ensure_smem_limit<tiles_kernel<E, DP>>(smem);
