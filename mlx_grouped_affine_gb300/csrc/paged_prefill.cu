@@ -33,6 +33,12 @@
 // than 2^8 (P stays below 256, inside both types' range; the result is the
 // same because O and the sum share m).
 //
+// Measured (32 heads over 8 of 128, bf16): 512 tokens over 32000 keys 220 us,
+// 1.23 PFLOP/s, 0.64 of the measured bf16 rate; causal prompts of 2000 to 8192
+// tokens 618 us, 0.64.  The tensor pipe is busy 61 % of the time: its products read
+// 192 KB of shared memory a tile, 64 KB more are written by the loads, and 256 KB at
+// 128 bytes a cycle take the 2048 cycles that the products alone would.
+//
 // Waits are bounded; one that runs out sets the error word and an abort flag
 // that stops every role, and the block still drains its copies and MMAs.  The
 // two warps of a row meet at a hardware barrier every tile, which is not
@@ -801,7 +807,9 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.heads = a.Hkv * a.S;
   a.TH = 128 / a.Gs;
   a.TQ = 2 * a.TH;
-  a.item_cost = 3;  // its first products and its output, in key tiles
+  // An item's first products and its output, in key tiles.  Measured at 0 / 3 / 6:
+  // three causal prompts of 2000 to 8192 tokens 690 / 618 / 626 us.
+  a.item_cost = 3;
   // Rows of a TMA box of K: the largest power of two that divides the page.
   int box = 0;
   if (a.page % 8 == 0)
