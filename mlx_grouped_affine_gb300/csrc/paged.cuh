@@ -163,12 +163,13 @@ __device__ __forceinline__ void cursor_next(const AttnArgs &a, Cursor &c) {
   c.left = max(c.left - a.item_cost, 0);
 }
 
-// The cursor's item from its unit u on, with `left` units from there.
+// The cursor's item from its unit u on, with `left` units from there.  (u is one of
+// the item's; the bound holds a block whose lengths changed under it.)
 template <int KT>
 __device__ __forceinline__ void cursor_start(const AttnArgs &a, Cursor &c, int u, long long left) {
   cursor_item<KT>(a, c);
   const int skip = max(a.item_cost - u, 0);
-  c.at = max(u - a.item_cost, 0);
+  c.at = min(max(u - a.item_cost, 0), c.tiles - 1);
   c.left = static_cast<int>(max(left - skip, 0ll));
 }
 
@@ -183,7 +184,6 @@ __device__ __forceinline__ long long mul_div(long long x, long long y, long long
 template <int NT>
 struct PlanScratch {
   long long warp_sum[NT / 32];
-  long long total;
   long long found_before, found_tiles;  // tiles before the found request, and its own
   int found;
   unsigned marks[NT / 32];
@@ -235,9 +235,9 @@ __device__ long long request_tiles(const AttnArgs &a, int base, PlanScratch<NT> 
     big = items_of(a, r) > kOwnItems;
     if (!big) mine = head_tiles<KT>(a, r, 0, 1) * a.heads;
   }
+  if (!__syncthreads_or(big)) return mine;
   // Long requests one after another, their items spread over the block.
   const unsigned m = __ballot_sync(0xffffffffu, big);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = m;
   __syncthreads();
   for (int w = 0; w < NT / 32; ++w) {
@@ -278,13 +278,17 @@ __device__ __forceinline__ void leave_desc(const AttnArgs &a, const Cursor &c, i
 // desc[part] the cut item that the block continues.
 template <int NT, int KT>
 __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratch<NT> &s) {
-  // Total, keeping the first chunk's counts.
-  long long W = 0, total;
-  long long kept = 0;
+  if (threadIdx.x == 0) s.found = -1;
+  // Total, keeping the first chunk's sums.
+  long long W = 0, total, kept = 0, kept_incl = 0, kept_total = 0;
   for (int base = 0; base < a.B; base += NT) {
     const long long mine = request_tiles<NT, KT>(a, base, s);
-    if (base == 0) kept = mine;
-    block_scan<NT>(mine, s, &total);
+    const long long incl = block_scan<NT>(mine, s, &total);
+    if (base == 0) {
+      kept = mine;
+      kept_incl = incl;
+      kept_total = total;
+    }
     W += total;
   }
   const long long parts = min(W, static_cast<long long>(blocks));
@@ -297,11 +301,13 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   const long long t0 = mul_div(part, W, parts), t1 = mul_div(part + 1, W, parts);
   // The request that holds tile t0.
   long long before = 0;
-  __syncthreads();
-  if (threadIdx.x == 0) s.found = -1;
   for (int base = 0; base < a.B; base += NT) {
-    const long long mine = base == 0 ? kept : request_tiles<NT, KT>(a, base, s);
-    const long long incl = block_scan<NT>(mine, s, &total) + before;
+    long long mine = kept, incl = kept_incl;
+    total = kept_total;
+    if (base != 0) {
+      mine = request_tiles<NT, KT>(a, base, s);
+      incl = block_scan<NT>(mine, s, &total) + before;
+    }
     if (t0 < incl && t0 >= incl - mine) {
       s.found = base + threadIdx.x;
       s.found_before = incl - mine;
@@ -322,27 +328,31 @@ __device__ Cursor plan_block(const AttnArgs &a, int part, int blocks, PlanScratc
   const long long per_head = mul_div(s.found_tiles, 1, a.heads);
   const int h = static_cast<int>(mul_div(in_request, 1, per_head));
   const long long in_head = in_request - h * per_head;
-  before = 0;
   const int items = items_of(a, r);
-  __syncthreads();
-  if (threadIdx.x == 0) s.cursor.qt = s.cursor.at = 0;
-  for (int base = 0; base < items; base += NT) {
-    const int q = base + threadIdx.x;
-    const long long mine = q < items ? item_tiles<KT>(a, r, q).tiles + a.item_cost : 0;
-    const long long incl = block_scan<NT>(mine, s, &total) + before;
-    if (in_head < incl && in_head >= incl - mine) {
-      s.cursor.qt = q;
-      s.cursor.at = static_cast<int>(in_head - (incl - mine));
+  int at = static_cast<int>(in_head);  // its unit of the item
+  c.qt = 0;
+  if (items > 1) {
+    before = 0;
+    if (threadIdx.x == 0) s.cursor.qt = s.cursor.at = 0;
+    for (int base = 0; base < items; base += NT) {
+      const int q = base + threadIdx.x;
+      const long long mine = q < items ? item_tiles<KT>(a, r, q).tiles + a.item_cost : 0;
+      const long long incl = block_scan<NT>(mine, s, &total) + before;
+      if (in_head < incl && in_head >= incl - mine) {
+        s.cursor.qt = q;
+        s.cursor.at = static_cast<int>(in_head - (incl - mine));
+      }
+      before += total;
+      if (before > in_head) break;
     }
-    before += total;
-    if (before > in_head) break;
+    __syncthreads();
+    c.qt = s.cursor.qt;
+    at = s.cursor.at;
   }
-  __syncthreads();
   c.r = r;
   c.b = b;
   c.h = h;
-  c.qt = s.cursor.qt;
-  cursor_start<KT>(a, c, s.cursor.at, t1 - t0);
+  cursor_start<KT>(a, c, at, t1 - t0);
   if (threadIdx.x == 0) leave_desc(a, c, part, t0, parts, W);
   return c;
 }
