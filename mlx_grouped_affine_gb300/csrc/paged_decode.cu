@@ -16,12 +16,12 @@
 // when the item ends.
 //
 // Measured: 64 requests of 100 to 8000 keys, 8 kv heads of 128, bf16: 1.15 GB in
-// 187 us, 6.2 TB/s, 0.91 of the measured copy rate.  Keys arrive 11 us after the
-// launch, blocks end after 129 to 186 us (whole groups of SMs are slower than others),
-// the join takes 5.  One request of 1001 keys: 13.4 us, all of it latency.  (K and V
-// by TMA boxes of 16 rows instead: 206 us; more blocks than are resident: 210 and up;
-// a tenth or less of the work in a second, smaller wave: 187 to 190 and 47 instead of
-// 42 for three requests of up to 131k keys.)
+// 187 us, 6.2 TB/s, 0.91 of the measured copy rate.  Keys arrive 6 to 11 us after
+// the launch, blocks end after 122 to 190 us (whole groups of SMs are slower than
+// others), the join takes 5.  Three requests of up to 131k keys: 39 us.  One request
+// of 1001 keys: 12.9 us, all of it latency.  (K and V by TMA boxes of 16 rows instead:
+// 206 us; more blocks than are resident: 210 and up; a tenth or less of the work in a
+// second, smaller wave: 187 to 190, and the three requests 5 us more.)
 #include "paged.cuh"
 
 namespace qmm {
@@ -367,8 +367,8 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.heads = a.Hkv * a.S;
   a.TQ = a.TH = R / a.Gs;
   // An item's queries, the join of its warps and its output, in key tiles.  Measured
-  // at 0 / 3 / 6 / 10 / 20: 64 ragged requests 195 / 193 / 187 / 188 / 192 us, three of
-  // up to 131k keys 48 / 46 / 41 / 40 / 39, drafts in a window 57 / 54 / 51 / 51 / 52.
+  // at 0 / 3 / 6 / 10 / 20: 64 ragged requests 190 / 190 / 187 / 189 / 191 us, three of
+  // up to 131k keys 44 / 42 / 39 / 38 / 38, drafts in a window 53 / 51 / 50 / 51 / 52.
   a.item_cost = 6;
   constexpr size_t smem = Tile<DP>::SMEM;
   const cudaError_t e = ensure_smem_limit<decode_kernel<E, DP>>(smem);

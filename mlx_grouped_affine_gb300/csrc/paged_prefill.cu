@@ -35,7 +35,7 @@
 //
 // Measured (32 heads over 8 of 128, bf16): 512 tokens over 32000 keys 220 us,
 // 1.23 PFLOP/s, 0.64 of the measured bf16 rate; causal prompts of 2000 to 8192
-// tokens 618 us, 0.64.  The tensor pipe is busy 61 % of the time: its products read
+// tokens 618 to 628 us, 0.63 to 0.64.  The tensor pipe is busy 61 % of the time: its products read
 // 192 KB of shared memory a tile, 64 KB more are written by the loads, and 256 KB at
 // 128 bytes a cycle take the 2048 cycles that the products alone would.
 //
@@ -808,7 +808,7 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.TH = 128 / a.Gs;
   a.TQ = 2 * a.TH;
   // An item's first products and its output, in key tiles.  Measured at 0 / 3 / 6:
-  // three causal prompts of 2000 to 8192 tokens 690 / 618 / 626 us.
+  // three causal prompts of 2000 to 8192 tokens 690 / 618 / 626 and 699 / 628 / 625 us.
   a.item_cost = 3;
   // Rows of a TMA box of K: the largest power of two that divides the page.
   int box = 0;

@@ -7,7 +7,7 @@
 // feed 16 multiply-adds), the softmax statistics of a row in the 16 lanes that
 // share it, and 4 rows x DP/16 columns of output a thread in registers.  Its
 // multiply-adds and the shared-memory loads that feed them bound it: five requests
-// of 1 to 130 tokens, up to 2000 keys, fp32 heads of 64 take 53 us, about 12 of
+// of 1 to 130 tokens, up to 2000 keys, fp32 heads of 64 take 51 us, about 12 of
 // them at the fp32 units' rate.  (Two blocks an SM; three or four: 53 to 60 us.  Tiles
 // loaded ahead by cp.async: 57 against 55.5 us.)
 #include "paged.cuh"
@@ -248,7 +248,7 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   a.Gs = (a.G + a.S - 1) / a.S;
   a.heads = a.Hkv * a.S;
   a.TQ = a.TH = R / a.Gs;
-  a.item_cost = 1;  // measured at 0 / 1 / 3 on the five requests above: 55 / 53 / 58 us
+  a.item_cost = 1;  // measured at 0 / 1 / 3 on the five requests above: 53 / 51 / 56 us
   constexpr size_t smem = smem_bytes<DP>();
   const cudaError_t e = ensure_smem_limit<tiles_kernel<E, DP>>(smem);
   if (e != cudaSuccess) return e;
