@@ -1,5 +1,6 @@
 // qmm_paged_attention: which kernel serves a call.
 #include "paged.cuh"
+#include "workspace.h"
 
 namespace qmm {
 
@@ -75,15 +76,19 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
   a.min_rows = 0;
   a.max_rows = 0x7FFFFFFF;
   // The workspace: block descriptors and pieces of cut items, a region for
-  // each of the two kernels that a call may launch.
-  char *ws = static_cast<char *>(workspace);
+  // each of the two kernels that a call may launch.  Its base here and the offsets of
+  // regions, pieces and rows are multiples of 32 bytes, the prompt kernel's widest
+  // store.
+  static_assert(kDescBytes % kWorkspaceAlign == 0 && kFewBytes % kWorkspaceAlign == 0, "regions are aligned");
+  const Workspace room = aligned_workspace(workspace, workspace_bytes);
+  char *ws = room.base;
   auto region = [&](paged::AttnArgs &x, size_t at) {
     x.desc = reinterpret_cast<int *>(ws + at);
     x.ws = reinterpret_cast<float *>(ws + at + kDescBytes);
   };
   region(a, 0);
   if (pool.type == kTypeF32 || a.D > 128)
-    return launch_attention_tiles(a, pool.type, workspace_bytes - kDescBytes, stream);
+    return launch_attention_tiles(a, pool.type, room.bytes - kDescBytes, stream);
   // Few rows a kv head: the kernel of 16-row items, whose cost is the bytes of K
   // and V; many: the one of 256-row items, whose cost is the tensor pipe's.  The
   // second takes scores times a positive scale only.
@@ -101,7 +106,7 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
     const cudaError_t e = launch_attention_decode(a, pool.type, kFewBytes - kDescBytes, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_attention_prefill(many, pool.type, workspace_bytes - kFewBytes - kDescBytes, stream);
+  return launch_attention_prefill(many, pool.type, room.bytes - kFewBytes - kDescBytes, stream);
 }
 
 }  // namespace qmm
