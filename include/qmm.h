@@ -444,13 +444,15 @@ typedef struct {
  *   tokens       room in positions and slots
  *   starts       int32 [requests + 1]: request b's new tokens are tokens
  *                starts[b] .. starts[b + 1] - 1 of the step
- *   seq_lens     int32 [requests]: past + new
+ *   seq_lens     int32 [requests]: past + new; may be past_lens itself (lengths
+ *                updated in place)
  *   positions    int32 [tokens]: past + i for new token i
  *   slots        int32 [tokens]: the token's slot in the pool.  Tokens past
  *                starts[requests] get position 0 and slot -1.
  *   next_free_out int32 [1]: next_free moved past the pages taken; not the
  *                same address as next_free
  *
+ * No output may lie over an input (but seq_lens as above) or over another output.
  * Pages go to requests in order, and to each in the order of its tokens.
  * QMM_ERR_INDEX in the device error word: free_pages ran out (entries and
  * slots are then -1), a length is negative (taken as 0), a request outgrew its

@@ -254,6 +254,18 @@ qmm_status check_rows(const char *op, const char *name, const void *p, int64_t s
   return QMM_OK;
 }
 
+// A call's array of int32, and whether two share memory.
+struct Array {
+  const char *name;
+  const void *p;
+  uint64_t bytes;
+};
+bool overlap(const Array &a, const Array &b) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  if (a.bytes == 0 || b.bytes == 0) return false;
+  return x <= y ? y - x < a.bytes : x - y < b.bytes;
+}
+
 }  // namespace
 
 namespace qmm {
@@ -528,6 +540,24 @@ qmm_status qmm_page_plan(const int32_t *past_lens, const int32_t *new_lens, int6
   if (next_free && (!aligned16(next_free) || next_free == next_free_out))
     return fail(QMM_ERR_INVALID_ARG,
                 "%s: next_free must be 16-byte aligned and not the address of next_free_out", op);
+  // Blocks read the inputs all through the launch, so no output may lie over one.
+  const uint64_t R = requests, T = tokens;
+  const uint64_t table = R == 0 ? 0 : static_cast<uint64_t>(table_stride) > (uint64_t(1) << 61) / R
+                                          ? uint64_t(1) << 63 : 4 * R * static_cast<uint64_t>(table_stride);
+  const Array in[] = {{"past_lens", past_lens, 4 * R}, {"new_lens", new_lens, 4 * R},
+                      {"free_pages", free_pages, 4 * static_cast<uint64_t>(free_count)},
+                      {"next_free", next_free, next_free ? 4u : 0u}};
+  const Array out[] = {{"block_table", block_table, table}, {"starts", starts, 4 * (R + 1)},
+                       {"seq_lens", seq_lens, 4 * R}, {"positions", positions, 4 * T},
+                       {"slots", slots, 4 * T}, {"next_free_out", next_free_out, 4}};
+  for (const Array &o : out) {
+    for (const Array &i : in)
+      if (overlap(o, i) && !(o.p == seq_lens && i.p == past_lens && seq_lens == past_lens))
+        return fail(QMM_ERR_INVALID_ARG, "%s: %s lies over %s (only seq_lens may be past_lens)", op, o.name, i.name);
+    for (const Array &other : out)
+      if (&o < &other && overlap(o, other))
+        return fail(QMM_ERR_INVALID_ARG, "%s: %s and %s overlap", op, o.name, other.name);
+  }
   return cuda_status(qmm::launch_page_plan(past_lens, new_lens, static_cast<int>(requests), free_pages,
                                            static_cast<int>(free_count), next_free, page_size,
                                            block_table, table_stride, static_cast<int>(tokens), starts,

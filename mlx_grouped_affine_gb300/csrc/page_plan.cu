@@ -9,7 +9,9 @@
 //
 // One launch, no communication between blocks: every block computes the
 // prefix sums of all requests (a few hundred bytes to some KB from L2) and
-// then fills its own stretch of tokens and pages.  The bytes are few; what it
+// then fills its own stretch of tokens and pages.  (Lengths updated in place: the
+// blocks read past lengths all through the launch, so where there are several a
+// second, small launch writes the new ones.)  The bytes are few; what it
 // costs is the chain launch - lengths - scan - table or free entry - store:
 // 4 us for 256 requests of a token each, 9 for 1000 requests with 256k tokens.
 #include "paged.cuh"
@@ -71,6 +73,20 @@ __device__ __forceinline__ int last_at_most(const long long *v, int n, long long
   return lo;
 }
 
+// Request b's lengths before and after the step; nothing past what positions can
+// count or the table's rows can hold.  (Plain loads: `past` may be `seq`, which the
+// same thread writes afterwards.)
+struct Lengths {
+  int past, len;
+  bool bad;
+};
+__device__ __forceinline__ Lengths lengths_of(const PlanArgs &a, int b) {
+  const int p = a.past[b], n = a.fresh_tokens[b];
+  const long long most = min(static_cast<long long>(a.width) * a.page, 0x7FFFFFFFll);
+  const long long past = max(p, 0), len = past + max(n, 0);
+  return Lengths{static_cast<int>(min(past, most)), static_cast<int>(min(len, most)), p < 0 || n < 0 || len > most};
+}
+
 __global__ void __launch_bounds__(NT) page_plan_kernel(PlanArgs a) {
   __shared__ Pair sums[NT / 32];
   __shared__ long long first_token[NT], first_page[NT];
@@ -87,17 +103,12 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(PlanArgs a) {
     Pair mine{0, 0};
     int past = 0;
     if (b < a.requests) {
-      const int p = __ldg(a.past + b), n = __ldg(a.fresh_tokens + b);
-      past = max(p, 0);
-      long long len = static_cast<long long>(past) + max(n, 0);
-      // Nothing past what positions can count or the table's rows can hold.
-      const long long most = min(static_cast<long long>(a.width) * P, 0x7FFFFFFFll);
-      bad |= p < 0 || n < 0 || len > most;
-      past = static_cast<int>(min(static_cast<long long>(past), most));
-      len = min(len, most);
-      mine.x = len - past;
-      mine.y = (len + P - 1) / P - (past + static_cast<long long>(P) - 1) / P;
-      if (blockIdx.x == 0) a.seq[b] = static_cast<int>(len);
+      const Lengths x = lengths_of(a, b);
+      bad |= x.bad;
+      past = x.past;
+      mine.x = x.len - x.past;
+      mine.y = (x.len + static_cast<long long>(P) - 1) / P - (x.past + static_cast<long long>(P) - 1) / P;
+      if (blockIdx.x == 0 && a.seq) a.seq[b] = x.len;
     }
     Pair total;
     const Pair incl = scan_pair(mine, sums, &total);
@@ -164,6 +175,11 @@ __global__ void __launch_bounds__(NT) page_plan_kernel(PlanArgs a) {
   if (bad) atomicOr(a.err, kErrIndexBit);
 }
 
+__global__ void __launch_bounds__(NT) lengths_in_place_kernel(PlanArgs a) {
+  const long long b = blockIdx.x * static_cast<long long>(NT) + threadIdx.x;
+  if (b < a.requests) a.seq[b] = lengths_of(a, static_cast<int>(b)).len;
+}
+
 }  // namespace
 
 cudaError_t launch_page_plan(const int *past, const int *fresh, int requests, const int *free_pages,
@@ -178,7 +194,14 @@ cudaError_t launch_page_plan(const int *past, const int *fresh, int requests, co
   int64_t blocks = (static_cast<int64_t>(tokens) + NT - 1) / NT;
   if (blocks > sm_count()) blocks = sm_count();
   if (blocks < 1) blocks = 1;
+  // In place, a single block's thread reads a length before it writes it.
+  const bool later = seq == past && blocks > 1;
+  if (later) a.seq = nullptr;
   page_plan_kernel<<<static_cast<unsigned>(blocks), NT, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (!later || e != cudaSuccess) return e;
+  a.seq = seq;
+  lengths_in_place_kernel<<<static_cast<unsigned>((static_cast<int64_t>(requests) + NT - 1) / NT), NT, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
