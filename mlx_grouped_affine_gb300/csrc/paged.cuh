@@ -501,10 +501,13 @@ struct Copier {
   }
 };
 
-// Columns [d0, d1) of an output row by one warp, from the keys it sees alone.  The tiled kernels
-// multiply masked keys by weight zero, which is no longer nothing when such a
-// key's V is not finite; a row that came out non-finite is done again here,
-// where a key that the row does not see is never read.
+// Columns [d0, d1) of an output row by one warp, from the keys it sees alone.  The
+// tiled kernels multiply masked keys by weight zero, which is no longer nothing when
+// such a key's V is not finite; a row that came out non-finite is done again here,
+// where a key that the row does not see is never read.  Not so where its sum of
+// weights is not finite: that sum has the keys it sees alone, so one of their scores
+// is not finite and the row is NaN either way.  (One key after another, about a
+// microsecond each: the callers' test for that keeps a NaN in K from costing it.)
 template <typename E>
 __device__ __noinline__ void row_alone(const AttnArgs &a, int b, int head, int i, int d0, int d1) {
   using T = typename Elem<E>::type;
@@ -568,6 +571,8 @@ __device__ __forceinline__ float *slot_of(const AttnArgs &a, int block, int begi
 // thread has whole columns, four at a time.  The order of the sums is fixed by P
 // alone.  (6 items of 51 pieces took 27 us with a warp per row; 64 items of 256
 // rows in two or three pieces took 46 us with a block for all of an item's rows.)
+// Two blocks an SM (64 registers), so that the blocks of all cut items run at once:
+// at 70 registers and one block five fp32 requests take 52.7 us in place of 50.4.
 constexpr int kJoinThreads = 512;
 constexpr int kJoinLanes = 16;
 
@@ -576,7 +581,7 @@ template <int R>
 constexpr int join_weights(int blocks) { return 2 * R + 3 * blocks; }
 
 template <typename E, int R, int DP>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const __grid_constant__ AttnArgs a) {
   using T = typename Elem<E>::type;
   extern __shared__ float weight[];  // [rows][P]
   __shared__ float4 sums[kJoinThreads];
@@ -729,8 +734,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
   }
   __syncthreads();
+#pragma unroll 1
   for (int x = warp; x < rows; x += kJoinThreads / 32) {
     const int row = row0 + x;
+    if (isnan(weight[x * P])) continue;  // the row's sum is not finite
     if (!(bad_rows[row / 32] >> (row & 31) & 1u)) continue;
     int i, head;
     if (!row_of(a, r, h, qt, row, &i, &head)) continue;

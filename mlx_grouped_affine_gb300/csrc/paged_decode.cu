@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ A
         a.lse[token * a.Hq + head] = (M + log2f(L)) * kLn2;
       }
     }
-    const unsigned votes = __ballot_sync(0xffffffffu, bad);
+    const unsigned votes = __ballot_sync(0xffffffffu, bad && isfinite(L));
     if (votes) {
       __syncwarp();
 #pragma unroll 1

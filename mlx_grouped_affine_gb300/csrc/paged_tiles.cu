@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(NT) tiles_kernel(const __grid_constant__ AttnA
         if (kt == 0 && a.lse) a.lse[token * a.Hq + head] = (m[i] + log2f(l[i])) * kLn2;
       }
       // Both half-warps' rows, one after the other, by the whole warp.
-      const unsigned votes = __ballot_sync(0xffffffffu, bad);
+      const unsigned votes = __ballot_sync(0xffffffffu, bad && isfinite(l[i]));
       if (votes) {
         __syncwarp();
 #pragma unroll 1
