@@ -774,7 +774,7 @@ cudaError_t query_map(const AttnArgs &a, int type, CUtensorMap *q);
 cudaError_t key_map(const AttnArgs &a, int type, int rows, CUtensorMap *k);
 }  // namespace paged
 
-// paged_tiles.cu: every type and head size on the CUDA cores.
+// paged_tiles.cu: fp32, and 16-bit types with heads above 128, on the CUDA cores.
 cudaError_t launch_attention_tiles(paged::AttnArgs a, int type, size_t ws_bytes, cudaStream_t stream);
 // paged_decode.cu: 16-bit types, heads of at most 128, few rows per kv head.
 cudaError_t launch_attention_decode(const paged::AttnArgs &a, int type, size_t ws_bytes, cudaStream_t stream);

@@ -1,6 +1,6 @@
-// Paged attention in fp32 on the CUDA cores: any element type, head sizes up
-// to 256.  (16-bit types with heads of at most 128 have tensor-core kernels;
-// this one serves fp32, whose products no tensor form keeps, and larger heads.)
+// Paged attention in fp32 on the CUDA cores: fp32 elements, whose products no tensor
+// form keeps, and 16-bit ones in heads of 136 to 256.  (16-bit types with heads of at
+// most 128 have tensor-core kernels.)
 //
 // A block has items of 32 rows and walks key tiles of 64: K and V widened to
 // fp32 in shared memory, a 4 x 4 patch of scores a thread (two float4 loads
@@ -260,20 +260,15 @@ cudaError_t launch_t(AttnArgs a, size_t ws_bytes, cudaStream_t stream) {
   return le != cudaSuccess ? le : launch_join<E, R, DP>(a, blocks, stream);
 }
 
-template <typename E>
-cudaError_t launch_e(const AttnArgs &a, size_t ws_bytes, cudaStream_t stream) {
-  if (a.D <= 64) return launch_t<E, 64>(a, ws_bytes, stream);
-  if (a.D <= 128) return launch_t<E, 128>(a, ws_bytes, stream);
-  return launch_t<E, 256>(a, ws_bytes, stream);
-}
-
 }  // namespace
 }  // namespace paged
 
 cudaError_t launch_attention_tiles(paged::AttnArgs a, int type, size_t ws_bytes, cudaStream_t stream) {
-  if (type == kTypeBF16) return paged::launch_e<ElemBF16>(a, ws_bytes, stream);
-  if (type == kTypeF16) return paged::launch_e<ElemF16>(a, ws_bytes, stream);
-  return paged::launch_e<paged::ElemF32>(a, ws_bytes, stream);
+  if (type == kTypeBF16) return paged::launch_t<ElemBF16, 256>(a, ws_bytes, stream);
+  if (type == kTypeF16) return paged::launch_t<ElemF16, 256>(a, ws_bytes, stream);
+  if (a.D <= 64) return paged::launch_t<paged::ElemF32, 64>(a, ws_bytes, stream);
+  if (a.D <= 128) return paged::launch_t<paged::ElemF32, 128>(a, ws_bytes, stream);
+  return paged::launch_t<paged::ElemF32, 256>(a, ws_bytes, stream);
 }
 
 }  // namespace qmm
