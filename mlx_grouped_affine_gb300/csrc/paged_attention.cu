@@ -96,8 +96,9 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
   if (most_rows <= kFewRows || !(scale > 0.f))
     return launch_attention_decode(a, pool.type, kFewBytes - kDescBytes, stream);
   // Requests of both kinds: one kernel after the other, each leaving the
-  // other's requests alone; not when no request can be of the first kind.
-  const bool few = requests > 1 && tokens <= (requests - 1) * max_new + kFewRows / a.G;
+  // other's requests alone; not when no request can be of the first kind: groups are
+  // wider than its rows, or the other requests' tokens at the most leave no few for one.
+  const bool few = requests > 1 && a.G <= kFewRows && tokens <= (requests - 1) * max_new + kFewRows / a.G;
   paged::AttnArgs many = a;
   region(many, kFewBytes);
   if (few) {
