@@ -80,7 +80,8 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int b) {
 
 // Keys [lo, hi) that the row of new token i sees: its position is
 // p = len - n + i; causal rows see keys up to p, a window the last `window`
-// of them.  lo >= hi for a row that sees nothing.
+// of them.  lo >= hi for a row that sees nothing.  hi may be 2^31 - 1 and a tile then
+// ends at 2^31: bounds are compared by differences, which an int holds.
 struct Span {
   int lo, hi;
 };
@@ -428,7 +429,7 @@ struct Block {
 };
 __device__ __forceinline__ Block look_up(const AttnArgs &a, int b, int key, int lo, int hi) {
   Block x{0, 0, 0};
-  if (key + 8 <= lo || key >= hi) return x;
+  if (lo - key >= 8 || key >= hi) return x;
   x.how = 2;
   if (a.page % 8 == 0) {
     x.how = 1;
@@ -472,7 +473,7 @@ struct Copier {
   __device__ __forceinline__ void copy(const AttnArgs &a, const void *pool, int64_t off, uint32_t dst, int b,
                                        int kv, int key, int lo, int hi) const {
     const uint16_t *src = static_cast<const uint16_t *>(pool) + col;
-    if (off >= 0 && key >= lo && key + 8 <= hi) {
+    if (off >= 0 && key >= lo && hi - key >= 8) {
       src += off + first * a.token_stride;
 #pragma unroll
       for (int i = 0; i < N; ++i) {

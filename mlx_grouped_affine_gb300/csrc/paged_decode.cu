@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(NT, 2) decode_kernel(const __grid_constant__ A
           }
         }
       }
-      const bool masked = key0 < deep_lo || key0 + KW > deep_hi;
+      const bool masked = key0 < deep_lo || deep_hi - key0 < KW;
       float top[2] = {m[0], m[1]};
 #pragma unroll
       for (int x = 0; x < NC; ++x)

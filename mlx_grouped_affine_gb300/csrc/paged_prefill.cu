@@ -337,11 +337,11 @@ __device__ void key_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, c
       Block next;
       auto look = [&](int tile) {
         next = Block{0, 0, 0};
-        const int key = tile * KT + rows * lane;
         if (rows * lane >= KT || tile >= p.any.to) return;
+        const int key = tile * KT + rows * lane;
         if (!box) {
           next = look_up(a, c.b, key, c.lo, c.hi);
-        } else if (key + rows > c.lo && key < c.hi) {
+        } else if (c.lo - key < rows && key < c.hi) {
           const int pg = key / a.page;
           next = Block{1, __ldg(a.table + c.b * a.table_stride + pg), key - pg * a.page};
         }
@@ -622,7 +622,7 @@ __device__ void softmax_role(const AttnArgs &a, Barriers *bars, uint32_t tmem) {
     for (int j = from; j < to_tile; ++j) {
       dead = dead || !wait_warp(&bars->s_full[h], s_count & 1, abort, a.err, a.spin_limit);
       ++s_count;
-      const bool deep = j * KT >= deep_lo && j * KT + KT <= deep_hi;
+      const bool deep = j * KT >= deep_lo && deep_hi - j * KT >= KT;
       float s[32], top = kNegInf;
       if (!dead) {
         tc_fence_after();
