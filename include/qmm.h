@@ -457,8 +457,8 @@ typedef struct {
  * QMM_ERR_INDEX in the device error word: free_pages ran out (entries and
  * slots are then -1), a length is negative (taken as 0), a request outgrew its
  * table row or the tokens their room (cut off there), or a page id's slot is
- * outside [0, 2^31).  requests, free_count, tokens at least 0 and below 2^31;
- * page_size 1 to 65536; table_stride at least 1.
+ * outside [0, 2^31).  requests at least 0 and at most 2^31 - 1024, free_count and
+ * tokens below 2^31; page_size 1 to 65536; table_stride at least 1.
  */
 qmm_status qmm_page_plan(const int32_t *past_lens, const int32_t *new_lens, int64_t requests,
                          const int32_t *free_pages, int64_t free_count, const int32_t *next_free,
@@ -507,7 +507,8 @@ qmm_status qmm_rope_append(const void *q, int64_t q_stride, const void *k, int64
  *
  *   q            [tokens, q_heads * head_dim] of cache->dtype, tokens q_stride
  *                apart; q_heads a multiple of cache->heads: query head h reads
- *                key head h / (q_heads / cache->heads)
+ *                key head h / (q_heads / cache->heads).  tokens and requests at
+ *                most 2^31 - 1024
  *   block_table  int32 [requests, table_stride], starts int32 [requests + 1],
  *                seq_lens int32 [requests]: as qmm_page_plan writes them.  New
  *                token i of request b, row starts[b] + i of q, has position
@@ -517,8 +518,8 @@ qmm_status qmm_rope_append(const void *q, int64_t q_stride, const void *k, int64
  *                rounding
  *   causal       1: a row sees keys 0 .. p; 0: every key of its request
  *   window       > 0: of those only keys p - window + 1 and later; 0: all
- *   out          like q, tokens out_stride apart.  A row that sees no key is
- *                zero.  Rows of q past starts[requests] stay unwritten.
+ *   out          like q, tokens out_stride apart, over no input.  A row that sees
+ *                no key is zero.  Rows of q past starts[requests] stay unwritten.
  *   lse          fp32 [tokens, q_heads]: log of the sum of exponentials of the
  *                scaled scores (-infinity where no key is seen), or NULL
  *   workspace    device memory of at least QMM_ATTENTION_WORKSPACE_BYTES,

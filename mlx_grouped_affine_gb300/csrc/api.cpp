@@ -213,6 +213,8 @@ qmm_status matmul_impl(const char *op, const void *x, qmm_dtype x_dtype, int64_t
 // ----------------------------------------------- paged attention checks ----
 
 bool count31(int64_t n) { return n >= 0 && n <= 0x7FFFFFFF; }
+// A count that kernels walk in steps of a block (up to 1023 past its end) in 32 bits.
+bool count_steps(int64_t n) { return n >= 0 && n <= 0x7FFFFFFF - 1023; }
 
 // A cache as the kernels take it, with q_heads query heads over it.
 qmm_status check_cache(const char *op, const qmm_paged_cache *c, int q_heads, qmm::PagedPool *pool) {
@@ -523,6 +525,7 @@ qmm_status qmm_page_plan(const int32_t *past_lens, const int32_t *new_lens, int6
   const char *op = "qmm_page_plan";
   if (!count31(requests) || !count31(free_count) || !count31(tokens))
     return fail(QMM_ERR_INVALID_ARG, "%s: requests, free_count and tokens must be in [0, 2^31)", op);
+  if (!count_steps(requests)) return fail(QMM_ERR_INVALID_ARG, "%s: requests must be at most 2^31 - 1024", op);
   if (page_size < 1 || page_size > 65536)
     return fail(QMM_ERR_INVALID_ARG, "%s: page_size %d is not in [1, 65536]", op, page_size);
   if (table_stride < 1)
@@ -628,6 +631,8 @@ qmm_status qmm_paged_attention(const void *q, int64_t q_stride, int64_t tokens, 
   if ((st = check_cache(op, cache, q_heads, &pool)) != QMM_OK) return st;
   if (!count31(tokens) || !count31(requests) || !count31(max_new) || !count31(window))
     return fail(QMM_ERR_INVALID_ARG, "%s: tokens, requests, max_new and window must be in [0, 2^31)", op);
+  if (!count_steps(tokens) || !count_steps(requests))
+    return fail(QMM_ERR_INVALID_ARG, "%s: tokens and requests must be at most 2^31 - 1024", op);
   if (table_stride < 1) return fail(QMM_ERR_INVALID_ARG, "%s: table_stride must be at least 1", op);
   if (causal != 0 && causal != 1)
     return fail(QMM_ERR_INVALID_ARG, "%s: causal must be 0 or 1, got %d", op, causal);
