@@ -376,12 +376,15 @@ struct ElemF32 {};
 template <typename E>
 struct Elem {
   using type = uint16_t;
+  // The sign, and the lowest bit of the exponent, in each element of a word.
+  static constexpr uint32_t kSign = 0x80008000u, kExponent = E::kF16 ? 0x04000400u : 0x00800080u;
   __device__ static __forceinline__ float to_f32(uint16_t v) { return E::to_f32(v); }
   __device__ static __forceinline__ uint16_t from_f32(float v) { return E::from_f32(v); }
 };
 template <>
 struct Elem<ElemF32> {
   using type = float;
+  static constexpr uint32_t kSign = 0x80000000u, kExponent = 0x00800000u;
   __device__ static __forceinline__ float to_f32(float v) { return v; }
   __device__ static __forceinline__ float from_f32(float v) { return v; }
 };
@@ -502,21 +505,50 @@ struct Copier {
   }
 };
 
+// Whether a key that row i does not see, but that its item's tiles hold for other rows
+// (at most the item's tokens at either end of the row's keys), has a V that is not
+// finite: an element's exponent has all bits set, so that one more at its lowest bit
+// carries into the sign's place.  By one warp, a key a lane.  Small, because the size of
+// code that a kernel seldom reaches shows in its time: three long requests take 37 us,
+// with this loop four times unrolled and plain tests 40.
+template <typename E>
+__device__ __forceinline__ bool unseen_not_finite(const AttnArgs &a, const Request &r, const Span &s, int b, int h,
+                                                  int i) {
+  using T = typename Elem<E>::type;
+  constexpr uint32_t kSign = Elem<E>::kSign, kOne = Elem<E>::kExponent;
+  const int i0 = i / a.TQ * a.TQ, i1 = min(r.n - i0, a.TQ) - 1 + i0;
+  const int lo = span_of(a, r, i0).lo, before = max(s.lo - lo, 0), after = max(span_of(a, r, i1).hi - s.hi, 0);
+  uint32_t bad = 0;
+  for (int x = threadIdx.x & 31; x < before + after; x += 32) {
+    const int64_t off = key_offset(a, b, h, x < before ? lo + x : s.hi + (x - before));
+    if (off < 0) continue;
+    const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.v) + off);
+#pragma unroll 1
+    for (int d = 0; d < a.D; d += 16 / sizeof(T)) {
+      const uint4 w = *v++;
+      bad |= ((w.x & ~kSign) + kOne) | ((w.y & ~kSign) + kOne) | ((w.z & ~kSign) + kOne) | ((w.w & ~kSign) + kOne);
+    }
+  }
+  return __any_sync(0xffffffffu, bad & kSign);
+}
+
 // Columns [d0, d1) of an output row by one warp, from the keys it sees alone.  The
 // tiled kernels multiply masked keys by weight zero, which is no longer nothing when
-// such a key's V is not finite; a row that came out non-finite is done again here,
-// where a key that the row does not see is never read.  Not so where its sum of
-// weights is not finite: that sum has the keys it sees alone, so one of their scores
-// is not finite and the row is NaN either way.  (One key after another, about a
-// microsecond each: the callers' test for that keeps a NaN in K from costing it.)
+// such a key's V is not finite; a row that came out non-finite for that is done again
+// here, where a key that the row does not see is never read.  That takes about a
+// microsecond a key, so it is left out where the row is non-finite of itself:
+// callers do so where its sum of weights is not finite (it has the keys that the row
+// sees alone, so one of their scores is not and the row is NaN either way), and here
+// where no unseen key's V is to blame.
 template <typename E>
 __device__ __noinline__ void row_alone(const AttnArgs &a, int b, int head, int i, int d0, int d1) {
   using T = typename Elem<E>::type;
   const int lane = threadIdx.x & 31;
+  const int h = head / a.G;
   const Request r = request_of(a, b);
   const Span s = span_of(a, r, i);
+  if (!unseen_not_finite<E>(a, r, s, b, h, i)) return;
   const int64_t token = r.first + i;
-  const int h = head / a.G;
   const T *q = static_cast<const T *>(a.q) + token * a.q_stride + static_cast<int64_t>(head) * a.D;
   float o[8], qv[8];
   const int n = (a.D + 31) / 32;

@@ -559,13 +559,10 @@ __device__ __forceinline__ void weights(const float (&s)[32], float scale, float
   }
 }
 
-// What a row's thread leaves in its first column of output where the row is to be done
-// again: a NaN that no rounding makes (those have all bits of the significand set).
-constexpr uint16_t kAgain = 0x7FE5;
-
-// The rows that the block wrote whole, once more where a thread marked them.  Called
-// after everything else, when some thread did, so that the tile loop makes no calls.
-template <typename E, int DP>
+// The rows that the block wrote whole, once more where one is not finite.  Called
+// after everything else, when some thread saw such a value in a row whose sum is
+// finite, so that the tile loop makes no calls.
+template <typename E>
 __device__ __noinline__ void redo_rows(const AttnArgs &a, Cursor c) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   while (c.left > 0) {
@@ -575,9 +572,9 @@ __device__ __noinline__ void redo_rows(const AttnArgs &a, Cursor c) {
       if (!row_of(a, c.r, c.h, c.qt, row, &i, &head)) continue;
       const uint16_t *out = static_cast<const uint16_t *>(a.out) +
                             (static_cast<int64_t>(c.r.first) + i) * a.out_stride + static_cast<int64_t>(head) * a.D;
-      const bool again = out[0] == kAgain || (a.D > DP / 2 && out[DP / 2] == kAgain);
-      __syncwarp();
-      if (again) row_alone<E>(a, c.b, head, i, 0, a.D);
+      bool bad = false;
+      for (int d = lane; d < a.D; d += 32) bad |= !isfinite(E::to_f32(out[d]));
+      if (__any_sync(0xffffffffu, bad)) row_alone<E>(a, c.b, head, i, 0, a.D);
     }
     piece_done(a, c, p);
   }
@@ -730,10 +727,7 @@ __device__ void softmax_role(const AttnArgs &a, Barriers *bars, uint32_t tmem) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->o_empty[h]);
       }
-      if (bad && live && whole && cols > 0 && isfinite(l)) {
-        *out = kAgain;
-        bars->redo = 1;
-      }
+      if (bad && live && whole && isfinite(l)) bars->redo = 1;
     }
     continues = false;
     // Both warps have read the cursor; one moves it on.
@@ -808,7 +802,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
-  if (bars->redo && !bars->abort) redo_rows<E, DP>(a, bars->start);
+  if (bars->redo && !bars->abort) redo_rows<E>(a, bars->start);
 }
 
 template <typename E, int DP>
