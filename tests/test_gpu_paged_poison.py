@@ -44,9 +44,9 @@ SHAPES = {"long": [(60000, 1)], "many": [(900, 1)] * 200, "chunk": [(20000, 64)]
 @pytest.mark.parametrize("shape", sorted(SHAPES))
 @pytest.mark.parametrize("what", ["q", "k"])
 def test_a_row_whose_scores_are_not_finite_costs_what_others_cost(dtype, dim, shape, what):
-    """A row that sees a NaN score is NaN, and nothing is done for it again: before, one
-    warp walked all of the row's keys, 10 to 1000 times the call's time (at each shape
-    here).  The bound, three times, is far from either."""
+    """A row that sees a NaN score is NaN, and nothing is done for it again: one warp that
+    walked all of the row's keys took 130 ms over the long cache, 2.6 ms over the many.
+    The bound, three times the clean call's time, is far from either."""
     lens = SHAPES[shape]
     pool, q, news = setup(lens, 4, dim, dtype)
     call = lambda: attend(pool, q, news, 8, dim ** -0.5)  # noqa: E731
@@ -77,8 +77,8 @@ def test_a_row_whose_scores_are_not_finite_costs_what_others_cost(dtype, dim, sh
 def test_a_value_that_is_not_finite_where_rows_see_it_costs_little(dtype, dim, shape, value):
     """V of key 5 of the last request's first head is not finite in one column, every
     score is: the rows that see it are not finite there, of themselves, and only the few
-    that do not see it beside those that do are done again.  Before, all were: 60 ms
-    over the long cache.  The bound is ten times the clean call's time, for prompts whose
+    that do not see it beside those that do are done again.  With all of them it took 130
+    ms over the long cache, 24 ms for the prompts (0.45 now).  The bound is ten times the clean call's time, for prompts whose
     rows each look over their item's other keys."""
     lens = SHAPES[shape]
     pool, q, news = setup(lens, 4, dim, dtype)
