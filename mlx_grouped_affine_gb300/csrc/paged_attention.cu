@@ -31,8 +31,8 @@ namespace {
 constexpr size_t kDescBytes = 16 << 10;  // 32 bytes for each of up to 512 blocks
 constexpr size_t kFewBytes = 12 << 20;   // region of the kernel of few rows
 // Rows a kv head that it takes.  Measured, few / many kernel in us: 16 requests
-// over 4000 keys 64 / 83 at 16 rows, 85 / 83 at 32, 176 / 85 at 64; one over 32000
-// keys 39 / 53, 44 / 54, 71 / 54; 4 over 300 keys 15 / 23, 15 / 24, 18 / 26.
+// over 4000 keys 58 / 80 at 16 rows, 82 / 81 at 32, 173 / 83 at 64; one over 32000
+// keys 35 / 50, 40 / 50, 64 / 50; 4 over 300 keys 14 / 23, 15 / 23, 18 / 25.
 constexpr int kFewRows = 32;
 }  // namespace
 
@@ -95,9 +95,11 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
   const int64_t most_rows = max_new * a.G;
   if (most_rows <= kFewRows || !(scale > 0.f))
     return launch_attention_decode(a, pool.type, kFewBytes - kDescBytes, stream);
-  // Requests of both kinds: one kernel after the other, each leaving the
-  // other's requests alone; not when no request can be of the first kind: groups are
-  // wider than its rows, or the other requests' tokens at the most leave no few for one.
+  // Requests of both kinds: one kernel after the other, each leaving the other's
+  // requests alone (63 single tokens over 100 to 8000 keys and 512 tokens over 8000: 266
+  // us; each alone 170 and 83).  Not when no request can be of the first kind: a group
+  // has more heads than that kernel takes rows, or there are more tokens than the other
+  // requests can have.
   const bool few = requests > 1 && a.G <= kFewRows && tokens <= (requests - 1) * max_new + kFewRows / a.G;
   paged::AttnArgs many = a;
   region(many, kFewBytes);

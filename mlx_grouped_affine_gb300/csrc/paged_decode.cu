@@ -18,10 +18,10 @@
 // below 2^-40 (not 2^-14 and 2^-25: a long flat tail would go missing).
 //
 // Measured: 64 requests of 100 to 8000 keys, 8 kv heads of 128, bf16: 1.15 GB in
-// 187 us, 6.2 TB/s, 0.91 of the measured copy rate.  Keys arrive 6 to 11 us after
+// 186 us (190 as called), 6.2 TB/s, 0.91 of the measured copy rate.  Keys arrive 6 to 11 us after
 // the launch, blocks end after 122 to 190 us (whole groups of SMs are slower than
-// others), the join takes 5.  Three requests of up to 131k keys: 39 us.  One request
-// of 1001 keys: 12.9 us, all of it latency.  (K and V by TMA boxes of 16 rows instead:
+// others), the join takes 5.  Three requests of up to 131k keys: 37 us.  One request
+// of 1001 keys: 12.3 us, all of it latency.  (K and V by TMA boxes of 16 rows instead:
 // 206 us; more blocks than are resident: 210 and up; a tenth or less of the work in a
 // second, smaller wave: 187 to 190, and the three requests 5 us more.)
 #include "paged.cuh"

@@ -35,10 +35,14 @@
 // the type's range, and keeps all bits down to 2^-21 of the row's largest weight.
 //
 // Measured (32 heads over 8 of 128, bf16): 512 tokens over 32000 keys 220 us,
-// 1.23 PFLOP/s, 0.64 of the measured bf16 rate; causal prompts of 2000 to 8192
-// tokens 618 to 628 us, 0.63 to 0.64.  The tensor pipe is busy 61 % of the time: its products read
-// 192 KB of shared memory a tile, 64 KB more are written by the loads, and 256 KB at
-// 128 bytes a cycle take the 2048 cycles that the products alone would.
+// 1.23 PFLOP/s, 0.64 of the measured bf16 rate (as called 228 us, 0.62); causal prompts
+// of 2000 to 8192 tokens 615 to 628 us, 0.63 to 0.65 (622 to 646, 0.61 to 0.64).  The
+// tensor pipe is busy 61 % of the time: its products read 192 KB of shared memory a
+// tile, 64 KB more are written by the loads, and 256 KB at 128 bytes a cycle take the
+// 2048 cycles that the products alone would.  Beside that the chunk reads K and V from
+// HBM 7.5 times (its items are at different keys at one time): 4.8 TB/s, 0.71 of the
+// copy rate.  Heads of 72 to 120 are padded to 128 in products and loads and take the
+// time of 128 (prompts with heads of 80 and 96: 607 and 608 us).
 //
 // Waits are bounded; one that runs out sets the error word and an abort flag
 // that stops every role, and the block still drains its copies and MMAs.  The

@@ -7,8 +7,11 @@
 // feed 16 multiply-adds), the softmax statistics of a row in the 16 lanes that
 // share it, and 4 rows x DP/16 columns of output a thread in registers.  Its
 // multiply-adds and the shared-memory loads that feed them bound it: five requests
-// of 1 to 130 tokens, up to 2000 keys, fp32 heads of 64 take 51 us, about 12 of
-// them at the fp32 units' rate.  (Two blocks an SM; three or four: 53 to 60 us.  Tiles
+// of 1 to 130 tokens, up to 2000 keys, fp32 heads of 64 take 50 us, about 12 of
+// them at the fp32 units' rate; four fp32 prompts of 500 to 2048 tokens, heads of 128,
+// 2.14 ms, 31 TFLOP/s, 0.39 of that rate.  Single tokens leave most of an item's rows
+// empty: 64 requests of 100 to 8000 keys, groups of 4 in 32 rows, take 1.3 ms in fp32 and
+// 4.4 ms in bf16 heads of 256 (one block an SM), 0.26 and 0.08 of the bytes' rate.  (Two blocks an SM; three or four: 53 to 60 us.  Tiles
 // loaded ahead by cp.async: 57 against 55.5 us.)
 #include "paged.cuh"
 
