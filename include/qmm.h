@@ -529,7 +529,8 @@ qmm_status qmm_rope_append(const void *q, int64_t q_stride, const void *k, int64
  * A key that a row does not see has no part in the row, whatever its k and v
  * hold (infinities and NaN, stale rows of a page).  16-bit types: products of
  * the elements, fp32 scores, sums and statistics, weights rounded once to the
- * element type for the product with v.  fp32: fp32 throughout.  Results
+ * element type for the product with v (scaled scores above 2^26 in size, which
+ * fp32 counts in steps of 8, may lose their weights in it).  fp32: fp32 throughout.  Results
  * repeat bit for bit.  Lengths are clamped to the tensors' sizes; a table
  * entry outside [0, num_pages) that a row needs reads as zero keys and values
  * and sets QMM_ERR_INDEX in the device error word.
