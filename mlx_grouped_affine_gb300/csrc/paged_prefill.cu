@@ -33,8 +33,8 @@
 // than 2^8 (P stays below 256; the result is the same because O and the sum share
 // m).  For fp16 m is raised to 2^7 below the maximum, so that P reaches 2^15, half of
 // the type's range, and keeps all bits down to 2^-21 of the row's largest weight.  The
-// products in P's exponents are exact and m is rounded, 2^-24 of it: with scores of 2^20
-// and more m is the maximum itself, so that P is 2^that at most.
+// products in P's exponents are exact and m is rounded, 2^-24 of it: in fp16 with scores
+// of 2^20 and more m is the maximum itself, so that P is 2^that at most.
 //
 // Measured (32 heads over 8 of 128, bf16): 512 tokens over 32000 keys 220 us,
 // 1.23 PFLOP/s, 0.64 of the measured bf16 rate (as called 228 us, 0.62); causal prompts
@@ -69,7 +69,7 @@ constexpr int NT = 32 * (kSoftmaxWarps + 2 + kValueWarps);
 constexpr uint32_t kDrainPolls = 1u << 14;  // for copies under way after a wait ran out: milliseconds
 constexpr int KC = KT / 2;    // columns of S a softmax thread has
 // log2 by which scores exceed the row's reference when it is set, and beyond that
-// before it is set again; both nothing for scores from kHuge on.
+// before it is set again; in fp16 both nothing for scores from kHuge on.
 template <typename E>
 constexpr float kRaise = E::kF16 ? 7.f : 0.f;
 constexpr float kLazy = 8.f, kHuge = 0x1p20f;
@@ -639,11 +639,11 @@ __device__ void softmax_role(const AttnArgs &a, Barriers *bars, uint32_t tmem) {
         top = fmaxf(top, chunk_top(s)) * a.scale_log2;
       }
       // Raise the reference when a score is far above it (and in the first tile).
-      if (meet_any(meeting, !dead && top > m + (fabsf(top) < kHuge ? kRaise<E> + kLazy : 0.f))) {
+      if (meet_any(meeting, !dead && top > m + (!E::kF16 || fabsf(top) < kHuge ? kRaise<E> + kLazy : 0.f))) {
         bars->exchange[warp][lane] = top;
         meet(meeting);
         const float most = fmaxf(top, bars->exchange[warp ^ 4][lane]);
-        const float up = fmaxf(m, fabsf(most) < kHuge ? most - kRaise<E> : most);
+        const float up = fmaxf(m, E::kF16 && fabsf(most) < kHuge ? most - kRaise<E> : most);
         const float f = exp2_fast(m - (up == kNegInf ? 0.f : up));
         m = up;
         l *= f;

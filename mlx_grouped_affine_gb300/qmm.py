@@ -232,7 +232,8 @@ def qmm_quantized_matmul_typed(x, x_dtype, M, w, scales, biases, sb_dtype, N, K,
 def qmm_page_plan(past_lens, new_lens, requests, free_pages, free_count, next_free, page_size,
                   block_table, table_stride, tokens, starts, seq_lens, positions, slots,
                   next_free_out, stream=None):
-    """Block table, slot map and positions of a step from the requests' lengths."""
+    """Block table, slot map and positions of a step from the requests' lengths; seq_lens
+    may be past_lens (lengths updated in place), nothing else may overlap."""
     _check(lib().qmm_page_plan(_ptr(past_lens), _ptr(new_lens), requests, _ptr(free_pages),
                                free_count, _ptr(next_free), page_size, _ptr(block_table),
                                table_stride, tokens, _ptr(starts), _ptr(seq_lens),
