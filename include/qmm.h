@@ -544,6 +544,126 @@ qmm_status qmm_paged_attention(const void *q, int64_t q_stride, int64_t tokens, 
                                int64_t out_stride, float *lse, void *workspace,
                                int64_t workspace_bytes, qmm_stream_t stream);
 
+/* ---------------------------------------- block-scaled 8-bit floats ----
+ * The other format that checkpoints keep projections in (the pages have no
+ * counterpart): e4m3 codes (1 sign, 4 exponent and 3 fraction bits, no infinities,
+ * largest 448; 0x7F and 0xFF are NaN), one byte each and row-major, with one fp32
+ * scale for each block of 128 columns: of one row (activations) or of 128 rows
+ * (weights).  The last block of a row or column of blocks may be partial.  A value
+ * is its code's value times its block's scale.  Columns are a multiple of 16. */
+
+/*
+ * qmm_block_quantize -- codes and scales of x.
+ *
+ *   x           [rows, cols] of x_dtype
+ *   block_rows  1 (a scale per row and 128 columns) or 128 (per 128 x 128 block)
+ *   codes       uint8 [rows, cols]
+ *   scales      fp32 [ceil(rows / block_rows), ceil(cols / 128)]
+ *
+ * scale = the block's largest magnitude / 448, rounded once to fp32, at least
+ * 2^-126; code = the e4m3 value nearest to x / scale (the exact quotient, ties to
+ * even).  A NaN in a block makes its scale and codes NaN; an infinity makes its
+ * scale infinite, its own code NaN and the others 0.  codes and scales overlap
+ * neither x nor each other.
+ */
+qmm_status qmm_block_quantize(const void *x, qmm_dtype x_dtype, int64_t rows, int64_t cols,
+                              int block_rows, uint8_t *codes, float *scales, qmm_stream_t stream);
+
+/*
+ * qmm_block_matmul -- y = A . W^T of block-scaled operands.
+ *
+ *   a, a_scales  uint8 [M, K], fp32 [M, ceil(K / 128)]
+ *   w, w_scales  uint8 [N, K], fp32 [ceil(N / 128), ceil(K / 128)]
+ *   y            [M, N] of y_dtype (QMM_F32, QMM_BF16 or QMM_F16), over no input
+ *
+ * y[m, n] = sum over blocks b of a_scales[m, b] w_scales[n / 128, b] times the sum
+ * over the block's columns of a[m, k] w[n, k]: products exact, sums fp32, y rounded
+ * once.  Results repeat bit for bit.  K > 0 and a multiple of 16; M, N, K below 2^31.
+ */
+qmm_status qmm_block_matmul(const uint8_t *a, const float *a_scales, int64_t M, const uint8_t *w,
+                            const float *w_scales, int64_t N, int64_t K, void *y,
+                            qmm_dtype y_dtype, qmm_stream_t stream);
+
+/* ------------------------------------------------ mixture of experts ----
+ * The feed-forward of a layer with routed experts, for the few tokens of a decode
+ * step: qmm_moe_layer from the router's logits, or qmm_moe_route and qmm_moe_experts
+ * (any routing).  Many tokens (a prompt) go through qmm_moe_route and qmm_gather_qmm.
+ * (nuvec_core quantized.rs, `gather_qmm`, is one product of such a layer.) */
+
+/* How a logit becomes a weight. */
+typedef enum { QMM_SCORE_SOFTMAX = 0, QMM_SCORE_SIGMOID = 1 } qmm_scoring;
+
+/* The three weights of `experts` gated feed-forwards in the packed format above, expert
+ * after expert: gate and up [experts, inner, hidden], down [experts, hidden, inner]. */
+typedef struct {
+    const uint32_t *gate, *up, *down;                        /* device */
+    const void *gate_scales, *up_scales, *down_scales;       /* of sb_dtype */
+    const void *gate_biases, *up_biases, *down_biases;
+    qmm_dtype sb_dtype;
+    int64_t experts;      /* 1 to 1024 */
+    int64_t hidden;       /* multiples of group_size, below 2^31 */
+    int64_t inner;
+    int32_t group_size, bits;
+} qmm_experts;
+
+/*
+ * qmm_moe_route -- the top_k experts of each token and their weights.
+ *
+ *   logits     [tokens, experts] of dtype; experts 1 to 1024
+ *   top_k      1 to min(experts, 32)
+ *   scoring    QMM_SCORE_SOFTMAX (over all experts of the row) or QMM_SCORE_SIGMOID
+ *   normalize  1: the row's chosen scores are divided by their sum
+ *   scale      factor of every weight (finite)
+ *   ids        int32 [tokens, top_k]: largest logits first, of equal ones (+0 and -0
+ *              are equal) the lowest index first
+ *   weights    fp32 [tokens, top_k]
+ *
+ * A logit of -infinity (a masked expert) has score 0, a NaN counts as -infinity; in a
+ * row that has nothing else every weight is 0.  Logits of +infinity share a softmax
+ * equally.  fp32 throughout.  Outputs overlap neither the logits nor each other.
+ */
+qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t tokens, int64_t experts,
+                         int top_k, qmm_scoring scoring, int normalize, float scale,
+                         int32_t *ids, float *weights, qmm_stream_t stream);
+
+/*
+ * qmm_moe_experts -- y[t] = sum over j of weights[t, j] *
+ * down_e(silu(gate_e(x[t])) * up_e(x[t])) with e = ids[t, j], for a few tokens.
+ *
+ *   x          [tokens, hidden] of x_dtype; tokens at most 64
+ *   ids        int32 [tokens, top_k]; weights fp32 [tokens, top_k]; top_k 1 to 32,
+ *              tokens * top_k at most 512.  An expert may come twice in a row.
+ *   experts    the weights (a host struct of device pointers)
+ *   y          [tokens, hidden] of y_dtype: QMM_F32 or x_dtype.  Over no input.
+ *   workspace  device memory of at least qmm_moe_workspace_bytes(...), whatever it
+ *              holds; calls that may overlap on the GPU need one each
+ *
+ * A slot whose weight is 0 (a masked expert) has no part in y, whatever its expert
+ * holds.  An id outside [0, experts) has none either and is reported by
+ * qmm_get_device_error as QMM_ERR_INDEX.  Each weight is scale * code + bias as it
+ * stands (codes are not rounded, scales and biases applied in fp32), x exact, sums
+ * fp32; silu(gate) * up keeps 15 bits or more for 16-bit x_dtype, 24 for fp32; y is
+ * rounded once.  Results repeat bit for bit.  Each expert that is asked for is
+ * streamed from memory once for every 16 of its slots.
+ */
+qmm_status qmm_moe_experts(const void *x, qmm_dtype x_dtype, int64_t tokens, const int32_t *ids,
+                           const float *weights, int top_k, const qmm_experts *experts, void *y,
+                           qmm_dtype y_dtype, void *workspace, int64_t workspace_bytes,
+                           qmm_stream_t stream);
+
+/*
+ * qmm_moe_layer -- qmm_moe_route on logits [tokens, experts->experts] and
+ * qmm_moe_experts on what it gives, in one call that writes neither ids nor weights.
+ */
+qmm_status qmm_moe_layer(const void *x, qmm_dtype x_dtype, int64_t tokens, const void *logits,
+                         qmm_dtype logits_dtype, int top_k, qmm_scoring scoring, int normalize,
+                         float scale, const qmm_experts *experts, void *y, qmm_dtype y_dtype,
+                         void *workspace, int64_t workspace_bytes, qmm_stream_t stream);
+
+/* Bytes of workspace for calls of at most `tokens` tokens and `top_k` experts each (host
+ * only; no GPU needed); -1 where a size is out of its range. */
+int64_t qmm_moe_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inner);
+
 #ifdef __cplusplus
 }
 #endif

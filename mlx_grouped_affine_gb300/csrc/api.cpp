@@ -256,7 +256,7 @@ qmm_status check_rows(const char *op, const char *name, const void *p, int64_t s
   return QMM_OK;
 }
 
-// A call's array of int32, and whether two share memory.
+// An array of a call, and whether two share memory.
 struct Array {
   const char *name;
   const void *p;
@@ -266,6 +266,126 @@ bool overlap(const Array &a, const Array &b) {
   const uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
   if (a.bytes == 0 || b.bytes == 0) return false;
   return x <= y ? y - x < a.bytes : x - y < b.bytes;
+}
+
+// No output over an input or over another output.
+qmm_status check_apart(const char *op, const Array *in, int inputs, const Array *out, int outputs) {
+  for (int o = 0; o < outputs; ++o) {
+    for (int i = 0; i < inputs; ++i)
+      if (overlap(out[o], in[i]))
+        return fail(QMM_ERR_INVALID_ARG, "%s: %s lies over %s", op, out[o].name, in[i].name);
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o], out[i]))
+        return fail(QMM_ERR_INVALID_ARG, "%s: %s and %s overlap", op, out[i].name, out[o].name);
+  }
+  return QMM_OK;
+}
+
+// Whether rows * cols elements and their bytes can be counted in 64 bits.
+bool small_enough(int64_t rows, int64_t cols) {
+  return rows == 0 || cols == 0 || rows <= (int64_t(1) << 58) / cols;
+}
+uint64_t type_bytes(qmm_dtype d) { return d == QMM_F32 ? 4 : 2; }
+int64_t blocks128(int64_t n) { return (n + 127) / 128; }
+
+qmm_status check_routing(const char *op, int64_t experts, int top_k, qmm_scoring scoring,
+                         int normalize, float scale, qmm_dtype dtype) {
+  if (!known_dtype(dtype))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: unknown logits dtype %d", op, static_cast<int>(dtype));
+  if (experts < 1 || experts > qmm::kMoeMaxExperts)
+    return fail(QMM_ERR_INVALID_ARG, "%s: %lld experts, not in [1, %d]", op, (long long)experts,
+                qmm::kMoeMaxExperts);
+  if (top_k < 1 || top_k > qmm::kMoeMaxTop || top_k > experts)
+    return fail(QMM_ERR_INVALID_ARG, "%s: top_k %d is not in [1, min(experts, %d)]", op, top_k,
+                qmm::kMoeMaxTop);
+  if (scoring != QMM_SCORE_SOFTMAX && scoring != QMM_SCORE_SIGMOID)
+    return fail(QMM_ERR_INVALID_ARG, "%s: unknown scoring %d", op, static_cast<int>(scoring));
+  if (normalize != 0 && normalize != 1)
+    return fail(QMM_ERR_INVALID_ARG, "%s: normalize must be 0 or 1, got %d", op, normalize);
+  if (!std::isfinite(scale)) return fail(QMM_ERR_INVALID_ARG, "%s: scale is not finite", op);
+  return QMM_OK;
+}
+
+// The experts' weights: sizes, pointers; their bytes as arrays (9 of them).
+qmm_status check_experts(const char *op, const qmm_experts *e, qmm::ExpertWeights *out, Array *arrays) {
+  if (!e) return fail(QMM_ERR_INVALID_ARG, "%s: experts is null", op);
+  qmm_status st;
+  if ((st = check_params(op, e->group_size, e->bits)) != QMM_OK) return st;
+  if (!known_dtype(e->sb_dtype))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: unknown scale dtype %d", op, static_cast<int>(e->sb_dtype));
+  if (e->experts < 1 || e->experts > qmm::kMoeMaxExperts)
+    return fail(QMM_ERR_INVALID_ARG, "%s: %lld experts, not in [1, %d]", op, (long long)e->experts,
+                qmm::kMoeMaxExperts);
+  if (!count_steps(e->hidden) || !count_steps(e->inner) || e->hidden < 1 || e->inner < 1 ||
+      e->hidden % e->group_size != 0 || e->inner % e->group_size != 0)
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: hidden (%lld) and inner (%lld) must be positive multiples of group size %d, below 2^31 - 1024",
+                op, (long long)e->hidden, (long long)e->inner, e->group_size);
+  if (!small_enough(e->hidden * e->inner, 8 * e->experts))
+    return fail(QMM_ERR_INVALID_ARG, "%s: the experts are too large", op);
+  const uint32_t *w[3] = {e->gate, e->up, e->down};
+  const void *s[3] = {e->gate_scales, e->up_scales, e->down_scales};
+  const void *b[3] = {e->gate_biases, e->up_biases, e->down_biases};
+  static const char *const names[9] = {"gate", "up", "down", "gate_scales", "up_scales",
+                                       "down_scales", "gate_biases", "up_biases", "down_biases"};
+  const uint64_t weights = static_cast<uint64_t>(e->experts) * e->hidden * e->inner;
+  const uint64_t sb = weights / e->group_size * type_bytes(e->sb_dtype);
+  for (int i = 0; i < 3; ++i) {
+    arrays[i] = {names[i], w[i], weights / 8 * e->bits};
+    arrays[3 + i] = {names[3 + i], s[i], sb};
+    arrays[6 + i] = {names[6 + i], b[i], sb};
+    out->w[i] = w[i];
+    out->scales[i] = s[i];
+    out->biases[i] = b[i];
+  }
+  for (int i = 0; i < 9; ++i)
+    if (!arrays[i].p || !aligned16(arrays[i].p))
+      return fail(QMM_ERR_INVALID_ARG, "%s: %s must be a non-null 16-byte aligned pointer", op, names[i]);
+  out->sb_type = static_cast<int>(e->sb_dtype);
+  out->experts = static_cast<int>(e->experts);
+  out->hidden = static_cast<int>(e->hidden);
+  out->inner = static_cast<int>(e->inner);
+  out->group = e->group_size;
+  out->bits = e->bits;
+  return QMM_OK;
+}
+
+// qmm_moe_experts and qmm_moe_layer, whose routing is checked but for its pointers.
+qmm_status moe_impl(const char *op, const void *x, qmm_dtype x_dtype, int64_t tokens,
+                    const qmm::Routing &r, const qmm_experts *experts, void *y, qmm_dtype y_dtype,
+                    void *workspace, int64_t workspace_bytes, qmm_stream_t stream) {
+  qmm::ExpertWeights w;
+  Array in[12], out[2];
+  qmm_status st;
+  if ((st = check_experts(op, experts, &w, in)) != QMM_OK) return st;
+  if (!known_dtype(x_dtype))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: unknown x dtype %d", op, static_cast<int>(x_dtype));
+  if ((st = check_out_dtype(op, y_dtype, x_dtype)) != QMM_OK) return st;
+  if (tokens < 0 || tokens > qmm::kMoeMaxTokens || tokens * r.top_k > qmm::kMoeMaxSlots)
+    return fail(QMM_ERR_INVALID_ARG, "%s: %lld tokens of %d experts (at most %d tokens, %d of both)", op,
+                (long long)tokens, r.top_k, qmm::kMoeMaxTokens, qmm::kMoeMaxSlots);
+  if (tokens == 0) return QMM_OK;
+  const uint64_t T = tokens, slots = T * r.top_k;
+  in[9] = {"x", x, T * w.hidden * type_bytes(x_dtype)};
+  in[10] = r.logits ? Array{"logits", r.logits, T * w.experts * (r.type == qmm::kTypeF32 ? 4u : 2u)}
+                    : Array{"ids", r.ids, 4 * slots};
+  in[11] = r.logits ? Array{"logits", nullptr, 0} : Array{"weights", r.weights, 4 * slots};
+  out[0] = {"y", y, T * w.hidden * type_bytes(y_dtype)};
+  out[1] = {"workspace", workspace, static_cast<uint64_t>(workspace_bytes < 0 ? 0 : workspace_bytes)};
+  const int64_t need = qmm::moe_workspace_bytes(tokens, r.top_k, w.hidden, w.inner);
+  for (const Array &a : {in[9], in[10], in[11], out[0], out[1]})
+    if (a.bytes > 0 && (!a.p || !aligned16(a.p)))
+      return fail(QMM_ERR_INVALID_ARG, "%s: %s must be a non-null 16-byte aligned pointer", op, a.name);
+  if (workspace_bytes < need)
+    return fail(QMM_ERR_INVALID_ARG, "%s: the workspace needs %lld bytes, got %lld", op, (long long)need,
+                (long long)workspace_bytes);
+  out[1].bytes = need;
+  if ((st = check_apart(op, in, 12, out, 2)) != QMM_OK) return st;
+  return cuda_status(qmm::launch_moe_experts(x, static_cast<int>(x_dtype), static_cast<int>(tokens), r, w,
+                                             y, static_cast<int>(y_dtype), workspace,
+                                             static_cast<size_t>(need),
+                                             reinterpret_cast<cudaStream_t>(stream)),
+                     op);
 }
 
 }  // namespace
@@ -658,6 +778,122 @@ qmm_status qmm_paged_attention(const void *q, int64_t q_stride, int64_t tokens, 
                                                  static_cast<size_t>(workspace_bytes),
                                                  reinterpret_cast<cudaStream_t>(stream)),
                      op);
+}
+
+// ------------------------------------------ block-scaled 8-bit floats ----
+
+qmm_status qmm_block_quantize(const void *x, qmm_dtype x_dtype, int64_t rows, int64_t cols,
+                              int block_rows, uint8_t *codes, float *scales, qmm_stream_t stream) {
+  const char *op = "qmm_block_quantize";
+  if (!known_dtype(x_dtype))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: unknown x dtype %d", op, static_cast<int>(x_dtype));
+  if (block_rows != 1 && block_rows != 128)
+    return fail(QMM_ERR_INVALID_ARG, "%s: block_rows must be 1 or 128, got %d", op, block_rows);
+  if (!count_steps(rows) || !count_steps(cols) || cols % 16 != 0)
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: rows (%lld) and cols (%lld) must be in [0, 2^31 - 1024], cols a multiple of 16", op,
+                (long long)rows, (long long)cols);
+  if (rows == 0 || cols == 0) return QMM_OK;
+  const uint64_t n = static_cast<uint64_t>(rows) * cols;
+  const int64_t groups = block_rows == 1 ? rows : blocks128(rows);
+  const Array in[] = {{"x", x, n * type_bytes(x_dtype)}};
+  const Array out[] = {{"codes", codes, n},
+                       {"scales", scales, 4 * static_cast<uint64_t>(groups) * blocks128(cols)}};
+  for (const Array &a : {in[0], out[0], out[1]})
+    if (!a.p || !aligned16(a.p))
+      return fail(QMM_ERR_INVALID_ARG, "%s: %s must be a non-null 16-byte aligned pointer", op, a.name);
+  const qmm_status st = check_apart(op, in, 1, out, 2);
+  if (st != QMM_OK) return st;
+  return cuda_status(qmm::launch_block_quantize(x, static_cast<int>(x_dtype), rows, cols,
+                                                block_rows != 1, codes, scales,
+                                                reinterpret_cast<cudaStream_t>(stream)),
+                     op);
+}
+
+qmm_status qmm_block_matmul(const uint8_t *a, const float *a_scales, int64_t M, const uint8_t *w,
+                            const float *w_scales, int64_t N, int64_t K, void *y,
+                            qmm_dtype y_dtype, qmm_stream_t stream) {
+  const char *op = "qmm_block_matmul";
+  if (!known_dtype(y_dtype))
+    return fail(QMM_ERR_UNSUPPORTED, "%s: unknown output dtype %d", op, static_cast<int>(y_dtype));
+  if (!count_steps(M) || !count_steps(N) || !count_steps(K) || K < 16 || K % 16 != 0)
+    return fail(QMM_ERR_INVALID_ARG,
+                "%s: M (%lld), N (%lld) and K (%lld) must be in [0, 2^31 - 1024], K a positive multiple of 16",
+                op, (long long)M, (long long)N, (long long)K);
+  if (M == 0 || N == 0) return QMM_OK;
+  const uint64_t kb = blocks128(K);
+  const Array in[] = {{"a", a, static_cast<uint64_t>(M) * K}, {"a_scales", a_scales, 4 * M * kb},
+                      {"w", w, static_cast<uint64_t>(N) * K}, {"w_scales", w_scales, 4 * blocks128(N) * kb}};
+  const Array out[] = {{"y", y, static_cast<uint64_t>(M) * N * type_bytes(y_dtype)}};
+  for (const Array &p : {in[0], in[1], in[2], in[3], out[0]})
+    if (!p.p || !aligned16(p.p))
+      return fail(QMM_ERR_INVALID_ARG, "%s: %s must be a non-null 16-byte aligned pointer", op, p.name);
+  const qmm_status st = check_apart(op, in, 4, out, 1);
+  if (st != QMM_OK) return st;
+  return cuda_status(qmm::launch_block_matmul(a, a_scales, static_cast<int>(M), w, w_scales,
+                                              static_cast<int>(N), static_cast<int>(K), y,
+                                              static_cast<int>(y_dtype),
+                                              reinterpret_cast<cudaStream_t>(stream)),
+                     op);
+}
+
+// ------------------------------------------------- mixture of experts ----
+
+qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t tokens, int64_t experts,
+                         int top_k, qmm_scoring scoring, int normalize, float scale, int32_t *ids,
+                         float *weights, qmm_stream_t stream) {
+  const char *op = "qmm_moe_route";
+  qmm_status st;
+  if ((st = check_routing(op, experts, top_k, scoring, normalize, scale, dtype)) != QMM_OK) return st;
+  if (!count_steps(tokens))
+    return fail(QMM_ERR_INVALID_ARG, "%s: tokens must be in [0, 2^31 - 1024]", op);
+  if (tokens == 0) return QMM_OK;
+  const uint64_t T = tokens;
+  const Array in[] = {{"logits", logits, T * experts * type_bytes(dtype)}};
+  const Array out[] = {{"ids", ids, 4 * T * top_k}, {"weights", weights, 4 * T * top_k}};
+  for (const Array &a : {in[0], out[0], out[1]})
+    if (!a.p || !aligned16(a.p))
+      return fail(QMM_ERR_INVALID_ARG, "%s: %s must be a non-null 16-byte aligned pointer", op, a.name);
+  if ((st = check_apart(op, in, 1, out, 2)) != QMM_OK) return st;
+  const qmm::Routing r{logits, static_cast<int>(dtype), top_k, scoring == QMM_SCORE_SIGMOID,
+                       normalize != 0, scale, nullptr, nullptr};
+  return cuda_status(qmm::launch_moe_route(r, tokens, static_cast<int>(experts), ids, weights,
+                                           reinterpret_cast<cudaStream_t>(stream)),
+                     op);
+}
+
+qmm_status qmm_moe_experts(const void *x, qmm_dtype x_dtype, int64_t tokens, const int32_t *ids,
+                           const float *weights, int top_k, const qmm_experts *experts, void *y,
+                           qmm_dtype y_dtype, void *workspace, int64_t workspace_bytes,
+                           qmm_stream_t stream) {
+  const char *op = "qmm_moe_experts";
+  if (top_k < 1 || top_k > qmm::kMoeMaxTop)
+    return fail(QMM_ERR_INVALID_ARG, "%s: top_k %d is not in [1, %d]", op, top_k, qmm::kMoeMaxTop);
+  const qmm::Routing r{nullptr, qmm::kTypeF32, top_k, false, false, 1.0f, ids, weights};
+  return moe_impl(op, x, x_dtype, tokens, r, experts, y, y_dtype, workspace, workspace_bytes, stream);
+}
+
+qmm_status qmm_moe_layer(const void *x, qmm_dtype x_dtype, int64_t tokens, const void *logits,
+                         qmm_dtype logits_dtype, int top_k, qmm_scoring scoring, int normalize,
+                         float scale, const qmm_experts *experts, void *y, qmm_dtype y_dtype,
+                         void *workspace, int64_t workspace_bytes, qmm_stream_t stream) {
+  const char *op = "qmm_moe_layer";
+  qmm_status st;
+  if (!experts) return fail(QMM_ERR_INVALID_ARG, "%s: experts is null", op);
+  if ((st = check_routing(op, experts->experts, top_k, scoring, normalize, scale, logits_dtype)) != QMM_OK)
+    return st;
+  if (tokens != 0 && (!logits || !aligned16(logits)))
+    return fail(QMM_ERR_INVALID_ARG, "%s: logits must be a non-null 16-byte aligned pointer", op);
+  const qmm::Routing r{logits, static_cast<int>(logits_dtype), top_k, scoring == QMM_SCORE_SIGMOID,
+                       normalize != 0, scale, nullptr, nullptr};
+  return moe_impl(op, x, x_dtype, tokens, r, experts, y, y_dtype, workspace, workspace_bytes, stream);
+}
+
+int64_t qmm_moe_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inner) {
+  if (tokens < 0 || tokens > qmm::kMoeMaxTokens || top_k < 1 || top_k > qmm::kMoeMaxTop ||
+      tokens * top_k > qmm::kMoeMaxSlots || !count_steps(hidden) || !count_steps(inner))
+    return -1;
+  return static_cast<int64_t>(qmm::moe_workspace_bytes(tokens, top_k, hidden, inner));
 }
 
 qmm_status qmm_get_device_error(qmm_stream_t stream) {

@@ -179,4 +179,42 @@ cudaError_t launch_paged_attention(const void *q, int64_t q_stride, int tokens, 
                                    int64_t out_stride, float *lse, void *workspace,
                                    size_t workspace_bytes, cudaStream_t stream);
 
+// block_quantize.cu
+cudaError_t launch_block_quantize(const void *x, int x_type, int64_t rows, int64_t cols,
+                                  bool square, uint8_t *codes, float *scales, cudaStream_t stream);
+
+// block_matmul.cu
+cudaError_t launch_block_matmul(const uint8_t *a, const float *a_scales, int M, const uint8_t *w,
+                                const float *w_scales, int N, int K, void *y, int y_type,
+                                cudaStream_t stream);
+
+// Routing of a row of logits (qmm_moe_route).
+struct Routing {
+  const void *logits;  // [tokens, experts] of type; null: ids and weights are given
+  int type;
+  int top_k;
+  bool sigmoid, normalize;
+  float scale;
+  const int *ids;  // [tokens, top_k], where logits is null
+  const float *weights;
+};
+
+// The experts' weights (qmm_experts): gate, up, down.
+struct ExpertWeights {
+  const uint32_t *w[3];
+  const void *scales[3], *biases[3];
+  int sb_type, experts, hidden, inner, group, bits;
+};
+constexpr int kMoeMaxTokens = 64, kMoeMaxSlots = 512, kMoeMaxExperts = 1024, kMoeMaxTop = 32;
+
+// moe_route.cu
+cudaError_t launch_moe_route(const Routing &r, int64_t tokens, int experts, int *ids,
+                             float *weights, cudaStream_t stream);
+
+// moe_experts.cu
+cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Routing &r,
+                               const ExpertWeights &w, void *y, int y_type, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner);
+
 }  // namespace qmm

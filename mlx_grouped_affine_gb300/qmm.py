@@ -18,7 +18,10 @@ EXPORTS = ("qmm_quantize", "qmm_dequantize", "qmm_quantized_matmul", "qmm_quanti
            "qmm_gather_qmm", "qmm_gemv_gate_up", "qmm_gemv_silu_gate", "qmm_rows",
            "qmm_last_error", "qmm_get_device_error", "qmm_set_launch_flags", "qmm_set_wait_limit",
            "qmm_promote_types", "qmm_dequantize_typed", "qmm_rows_typed", "qmm_quantize_typed",
-           "qmm_quantized_matmul_typed", "qmm_page_plan", "qmm_rope_append", "qmm_paged_attention")
+           "qmm_quantized_matmul_typed", "qmm_page_plan", "qmm_rope_append", "qmm_paged_attention",
+           "qmm_block_quantize", "qmm_block_matmul", "qmm_moe_route", "qmm_moe_experts",
+           "qmm_moe_layer", "qmm_moe_workspace_bytes")
+QMM_SCORE_SOFTMAX, QMM_SCORE_SIGMOID = 0, 1
 QMM_ATTENTION_WORKSPACE_BYTES = 64 << 20
 
 _lib = None
@@ -38,6 +41,22 @@ class PagedCache(ctypes.Structure):
         super().__init__(_ptr(k), _ptr(v), dtype, num_pages, page_size, heads, head_dim,
                          page_stride, head_stride, token_stride)
         self.pools = (k, v)
+
+
+class Experts(ctypes.Structure):
+    """qmm_experts: gate, up and down, each (words, scales, biases) of all experts (tensors
+    or addresses).  Keeps its tensors alive."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in (
+        "gate", "up", "down", "gate_scales", "up_scales", "down_scales", "gate_biases",
+        "up_biases", "down_biases")] +
+        [("sb_dtype", ctypes.c_int), ("experts", ctypes.c_int64), ("hidden", ctypes.c_int64),
+         ("inner", ctypes.c_int64), ("group_size", ctypes.c_int32), ("bits", ctypes.c_int32)])
+
+    def __init__(self, gate, up, down, sb_dtype, experts, hidden, inner, group_size, bits):
+        parts = (gate, up, down)
+        super().__init__(*[_ptr(p[i]) for i in range(3) for p in parts], sb_dtype, experts, hidden,
+                         inner, group_size, bits)
+        self.parts = parts
 
 
 class QmmError(RuntimeError):
@@ -73,7 +92,16 @@ def lib():
                                       P, I64, I, I, P, P, I64, C, P]
         L.qmm_paged_attention.argtypes = [P, I64, I64, I, C, P, I64, P, P, I64, I64, F, I, I64, P,
                                           I64, P, P, I64, P]
-        for f in ("qmm_page_plan", "qmm_rope_append", "qmm_paged_attention",
+        W = ctypes.POINTER(Experts)
+        L.qmm_block_quantize.argtypes = [P, I, I64, I64, I, P, P, P]
+        L.qmm_block_matmul.argtypes = [P, P, I64, P, P, I64, I64, P, I, P]
+        L.qmm_moe_route.argtypes = [P, I, I64, I64, I, I, I, F, P, P, P]
+        L.qmm_moe_experts.argtypes = [P, I, I64, P, P, I, W, P, I, P, I64, P]
+        L.qmm_moe_layer.argtypes = [P, I, I64, P, I, I, I, I, F, W, P, I, P, I64, P]
+        L.qmm_moe_workspace_bytes.argtypes = [I64, I, I64, I64]
+        L.qmm_moe_workspace_bytes.restype = I64
+        for f in ("qmm_block_quantize", "qmm_block_matmul", "qmm_moe_route", "qmm_moe_experts",
+                  "qmm_moe_layer", "qmm_page_plan", "qmm_rope_append", "qmm_paged_attention",
                   "qmm_quantize", "qmm_dequantize", "qmm_quantized_matmul", "qmm_quantized_matmul_noalloc",
                   "qmm_gather_qmm", "qmm_gemv_gate_up", "qmm_gemv_silu_gate", "qmm_rows",
                   "qmm_get_device_error", "qmm_promote_types", "qmm_dequantize_typed",
@@ -262,3 +290,46 @@ def qmm_paged_attention(q, q_stride, tokens, q_heads, cache, block_table, table_
                                      table_stride, _ptr(starts), _ptr(seq_lens), requests, max_new,
                                      scale, int(causal), window, _ptr(out), out_stride, _ptr(lse),
                                      _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qmm_block_quantize(x, x_dtype, rows, cols, block_rows, codes, scales, stream=None):
+    """e4m3 codes and fp32 scales of x, a scale per 128 columns of one row (block_rows 1)
+    or of 128 rows (block_rows 128)."""
+    _check(lib().qmm_block_quantize(_ptr(x), x_dtype, rows, cols, block_rows, _ptr(codes),
+                                    _ptr(scales), _stream(stream)))
+
+
+def qmm_block_matmul(a, a_scales, M, w, w_scales, N, K, y, y_dtype, stream=None):
+    """y = A . W^T of e4m3 codes with a scale per row and 128 columns (A) and per 128 x 128
+    block (W)."""
+    _check(lib().qmm_block_matmul(_ptr(a), _ptr(a_scales), M, _ptr(w), _ptr(w_scales), N, K,
+                                  _ptr(y), y_dtype, _stream(stream)))
+
+
+def qmm_moe_route(logits, dtype, tokens, experts, top_k, scoring, normalize, scale, ids, weights,
+                  stream=None):
+    """The top_k experts of each token (int32 ids, fp32 weights) from router logits."""
+    _check(lib().qmm_moe_route(_ptr(logits), dtype, tokens, experts, top_k, scoring,
+                               int(normalize), scale, _ptr(ids), _ptr(weights), _stream(stream)))
+
+
+def qmm_moe_experts(x, x_dtype, tokens, ids, weights, top_k, experts, y, y_dtype, workspace,
+                    workspace_bytes, stream=None):
+    """Gated feed-forward of each token's experts (an Experts), weighted and summed, for
+    the few tokens of a decode step."""
+    _check(lib().qmm_moe_experts(_ptr(x), x_dtype, tokens, _ptr(ids), _ptr(weights), top_k,
+                                 experts, _ptr(y), y_dtype, _ptr(workspace), workspace_bytes,
+                                 _stream(stream)))
+
+
+def qmm_moe_layer(x, x_dtype, tokens, logits, logits_dtype, top_k, scoring, normalize, scale,
+                  experts, y, y_dtype, workspace, workspace_bytes, stream=None):
+    """qmm_moe_route and qmm_moe_experts in one call."""
+    _check(lib().qmm_moe_layer(_ptr(x), x_dtype, tokens, _ptr(logits), logits_dtype, top_k,
+                               scoring, int(normalize), scale, experts, _ptr(y), y_dtype,
+                               _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qmm_moe_workspace_bytes(tokens, top_k, hidden, inner):
+    """Bytes of workspace of qmm_moe_experts and qmm_moe_layer (host-only; -1: bad sizes)."""
+    return int(lib().qmm_moe_workspace_bytes(tokens, top_k, hidden, inner))
