@@ -601,7 +601,7 @@ typedef struct {
     const void *gate_biases, *up_biases, *down_biases;
     qmm_dtype sb_dtype;
     int64_t experts;      /* 1 to 1024 */
-    int64_t hidden;       /* multiples of group_size, below 2^31 */
+    int64_t hidden;       /* multiples of group_size, at most 2^20 */
     int64_t inner;
     int32_t group_size, bits;
 } qmm_experts;

@@ -18,7 +18,8 @@ LIBRARY = os.path.join(HERE, "libqmm.so")
 SOURCES = ("api.cpp", "tensormap.cpp", "dequant.cu", "gemv.cu", "gemv_gather.cu", "gemv_f16.cu",
            "gemm_sm103.cu", "quantize.cu", "mm_f32.cu", "page_plan.cu", "rope_append.cu",
            "paged_attention.cu", "paged_tiles.cu", "paged_decode.cu", "paged_prefill.cu",
-           "block_quantize.cu", "block_matmul.cu", "moe_route.cu", "moe_experts.cu")
+           "block_quantize.cu", "block_matmul.cu", "moe_route.cu", "moe_experts.cu",
+           "moe_bits_1_2.cu", "moe_bits_3.cu", "moe_bits_4.cu", "moe_bits_5_6.cu", "moe_bits_8.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

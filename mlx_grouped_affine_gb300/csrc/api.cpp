@@ -281,10 +281,6 @@ qmm_status check_apart(const char *op, const Array *in, int inputs, const Array 
   return QMM_OK;
 }
 
-// Whether rows * cols elements and their bytes can be counted in 64 bits.
-bool small_enough(int64_t rows, int64_t cols) {
-  return rows == 0 || cols == 0 || rows <= (int64_t(1) << 58) / cols;
-}
 uint64_t type_bytes(qmm_dtype d) { return d == QMM_F32 ? 4 : 2; }
 int64_t blocks128(int64_t n) { return (n + 127) / 128; }
 
@@ -316,13 +312,11 @@ qmm_status check_experts(const char *op, const qmm_experts *e, qmm::ExpertWeight
   if (e->experts < 1 || e->experts > qmm::kMoeMaxExperts)
     return fail(QMM_ERR_INVALID_ARG, "%s: %lld experts, not in [1, %d]", op, (long long)e->experts,
                 qmm::kMoeMaxExperts);
-  if (!count_steps(e->hidden) || !count_steps(e->inner) || e->hidden < 1 || e->inner < 1 ||
-      e->hidden % e->group_size != 0 || e->inner % e->group_size != 0)
+  if (e->hidden < 1 || e->hidden > qmm::kMoeMaxSize || e->hidden % e->group_size != 0 || e->inner < 1 ||
+      e->inner > qmm::kMoeMaxSize || e->inner % e->group_size != 0)
     return fail(QMM_ERR_INVALID_ARG,
-                "%s: hidden (%lld) and inner (%lld) must be positive multiples of group size %d, below 2^31 - 1024",
+                "%s: hidden (%lld) and inner (%lld) must be positive multiples of group size %d, at most 2^20",
                 op, (long long)e->hidden, (long long)e->inner, e->group_size);
-  if (!small_enough(e->hidden * e->inner, 8 * e->experts))
-    return fail(QMM_ERR_INVALID_ARG, "%s: the experts are too large", op);
   const uint32_t *w[3] = {e->gate, e->up, e->down};
   const void *s[3] = {e->gate_scales, e->up_scales, e->down_scales};
   const void *b[3] = {e->gate_biases, e->up_biases, e->down_biases};
@@ -891,7 +885,8 @@ qmm_status qmm_moe_layer(const void *x, qmm_dtype x_dtype, int64_t tokens, const
 
 int64_t qmm_moe_workspace_bytes(int64_t tokens, int top_k, int64_t hidden, int64_t inner) {
   if (tokens < 0 || tokens > qmm::kMoeMaxTokens || top_k < 1 || top_k > qmm::kMoeMaxTop ||
-      tokens * top_k > qmm::kMoeMaxSlots || !count_steps(hidden) || !count_steps(inner))
+      tokens * top_k > qmm::kMoeMaxSlots || hidden < 0 || hidden > qmm::kMoeMaxSize || inner < 0 ||
+      inner > qmm::kMoeMaxSize)
     return -1;
   return static_cast<int64_t>(qmm::moe_workspace_bytes(tokens, top_k, hidden, inner));
 }

@@ -205,7 +205,8 @@ struct ExpertWeights {
   const void *scales[3], *biases[3];
   int sb_type, experts, hidden, inner, group, bits;
 };
-constexpr int kMoeMaxTokens = 64, kMoeMaxSlots = 512, kMoeMaxExperts = 1024, kMoeMaxTop = 32;
+constexpr int kMoeMaxTokens = 64, kMoeMaxSlots = 512, kMoeMaxExperts = 1024, kMoeMaxTop = 32,
+              kMoeMaxSize = 1 << 20;
 
 // moe_route.cu
 cudaError_t launch_moe_route(const Routing &r, int64_t tokens, int experts, int *ids,
