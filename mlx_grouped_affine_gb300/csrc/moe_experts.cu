@@ -35,6 +35,7 @@ cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Rout
   a.tokens = tokens;
   a.y = y;
   a.y_type = y_type;
+  a.wait_limit = wait_limit();
   a.x_plane = round128(n);
   a.x_planes = x_type == kTypeBF16 ? 1 : x_type == kTypeF16 ? 2 : 3;
   a.h = planes + 3 * a.x_plane;

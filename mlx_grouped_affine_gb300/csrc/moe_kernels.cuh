@@ -11,10 +11,12 @@
 // The weights that the routing asks for are streamed once; everything else (x, h, scales'
 // sectors) stays in L1 or L2.  Bound by memory, then by the instructions that spread codes
 // (9 per 8 codes of 4 bits).  A warp works on its own: 32 weight rows (two 16-row tiles of
-// the MMA, sharing the x operand) and a range of groups, whose codes each lane copies to
-// its own places in shared memory (cp.async, kDepth groups ahead), so that loads in flight
-// cost no registers and need no block barrier.  8 tokens fill the MMA's columns; 16 slots
-// of an expert are taken per pass over its weights.
+// the MMA, sharing the x operand) and a range of chunks of 128 or 256 columns.  A chunk's
+// codes come by TMA, a box of 16 rows per tile, into a ring of the warp's own, so that loads
+// in flight cost no registers and need no block barrier.  (Copies by the lanes themselves
+// touch eight rows an instruction and were held up at one cache line a cycle: 2500 cycles
+// for 2048 codes a warp.)  8 slots fill the MMA's columns; 16 slots of an expert are taken
+// per pass over its weights.
 #pragma once
 #include "moe_route.cuh"
 
@@ -38,48 +40,55 @@ struct MoeArgs {
   void *y;
   int y_type;
   unsigned *err;
+  uint32_t wait_limit;
 };
 
 // ------------------------------------------------------------- the plan ----
 // Which slots (token * top_k + place) go to which expert.  Every block works it out for
 // itself: that is cheaper than waiting for another kernel's answer.  A unit is an expert
-// with up to kMoePass of its slots; units are in order of experts, slots within them in
-// order of slots, so that all blocks agree.
+// with up to kMoePass of its slots; an expert's units follow one another, its slots are in
+// order, and experts come in the order of their first slots, so that all blocks agree.
 struct alignas(16) MoePlan {
   int units;
-  int table[kMoeMaxExperts];        // slots of an expert; then first slot | first unit << 16
+  int table[kMoeMaxExperts];                   // slots of an expert; then its first in `list` | first unit << 16
   short unit_expert[kMoeMaxSlots];
-  short unit_first[kMoeMaxSlots];   // in list
+  short unit_first[kMoeMaxSlots];              // in `list`
   short unit_count[kMoeMaxSlots];
-  short list[kMoeMaxSlots];         // slots by expert
-  short slot_expert[kMoeMaxSlots];  // -1: no part in y
-  short slot_place[kMoeMaxSlots];   // among its expert's slots
+  short list[kMoeMaxSlots];                    // slots, unit by unit
+  short slot_expert[kMoeMaxSlots];             // -1: no part in y
+  short slot_place[kMoeMaxSlots];              // among its expert's slots
   float slot_weight[kMoeMaxSlots];
 };
 
 template <int NV>
-__device__ __noinline__ void route_token(const Routing &r, int experts, int t, int lane, int &id, float &weight) {
-  route_row<NV>(r, experts, t, lane, id, weight);
+__device__ __noinline__ void route_token(Routing r, int experts, int t, int lane, int *id, float *weight) {
+  int i;
+  float w;
+  route_row<NV>(r, experts, t, lane, i, w);
+  *id = i;
+  *weight = w;
 }
 
-static __device__ __noinline__ void make_plan(const MoeArgs &a, MoePlan &p) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = a.route.top_k;
-  for (int e = threadIdx.x; e < a.w.experts; e += kMoeThreads) p.table[e] = 0;
-  for (int t = warp; t < a.tokens; t += kMoeWarps) {
+// By value: what is passed by reference would be read through memory again and again.
+static __device__ __noinline__ void make_plan(const Routing r, const int tokens, const int experts, unsigned *err,
+                                              MoePlan &p) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = r.top_k;
+  for (int e = threadIdx.x; e < experts; e += kMoeThreads) p.table[e] = 0;
+  for (int t = warp; t < tokens; t += kMoeWarps) {
     int id = -1;
     float weight = 0.0f;
-    if (!a.route.logits) {
-      if (lane < top) id = a.route.ids[t * top + lane], weight = a.route.weights[t * top + lane];
-    } else if (a.w.experts <= 128) {
-      route_token<4>(a.route, a.w.experts, t, lane, id, weight);
-    } else if (a.w.experts <= 256) {
-      route_token<8>(a.route, a.w.experts, t, lane, id, weight);
+    if (!r.logits) {
+      if (lane < top) id = r.ids[t * top + lane], weight = r.weights[t * top + lane];
+    } else if (experts <= 128) {
+      route_row<4>(r, experts, t, lane, id, weight);
+    } else if (experts <= 256) {
+      route_row<8>(r, experts, t, lane, id, weight);
     } else {
-      route_token<32>(a.route, a.w.experts, t, lane, id, weight);
+      route_token<32>(r, experts, t, lane, &id, &weight);
     }
     if (lane < top) {
-      if (id < 0 || id >= a.w.experts) {
-        if (blockIdx.x == 0) atomicOr(a.err, kErrIndexBit);
+      if (id < 0 || id >= experts) {
+        if (blockIdx.x == 0) atomicOr(err, kErrIndexBit);
         id = -1;
       }
       if (weight == 0.0f) id = -1;
@@ -88,7 +97,7 @@ static __device__ __noinline__ void make_plan(const MoeArgs &a, MoePlan &p) {
     }
   }
   __syncthreads();
-  const int slots = a.tokens * top;
+  const int slots = tokens * top;
   if (warp == 0) {
     for (int s0 = 0; s0 < slots; s0 += 32) {  // places: slots of the same expert before
       const int s = s0 + lane, e = s < slots ? p.slot_expert[s] : -1;
@@ -102,8 +111,9 @@ static __device__ __noinline__ void make_plan(const MoeArgs &a, MoePlan &p) {
       __syncwarp();
     }
     int before = 0;  // slots | units << 16 of the experts before
-    for (int e0 = 0; e0 < a.w.experts; e0 += 32) {
-      const int e = e0 + lane, n = e < a.w.experts ? p.table[e] : 0;
+    for (int s0 = 0; s0 < slots; s0 += 32) {  // units, at each expert's first slot
+      const int s = s0 + lane, e = s < slots ? p.slot_expert[s] : -1;
+      const int n = e >= 0 && p.slot_place[s] == 0 ? p.table[e] : 0;
       const int units = (n + kMoePass - 1) / kMoePass, own = n | units << 16;
       int sum = own;
 #pragma unroll
@@ -111,11 +121,12 @@ static __device__ __noinline__ void make_plan(const MoeArgs &a, MoePlan &p) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
         if (lane >= d) sum += o;
       }
-      const int at = before + sum - own, first = at & 0xFFFF, unit = at >> 16;
+      const int at = before + sum - own, unit = at >> 16;
+      __syncwarp();
       if (n > 0) p.table[e] = at;
       for (int i = 0; i < units; ++i) {
         p.unit_expert[unit + i] = static_cast<short>(e);
-        p.unit_first[unit + i] = static_cast<short>(first + i * kMoePass);
+        p.unit_first[unit + i] = static_cast<short>((at & 0xFFFF) + i * kMoePass);
         p.unit_count[unit + i] = static_cast<short>(min(kMoePass, n - i * kMoePass));
       }
       before += __shfl_sync(0xFFFFFFFFu, sum, 31);
@@ -139,7 +150,6 @@ struct Run {
   static constexpr int kCodes = G / 4;
   static constexpr int kBits = kCodes * BITS;
   static constexpr bool kWhole = kBits % 32 == 0;  // whole words, else shifted into place
-  static constexpr int kGroupWords = G * BITS / 32;
   static constexpr int words() {
     int n = 0;
     for (int t = 0; t < 4; ++t) {
@@ -149,15 +159,27 @@ struct Run {
     return n;
   }
   static constexpr int kWords = words();
-  // A copy's words: as many as the run's alignment (its own size) allows.
+  // Words read at once: as many as the run's alignment (its own size) allows.
   static constexpr int kPiece = !kWhole ? 1 : kWords % 4 == 0 ? 4 : kWords % 2 == 0 ? 2 : 1;
-  static constexpr int kPieces = kWords / kPiece;
   // Codes j and j + half of a word share a register (one mask for both) where a word holds
   // whole codes; otherwise neighbours do.
   static constexpr bool kSplit = kWhole && (BITS == 2 || BITS == 4 || BITS == 8);
   static constexpr int kSub = kCodes < 16 ? kCodes : 16;  // codes spread at a time
-  static constexpr int kDepth = kWords <= 2 ? 6 : kWords <= 4 ? 4 : kWords <= 6 ? 3 : 2;
-  static constexpr int kStageBytes = 32 * (16 * kWords + 8);  // a warp's group: codes, then scales
+  // A chunk: what a warp's ring holds per stage of each row, at most 128 bytes.
+  static constexpr int kChunk = BITS <= 4 ? 256 : 128;
+  static constexpr int kSteps = kChunk / G;
+  static constexpr int kRowBytes = kChunk * BITS / 8;
+  static constexpr int kStageBytes = 2 * 16 * kRowBytes;
+  static constexpr int kDepth = kStageBytes >= 4096 ? 2 : kStageBytes >= 3072 ? 3 : 4;
+  static constexpr CUtensorMapSwizzle kSwizzle = kRowBytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                 : kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                                   : CU_TENSOR_MAP_SWIZZLE_NONE;
+  // Place of byte `off` of a box: TMA swaps 16-byte units so that rows start in other banks.
+  __device__ static __forceinline__ uint32_t place(uint32_t off) {
+    if constexpr (kRowBytes == 128) return off ^ (off >> 3 & 0x70u);
+    if constexpr (kRowBytes == 64) return off ^ (off >> 3 & 0x30u);
+    return off;
+  }
 };
 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
@@ -168,8 +190,9 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
 
 // Codes as bf16 pairs, each code * 2^-6.  A bf16 pattern P <= 0xFF is worth P * 2^-133, so
 // a code at bit o of a half reads as c * 2^(o - 133), and times 2^(127 - o) it is exact and
-// normal.  (kCodeScale undoes the 2^-6.)
-constexpr float kCodeScale = 64.0f;
+// normal.  sum(x) is taken times 2^-6 too, and the sums times 2^6 at the end.
+constexpr float kUnscale = 64.0f;
+constexpr uint32_t kOnes = 0x3C803C80u;  // 2^-6
 template <int BITS, int G>
 __device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
   using R = Run<BITS, G>;
@@ -226,67 +249,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 
 // ------------------------------------------------------------- the ring ----
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32_t bytes = BYTES) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(bytes)
-                 : "memory");
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
 }
 
-// Where a lane's codes, scale and bias of a unit's rows are: tile 0 and 1 at rows g (and 8
-// rows on, g + 8), of two matrices or of one.
-struct RowPtrs {
-  const char *w[2];
-  const char *s, *b;  // of the row whose scale this lane copies: tile t / 2, half t % 2
-};
-
-template <int BITS, int G>
-struct Ring {
-  using R = Run<BITS, G>;
-  uint32_t base;        // this warp's stages
-  int64_t half_bytes;   // 8 rows of codes
-  int sb_bytes;
-  int lane;
-
-  // The copies of group j of the rows, as one commit group (empty if !live).
-  __device__ __forceinline__ void issue(int stage, const RowPtrs &p, int j, bool live) const {
-    if (live) {
-      const uint32_t st = base + stage * R::kStageBytes;
-      const int t = lane % 4;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const char *src = p.w[q / 2] + (q % 2) * half_bytes + static_cast<int64_t>(j) * (R::kGroupWords * 4);
-        if constexpr (R::kWhole) {
-          src += t * (R::kWords * 4);
-#pragma unroll
-          for (int i = 0; i < R::kPieces; ++i)
-            copy_async<4 * R::kPiece>(st + ((q * R::kPieces + i) * 32 + lane) * (4 * R::kPiece), src + 4 * R::kPiece * i);
-        } else {
-          const int first = t * R::kBits / 32;
-#pragma unroll
-          for (int i = 0; i < R::kWords; ++i) {
-            const bool in = first + i < R::kGroupWords;
-            copy_async<4>(st + ((q * R::kWords + i) * 32 + lane) * 4, src + 4 * (in ? first + i : 0), in ? 4u : 0u);
-          }
-        }
-      }
-      // scale and bias: the aligned word that holds them
-      const uint32_t sb = st + 32 * 16 * R::kWords + ((t * 8 + lane / 4) * 8);
-      const int64_t off = static_cast<int64_t>(j) * sb_bytes;
-      copy_async<4>(sb, reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(p.s + off) & ~uintptr_t(3)));
-      copy_async<4>(sb + 4, reinterpret_cast<const char *>(reinterpret_cast<uintptr_t>(p.b + off) & ~uintptr_t(3)));
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-};
-
-__device__ __forceinline__ uint2 lds2(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t *v) {
   if constexpr (N == 4)
@@ -297,6 +266,49 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t *v) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a));
 }
 
+// Scales and biases of a chunk, of the row that this lane stands for: row g + 8 (t % 2) of
+// tile t / 2 for lane 4 g + t.  16-bit types are kept in pairs.
+template <int STEPS>
+struct Scales {
+  uint32_t s[STEPS], b[STEPS];
+  __device__ __forceinline__ void load(const char *ps, const char *pb, int type, int64_t at, int j0, int groups) {
+    // (rows begin at multiples of `groups`, so whole chunks are aligned where it is one of STEPS)
+    if (type == kTypeF32) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const bool in = j0 + i < groups;
+        s[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(ps) + at + j0 + i) : 0u;
+        b[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(pb) + at + j0 + i) : 0u;
+      }
+      return;
+    }
+    const uint16_t *hs = reinterpret_cast<const uint16_t *>(ps) + at + j0, *hb = reinterpret_cast<const uint16_t *>(pb) + at + j0;
+    if (STEPS > 1 && groups % STEPS == 0) {
+      if constexpr (STEPS == 2) {
+        s[0] = __ldg(reinterpret_cast<const uint32_t *>(hs));
+        b[0] = __ldg(reinterpret_cast<const uint32_t *>(hb));
+      } else if constexpr (STEPS == 4) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(hs)), v = __ldg(reinterpret_cast<const uint2 *>(hb));
+        s[0] = u.x, s[1] = u.y, b[0] = v.x, b[1] = v.y;
+      } else if constexpr (STEPS == 8) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(hs)), v = __ldg(reinterpret_cast<const uint4 *>(hb));
+        s[0] = u.x, s[1] = u.y, s[2] = u.z, s[3] = u.w;
+        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; i += 2) {
+      uint32_t h[4] = {};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (i + k < STEPS && j0 + i + k < groups) h[k] = __ldg(hs + i + k), h[2 + k] = __ldg(hb + i + k);
+      s[i / 2] = h[0] | h[1] << 16;
+      b[i / 2] = h[2] | h[3] << 16;
+    }
+  }
+};
+
 // The MMA's columns: rows of x (or h) of up to 16 slots, lane 4 g + t reading column g.
 struct Columns {
   const uint16_t *x[2];  // this lane's column of each half of the pass, at its run
@@ -306,83 +318,175 @@ struct Columns {
   int64_t plane;
 };
 
-// One group of 32 rows: acc[half][4 tile + 2 row half + column] += s sum(c x) + b sum(x).
+// One chunk of 32 rows: acc[half][4 tile + 2 row half + column] += s sum(c x) + b sum(x),
+// over its groups j0 .. (below `groups`).
 template <int BITS, int G>
-__device__ __forceinline__ void consume(const Ring<BITS, G> &ring, int stage, const Columns &c, int j, int sb_type,
-                                        uint32_t odd, float (&acc)[2][8]) {
+__device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns &c, int j0, int groups,
+                                        const Scales<Run<BITS, G>::kSteps> &sc, int sb_type, float (&acc)[2][8]) {
   using R = Run<BITS, G>;
-  const uint32_t st = ring.base + stage * R::kStageBytes;
-  const int lane = ring.lane, t = lane % 4;
-  float part[2][2][4] = {}, ones[2][4] = {};
-  uint32_t v[4][R::kWords + 1];
+  const int t = lane % 4;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int step = 0; step < R::kSteps; ++step) {
+    if (j0 + step >= groups) break;
+    float part[2][2][4] = {}, ones[2][4] = {};
+    uint32_t v[4][R::kWords + 1];
 #pragma unroll
-    for (int i = 0; i < R::kPieces; ++i)
-      lds_words<R::kPiece>(st + ((q * R::kPieces + i) * 32 + lane) * (4 * R::kPiece), &v[q][R::kPiece * i]);
-    v[q][R::kWords] = 0;
-    if constexpr (!R::kWhole) {
-      const uint32_t sh = t * R::kBits % 32;
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t box = stage + (q / 2) * (16 * R::kRowBytes);
+      const uint32_t at = (lane / 4 + (q % 2) * 8) * R::kRowBytes + step * (G * BITS / 8) + t * R::kBits / 32 * 4;
 #pragma unroll
-      for (int i = 0; i < R::kWords; ++i) v[q][i] = __funnelshift_r(v[q][i], v[q][i + 1], sh);
+      for (int i = 0; i < R::kWords; i += R::kPiece) lds_words<R::kPiece>(box + R::place(at + 4 * i), &v[q][i]);
+      v[q][R::kWords] = 0;
+      if constexpr (!R::kWhole) {
+        const uint32_t sh = t * R::kBits % 32;
+#pragma unroll
+        for (int i = 0; i < R::kWords; ++i) v[q][i] = __funnelshift_r(v[q][i], v[q][i + 1], sh);
+      }
     }
-  }
 #pragma unroll
-  for (int sub = 0; sub < R::kCodes / R::kSub; ++sub) {
-    uint32_t code[4][R::kSub / 2];
+    for (int sub = 0; sub < R::kCodes / R::kSub; ++sub) {
+      uint32_t code[4][R::kSub / 2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, code[q]);
+      for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, code[q]);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half < c.halves) {
-        for (int plane = c.planes - 1; plane >= 0; --plane) {  // the smallest parts first
-          uint32_t x[R::kSub / 2];
-          if (c.live[half]) {
-            pair_x<BITS, G>(c.x[half] + plane * c.plane + static_cast<int64_t>(j) * G + sub * R::kSub, x);
-          } else {
+      for (int half = 0; half < 2; ++half) {
+        if (half < c.halves) {
+          for (int plane = c.planes - 1; plane >= 0; --plane) {  // the smallest parts first
+            uint32_t x[R::kSub / 2];
+            if (c.live[half]) {
+              pair_x<BITS, G>(c.x[half] + plane * c.plane + (j0 + step) * G + sub * R::kSub, x);
+            } else {
 #pragma unroll
-            for (int i = 0; i < R::kSub / 2; ++i) x[i] = 0;
-          }
+              for (int i = 0; i < R::kSub / 2; ++i) x[i] = 0;
+            }
 #pragma unroll
-          for (int m = 0; m < R::kSub / 4; ++m) {
+            for (int m = 0; m < R::kSub / 4; ++m) {
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile)
-              mma_bf16(part[half][tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
-                       code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
-            constexpr uint32_t kOne = 0x3F803F80u;
-            mma_bf16(ones[half], kOne, kOne, kOne, kOne, x[2 * m], x[2 * m + 1]);
+              for (int tile = 0; tile < 2; ++tile)
+                mma_bf16(part[half][tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
+                         code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
+              mma_bf16(ones[half], kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
+            }
           }
         }
       }
     }
-  }
+    const uint32_t both = prmt(sc.s[step / 2], sc.b[step / 2], step & 1 ? 0x7632u : 0x5410u);  // 16-bit types
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint2 sb = lds2(st + 32 * 16 * R::kWords + (q * 8 + lane / 4) * 8);
-    float s, b;
-    if (sb_type == kTypeBF16) {
-      s = __uint_as_float(odd ? sb.x & 0xFFFF0000u : sb.x << 16);
-      b = __uint_as_float(odd ? sb.y & 0xFFFF0000u : sb.y << 16);
-    } else if (sb_type == kTypeF16) {
-      s = ElemF16::to_f32(odd ? sb.x >> 16 : sb.x & 0xFFFFu);
-      b = ElemF16::to_f32(odd ? sb.y >> 16 : sb.y & 0xFFFFu);
-    } else {
-      s = __uint_as_float(sb.x);
-      b = __uint_as_float(sb.y);
-    }
-    s *= kCodeScale;
+    for (int q = 0; q < 4; ++q) {
+      float s, b;
+      const int from = (lane & ~3) | q;
+      if (sb_type == kTypeF32) {
+        s = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.s[step], from));
+        b = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.b[step], from));
+      } else {
+        const uint32_t u = __shfl_sync(0xFFFFFFFFu, both, from);
+        if (sb_type == kTypeBF16) {
+          s = __uint_as_float(u << 16);
+          b = __uint_as_float(u & 0xFFFF0000u);
+        } else {
+          s = ElemF16::to_f32(u & 0xFFFFu);
+          b = ElemF16::to_f32(u >> 16);
+        }
+      }
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half < c.halves) {
+      for (int half = 0; half < 2; ++half) {
+        if (half < c.halves) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float &y = acc[half][2 * q + i];
-          y = fmaf(s, part[half][q / 2][2 * (q % 2) + i], fmaf(b, ones[half][i], y));
+          for (int i = 0; i < 2; ++i) {
+            float &y = acc[half][2 * q + i];
+            y = fmaf(s, part[half][q / 2][2 * (q % 2) + i], fmaf(b, ones[half][i], y));
+          }
         }
       }
     }
   }
 }
+
+// A weight whose boxes are loaded.  Rows that are no multiple of 16 bytes long (hidden or
+// inner times bits no multiple of 128, which 4 and 8 bits never are) are out of TMA's reach:
+// the warp then copies its chunks itself, as it comes to them.
+struct Source {
+  const CUtensorMap *map;
+  const uint32_t *w;  // where the warp copies, else null
+  int words;          // of a row
+};
+
+// A warp's ring of chunks.
+template <int BITS, int G>
+struct Ring {
+  using R = Run<BITS, G>;
+  uint32_t base;
+  uint64_t *bars;
+  int lane, in, out;
+  uint32_t parity;   // of the stage to read next
+  int flying;        // chunks issued and not yet waited for
+  bool dead;         // a wait ran out: nothing more is issued or read
+
+  __device__ __forceinline__ void init(unsigned char *stages, uint64_t *barriers, int warp, int lane_) {
+    base = smem_u32(stages) + warp * (R::kDepth * R::kStageBytes);
+    bars = barriers + warp * R::kDepth;
+    lane = lane_;
+    in = out = flying = 0;
+    parity = 0;
+    dead = false;
+    if (lane == 0) {
+      for (int i = 0; i < R::kDepth; ++i) mbar_init(&bars[i], 1);
+      asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncwarp();
+  }
+  // Chunk `chunk` of the 16 rows at y0 of map0 and at y1 of map1.
+  __device__ __forceinline__ void issue(const Source &s0, const Source &s1, int y0, int y1, int chunk) {
+    const uint32_t st = base + in * R::kStageBytes;
+    constexpr int kRowWords = R::kRowBytes / 4;
+    if (BITS != 4 && BITS != 8 && s0.w) {
+      for (int i = lane; i < 32 * kRowWords; i += 32) {
+        const int row = i / kRowWords, at = i - row * kRowWords, word = chunk * kRowWords + at;
+        const uint32_t *p = (row < 16 ? s0.w : s1.w) + static_cast<int64_t>((row < 16 ? y0 : y1) + row % 16) * s0.words;
+        const uint32_t v = word < s0.words ? __ldg(p + word) : 0u;
+        const uint32_t to = st + row / 16 * (R::kStageBytes / 2) + R::place((row % 16) * R::kRowBytes + 4 * at);
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+      }
+    } else if (lane == 0) {
+      mbar_expect_tx(&bars[in], R::kStageBytes);
+      load_box(st, s0.map, chunk * kRowWords, y0, &bars[in]);
+      load_box(st + R::kStageBytes / 2, s1.map, chunk * kRowWords, y1, &bars[in]);
+    }
+    in = in + 1 == R::kDepth ? 0 : in + 1;
+    ++flying;
+  }
+  // Waits for the oldest chunk; its stage, or 0 if the wait ran out.
+  __device__ __forceinline__ uint32_t wait(bool copied, uint32_t limit, unsigned *err) {
+    uint32_t polls = 0;
+    if (BITS != 4 && BITS != 8 && copied) {
+      __syncwarp();
+      return base + out * R::kStageBytes;
+    }
+    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity))) {
+      if (++polls >= limit) {
+        if (lane == 0) atomicOr(err, kErrTimeoutBit);
+        dead = true;
+        return 0;
+      }
+    }
+    return base + out * R::kStageBytes;
+  }
+  // The stage may be filled again.
+  __device__ __forceinline__ void done() {
+    __syncwarp();
+    out = out + 1 == R::kDepth ? 0 : out + 1;
+    if (out == 0) parity ^= 1;
+    --flying;
+  }
+  // No copy may land after the block has left.
+  __device__ __forceinline__ void drain(bool copied, uint32_t limit, unsigned *err) {
+    while (flying > 0) {
+      wait(copied, limit, err);
+      done();
+    }
+  }
+};
 
 // The bf16 planes of v: its leading bits cut off 8 at a time (three hold all 24).  What is
 // not finite stays in the first.
@@ -397,106 +501,121 @@ __device__ __forceinline__ void store_planes(uint16_t *p, int64_t plane, int pla
 
 // -------------------------------------------------------- gate and up ----
 
-struct alignas(16) GateUpShared {
+struct alignas(1024) GateUpShared {  // the ring follows: swizzled boxes want 1024
   MoePlan plan;
   alignas(16) float sums[kMoeWarps][32][kMoePass];
+  alignas(16) uint64_t bars[kMoeWarps * 4];
 };
-static_assert(sizeof(GateUpShared) % 16 == 0, "the ring's copies are 16 bytes wide");
+struct MoeMaps {
+  CUtensorMap gate, up, down;
+};
 
-// h = silu(gate x) * (up x).  An item is a unit and 16 rows of gate and of up, its groups
-// split over the block's warps and joined through shared memory.
+// h = silu(gate x) * (up x).  An item is a unit and 8 / ksplit tiles of 16 rows of gate and
+// of up; ksplit warps share a tile's chunks and join their sums through shared memory.
 template <int BITS, int G>
-__global__ void __launch_bounds__(kMoeThreads, 2) gate_up_kernel(const __grid_constant__ MoeArgs a) {
+__global__ void __launch_bounds__(kMoeThreads, 2)
+gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps maps, int ksplit) {
   using R = Run<BITS, G>;
-  extern __shared__ __align__(128) unsigned char raw[];
+  extern __shared__ __align__(1024) unsigned char raw[];
   GateUpShared &sh = *reinterpret_cast<GateUpShared *>(raw);
-  griddep_launch_dependents();
-  make_plan(a, sh.plan);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int tiles = a.w.inner / 16, groups = a.w.hidden / G;
-  const int items = sh.plan.units * tiles;
-  const int j0 = groups * warp / kMoeWarps, j1 = groups * (warp + 1) / kMoeWarps;
-  const int64_t row_bytes = static_cast<int64_t>(groups) * (R::kGroupWords * 4);
   Ring<BITS, G> ring;
-  ring.base = smem_u32(raw) + sizeof(GateUpShared) + warp * (R::kDepth * R::kStageBytes);
-  ring.half_bytes = 8 * row_bytes;
-  ring.sb_bytes = a.w.sb_type == kTypeF32 ? 4 : 2;
-  ring.lane = lane;
+  ring.init(raw + sizeof(GateUpShared), sh.bars, warp, lane);
+  griddep_launch_dependents();
+  make_plan(a.route, a.tokens, a.w.experts, a.err, sh.plan);
+  const int tiles = a.w.inner / 16, groups = a.w.hidden / G, chunks = (a.w.hidden + R::kChunk - 1) / R::kChunk;
+  const int wide = kMoeWarps / ksplit, parts = (tiles + wide - 1) / wide;
+  const int items = sh.plan.units * parts;
+  const int own = warp / ksplit, k = warp % ksplit;
+  const int c0 = chunks * k / ksplit, c1 = chunks * (k + 1) / ksplit;
+  const char *const scales = static_cast<const char *>(t < 2 ? a.w.scales[0] : a.w.scales[1]);
+  const char *const biases = static_cast<const char *>(t < 2 ? a.w.biases[0] : a.w.biases[1]);
 
-  RowPtrs p;
-  int load_item = blockIdx.x, load_j = j0;
-  auto point = [&](int item) {
-    const int unit = item / tiles, row0 = (item - unit * tiles) * 16;
-    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.inner + row0 + g;
-    p.w[0] = reinterpret_cast<const char *>(a.w.w[0]) + row * row_bytes;
-    p.w[1] = reinterpret_cast<const char *>(a.w.w[1]) + row * row_bytes;
-    const int64_t at = (row + 8 * (t % 2)) * groups * ring.sb_bytes;
-    p.s = static_cast<const char *>(a.w.scales[t / 2]) + at;
-    p.b = static_cast<const char *>(a.w.biases[t / 2]) + at;
+  const bool copied = static_cast<int64_t>(a.w.hidden) * BITS % 128 != 0;
+  const Source gate{&maps.gate, copied ? a.w.w[0] : nullptr, a.w.hidden / 32 * BITS};
+  const Source up{&maps.up, copied ? a.w.w[1] : nullptr, a.w.hidden / 32 * BITS};
+
+  // What is loaded next: a chunk of an item in which this warp has a tile.
+  int load_item = blockIdx.x, load_chunk = c0, load_row = 0;
+  auto settle = [&]() {
+    for (; load_item < items; load_item += gridDim.x) {
+      const int unit = load_item / parts, tile = (load_item - unit * parts) * wide + own;
+      if (tile < tiles) {
+        load_row = sh.plan.unit_expert[unit] * a.w.inner + tile * 16;
+        return;
+      }
+    }
   };
-  int stage_in = 0, stage_out = 0;
+  Scales<R::kSteps> next;
   auto load_next = [&]() {
-    const bool live = j0 < j1 && load_item < items;
-    if (live && load_j == j0) point(load_item);
-    ring.issue(stage_in, p, load_j, live);
-    stage_in = stage_in + 1 == R::kDepth ? 0 : stage_in + 1;
-    if (live && ++load_j == j1) load_j = j0, load_item += gridDim.x;
+    if (load_item >= items || ring.dead || c0 == c1) return;
+    ring.issue(gate, up, load_row, load_row, load_chunk);
+    if (++load_chunk == c1) load_chunk = c0, load_item += gridDim.x, settle();
   };
-  for (int i = 0; i < R::kDepth - 1; ++i) load_next();
+  settle();
+  for (int i = 0; i < R::kDepth; ++i) load_next();
 
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int unit = item / tiles, row0 = (item - unit * tiles) * 16;
-    const int count = sh.plan.unit_count[unit], first = sh.plan.unit_first[unit];
-    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.inner + row0 + g;
-    const uint32_t row_odd = static_cast<uint32_t>(row * groups);
-    Columns c;
-    c.halves = count > 8 ? 2 : 1;
-    c.planes = a.x_planes;
-    c.plane = a.x_plane;
+    const int unit = item / parts, tile0 = (item - unit * parts) * wide, tile = tile0 + own;
+    const int count = sh.plan.unit_count[unit];
+    const short *slots = &sh.plan.list[sh.plan.unit_first[unit]];
+    if (tile < tiles) {
+      const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.inner + tile * 16 + g + 8 * (t % 2);
+      Columns c;
+      c.halves = count > 8 ? 2 : 1;
+      c.planes = a.x_planes;
+      c.plane = a.x_plane;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      c.live[half] = 8 * half + g < count;
-      const int token = c.live[half] ? sh.plan.list[first + 8 * half + g] / a.route.top_k : 0;
-      c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
+      for (int half = 0; half < 2; ++half) {
+        c.live[half] = 8 * half + g < count;
+        const int token = c.live[half] ? slots[8 * half + g] / a.route.top_k : 0;
+        c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
+      }
+      float acc[2][8] = {};
+      if (c0 < c1) next.load(scales, biases, a.w.sb_type, row * groups, c0 * R::kSteps, groups);
+      for (int chunk = c0; chunk < c1 && !ring.dead; ++chunk) {
+        const Scales<R::kSteps> sc = next;
+        if (chunk + 1 < c1) next.load(scales, biases, a.w.sb_type, row * groups, (chunk + 1) * R::kSteps, groups);
+        const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
+        if (stage) {
+          consume<BITS, G>(stage, lane, c, chunk * R::kSteps, groups, sc, a.w.sb_type, acc);
+          ring.done();
+          load_next();
+        }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        if (half < c.halves)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float2 *>(&sh.sums[warp][(q / 2) * 16 + (q % 2) * 8 + g][half * 8 + 2 * t]) =
+                make_float2(acc[half][2 * q], acc[half][2 * q + 1]);
     }
-    float acc[2][8] = {};
-    for (int j = j0; j < j1; ++j) {
-      load_next();
-      asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
-      __syncwarp();
-      consume<BITS, G>(ring, stage_out, c, j, a.w.sb_type, (row_odd + j) & 1u, acc);
-      stage_out = stage_out + 1 == R::kDepth ? 0 : stage_out + 1;
-      __syncwarp();  // (scales are read across lanes: before the stage is filled again)
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-      if (half < c.halves)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<float2 *>(&sh.sums[warp][(q / 2) * 16 + (q % 2) * 8 + g][half * 8 + 2 * t]) =
-              make_float2(acc[half][2 * q], acc[half][2 * q + 1]);
     __syncthreads();
     const int r = threadIdx.x % 16;
-    for (int k = threadIdx.x / 16; k < count; k += kMoeThreads / 16) {
+    for (int i = threadIdx.x / 16; i < count * wide; i += kMoeThreads / 16) {
+      const int place = i / wide, of = i % wide;
+      if (tile0 + of >= tiles) continue;
       float gate = 0.0f, up = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kMoeWarps; ++i) gate += sh.sums[i][r][k], up += sh.sums[i][16 + r][k];
+      for (int w = of * ksplit; w < (of + 1) * ksplit; ++w)
+        gate += sh.sums[w][r][place], up += sh.sums[w][16 + r][place];
+      gate *= kUnscale, up *= kUnscale;
       const float h = gate / (1.0f + expf(-gate)) * up;
-      store_planes(a.h + static_cast<int64_t>(sh.plan.list[first + k]) * a.w.inner + row0 + r, a.h_plane, a.h_planes, h);
+      store_planes(a.h + static_cast<int64_t>(slots[place]) * a.w.inner + (tile0 + of) * 16 + r, a.h_plane, a.h_planes, h);
     }
     __syncthreads();  // before the next item's sums
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  ring.drain(copied, a.wait_limit, a.err);
 }
 
 // ---------------------------------------------------------------- down ----
 
-struct alignas(16) DownShared {
+struct alignas(1024) DownShared {  // then the ring, then z: float [slots][32]
   MoePlan plan;
   alignas(16) float heads[kMoeWarps][kMoePass][32];
-  // then z: float [slots][32], then the ring
+  alignas(16) uint64_t bars[kMoeWarps * 4];
+  unsigned char unit_from[kMoeMaxSlots], unit_to[kMoeMaxSlots];
 };
-static_assert(sizeof(DownShared) % 16 == 0, "the ring's copies are 16 bytes wide");
 
 __device__ __forceinline__ float remote_f32(uint32_t addr, uint32_t rank) {
   uint32_t far;
@@ -510,61 +629,63 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // y = sum over a token's slots of weight * (down h).  A cluster takes 32 rows of every
-// unit: the steps (unit, group), in order, are cut evenly over the cluster's warps, so a
-// warp's first unit may have begun in another warp.  Sums from a unit's first group on go
+// unit: the steps (unit, chunk), in order, are cut evenly over the cluster's warps, so a
+// warp's first unit may have begun in another warp.  Sums from a unit's first chunk on go
 // to z, those of a unit that began earlier to the warp's head; after the cluster's barrier
 // its blocks add them up, token by token, in a fixed order.
 template <int BITS, int G>
-__global__ void __launch_bounds__(kMoeThreads, 2) down_kernel(const __grid_constant__ MoeArgs a, int cluster) {
+__global__ void __launch_bounds__(kMoeThreads, 2)
+down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps maps, int cluster) {
   using R = Run<BITS, G>;
-  extern __shared__ __align__(128) unsigned char raw[];
+  extern __shared__ __align__(1024) unsigned char raw[];
   DownShared &sh = *reinterpret_cast<DownShared *>(raw);
-  float *z = reinterpret_cast<float *>(raw + sizeof(DownShared));
-  const int slots = a.tokens * a.route.top_k;
-  make_plan(a, sh.plan);
+  float *z = reinterpret_cast<float *>(raw + sizeof(DownShared) + kMoeWarps * R::kDepth * R::kStageBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * 32;
-  const int groups = a.w.inner / G, warps = cluster * kMoeWarps;
-  const int total = sh.plan.units * groups;  // at most 2^24: sizes are at most 2^20
-  auto begin_of = [&](int w) { return total * w / warps; };
-  const int step0 = begin_of(rank * kMoeWarps + warp), step1 = begin_of(rank * kMoeWarps + warp + 1);
-  const int64_t row_bytes = static_cast<int64_t>(groups) * (R::kGroupWords * 4);
   Ring<BITS, G> ring;
-  ring.base = smem_u32(z + slots * 32) + warp * (R::kDepth * R::kStageBytes);
-  ring.half_bytes = 8 * row_bytes;
-  ring.sb_bytes = a.w.sb_type == kTypeF32 ? 4 : 2;
-  ring.lane = lane;
+  ring.init(raw + sizeof(DownShared), sh.bars, warp, lane);
+  make_plan(a.route, a.tokens, a.w.experts, a.err, sh.plan);
+  const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * 32;
+  const int groups = a.w.inner / G, chunks = (a.w.inner + R::kChunk - 1) / R::kChunk;
+  const int total = sh.plan.units * chunks;  // at most 2^22: sizes are at most 2^20
+  // Warps that share the steps, none without any; warp w begins at step total * w / warps.
+  const int warps = min(cluster * kMoeWarps, total), self = rank * kMoeWarps + warp;
+  const int step0 = self < warps ? total * self / warps : total;
+  const int step1 = self < warps ? total * (self + 1) / warps : total;
+  // The warps that have a unit's first and last step: step s is in warp w where
+  // total * w / warps <= s < total * (w + 1) / warps, so w = ((s + 1) * warps - 1) / total.
+  for (int u = threadIdx.x; u < sh.plan.units; u += kMoeThreads) {
+    sh.unit_from[u] = static_cast<unsigned char>(((u * chunks + 1) * warps - 1) / total);
+    sh.unit_to[u] = static_cast<unsigned char>(((u + 1) * chunks * warps - 1) / total);
+  }
+  const char *const scales = static_cast<const char *>(a.w.scales[2]);
+  const char *const biases = static_cast<const char *>(a.w.biases[2]);
+  // this lane's row for scales: row g + 8 (t % 2) of tile t / 2
+  auto scale_row = [&](int unit) {
+    return static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.hidden + row0 + g + 8 * t;
+  };
 
-  RowPtrs p;
-  int load_step = step0, load_unit = step0 / groups, load_j = step0 - load_unit * groups;
-  const int first_unit = load_unit, first_j = load_j;
-  auto point = [&](int unit) {
-    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.hidden + row0 + g;
-    p.w[0] = reinterpret_cast<const char *>(a.w.w[2]) + row * row_bytes;
-    p.w[1] = p.w[0] + 16 * row_bytes;
-    const int64_t at = (row + 8 * t) * groups * ring.sb_bytes;  // row half t % 2 of tile t / 2
-    p.s = static_cast<const char *>(a.w.scales[2]) + at;
-    p.b = static_cast<const char *>(a.w.biases[2]) + at;
-  };
-  int stage_in = 0, stage_out = 0;
-  if (step0 < step1) point(load_unit);
+  const bool copied = static_cast<int64_t>(a.w.inner) * BITS % 128 != 0;
+  const Source down{&maps.down, copied ? a.w.w[2] : nullptr, a.w.inner / 32 * BITS};
+  const int first_unit = step0 / chunks, first_chunk = step0 - first_unit * chunks;
+  int load_step = step0, load_unit = first_unit, load_chunk = first_chunk;
   auto load_next = [&]() {
-    const bool live = load_step < step1;
-    if (live && load_j == groups) point(++load_unit), load_j = 0;
-    ring.issue(stage_in, p, load_j, live);
-    stage_in = stage_in + 1 == R::kDepth ? 0 : stage_in + 1;
-    ++load_step, ++load_j;
+    if (load_step >= step1 || ring.dead) return;
+    const int row = sh.plan.unit_expert[load_unit] * a.w.hidden + row0;
+    ring.issue(down, down, row, row + 16, load_chunk);
+    ++load_step;
+    if (++load_chunk == chunks) load_chunk = 0, ++load_unit;
   };
-  for (int i = 0; i < R::kDepth - 1; ++i) load_next();
+  for (int i = 0; i < R::kDepth; ++i) load_next();
+  Scales<R::kSteps> next;
+  if (step0 < step1) next.load(scales, biases, a.w.sb_type, scale_row(first_unit) * groups, first_chunk * R::kSteps, groups);
   griddep_wait();  // h is complete; the weights above do not depend on it
 
   int step = step0;
-  for (int unit = first_unit; step < step1; ++unit) {
-    const int j0 = unit == first_unit ? first_j : 0;
-    const int j1 = min(groups, j0 + (step1 - step));
-    const int count = sh.plan.unit_count[unit], first = sh.plan.unit_first[unit];
-    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.hidden + row0 + g;
-    const uint32_t row_odd = static_cast<uint32_t>(row * groups);
+  for (int unit = first_unit; step < step1 && !ring.dead; ++unit) {
+    const int j0 = unit == first_unit ? first_chunk : 0;
+    const int j1 = min(chunks, j0 + (step1 - step));
+    const int count = sh.plan.unit_count[unit];
+    const short *slots = &sh.plan.list[sh.plan.unit_first[unit]];
     Columns c;
     c.halves = count > 8 ? 2 : 1;
     c.planes = a.h_planes;
@@ -572,51 +693,52 @@ __global__ void __launch_bounds__(kMoeThreads, 2) down_kernel(const __grid_const
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       c.live[half] = 8 * half + g < count;
-      const int slot = c.live[half] ? sh.plan.list[first + 8 * half + g] : 0;
+      const int slot = c.live[half] ? slots[8 * half + g] : 0;
       c.x[half] = a.h + static_cast<int64_t>(slot) * a.w.inner + t * R::kCodes;
     }
     float acc[2][8] = {};
-    for (int j = j0; j < j1; ++j) {
-      load_next();
-      asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
-      __syncwarp();
-      consume<BITS, G>(ring, stage_out, c, j, a.w.sb_type, (row_odd + j) & 1u, acc);
-      stage_out = stage_out + 1 == R::kDepth ? 0 : stage_out + 1;
-      __syncwarp();
+    for (int j = j0; j < j1 && !ring.dead; ++j) {
+      const Scales<R::kSteps> sc = next;
+      ++step;
+      if (step < step1) {
+        const bool same = j + 1 < chunks;
+        next.load(scales, biases, a.w.sb_type, scale_row(same ? unit : unit + 1) * groups, same ? (j + 1) * R::kSteps : 0,
+                  groups);
+      }
+      const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
+      if (stage) {
+        consume<BITS, G>(stage, lane, c, j * R::kSteps, groups, sc, a.w.sb_type, acc);
+        ring.done();
+        load_next();
+      }
     }
-    step += j1 - j0;
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int k = half * 8 + 2 * t + i;
-        if (k < count) {
-          float *to = j0 == 0 ? z + sh.plan.list[first + k] * 32 : sh.heads[warp][k];
+        const int place = half * 8 + 2 * t + i;
+        if (place < count) {
+          float *to = j0 == 0 ? z + slots[place] * 32 : sh.heads[warp][place];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[half][2 * q + i];
+          for (int q = 0; q < 4; ++q) to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[half][2 * q + i] * kUnscale;
         }
       }
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  ring.drain(copied, a.wait_limit, a.err);
   cluster_barrier();
 
   const uint32_t z_at = smem_u32(z) + lane * 4, heads_at = smem_u32(sh.heads) + lane * 4;
-  for (int token = warp * cluster + rank; token < a.tokens; token += warps) {
+  for (int token = warp * cluster + rank; token < a.tokens; token += cluster * kMoeWarps) {
     float sum = 0.0f;
 #pragma unroll 4
     for (int k = 0; k < a.route.top_k; ++k) {
       const int slot = token * a.route.top_k + k, e = sh.plan.slot_expert[slot];
       if (e < 0) continue;
       const int place = sh.plan.slot_place[slot], unit = (sh.plan.table[e] >> 16) + place / kMoePass;
-      const int begin = unit * groups, end = begin + groups;
-      // the warp that has the unit's first step, and those that carry on
-      int w = (begin * warps + warps - 1) / total;
-      while (w > 0 && begin_of(w) > begin) --w;
-      while (begin_of(w + 1) <= begin) ++w;
-      float v = remote_f32(z_at + slot * 128, w / kMoeWarps);
-      for (++w; w < warps && begin_of(w) < end; ++w)
-        if (begin_of(w) < begin_of(w + 1))
-          v += remote_f32(heads_at + ((w % kMoeWarps) * kMoePass + place % kMoePass) * 128, w / kMoeWarps);
+      const int from = sh.unit_from[unit], to = sh.unit_to[unit];
+      float v = remote_f32(z_at + slot * 128, from / kMoeWarps);
+      for (int w = from + 1; w <= to; ++w)
+        v += remote_f32(heads_at + ((w % kMoeWarps) * kMoePass + place % kMoePass) * 128, w / kMoeWarps);
       sum = fmaf(sh.plan.slot_weight[slot], v, sum);
     }
     const int64_t at = static_cast<int64_t>(token) * a.w.hidden + row0 + lane;
@@ -628,30 +750,50 @@ __global__ void __launch_bounds__(kMoeThreads, 2) down_kernel(const __grid_const
 
 // -------------------------------------------------------------- launch ----
 
+// Boxes of 16 rows of a chunk, over all experts' rows (none where the kernels copy).
+template <int BITS, int G>
+cudaError_t weight_map(CUtensorMap *map, const uint32_t *w, int64_t rows, int cols) {
+  using R = Run<BITS, G>;
+  const uint64_t words = static_cast<uint64_t>(cols) * BITS / 32;
+  if (words % 4 != 0) return cudaSuccess;
+  return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, w, words, rows, words * 4, R::kRowBytes / 4, 16, R::kSwizzle);
+}
+
 template <int BITS, int G>
 cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   using R = Run<BITS, G>;
   const size_t ring = kMoeWarps * R::kDepth * R::kStageBytes;
   const int slots = a.tokens * a.route.top_k;
-  const int units = slots < a.w.experts ? slots : a.w.experts;  // near enough for the grid
+  MoeMaps maps = {};
+  const int64_t inner_rows = static_cast<int64_t>(a.w.experts) * a.w.inner;
+  const int64_t hidden_rows = static_cast<int64_t>(a.w.experts) * a.w.hidden;
+  cudaError_t e = weight_map<BITS, G>(&maps.gate, a.w.w[0], inner_rows, a.w.hidden);
+  if (e == cudaSuccess) e = weight_map<BITS, G>(&maps.up, a.w.w[1], inner_rows, a.w.hidden);
+  if (e == cudaSuccess) e = weight_map<BITS, G>(&maps.down, a.w.w[2], hidden_rows, a.w.inner);
+  if (e != cudaSuccess) return e;
   {
     constexpr auto kernel = gate_up_kernel<BITS, G>;
-    const size_t bytes = sizeof(GateUpShared) + ring;
-    cudaError_t e = ensure_smem_limit<kernel>(bytes);
+    const size_t bytes = sizeof(GateUpShared) + ring + 16;  // a run's last word may lie past its row
+    e = ensure_smem_limit<kernel>(bytes);
     if (e != cudaSuccess) return e;
-    const int64_t items = static_cast<int64_t>(units + slots / kMoePass) * (a.w.inner / 16);
-    const int64_t most = 2 * sm_count();
-    kernel<<<static_cast<unsigned>(items < most ? items : most), kMoeThreads, bytes, stream>>>(a);
+    // Ways to split a tile's chunks: the most that leave at most an eighth of the warps'
+    // turns empty.
+    const int chunks = (a.w.hidden + R::kChunk - 1) / R::kChunk;
+    int ksplit = kMoeWarps;
+    while (ksplit > 1 && 8 * ((chunks + ksplit - 1) / ksplit) * ksplit > 9 * chunks) ksplit /= 2;
+    const int wide = kMoeWarps / ksplit;
+    const int64_t items = static_cast<int64_t>(slots) * ((a.w.inner / 16 + wide - 1) / wide), most = 2 * sm_count();
+    kernel<<<static_cast<unsigned>(items < most ? items : most), kMoeThreads, bytes, stream>>>(a, maps, ksplit);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   constexpr auto kernel = down_kernel<BITS, G>;
   const size_t bytes = sizeof(DownShared) + static_cast<size_t>(slots) * 128 + ring;
-  const cudaError_t e = ensure_smem_limit<kernel>(bytes);
+  e = ensure_smem_limit<kernel>(bytes);
   if (e != cudaSuccess) return e;
   const int tiles = a.w.hidden / 32;
   int cluster = 1;
-  while (cluster < kMoeMaxCluster && tiles * cluster < 2 * sm_count()) cluster *= 2;
+  while (cluster < kMoeMaxCluster && tiles * cluster < sm_count()) cluster *= 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = cluster;
@@ -665,7 +807,7 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, cluster);
+  return cudaLaunchKernelEx(&cfg, kernel, a, maps, cluster);
 }
 
 template <int BITS>
