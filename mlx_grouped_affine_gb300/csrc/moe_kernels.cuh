@@ -166,11 +166,11 @@ struct Run {
   static constexpr bool kSplit = kWhole && (BITS == 2 || BITS == 4 || BITS == 8);
   static constexpr int kSub = kCodes < 16 ? kCodes : 16;  // codes spread at a time
   // A chunk: what a warp's ring holds per stage of each row, at most 128 bytes.
-  static constexpr int kChunk = BITS <= 4 ? 256 : 128;
+  static constexpr int kChunk = BITS <= 2 ? 256 : 128;
   static constexpr int kSteps = kChunk / G;
   static constexpr int kRowBytes = kChunk * BITS / 8;
   static constexpr int kStageBytes = 2 * 16 * kRowBytes;
-  static constexpr int kDepth = kStageBytes >= 4096 ? 2 : kStageBytes >= 3072 ? 3 : 4;
+  static constexpr int kDepth = kStageBytes >= 3072 ? 2 : kStageBytes >= 2048 ? 3 : 4;
   static constexpr CUtensorMapSwizzle kSwizzle = kRowBytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                                  : kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                                    : CU_TENSOR_MAP_SWIZZLE_NONE;
@@ -238,13 +238,15 @@ __device__ __forceinline__ void pair_x(const uint16_t *x, uint32_t (&p)[Run<BITS
   }
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+// d = a b + c, or a b where `first`.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first ? 0.0f : d[0]), "f"(first ? 0.0f : d[1]),
+        "f"(first ? 0.0f : d[2]), "f"(first ? 0.0f : d[3]));
 }
 
 // ------------------------------------------------------------- the ring ----
@@ -318,6 +320,29 @@ struct Columns {
   int64_t plane;
 };
 
+// The MMAs of up to 16 codes a lane with one plane of x, on top of what the sums hold
+// (nothing yet where `first`).
+template <int BITS, int G>
+__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2], const uint16_t *px, bool live,
+                                         bool first, float (&part)[2][4], float (&ones)[4]) {
+  using R = Run<BITS, G>;
+  uint32_t x[R::kSub / 2];
+  if (live) {
+    pair_x<BITS, G>(px, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R::kSub / 2; ++i) x[i] = 0;
+  }
+#pragma unroll
+  for (int m = 0; m < R::kSub / 4; ++m) {
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile)
+      mma_bf16(part[tile], first && m == 0, code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
+               code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
+    mma_bf16(ones, first && m == 0, kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
+  }
+}
+
 // One chunk of 32 rows: acc[half][4 tile + 2 row half + column] += s sum(c x) + b sum(x),
 // over its groups j0 .. (below `groups`).
 template <int BITS, int G>
@@ -328,7 +353,7 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns 
 #pragma unroll
   for (int step = 0; step < R::kSteps; ++step) {
     if (j0 + step >= groups) break;
-    float part[2][2][4] = {}, ones[2][4] = {};
+    float part[2][2][4], ones[2][4];
     uint32_t v[4][R::kWords + 1];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -348,26 +373,14 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns 
       uint32_t code[4][R::kSub / 2];
 #pragma unroll
       for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, code[q]);
+      const int at = (j0 + step) * G + sub * R::kSub;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         if (half < c.halves) {
-          for (int plane = c.planes - 1; plane >= 0; --plane) {  // the smallest parts first
-            uint32_t x[R::kSub / 2];
-            if (c.live[half]) {
-              pair_x<BITS, G>(c.x[half] + plane * c.plane + (j0 + step) * G + sub * R::kSub, x);
-            } else {
-#pragma unroll
-              for (int i = 0; i < R::kSub / 2; ++i) x[i] = 0;
-            }
-#pragma unroll
-            for (int m = 0; m < R::kSub / 4; ++m) {
-#pragma unroll
-              for (int tile = 0; tile < 2; ++tile)
-                mma_bf16(part[half][tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
-                         code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
-              mma_bf16(ones[half], kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
-            }
-          }
+          // the smallest parts first
+          multiply<BITS, G>(code, c.x[half] + (c.planes - 1) * c.plane + at, c.live[half], sub == 0, part[half], ones[half]);
+          for (int plane = c.planes - 2; plane >= 0; --plane)
+            multiply<BITS, G>(code, c.x[half] + plane * c.plane + at, c.live[half], false, part[half], ones[half]);
         }
       }
     }
@@ -399,6 +412,23 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns 
           }
         }
       }
+    }
+  }
+}
+
+// Brings a chunk of x of the unit's slots into L1 ahead of its use: a 4-byte copy of each
+// 32-byte sector to a place that nothing reads.
+template <int CHUNK, bool TOKENS>
+__device__ __forceinline__ void touch_x(uint32_t scratch, const uint16_t *x, int64_t plane, int planes, const short *slots,
+                                        int count, int top, int width, int chunk, int lane) {
+  constexpr int kSectors = CHUNK / 16;
+  const int all = count * kSectors;
+  for (int p = 0; p < planes; ++p) {
+    for (int i = lane; i < all; i += 32) {
+      const int slot = slots[i / kSectors], at = chunk * CHUNK + i % kSectors * 16;
+      const uint16_t *from = x + p * plane + static_cast<int64_t>(TOKENS ? slot / top : slot) * width + at;
+      if (at < width)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scratch + 4 * lane), "l"(from) : "memory");
     }
   }
 }
@@ -505,6 +535,7 @@ struct alignas(1024) GateUpShared {  // the ring follows: swizzled boxes want 10
   MoePlan plan;
   alignas(16) float sums[kMoeWarps][32][kMoePass];
   alignas(16) uint64_t bars[kMoeWarps * 4];
+  uint32_t unread[32];
 };
 struct MoeMaps {
   CUtensorMap gate, up, down;
@@ -536,12 +567,13 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   const Source up{&maps.up, copied ? a.w.w[1] : nullptr, a.w.hidden / 32 * BITS};
 
   // What is loaded next: a chunk of an item in which this warp has a tile.
-  int load_item = blockIdx.x, load_chunk = c0, load_row = 0;
+  int load_item = blockIdx.x, load_chunk = c0, load_row = 0, load_unit = 0;
   auto settle = [&]() {
     for (; load_item < items; load_item += gridDim.x) {
       const int unit = load_item / parts, tile = (load_item - unit * parts) * wide + own;
       if (tile < tiles) {
         load_row = sh.plan.unit_expert[unit] * a.w.inner + tile * 16;
+        load_unit = unit;
         return;
       }
     }
@@ -550,6 +582,8 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   auto load_next = [&]() {
     if (load_item >= items || ring.dead || c0 == c1) return;
     ring.issue(gate, up, load_row, load_row, load_chunk);
+    touch_x<R::kChunk, true>(smem_u32(sh.unread), a.x, a.x_plane, a.x_planes, &sh.plan.list[sh.plan.unit_first[load_unit]],
+                             sh.plan.unit_count[load_unit], a.route.top_k, a.w.hidden, load_chunk, lane);
     if (++load_chunk == c1) load_chunk = c0, load_item += gridDim.x, settle();
   };
   settle();
@@ -606,6 +640,7 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
     __syncthreads();  // before the next item's sums
   }
   ring.drain(copied, a.wait_limit, a.err);
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- down ----
@@ -614,6 +649,7 @@ struct alignas(1024) DownShared {  // then the ring, then z: float [slots][32]
   MoePlan plan;
   alignas(16) float heads[kMoeWarps][kMoePass][32];
   alignas(16) uint64_t bars[kMoeWarps * 4];
+  uint32_t unread[32];
   unsigned char unit_from[kMoeMaxSlots], unit_to[kMoeMaxSlots];
 };
 
@@ -668,17 +704,26 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   const Source down{&maps.down, copied ? a.w.w[2] : nullptr, a.w.inner / 32 * BITS};
   const int first_unit = step0 / chunks, first_chunk = step0 - first_unit * chunks;
   int load_step = step0, load_unit = first_unit, load_chunk = first_chunk;
-  auto load_next = [&]() {
+  auto touch_h = [&](int unit, int chunk) {
+    touch_x<R::kChunk, false>(smem_u32(sh.unread), a.h, a.h_plane, a.h_planes, &sh.plan.list[sh.plan.unit_first[unit]],
+                              sh.plan.unit_count[unit], 1, a.w.inner, chunk, lane);
+  };
+  auto load_next = [&](bool touch) {
     if (load_step >= step1 || ring.dead) return;
     const int row = sh.plan.unit_expert[load_unit] * a.w.hidden + row0;
     ring.issue(down, down, row, row + 16, load_chunk);
+    if (touch) touch_h(load_unit, load_chunk);
     ++load_step;
     if (++load_chunk == chunks) load_chunk = 0, ++load_unit;
   };
-  for (int i = 0; i < R::kDepth; ++i) load_next();
+  for (int i = 0; i < R::kDepth; ++i) load_next(false);
   Scales<R::kSteps> next;
   if (step0 < step1) next.load(scales, biases, a.w.sb_type, scale_row(first_unit) * groups, first_chunk * R::kSteps, groups);
   griddep_wait();  // h is complete; the weights above do not depend on it
+  for (int i = step0, u = first_unit, k = first_chunk; i < load_step; ++i) {
+    touch_h(u, k);
+    if (++k == chunks) k = 0, ++u;
+  }
 
   int step = step0;
   for (int unit = first_unit; step < step1 && !ring.dead; ++unit) {
@@ -709,7 +754,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
       if (stage) {
         consume<BITS, G>(stage, lane, c, j * R::kSteps, groups, sc, a.w.sb_type, acc);
         ring.done();
-        load_next();
+        load_next(true);
       }
     }
 #pragma unroll
@@ -725,6 +770,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
       }
   }
   ring.drain(copied, a.wait_limit, a.err);
+  asm volatile("cp.async.wait_all;" ::: "memory");
   cluster_barrier();
 
   const uint32_t z_at = smem_u32(z) + lane * 4, heads_at = smem_u32(sh.heads) + lane * 4;

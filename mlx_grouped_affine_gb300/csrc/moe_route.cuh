@@ -50,7 +50,7 @@ __device__ __forceinline__ void route_row(const Routing &r, int experts, int64_t
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const float l = key_logit(key[i]);
-        if (key[i] != 0u && l != -INFINITY) part += l == largest ? 1.0f : expf(l - largest);
+        if (key[i] != 0u && l != -INFINITY) part += l == largest ? 1.0f : __expf(l - largest);
       }
       total = warp_sum(part);
     }
@@ -79,12 +79,20 @@ __device__ __forceinline__ void route_row(const Routing &r, int experts, int64_t
   // exponentials of log sigmoid(l) = min(l, 0) - log(1 + exp(-|l|)): those of logits below
   // -88 do not fit fp32, but their ratios do.
   const bool relative = r.sigmoid && r.normalize;
-  const float x = relative ? fminf(l, 0.0f) - log1pf(expf(-fabsf(l))) : l;
-  if (relative) largest = __shfl_sync(0xFFFFFFFFu, x, 0);
-  if (lane < r.top_k && l != -INFINITY)
-    score = r.sigmoid && !relative ? 1.0f / (1.0f + expf(-l)) : x == largest ? 1.0f : expf(x - largest);
+  // (Few instructions: an expert kernel runs them once a block, each line of them a miss of
+  // the instruction cache.  __expf is off by 2^-21 and 2^-24 of its argument.)
+  float x = l;
+  if (relative) {
+    x = fminf(l, 0.0f) - log1pf(__expf(-fabsf(l)));
+    largest = __shfl_sync(0xFFFFFFFFu, x, 0);
+  }
+  if (lane < r.top_k && l != -INFINITY) {
+    const bool alone = r.sigmoid && !relative;
+    score = alone || x != largest ? __expf(alone ? -l : x - largest) : 1.0f;
+    if (alone) score = __fdividef(1.0f, 1.0f + score);
+  }
   if (r.normalize) total = warp_sum(score);
-  weight = total > 0.0f ? __fdiv_rn(score, total) * r.scale : 0.0f;
+  weight = total > 0.0f ? __fdividef(score, total) * r.scale : 0.0f;
 }
 
 }  // namespace qmm
