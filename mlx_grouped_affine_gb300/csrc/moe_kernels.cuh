@@ -26,6 +26,11 @@ constexpr int kMoeThreads = 256, kMoeWarps = kMoeThreads / 32;
 constexpr int kMoePass = 16;      // slots of an expert per pass over its weights
 constexpr int kMoeMaxCluster = 8;
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 // What the kernels share of a call.
 struct MoeArgs {
   Routing route;
@@ -238,15 +243,13 @@ __device__ __forceinline__ void pair_x(const uint16_t *x, uint32_t (&p)[Run<BITS
   }
 }
 
-// d = a b + c, or a b where `first`.
-__device__ __forceinline__ void mma_bf16(float (&d)[4], bool first, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first ? 0.0f : d[0]), "f"(first ? 0.0f : d[1]),
-        "f"(first ? 0.0f : d[2]), "f"(first ? 0.0f : d[3]));
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // ------------------------------------------------------------- the ring ----
@@ -311,49 +314,26 @@ struct Scales {
   }
 };
 
-// The MMA's columns: rows of x (or h) of up to 16 slots, lane 4 g + t reading column g.
+// The MMA's columns: rows of x (or h) of up to 8 HALVES slots, lane 4 g + t reading column g.
+template <int HALVES>
 struct Columns {
-  const uint16_t *x[2];  // this lane's column of each half of the pass, at its run
-  bool live[2];
-  int halves;            // halves of the pass in use: 1 or 2
+  const uint16_t *x[HALVES];  // this lane's column of each half of the pass, at its run
+  bool live[HALVES];
   int planes;
   int64_t plane;
 };
 
-// The MMAs of up to 16 codes a lane with one plane of x, on top of what the sums hold
-// (nothing yet where `first`).
-template <int BITS, int G>
-__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2], const uint16_t *px, bool live,
-                                         bool first, float (&part)[2][4], float (&ones)[4]) {
-  using R = Run<BITS, G>;
-  uint32_t x[R::kSub / 2];
-  if (live) {
-    pair_x<BITS, G>(px, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < R::kSub / 2; ++i) x[i] = 0;
-  }
-#pragma unroll
-  for (int m = 0; m < R::kSub / 4; ++m) {
-#pragma unroll
-    for (int tile = 0; tile < 2; ++tile)
-      mma_bf16(part[tile], first && m == 0, code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
-               code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
-    mma_bf16(ones, first && m == 0, kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
-  }
-}
-
-// One chunk of 32 rows: acc[half][4 tile + 2 row half + column] += s sum(c x) + b sum(x),
-// over its groups j0 .. (below `groups`).
-template <int BITS, int G>
-__device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns &c, int j0, int groups,
-                                        const Scales<Run<BITS, G>::kSteps> &sc, int sb_type, float (&acc)[2][8]) {
+// One chunk of 32 rows: acc[half][2 q + column] += s sum(c x) + b sum(x) over its groups
+// from j0 on (below `groups`), q = 2 tile + row half.
+template <int BITS, int G, int HALVES>
+__device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<HALVES> &c, int j0, int groups,
+                                        const Scales<Run<BITS, G>::kSteps> &sc, int sb_type, float (&acc)[HALVES][8]) {
   using R = Run<BITS, G>;
   const int t = lane % 4;
 #pragma unroll
   for (int step = 0; step < R::kSteps; ++step) {
     if (j0 + step >= groups) break;
-    float part[2][2][4], ones[2][4];
+    float part[HALVES][2][4] = {}, ones[HALVES][4] = {};
     uint32_t v[4][R::kWords + 1];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -373,46 +353,54 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns 
       uint32_t code[4][R::kSub / 2];
 #pragma unroll
       for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, code[q]);
-      const int at = (j0 + step) * G + sub * R::kSub;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half < c.halves) {
-          // the smallest parts first
-          multiply<BITS, G>(code, c.x[half] + (c.planes - 1) * c.plane + at, c.live[half], sub == 0, part[half], ones[half]);
-          for (int plane = c.planes - 2; plane >= 0; --plane)
-            multiply<BITS, G>(code, c.x[half] + plane * c.plane + at, c.live[half], false, part[half], ones[half]);
-        }
-      }
-    }
-    const uint32_t both = prmt(sc.s[step / 2], sc.b[step / 2], step & 1 ? 0x7632u : 0x5410u);  // 16-bit types
+      for (int half = 0; half < HALVES; ++half) {
+        // the smallest parts of x first
+        const uint16_t *px = c.x[half] + (j0 + step) * G + sub * R::kSub + (c.planes - 1) * c.plane;
+#pragma unroll 1
+        for (int plane = c.planes; plane > 0; --plane, px -= c.plane) {
+          uint32_t x[R::kSub / 2] = {};
+          if (c.live[half]) pair_x<BITS, G>(px, x);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float s, b;
-      const int from = (lane & ~3) | q;
-      if (sb_type == kTypeF32) {
-        s = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.s[step], from));
-        b = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.b[step], from));
-      } else {
-        const uint32_t u = __shfl_sync(0xFFFFFFFFu, both, from);
-        if (sb_type == kTypeBF16) {
-          s = __uint_as_float(u << 16);
-          b = __uint_as_float(u & 0xFFFF0000u);
-        } else {
-          s = ElemF16::to_f32(u & 0xFFFFu);
-          b = ElemF16::to_f32(u >> 16);
-        }
-      }
+          for (int m = 0; m < R::kSub / 4; ++m) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half < c.halves) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float &y = acc[half][2 * q + i];
-            y = fmaf(s, part[half][q / 2][2 * (q % 2) + i], fmaf(b, ones[half][i], y));
+            for (int tile = 0; tile < 2; ++tile)
+              mma_bf16(part[half][tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
+                       code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
+            mma_bf16(ones[half], kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
           }
         }
       }
     }
+    float sq[4], bq[4];
+    if (sb_type == kTypeF32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sq[q] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.s[step], q, 4));
+        bq[q] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.b[step], q, 4));
+      }
+    } else {
+      const uint32_t both = prmt(sc.s[step / 2], sc.b[step / 2], step & 1 ? 0x7632u : 0x5410u);
+      uint32_t u[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) u[q] = __shfl_sync(0xFFFFFFFFu, both, q, 4);
+      if (sb_type == kTypeBF16) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sq[q] = __uint_as_float(u[q] << 16), bq[q] = __uint_as_float(u[q] & 0xFFFF0000u);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sq[q] = ElemF16::to_f32(u[q] & 0xFFFFu), bq[q] = ElemF16::to_f32(u[q] >> 16);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int half = 0; half < HALVES; ++half)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float &y = acc[half][2 * q + i];
+          y = fmaf(sq[q], part[half][q / 2][2 * (q % 2) + i], fmaf(bq[q], ones[half][i], y));
+        }
   }
 }
 
@@ -533,7 +521,9 @@ __device__ __forceinline__ void store_planes(uint16_t *p, int64_t plane, int pla
 
 struct alignas(1024) GateUpShared {  // the ring follows: swizzled boxes want 1024
   MoePlan plan;
-  alignas(16) float sums[kMoeWarps][32][kMoePass];
+  // [0]: sums of a task that goes on in the next warp, [1]: of one that began in an earlier
+  alignas(16) float sums[2][kMoeWarps][32][kMoePass];
+  int task[2][kMoeWarps];  // which; -1: none
   alignas(16) uint64_t bars[kMoeWarps * 4];
   uint32_t unread[32];
 };
@@ -541,106 +531,155 @@ struct MoeMaps {
   CUtensorMap gate, up, down;
 };
 
-// h = silu(gate x) * (up x).  An item is a unit and 8 / ksplit tiles of 16 rows of gate and
-// of up; ksplit warps share a tile's chunks and join their sums through shared memory.
+__device__ __forceinline__ float silu_times(float gate, float up) {
+  gate *= kUnscale, up *= kUnscale;
+  return __fdividef(gate, 1.0f + expf(-gate)) * up;
+}
+
+// h = silu(gate x) * (up x).  A task is a unit and 16 rows of gate and of up.  A block has
+// a run of tasks, whose chunks, in order, are cut evenly over its warps; a task within one
+// warp is finished there (gate and up of a row are in the same lane), one that is cut is
+// joined through shared memory at the end.
+template <int BITS, int G>
+struct GateUp {
+  using R = Run<BITS, G>;
+  const MoeArgs &a;
+  GateUpShared &sh;
+  Ring<BITS, G> ring;
+  Source gate, up;
+  const char *scales, *biases;
+  bool copied;
+  int lane, warp, tiles, groups, chunks;
+  int first_unit, first_tile;        // the block's first task
+  int task, chunk, unit, tile, left;  // what is multiplied next, chunks left to this warp
+  int l_chunk, l_unit, l_tile, l_left;  // what is loaded next
+  bool l_fresh;                       // its unit's x is not in L1 yet
+  Scales<R::kSteps> next;
+
+  __device__ __forceinline__ void advance_load() {
+    if (l_left <= 0 || ring.dead) return;
+    const int row = sh.plan.unit_expert[l_unit] * a.w.inner + l_tile * 16;
+    ring.issue(gate, up, row, row, l_chunk);
+    if (l_fresh)
+      touch_x<R::kChunk, true>(smem_u32(sh.unread), a.x, a.x_plane, a.x_planes, &sh.plan.list[sh.plan.unit_first[l_unit]],
+                               sh.plan.unit_count[l_unit], a.route.top_k, a.w.hidden, l_chunk, lane);
+    --l_left;
+    if (++l_chunk == chunks) {
+      l_chunk = 0;
+      l_fresh = false;
+      if (++l_tile == tiles) l_tile = 0, ++l_unit, l_fresh = true;
+    }
+  }
+  // The next chunk's scales, of the row that this lane stands for.
+  __device__ __forceinline__ void load_scales(int u, int at_tile, int at_chunk) {
+    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[u]) * a.w.inner + at_tile * 16 + lane / 4 + 8 * (lane % 2);
+    next.load(scales, biases, a.w.sb_type, row * groups, at_chunk * R::kSteps, groups);
+  }
+
+  template <int HALVES>
+  __device__ __forceinline__ void run_task() {
+    const int g = lane / 4, t = lane % 4, count = sh.plan.unit_count[unit];
+    const short *slots = &sh.plan.list[sh.plan.unit_first[unit]];
+    Columns<HALVES> c;
+    c.planes = a.x_planes;
+    c.plane = a.x_plane;
+#pragma unroll
+    for (int half = 0; half < HALVES; ++half) {
+      c.live[half] = 8 * half + g < count;
+      const int token = c.live[half] ? slots[8 * half + g] / a.route.top_k : 0;
+      c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
+    }
+    float acc[HALVES][8] = {};
+    const int c0 = chunk, c1 = min(chunks, chunk + left);
+    for (; chunk < c1 && !ring.dead; ++chunk) {
+      const Scales<R::kSteps> sc = next;
+      if (--left > 0) {
+        const bool same = chunk + 1 < chunks, last = tile + 1 == tiles;
+        load_scales(same || !last ? unit : unit + 1, same ? tile : last ? 0 : tile + 1, same ? chunk + 1 : 0);
+      }
+      const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
+      if (stage) {
+        consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kSteps, groups, sc, a.w.sb_type, acc);
+        ring.done();
+        advance_load();
+      }
+    }
+    if (c0 == 0 && c1 == chunks) {
+#pragma unroll
+      for (int half = 0; half < HALVES; ++half)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int place = 8 * half + 2 * t + i;
+          if (place < count) {
+            uint16_t *to = a.h + static_cast<int64_t>(slots[place]) * a.w.inner + tile * 16 + g;
+            store_planes(to, a.h_plane, a.h_planes, silu_times(acc[half][i], acc[half][4 + i]));
+            store_planes(to + 8, a.h_plane, a.h_planes, silu_times(acc[half][2 + i], acc[half][6 + i]));
+          }
+        }
+    } else {
+      const int kind = c0 == 0 ? 0 : 1;
+      if (lane == 0) sh.task[kind][warp] = task;
+#pragma unroll
+      for (int half = 0; half < HALVES; ++half)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float2 *>(&sh.sums[kind][warp][(q / 2) * 16 + (q % 2) * 8 + g][half * 8 + 2 * t]) =
+              make_float2(acc[half][2 * q], acc[half][2 * q + 1]);
+    }
+    chunk = 0;
+    ++task;
+    if (++tile == tiles) tile = 0, ++unit;
+  }
+};
+
 template <int BITS, int G>
 __global__ void __launch_bounds__(kMoeThreads, 2)
-gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps maps, int ksplit) {
+gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps maps) {
   using R = Run<BITS, G>;
   extern __shared__ __align__(1024) unsigned char raw[];
-  GateUpShared &sh = *reinterpret_cast<GateUpShared *>(raw);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  Ring<BITS, G> ring;
-  ring.init(raw + sizeof(GateUpShared), sh.bars, warp, lane);
+  GateUp<BITS, G> s{a, *reinterpret_cast<GateUpShared *>(raw)};
+  s.warp = threadIdx.x / 32, s.lane = threadIdx.x % 32;
+  s.ring.init(raw + sizeof(GateUpShared), s.sh.bars, s.warp, s.lane);
+  if (threadIdx.x < 2 * kMoeWarps) s.sh.task[threadIdx.x / kMoeWarps][threadIdx.x % kMoeWarps] = -1;
   griddep_launch_dependents();
-  make_plan(a.route, a.tokens, a.w.experts, a.err, sh.plan);
-  const int tiles = a.w.inner / 16, groups = a.w.hidden / G, chunks = (a.w.hidden + R::kChunk - 1) / R::kChunk;
-  const int wide = kMoeWarps / ksplit, parts = (tiles + wide - 1) / wide;
-  const int items = sh.plan.units * parts;
-  const int own = warp / ksplit, k = warp % ksplit;
-  const int c0 = chunks * k / ksplit, c1 = chunks * (k + 1) / ksplit;
-  const char *const scales = static_cast<const char *>(t < 2 ? a.w.scales[0] : a.w.scales[1]);
-  const char *const biases = static_cast<const char *>(t < 2 ? a.w.biases[0] : a.w.biases[1]);
-
-  const bool copied = static_cast<int64_t>(a.w.hidden) * BITS % 128 != 0;
-  const Source gate{&maps.gate, copied ? a.w.w[0] : nullptr, a.w.hidden / 32 * BITS};
-  const Source up{&maps.up, copied ? a.w.w[1] : nullptr, a.w.hidden / 32 * BITS};
-
-  // What is loaded next: a chunk of an item in which this warp has a tile.
-  int load_item = blockIdx.x, load_chunk = c0, load_row = 0, load_unit = 0;
-  auto settle = [&]() {
-    for (; load_item < items; load_item += gridDim.x) {
-      const int unit = load_item / parts, tile = (load_item - unit * parts) * wide + own;
-      if (tile < tiles) {
-        load_row = sh.plan.unit_expert[unit] * a.w.inner + tile * 16;
-        load_unit = unit;
-        return;
-      }
-    }
-  };
-  Scales<R::kSteps> next;
-  auto load_next = [&]() {
-    if (load_item >= items || ring.dead || c0 == c1) return;
-    ring.issue(gate, up, load_row, load_row, load_chunk);
-    touch_x<R::kChunk, true>(smem_u32(sh.unread), a.x, a.x_plane, a.x_planes, &sh.plan.list[sh.plan.unit_first[load_unit]],
-                             sh.plan.unit_count[load_unit], a.route.top_k, a.w.hidden, load_chunk, lane);
-    if (++load_chunk == c1) load_chunk = c0, load_item += gridDim.x, settle();
-  };
-  settle();
-  for (int i = 0; i < R::kDepth; ++i) load_next();
-
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int unit = item / parts, tile0 = (item - unit * parts) * wide, tile = tile0 + own;
-    const int count = sh.plan.unit_count[unit];
-    const short *slots = &sh.plan.list[sh.plan.unit_first[unit]];
-    if (tile < tiles) {
-      const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.inner + tile * 16 + g + 8 * (t % 2);
-      Columns c;
-      c.halves = count > 8 ? 2 : 1;
-      c.planes = a.x_planes;
-      c.plane = a.x_plane;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        c.live[half] = 8 * half + g < count;
-        const int token = c.live[half] ? slots[8 * half + g] / a.route.top_k : 0;
-        c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
-      }
-      float acc[2][8] = {};
-      if (c0 < c1) next.load(scales, biases, a.w.sb_type, row * groups, c0 * R::kSteps, groups);
-      for (int chunk = c0; chunk < c1 && !ring.dead; ++chunk) {
-        const Scales<R::kSteps> sc = next;
-        if (chunk + 1 < c1) next.load(scales, biases, a.w.sb_type, row * groups, (chunk + 1) * R::kSteps, groups);
-        const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
-        if (stage) {
-          consume<BITS, G>(stage, lane, c, chunk * R::kSteps, groups, sc, a.w.sb_type, acc);
-          ring.done();
-          load_next();
-        }
-      }
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        if (half < c.halves)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float2 *>(&sh.sums[warp][(q / 2) * 16 + (q % 2) * 8 + g][half * 8 + 2 * t]) =
-                make_float2(acc[half][2 * q], acc[half][2 * q + 1]);
-    }
-    __syncthreads();
-    const int r = threadIdx.x % 16;
-    for (int i = threadIdx.x / 16; i < count * wide; i += kMoeThreads / 16) {
-      const int place = i / wide, of = i % wide;
-      if (tile0 + of >= tiles) continue;
-      float gate = 0.0f, up = 0.0f;
-      for (int w = of * ksplit; w < (of + 1) * ksplit; ++w)
-        gate += sh.sums[w][r][place], up += sh.sums[w][16 + r][place];
-      gate *= kUnscale, up *= kUnscale;
-      const float h = gate / (1.0f + expf(-gate)) * up;
-      store_planes(a.h + static_cast<int64_t>(slots[place]) * a.w.inner + (tile0 + of) * 16 + r, a.h_plane, a.h_planes, h);
-    }
-    __syncthreads();  // before the next item's sums
+  make_plan(a.route, a.tokens, a.w.experts, a.err, s.sh.plan);
+  s.tiles = a.w.inner / 16, s.groups = a.w.hidden / G, s.chunks = (a.w.hidden + R::kChunk - 1) / R::kChunk;
+  const int64_t tasks = static_cast<int64_t>(s.sh.plan.units) * s.tiles;
+  const int t0 = static_cast<int>(tasks * blockIdx.x / gridDim.x), t1 = static_cast<int>(tasks * (blockIdx.x + 1) / gridDim.x);
+  const int64_t steps = static_cast<int64_t>(t1 - t0) * s.chunks;
+  const int from = static_cast<int>(steps * s.warp / kMoeWarps);
+  s.left = s.l_left = static_cast<int>(steps * (s.warp + 1) / kMoeWarps) - from;
+  s.task = t0 + from / s.chunks;
+  s.chunk = s.l_chunk = from % s.chunks;
+  s.unit = s.l_unit = s.task / s.tiles;
+  s.tile = s.l_tile = s.task % s.tiles;
+  s.l_fresh = true;
+  s.copied = static_cast<int64_t>(a.w.hidden) * BITS % 128 != 0;
+  s.gate = Source{&maps.gate, s.copied ? a.w.w[0] : nullptr, a.w.hidden / 32 * BITS};
+  s.up = Source{&maps.up, s.copied ? a.w.w[1] : nullptr, a.w.hidden / 32 * BITS};
+  s.scales = static_cast<const char *>(s.lane % 4 < 2 ? a.w.scales[0] : a.w.scales[1]);
+  s.biases = static_cast<const char *>(s.lane % 4 < 2 ? a.w.biases[0] : a.w.biases[1]);
+  for (int i = 0; i < R::kDepth; ++i) s.advance_load();
+  if (s.left > 0) s.load_scales(s.unit, s.tile, s.chunk);
+  while (s.left > 0 && !s.ring.dead) {
+    if (s.sh.plan.unit_count[s.unit] > 8) s.template run_task<2>();
+    else s.template run_task<1>();
   }
-  ring.drain(copied, a.wait_limit, a.err);
+  s.ring.drain(s.copied, a.wait_limit, a.err);
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  const int r = threadIdx.x % 16, place = threadIdx.x / 16;
+  for (int w = 0; w < kMoeWarps; ++w) {
+    const int task = s.sh.task[0][w];
+    if (task < 0) continue;
+    const int unit = task / s.tiles, tile = task % s.tiles;
+    if (place >= s.sh.plan.unit_count[unit]) continue;
+    float gate = s.sh.sums[0][w][r][place], up = s.sh.sums[0][w][16 + r][place];
+    for (int v = w + 1; v < kMoeWarps; ++v)
+      if (s.sh.task[1][v] == task) gate += s.sh.sums[1][v][r][place], up += s.sh.sums[1][v][16 + r][place];
+    const int slot = s.sh.plan.list[s.sh.plan.unit_first[unit] + place];
+    store_planes(a.h + static_cast<int64_t>(slot) * a.w.inner + tile * 16 + r, a.h_plane, a.h_planes, silu_times(gate, up));
+  }
 }
 
 // ---------------------------------------------------------------- down ----
@@ -726,22 +765,21 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   }
 
   int step = step0;
-  for (int unit = first_unit; step < step1 && !ring.dead; ++unit) {
-    const int j0 = unit == first_unit ? first_chunk : 0;
+  auto run_unit = [&](auto halves, int unit, int j0) {
+    constexpr int HALVES = decltype(halves)::value;
     const int j1 = min(chunks, j0 + (step1 - step));
     const int count = sh.plan.unit_count[unit];
     const short *slots = &sh.plan.list[sh.plan.unit_first[unit]];
-    Columns c;
-    c.halves = count > 8 ? 2 : 1;
+    Columns<HALVES> c;
     c.planes = a.h_planes;
     c.plane = a.h_plane;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < HALVES; ++half) {
       c.live[half] = 8 * half + g < count;
       const int slot = c.live[half] ? slots[8 * half + g] : 0;
       c.x[half] = a.h + static_cast<int64_t>(slot) * a.w.inner + t * R::kCodes;
     }
-    float acc[2][8] = {};
+    float acc[HALVES][8] = {};
     for (int j = j0; j < j1 && !ring.dead; ++j) {
       const Scales<R::kSteps> sc = next;
       ++step;
@@ -752,13 +790,13 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
       }
       const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
       if (stage) {
-        consume<BITS, G>(stage, lane, c, j * R::kSteps, groups, sc, a.w.sb_type, acc);
+        consume<BITS, G, HALVES>(stage, lane, c, j * R::kSteps, groups, sc, a.w.sb_type, acc);
         ring.done();
         load_next(true);
       }
     }
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int half = 0; half < HALVES; ++half)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int place = half * 8 + 2 * t + i;
@@ -768,6 +806,11 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
           for (int q = 0; q < 4; ++q) to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[half][2 * q + i] * kUnscale;
         }
       }
+  };
+  for (int unit = first_unit; step < step1 && !ring.dead; ++unit) {
+    const int j0 = unit == first_unit ? first_chunk : 0;
+    if (sh.plan.unit_count[unit] > 8) run_unit(Int<2>(), unit, j0);
+    else run_unit(Int<1>(), unit, j0);
   }
   ring.drain(copied, a.wait_limit, a.err);
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -822,14 +865,8 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
     const size_t bytes = sizeof(GateUpShared) + ring + 16;  // a run's last word may lie past its row
     e = ensure_smem_limit<kernel>(bytes);
     if (e != cudaSuccess) return e;
-    // Ways to split a tile's chunks: the most that leave at most an eighth of the warps'
-    // turns empty.
-    const int chunks = (a.w.hidden + R::kChunk - 1) / R::kChunk;
-    int ksplit = kMoeWarps;
-    while (ksplit > 1 && 8 * ((chunks + ksplit - 1) / ksplit) * ksplit > 9 * chunks) ksplit /= 2;
-    const int wide = kMoeWarps / ksplit;
-    const int64_t items = static_cast<int64_t>(slots) * ((a.w.inner / 16 + wide - 1) / wide), most = 2 * sm_count();
-    kernel<<<static_cast<unsigned>(items < most ? items : most), kMoeThreads, bytes, stream>>>(a, maps, ksplit);
+    const int64_t tasks = static_cast<int64_t>(slots) * (a.w.inner / 16), most = 2 * sm_count();
+    kernel<<<static_cast<unsigned>(tasks < most ? tasks : most), kMoeThreads, bytes, stream>>>(a, maps);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
