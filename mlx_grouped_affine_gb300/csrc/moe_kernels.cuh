@@ -171,19 +171,18 @@ struct Run {
   static constexpr bool kSplit = kWhole && (BITS == 2 || BITS == 4 || BITS == 8);
   static constexpr int kSub = kCodes < 16 ? kCodes : 16;  // codes spread at a time
   // A chunk: what a warp's ring holds per stage of each row, at most 128 bytes.
-  static constexpr int kChunk = BITS <= 2 ? 256 : 128;
+  static constexpr int kChunk = BITS <= 4 ? 256 : 128;
   static constexpr int kSteps = kChunk / G;
   static constexpr int kRowBytes = kChunk * BITS / 8;
   static constexpr int kStageBytes = 2 * 16 * kRowBytes;
-  static constexpr int kDepth = kStageBytes >= 3072 ? 2 : kStageBytes >= 2048 ? 3 : 4;
+  static constexpr int kDepth = kStageBytes >= 3072 ? 2 : 4;
   static constexpr CUtensorMapSwizzle kSwizzle = kRowBytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                                  : kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                                    : CU_TENSOR_MAP_SWIZZLE_NONE;
-  // Place of byte `off` of a box: TMA swaps 16-byte units so that rows start in other banks.
-  __device__ static __forceinline__ uint32_t place(uint32_t off) {
-    if constexpr (kRowBytes == 128) return off ^ (off >> 3 & 0x70u);
-    if constexpr (kRowBytes == 64) return off ^ (off >> 3 & 0x30u);
-    return off;
+  // TMA swaps 16-byte units of a box's rows so that rows start in other banks: byte `off`
+  // of row r is at r * kRowBytes + (off ^ swap(r)), the same for r + 8.
+  __device__ static __forceinline__ uint32_t swap(uint32_t r) {
+    return kRowBytes == 128 ? (r & 7u) << 4 : kRowBytes == 64 ? (r >> 1 & 3u) << 4 : 0u;
   }
 };
 
@@ -243,15 +242,6 @@ __device__ __forceinline__ void pair_x(const uint16_t *x, uint32_t (&p)[Run<BITS
   }
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // ------------------------------------------------------------- the ring ----
 
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
@@ -275,75 +265,126 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t *v) {
 // tile t / 2 for lane 4 g + t.  16-bit types are kept in pairs.
 template <int STEPS>
 struct Scales {
+  static constexpr int kPairs = (STEPS + 1) / 2;
   uint32_t s[STEPS], b[STEPS];
-  __device__ __forceinline__ void load(const char *ps, const char *pb, int type, int64_t at, int j0, int groups) {
-    // (rows begin at multiples of `groups`, so whole chunks are aligned where it is one of STEPS)
-    if (type == kTypeF32) {
-#pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
-        const bool in = j0 + i < groups;
-        s[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(ps) + at + j0 + i) : 0u;
-        b[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(pb) + at + j0 + i) : 0u;
-      }
-      return;
+
+  template <int N>
+  __device__ static __forceinline__ void load_words(const void *p, uint32_t *v) {
+    if constexpr (N == 4) {
+      const uint4 u = __ldg(static_cast<const uint4 *>(p));
+      v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    } else if constexpr (N == 2) {
+      const uint2 u = __ldg(static_cast<const uint2 *>(p));
+      v[0] = u.x, v[1] = u.y;
+    } else {
+      v[0] = __ldg(static_cast<const uint32_t *>(p));
     }
-    const uint16_t *hs = reinterpret_cast<const uint16_t *>(ps) + at + j0, *hb = reinterpret_cast<const uint16_t *>(pb) + at + j0;
-    if (STEPS > 1 && groups % STEPS == 0) {
-      if constexpr (STEPS == 2) {
-        s[0] = __ldg(reinterpret_cast<const uint32_t *>(hs));
-        b[0] = __ldg(reinterpret_cast<const uint32_t *>(hb));
-      } else if constexpr (STEPS == 4) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(hs)), v = __ldg(reinterpret_cast<const uint2 *>(hb));
-        s[0] = u.x, s[1] = u.y, b[0] = v.x, b[1] = v.y;
-      } else if constexpr (STEPS == 8) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(hs)), v = __ldg(reinterpret_cast<const uint4 *>(hb));
-        s[0] = u.x, s[1] = u.y, s[2] = u.z, s[3] = u.w;
-        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
-      }
-      return;
+  }
+  // From ps and pb on, `count` groups of them.  `whole`: 16-bit types, rows of whole chunks
+  // (which are then aligned, as every row is).
+  __device__ __forceinline__ void load(const char *ps, const char *pb, int type, bool whole, int count) {
+    if (STEPS > 1 && whole) {
+      load_words<kPairs>(ps, s);
+      load_words<kPairs>(pb, b);
+    } else {
+      load_some(ps, pb, type, count);
     }
+  }
+  __device__ __forceinline__ void load_some(const char *ps, const char *pb, int type, int count) {
 #pragma unroll
-    for (int i = 0; i < STEPS; i += 2) {
-      uint32_t h[4] = {};
+    for (int i = 0; i < STEPS; ++i) s[i] = b[i] = 0;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (i + k < STEPS && j0 + i + k < groups) h[k] = __ldg(hs + i + k), h[2 + k] = __ldg(hb + i + k);
-      s[i / 2] = h[0] | h[1] << 16;
-      b[i / 2] = h[2] | h[3] << 16;
+    for (int i = 0; i < STEPS; ++i) {
+      if (i >= count) break;
+      if (type == kTypeF32) {
+        s[i] = __ldg(reinterpret_cast<const uint32_t *>(ps) + i);
+        b[i] = __ldg(reinterpret_cast<const uint32_t *>(pb) + i);
+      } else {
+        s[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(ps) + i)) << (16 * (i % 2));
+        b[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(pb) + i)) << (16 * (i % 2));
+      }
     }
   }
 };
 
-// The MMA's columns: rows of x (or h) of up to 8 HALVES slots, lane 4 g + t reading column g.
+// The MMA's columns: rows of x (or h) of up to 8 HALVES slots, lane 4 g + t reading column
+// g.  Columns without a slot repeat the first: nothing looks at their sums.
 template <int HALVES>
 struct Columns {
   const uint16_t *x[HALVES];  // this lane's column of each half of the pass, at its run
-  bool live[HALVES];
   int planes;
   int64_t plane;
 };
 
-// One chunk of 32 rows: acc[half][2 q + column] += s sum(c x) + b sum(x) over its groups
-// from j0 on (below `groups`), q = 2 tile + row half.
+// d = a b (FIRST) or d += a b.
+template <bool FIRST>
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The products of up to 16 codes a lane with one plane of x.
+template <int BITS, int G, bool FIRST>
+__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2], const uint16_t *px,
+                                         float (&part)[2][4], float (&ones)[4]) {
+  using R = Run<BITS, G>;
+  uint32_t x[R::kSub / 2];
+  pair_x<BITS, G>(px, x);
+#pragma unroll
+  for (int tile = 0; tile < 2; ++tile)
+    mma_bf16<FIRST>(part[tile], code[2 * tile][0], code[2 * tile + 1][0], code[2 * tile][1], code[2 * tile + 1][1], x[0], x[1]);
+  mma_bf16<FIRST>(ones, kOnes, kOnes, kOnes, kOnes, x[0], x[1]);
+#pragma unroll
+  for (int m = 1; m < R::kSub / 4; ++m) {
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile)
+      mma_bf16<false>(part[tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
+                      code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
+    mma_bf16<false>(ones, kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
+  }
+}
+
+// One chunk of 32 rows: acc[half][2 q + column] += s sum(c x) + b sum(x) over its `count`
+// groups, q = 2 tile + row half; `at` is the chunk's first column.
 template <int BITS, int G, int HALVES>
-__device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<HALVES> &c, int j0, int groups,
+__device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<HALVES> &c, int at, int count,
                                         const Scales<Run<BITS, G>::kSteps> &sc, int sb_type, float (&acc)[HALVES][8]) {
   using R = Run<BITS, G>;
-  const int t = lane % 4;
+  const int g = lane / 4, t = lane % 4;
+  const uint32_t rows = stage + g * R::kRowBytes, flip = (t * R::kBits / 32 * 4) ^ R::swap(g);
+  const uint16_t *px[HALVES];
+#pragma unroll
+  for (int half = 0; half < HALVES; ++half) px[half] = c.x[half] + at;
 #pragma unroll
   for (int step = 0; step < R::kSteps; ++step) {
-    if (j0 + step >= groups) break;
-    float part[HALVES][2][4] = {}, ones[HALVES][4] = {};
+    if (step >= count) break;
+    float part[HALVES][2][4], ones[HALVES][4];
     uint32_t v[4][R::kWords + 1];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t box = stage + (q / 2) * (16 * R::kRowBytes);
-      const uint32_t at = (lane / 4 + (q % 2) * 8) * R::kRowBytes + step * (G * BITS / 8) + t * R::kBits / 32 * 4;
+    for (int i = 0; i < R::kWords; i += R::kPiece) {
+      // (a row's 16-byte units keep their order where nothing is swapped)
+      const uint32_t off = step * (G * BITS / 8) + 4 * i;
+      const uint32_t from = rows + (R::kSwizzle == CU_TENSOR_MAP_SWIZZLE_NONE ? off + flip : R::kWhole ? off ^ flip
+                                        : ((off + t * R::kBits / 32 * 4) ^ R::swap(g)));
 #pragma unroll
-      for (int i = 0; i < R::kWords; i += R::kPiece) lds_words<R::kPiece>(box + R::place(at + 4 * i), &v[q][i]);
-      v[q][R::kWords] = 0;
-      if constexpr (!R::kWhole) {
-        const uint32_t sh = t * R::kBits % 32;
+      for (int q = 0; q < 4; ++q) lds_words<R::kPiece>(from + q * (8 * R::kRowBytes), &v[q][i]);
+    }
+    if constexpr (!R::kWhole) {
+      const uint32_t sh = t * R::kBits % 32;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v[q][R::kWords] = 0;
 #pragma unroll
         for (int i = 0; i < R::kWords; ++i) v[q][i] = __funnelshift_r(v[q][i], v[q][i + 1], sh);
       }
@@ -355,21 +396,12 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
       for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, code[q]);
 #pragma unroll
       for (int half = 0; half < HALVES; ++half) {
-        // the smallest parts of x first
-        const uint16_t *px = c.x[half] + (j0 + step) * G + sub * R::kSub + (c.planes - 1) * c.plane;
+        const uint16_t *p = px[half] + step * G + sub * R::kSub;
+        if (sub == 0) multiply<BITS, G, true>(code, p, part[half], ones[half]);
+        else multiply<BITS, G, false>(code, p, part[half], ones[half]);
 #pragma unroll 1
-        for (int plane = c.planes; plane > 0; --plane, px -= c.plane) {
-          uint32_t x[R::kSub / 2] = {};
-          if (c.live[half]) pair_x<BITS, G>(px, x);
-#pragma unroll
-          for (int m = 0; m < R::kSub / 4; ++m) {
-#pragma unroll
-            for (int tile = 0; tile < 2; ++tile)
-              mma_bf16(part[half][tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
-                       code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
-            mma_bf16(ones[half], kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
-          }
-        }
+        for (int plane = 1; plane < c.planes; ++plane)
+          multiply<BITS, G, false>(code, p + plane * c.plane, part[half], ones[half]);
       }
     }
     float sq[4], bq[4];
@@ -463,7 +495,7 @@ struct Ring {
         const int row = i / kRowWords, at = i - row * kRowWords, word = chunk * kRowWords + at;
         const uint32_t *p = (row < 16 ? s0.w : s1.w) + static_cast<int64_t>((row < 16 ? y0 : y1) + row % 16) * s0.words;
         const uint32_t v = word < s0.words ? __ldg(p + word) : 0u;
-        const uint32_t to = st + row / 16 * (R::kStageBytes / 2) + R::place((row % 16) * R::kRowBytes + 4 * at);
+        const uint32_t to = st + row / 16 * (R::kStageBytes / 2) + (row % 16) * R::kRowBytes + ((4 * at) ^ R::swap(row));
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
       }
     } else if (lane == 0) {
@@ -476,17 +508,17 @@ struct Ring {
   }
   // Waits for the oldest chunk; its stage, or 0 if the wait ran out.
   __device__ __forceinline__ uint32_t wait(bool copied, uint32_t limit, unsigned *err) {
-    uint32_t polls = 0;
     if (BITS != 4 && BITS != 8 && copied) {
       __syncwarp();
-      return base + out * R::kStageBytes;
-    }
-    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity))) {
-      if (++polls >= limit) {
-        if (lane == 0) atomicOr(err, kErrTimeoutBit);
-        dead = true;
-        return 0;
-      }
+    } else if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity))) {
+      uint32_t polls = 0;
+      do {
+        if (++polls >= limit) {
+          if (lane == 0) atomicOr(err, kErrTimeoutBit);
+          dead = true;
+          return 0;
+        }
+      } while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity)));
     }
     return base + out * R::kStageBytes;
   }
@@ -521,9 +553,8 @@ __device__ __forceinline__ void store_planes(uint16_t *p, int64_t plane, int pla
 
 struct alignas(1024) GateUpShared {  // the ring follows: swizzled boxes want 1024
   MoePlan plan;
-  // [0]: sums of a task that goes on in the next warp, [1]: of one that began in an earlier
-  alignas(16) float sums[2][kMoeWarps][32][kMoePass];
-  int task[2][kMoeWarps];  // which; -1: none
+  alignas(16) float heads[kMoeWarps][32 * kMoePass];  // sums of a warp's first task where it began in an earlier one
+  int task[2][kMoeWarps];  // the task that goes on in the next warp, the head's; -1: none
   alignas(16) uint64_t bars[kMoeWarps * 4];
   uint32_t unread[32];
 };
@@ -554,6 +585,10 @@ struct GateUp {
   int task, chunk, unit, tile, left;  // what is multiplied next, chunks left to this warp
   int l_chunk, l_unit, l_tile, l_left;  // what is loaded next
   bool l_fresh;                       // its unit's x is not in L1 yet
+  int s_chunk, s_unit, s_tile;        // whose scales are loaded next, and where they are
+  int64_t s_at;
+  int sb_bytes;
+  bool whole;
   Scales<R::kSteps> next;
 
   __device__ __forceinline__ void advance_load() {
@@ -571,11 +606,24 @@ struct GateUp {
     }
   }
   // The next chunk's scales, of the row that this lane stands for.
-  __device__ __forceinline__ void load_scales(int u, int at_tile, int at_chunk) {
-    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[u]) * a.w.inner + at_tile * 16 + lane / 4 + 8 * (lane % 2);
-    next.load(scales, biases, a.w.sb_type, row * groups, at_chunk * R::kSteps, groups);
+  __device__ __forceinline__ void load_scales() {
+    next.load(scales + s_at, biases + s_at, a.w.sb_type, whole, groups - s_chunk * R::kSteps);
+    s_at += R::kSteps * sb_bytes;
+    if (++s_chunk == chunks) {
+      if (++s_tile == tiles) s_tile = 0, ++s_unit;
+      s_chunk = 0;
+      if (s_unit < sh.plan.units) point_scales();
+    }
+  }
+  __device__ __forceinline__ void point_scales() {
+    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[s_unit]) * a.w.inner + s_tile * 16 + lane / 4 + 8 * (lane % 2);
+    s_at = (row * groups + s_chunk * R::kSteps) * sb_bytes;
   }
 
+  __device__ __forceinline__ float *starts(int w) const {
+    static_assert(R::kDepth * R::kStageBytes >= 32 * kMoePass * 4, "a warp's sums fit its ring");
+    return reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(&sh) + sizeof(GateUpShared) + w * (R::kDepth * R::kStageBytes));
+  }
   template <int HALVES>
   __device__ __forceinline__ void run_task() {
     const int g = lane / 4, t = lane % 4, count = sh.plan.unit_count[unit];
@@ -585,21 +633,17 @@ struct GateUp {
     c.plane = a.x_plane;
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) {
-      c.live[half] = 8 * half + g < count;
-      const int token = c.live[half] ? slots[8 * half + g] / a.route.top_k : 0;
+      const int token = slots[8 * half + g < count ? 8 * half + g : 0] / a.route.top_k;
       c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
     }
     float acc[HALVES][8] = {};
     const int c0 = chunk, c1 = min(chunks, chunk + left);
     for (; chunk < c1 && !ring.dead; ++chunk) {
       const Scales<R::kSteps> sc = next;
-      if (--left > 0) {
-        const bool same = chunk + 1 < chunks, last = tile + 1 == tiles;
-        load_scales(same || !last ? unit : unit + 1, same ? tile : last ? 0 : tile + 1, same ? chunk + 1 : 0);
-      }
+      if (--left > 0) load_scales();
       const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
       if (stage) {
-        consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kSteps, groups, sc, a.w.sb_type, acc);
+        consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, sc, a.w.sb_type, acc);
         ring.done();
         advance_load();
       }
@@ -619,11 +663,13 @@ struct GateUp {
     } else {
       const int kind = c0 == 0 ? 0 : 1;
       if (lane == 0) sh.task[kind][warp] = task;
+      // a task that goes on is the warp's last: its ring is free
+      float *to = kind ? sh.heads[warp] : starts(warp);
 #pragma unroll
       for (int half = 0; half < HALVES; ++half)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<float2 *>(&sh.sums[kind][warp][(q / 2) * 16 + (q % 2) * 8 + g][half * 8 + 2 * t]) =
+          *reinterpret_cast<float2 *>(to + ((q / 2) * 16 + (q % 2) * 8 + g) * kMoePass + half * 8 + 2 * t) =
               make_float2(acc[half][2 * q], acc[half][2 * q + 1]);
     }
     chunk = 0;
@@ -660,7 +706,10 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   s.scales = static_cast<const char *>(s.lane % 4 < 2 ? a.w.scales[0] : a.w.scales[1]);
   s.biases = static_cast<const char *>(s.lane % 4 < 2 ? a.w.biases[0] : a.w.biases[1]);
   for (int i = 0; i < R::kDepth; ++i) s.advance_load();
-  if (s.left > 0) s.load_scales(s.unit, s.tile, s.chunk);
+  s.sb_bytes = a.w.sb_type == kTypeF32 ? 4 : 2;
+  s.whole = a.w.sb_type != kTypeF32 && s.groups % R::kSteps == 0;
+  s.s_chunk = s.chunk, s.s_unit = s.unit, s.s_tile = s.tile;
+  if (s.left > 0) s.point_scales(), s.load_scales();
   while (s.left > 0 && !s.ring.dead) {
     if (s.sh.plan.unit_count[s.unit] > 8) s.template run_task<2>();
     else s.template run_task<1>();
@@ -674,9 +723,10 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
     if (task < 0) continue;
     const int unit = task / s.tiles, tile = task % s.tiles;
     if (place >= s.sh.plan.unit_count[unit]) continue;
-    float gate = s.sh.sums[0][w][r][place], up = s.sh.sums[0][w][16 + r][place];
+    const int at = r * kMoePass + place, two = 16 * kMoePass;
+    float gate = s.starts(w)[at], up = s.starts(w)[at + two];
     for (int v = w + 1; v < kMoeWarps; ++v)
-      if (s.sh.task[1][v] == task) gate += s.sh.sums[1][v][r][place], up += s.sh.sums[1][v][16 + r][place];
+      if (s.sh.task[1][v] == task) gate += s.sh.heads[v][at], up += s.sh.heads[v][at + two];
     const int slot = s.sh.plan.list[s.sh.plan.unit_first[unit] + place];
     store_planes(a.h + static_cast<int64_t>(slot) * a.w.inner + tile * 16 + r, a.h_plane, a.h_planes, silu_times(gate, up));
   }
@@ -735,8 +785,13 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   const char *const scales = static_cast<const char *>(a.w.scales[2]);
   const char *const biases = static_cast<const char *>(a.w.biases[2]);
   // this lane's row for scales: row g + 8 (t % 2) of tile t / 2
-  auto scale_row = [&](int unit) {
-    return static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.hidden + row0 + g + 8 * t;
+  const int sb_bytes = a.w.sb_type == kTypeF32 ? 4 : 2;
+  const bool whole = a.w.sb_type != kTypeF32 && groups % R::kSteps == 0;
+  Scales<R::kSteps> next;
+  auto load_scales = [&](int unit, int chunk) {
+    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.hidden + row0 + g + 8 * t;
+    const int64_t at = (row * groups + chunk * R::kSteps) * sb_bytes;
+    next.load(scales + at, biases + at, a.w.sb_type, whole, groups - chunk * R::kSteps);
   };
 
   const bool copied = static_cast<int64_t>(a.w.inner) * BITS % 128 != 0;
@@ -756,8 +811,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     if (++load_chunk == chunks) load_chunk = 0, ++load_unit;
   };
   for (int i = 0; i < R::kDepth; ++i) load_next(false);
-  Scales<R::kSteps> next;
-  if (step0 < step1) next.load(scales, biases, a.w.sb_type, scale_row(first_unit) * groups, first_chunk * R::kSteps, groups);
+  if (step0 < step1) load_scales(first_unit, first_chunk);
   griddep_wait();  // h is complete; the weights above do not depend on it
   for (int i = step0, u = first_unit, k = first_chunk; i < load_step; ++i) {
     touch_h(u, k);
@@ -775,8 +829,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     c.plane = a.h_plane;
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) {
-      c.live[half] = 8 * half + g < count;
-      const int slot = c.live[half] ? slots[8 * half + g] : 0;
+      const int slot = slots[8 * half + g < count ? 8 * half + g : 0];
       c.x[half] = a.h + static_cast<int64_t>(slot) * a.w.inner + t * R::kCodes;
     }
     float acc[HALVES][8] = {};
@@ -785,12 +838,11 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
       ++step;
       if (step < step1) {
         const bool same = j + 1 < chunks;
-        next.load(scales, biases, a.w.sb_type, scale_row(same ? unit : unit + 1) * groups, same ? (j + 1) * R::kSteps : 0,
-                  groups);
+        load_scales(same ? unit : unit + 1, same ? j + 1 : 0);
       }
       const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
       if (stage) {
-        consume<BITS, G, HALVES>(stage, lane, c, j * R::kSteps, groups, sc, a.w.sb_type, acc);
+        consume<BITS, G, HALVES>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, sc, a.w.sb_type, acc);
         ring.done();
         load_next(true);
       }
