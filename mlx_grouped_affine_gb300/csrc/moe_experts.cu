@@ -1,16 +1,129 @@
-// qmm_moe_experts and qmm_moe_layer: gated feed-forward of each token's experts, in two
-// kernels (moe_kernels.cuh): gate and up with silu, then down with the sum over a token's
-// experts.  x that is not bf16 is first cut into bf16 planes that hold it exactly.
+// qmm_moe_experts and qmm_moe_layer: gated feed-forward of each token's experts.  The plan
+// (routing, which slots go to which expert) and x's bf16 planes in one small kernel, then
+// gate and up with silu, then down with the sum over a token's experts (moe_kernels.cuh).
+//
+// The plan is one block's work of a few microseconds, nearly all of it latency: misses of
+// the instruction cache, one trip to memory for the logits, two warp reductions a choice.
+// When every block of the expert kernels made its own plan instead, that was 24 000 cycles
+// at the start of each of them (16 tokens of 8 experts); reading it takes 1 500.
 #include "moe_kernels.cuh"
+#include "moe_route.cuh"
 #include "workspace.h"
 
 namespace qmm {
 namespace {
 
-__global__ void __launch_bounds__(256)
-planes_kernel(const void *__restrict__ x, int type, int64_t n, uint16_t *__restrict__ planes, int64_t plane, int count) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
-    store_planes(planes + i, plane, count, load_logit(x, type, i));
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+
+struct PlanShared {
+  alignas(16) short expert[kMoeMaxSlots];  // of a slot; -1: no part in y
+  short place[kMoeMaxSlots];               // among its expert's slots
+  float weight[kMoeMaxSlots];
+  int table[kMoeMaxExperts];               // of experts that have slots: the first in `list` | first unit << 16
+  int part[kMoeMaxSlots / 32];
+};
+
+template <int NV>
+__device__ __noinline__ void route_tokens(const Routing r, int tokens, int experts, PlanShared &p) {
+  const int lane = threadIdx.x % 32;
+  for (int t = threadIdx.x / 32; t < tokens; t += kPlanWarps) {
+    int id[1];
+    float weight[1];
+    route_rows<NV, 1>(r, experts, t, tokens, lane, id, weight);
+    if (lane < r.top_k) {
+      p.expert[t * r.top_k + lane] = static_cast<short>(weight[0] == 0.0f ? -1 : id[0]);
+      p.weight[t * r.top_k + lane] = weight[0];
+    }
+  }
+}
+
+__device__ void make_plan(const Routing r, const int tokens, const int experts, unsigned *err, PlanShared &p,
+                          MoePlan *out) {
+  const int slots = tokens * r.top_k, s = threadIdx.x, lane = s % 32;
+  if (!r.logits) {
+    if (s < slots) {
+      int id = r.ids[s];
+      const float weight = r.weights[s];
+      if (id < 0 || id >= experts) {
+        atomicOr(err, kErrIndexBit);
+        id = -1;
+      }
+      p.expert[s] = static_cast<short>(weight == 0.0f ? -1 : id);
+      p.weight[s] = weight;
+    }
+  } else if (experts <= 128) {
+    route_tokens<4>(r, tokens, experts, p);
+  } else if (experts <= 256) {
+    route_tokens<8>(r, tokens, experts, p);
+  } else {
+    route_tokens<32>(r, tokens, experts, p);
+  }
+  if (s >= slots && s < (slots + 7) / 8 * 8) p.expert[s] = -1;
+  __syncthreads();
+  // Slots of the same expert, before this one and in all: every pair of slots is compared.
+  // Then the scan over slots of (slots, units) that begin with each expert's first slot.
+  int mine = 0, sum = 0;
+  if (s / 32 * 32 < slots) {  // (whole warps)
+    const int e = s < slots ? p.expert[s] : -1;
+    int before = 0, all = 0;
+    for (int o = 0; o < slots; o += 8) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(&p.expert[o]);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool same = static_cast<short>(w[k / 2] >> (16 * (k % 2))) == e;
+        all += same;
+        before += same && o + k < s;
+      }
+    }
+    if (e >= 0) p.place[s] = static_cast<short>(before);
+    if (e >= 0 && before == 0) mine = all | (all + kMoePass - 1) / kMoePass << 16;
+    sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    if (lane == 31) p.part[s / 32] = sum;
+  }
+  __syncthreads();
+  if (s / 32 * 32 < slots) {
+    int at = sum - mine;
+    for (int k = 0; k < s / 32; ++k) at += p.part[k];
+    if (mine) {
+      const int e = p.expert[s], n = mine & 0xFFFF, units = mine >> 16, unit = at >> 16;
+      p.table[e] = at;
+      for (int k = 0; k < units; ++k) {
+        out->unit_expert[unit + k] = static_cast<short>(e);
+        out->unit_first[unit + k] = static_cast<short>((at & 0xFFFF) + k * kMoePass);
+        out->unit_count[unit + k] = static_cast<short>(min(kMoePass, n - k * kMoePass));
+      }
+    }
+    if (s / 32 == (slots - 1) / 32 && lane == 31) out->units = (at + mine) >> 16;
+  }
+  __syncthreads();
+  if (s < slots) {
+    const int e = p.expert[s], at = e < 0 ? 0 : p.table[e], place = e < 0 ? 0 : p.place[s];
+    if (e >= 0) out->list[(at & 0xFFFF) + place] = static_cast<short>(s);
+    out->slot_unit[s] = static_cast<short>(e < 0 ? -1 : (at >> 16) + place / kMoePass);
+    out->slot_place[s] = static_cast<short>(place % kMoePass);
+    out->slot_weight[s] = p.weight[s];
+  }
+}
+
+// Block 0: the plan.  The others: the planes of x (n elements), where it is not bf16.
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const __grid_constant__ Routing r, int tokens, int experts, unsigned *err, MoePlan *plan,
+            const void *__restrict__ x, int x_type, int64_t n, uint16_t *__restrict__ planes, int64_t plane, int count) {
+  __shared__ PlanShared shared;
+  griddep_launch_dependents();
+  if (blockIdx.x == 0) {
+    make_plan(r, tokens, experts, err, shared, plan);
+    return;
+  }
+  const int64_t stride = static_cast<int64_t>(gridDim.x - 1) * kPlanThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x - 1) * kPlanThreads + threadIdx.x; i < n; i += stride)
+    store_planes(planes + i, plane, count, load_logit(x, x_type, i));
 }
 
 int64_t round128(int64_t n) { return (n + 127) / 128 * 128; }
@@ -18,7 +131,8 @@ int64_t round128(int64_t n) { return (n + 127) / 128 * 128; }
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner) {
-  return static_cast<size_t>(kWorkspaceAlign + 2 * 3 * round128(tokens * hidden) + 2 * 3 * round128(tokens * top_k * inner));
+  return static_cast<size_t>(kWorkspaceAlign + round128(sizeof(MoePlan)) + 2 * 3 * round128(tokens * hidden) +
+                             2 * 3 * round128(tokens * top_k * inner));
 }
 
 cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Routing &r, const ExpertWeights &w,
@@ -28,29 +142,28 @@ cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Rout
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidSymbol;
   const Workspace ws = aligned_workspace(workspace, workspace_bytes);
+  MoePlan *plan = reinterpret_cast<MoePlan *>(ws.base);
+  uint16_t *planes = reinterpret_cast<uint16_t *>(ws.base + round128(sizeof(MoePlan)));
   const int64_t n = static_cast<int64_t>(tokens) * w.hidden;
-  uint16_t *planes = reinterpret_cast<uint16_t *>(ws.base);
   a.route = r;
   a.w = w;
   a.tokens = tokens;
   a.y = y;
   a.y_type = y_type;
+  a.plan = plan;
   a.wait_limit = wait_limit();
   a.x_plane = round128(n);
   a.x_planes = x_type == kTypeBF16 ? 1 : x_type == kTypeF16 ? 2 : 3;
+  a.x = x_type == kTypeBF16 ? static_cast<const uint16_t *>(x) : planes;
   a.h = planes + 3 * a.x_plane;
   a.h_plane = round128(static_cast<int64_t>(tokens) * r.top_k * w.inner);
   a.h_planes = x_type == kTypeF32 ? 3 : 2;
-  if (x_type == kTypeBF16) {
-    a.x = static_cast<const uint16_t *>(x);
-  } else {
-    a.x = planes;
-    const int64_t blocks = (n + 255) / 256, most = 8 * sm_count();
-    planes_kernel<<<static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream>>>(x, x_type, n, planes, a.x_plane,
-                                                                                         a.x_planes);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
+  const int64_t blocks = (n + kPlanThreads - 1) / kPlanThreads, most = 2 * sm_count();
+  const unsigned grid = x_type == kTypeBF16 ? 1u : 1u + static_cast<unsigned>(blocks < most ? blocks : most);
+  plan_kernel<<<grid, kPlanThreads, 0, stream>>>(r, tokens, w.experts, a.err, plan, x, x_type, n, planes, a.x_plane,
+                                                  a.x_planes);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   switch (w.bits) {
     case 1:
     case 2: return launch_moe_bits_1_2(a, stream);

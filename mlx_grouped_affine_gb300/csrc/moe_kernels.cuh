@@ -18,7 +18,7 @@
 // for 2048 codes a warp.)  8 slots fill the MMA's columns; 16 slots of an expert are taken
 // per pass over its weights.
 #pragma once
-#include "moe_route.cuh"
+#include "common.cuh"
 
 namespace qmm {
 
@@ -30,6 +30,8 @@ template <int N>
 struct Int {
   static constexpr int value = N;
 };
+
+struct MoePlan;
 
 // What the kernels share of a call.
 struct MoeArgs {
@@ -44,105 +46,41 @@ struct MoeArgs {
   int tokens;
   void *y;
   int y_type;
+  const MoePlan *plan;
   unsigned *err;
   uint32_t wait_limit;
 };
 
 // ------------------------------------------------------------- the plan ----
-// Which slots (token * top_k + place) go to which expert.  Every block works it out for
-// itself: that is cheaper than waiting for another kernel's answer.  A unit is an expert
-// with up to kMoePass of its slots; an expert's units follow one another, its slots are in
-// order, and experts come in the order of their first slots, so that all blocks agree.
-struct alignas(16) MoePlan {
+// Which slots (token * top_k + place) go to which expert (moe_experts.cu works it out).  A
+// unit is an expert with up to kMoePass of its slots; an expert's units follow one another,
+// its slots are in order, and experts come in the order of their first slots.
+struct MoePlan {
   int units;
-  int table[kMoeMaxExperts];                   // slots of an expert; then its first in `list` | first unit << 16
   short unit_expert[kMoeMaxSlots];
-  short unit_first[kMoeMaxSlots];              // in `list`
+  short unit_first[kMoeMaxSlots];   // in `list`
   short unit_count[kMoeMaxSlots];
-  short list[kMoeMaxSlots];                    // slots, unit by unit
-  short slot_expert[kMoeMaxSlots];             // -1: no part in y
-  short slot_place[kMoeMaxSlots];              // among its expert's slots
+  short list[kMoeMaxSlots];         // slots, unit by unit
+  short slot_unit[kMoeMaxSlots];    // -1: no part in y
+  short slot_place[kMoeMaxSlots];   // in its unit
   float slot_weight[kMoeMaxSlots];
 };
 
-template <int NV>
-__device__ __noinline__ void route_token(Routing r, int experts, int t, int lane, int *id, float *weight) {
-  int i;
-  float w;
-  route_row<NV>(r, experts, t, lane, i, w);
-  *id = i;
-  *weight = w;
-}
-
-// By value: what is passed by reference would be read through memory again and again.
-static __device__ __noinline__ void make_plan(const Routing r, const int tokens, const int experts, unsigned *err,
-                                              MoePlan &p) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, top = r.top_k;
-  for (int e = threadIdx.x; e < experts; e += kMoeThreads) p.table[e] = 0;
-  for (int t = warp; t < tokens; t += kMoeWarps) {
-    int id = -1;
-    float weight = 0.0f;
-    if (!r.logits) {
-      if (lane < top) id = r.ids[t * top + lane], weight = r.weights[t * top + lane];
-    } else if (experts <= 128) {
-      route_row<4>(r, experts, t, lane, id, weight);
-    } else if (experts <= 256) {
-      route_row<8>(r, experts, t, lane, id, weight);
-    } else {
-      route_token<32>(r, experts, t, lane, &id, &weight);
-    }
-    if (lane < top) {
-      if (id < 0 || id >= experts) {
-        if (blockIdx.x == 0) atomicOr(err, kErrIndexBit);
-        id = -1;
-      }
-      if (weight == 0.0f) id = -1;
-      p.slot_expert[t * top + lane] = static_cast<short>(id);
-      p.slot_weight[t * top + lane] = weight;
+// The block's copy of what the kernels need of it.  (From L2: a kernel that was launched
+// early may hold nothing older in L1, but this asks for no more than it needs.)
+__device__ __forceinline__ void read_plan(const MoePlan *from, MoePlan &p, int slots, bool slots_too) {
+  for (int i = threadIdx.x; i < slots; i += kMoeThreads) {
+    p.unit_expert[i] = __ldcg(&from->unit_expert[i]);
+    p.unit_first[i] = __ldcg(&from->unit_first[i]);
+    p.unit_count[i] = __ldcg(&from->unit_count[i]);
+    p.list[i] = __ldcg(&from->list[i]);
+    if (slots_too) {
+      p.slot_unit[i] = __ldcg(&from->slot_unit[i]);
+      p.slot_place[i] = __ldcg(&from->slot_place[i]);
+      p.slot_weight[i] = __ldcg(&from->slot_weight[i]);
     }
   }
-  __syncthreads();
-  const int slots = tokens * top;
-  if (warp == 0) {
-    for (int s0 = 0; s0 < slots; s0 += 32) {  // places: slots of the same expert before
-      const int s = s0 + lane, e = s < slots ? p.slot_expert[s] : -1;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
-      const int place = __popc(same & ((1u << lane) - 1u)) + (e < 0 ? 0 : p.table[e]);
-      __syncwarp();
-      if (e >= 0) {
-        p.slot_place[s] = static_cast<short>(place);
-        if (same >> lane == 1u) p.table[e] = place + 1;  // the last of them
-      }
-      __syncwarp();
-    }
-    int before = 0;  // slots | units << 16 of the experts before
-    for (int s0 = 0; s0 < slots; s0 += 32) {  // units, at each expert's first slot
-      const int s = s0 + lane, e = s < slots ? p.slot_expert[s] : -1;
-      const int n = e >= 0 && p.slot_place[s] == 0 ? p.table[e] : 0;
-      const int units = (n + kMoePass - 1) / kMoePass, own = n | units << 16;
-      int sum = own;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      const int at = before + sum - own, unit = at >> 16;
-      __syncwarp();
-      if (n > 0) p.table[e] = at;
-      for (int i = 0; i < units; ++i) {
-        p.unit_expert[unit + i] = static_cast<short>(e);
-        p.unit_first[unit + i] = static_cast<short>((at & 0xFFFF) + i * kMoePass);
-        p.unit_count[unit + i] = static_cast<short>(min(kMoePass, n - i * kMoePass));
-      }
-      before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    if (lane == 0) p.units = before >> 16;
-  }
-  __syncthreads();
-  for (int s = threadIdx.x; s < slots; s += kMoeThreads) {
-    const int e = p.slot_expert[s];
-    if (e >= 0) p.list[(p.table[e] & 0xFFFF) + p.slot_place[s]] = static_cast<short>(s);
-  }
+  if (threadIdx.x == 0) p.units = __ldcg(&from->units);
   __syncthreads();
 }
 
@@ -176,6 +114,8 @@ struct Run {
   static constexpr int kRowBytes = kChunk * BITS / 8;
   static constexpr int kStageBytes = 2 * 16 * kRowBytes;
   static constexpr int kDepth = kStageBytes >= 3072 ? 2 : 4;
+  // A warp's part of the ring: its stages, then a chunk's scales as every lane reads them.
+  static constexpr int kWarpBytes = kDepth * kStageBytes + (kSteps * 256 + 1023) / 1024 * 1024;
   static constexpr CUtensorMapSwizzle kSwizzle = kRowBytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
                                                  : kRowBytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                                    : CU_TENSOR_MAP_SWIZZLE_NONE;
@@ -185,12 +125,6 @@ struct Run {
     return kRowBytes == 128 ? (r & 7u) << 4 : kRowBytes == 64 ? (r >> 1 & 3u) << 4 : 0u;
   }
 };
-
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 
 // Codes as bf16 pairs, each code * 2^-6.  A bf16 pattern P <= 0xFF is worth P * 2^-133, so
 // a code at bit o of a half reads as c * 2^(o - 133), and times 2^(127 - o) it is exact and
@@ -209,13 +143,13 @@ __device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, uint32_
 #pragma unroll
       for (int j = 0; j < kHalf; ++j) {
         const int o = j * BITS % 8, sh = j * BITS - o;
-        p[i * kHalf + j] = bf16x2_mul((w >> sh) & (kMask << o), ((254u - o) << 7) * 0x00010001u);
+        p[i * kHalf + j] = bf16x2_fma((w >> sh) & (kMask << o), ((254u - o) << 7) * 0x00010001u, 0x80008000u);
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < R::kSub / 2; ++i)
-      p[i] = bf16x2_mul(pair_at<BITS>(v, sub * R::kSub + 2 * i), (254u << 7) * 0x00010001u);
+      p[i] = bf16x2_fma(pair_at<BITS>(v, sub * R::kSub + 2 * i), (254u << 7) * 0x00010001u, 0x80008000u);
   }
 }
 
@@ -280,6 +214,22 @@ struct Scales {
       v[0] = __ldg(static_cast<const uint32_t *>(p));
     }
   }
+  // As fp32 pairs (s, b) to `to`, [step][lane's row]: what every lane of the rows reads.
+  __device__ __forceinline__ void spread(uint32_t to, int lane, int type) const {
+    const uint32_t at = to + ((lane % 4) * 8 + lane / 4) * 8;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      float fs, fb;
+      if (type == kTypeF32) {
+        fs = __uint_as_float(s[i]), fb = __uint_as_float(b[i]);
+      } else {
+        const uint32_t u = prmt(s[i / 2], b[i / 2], i & 1 ? 0x7632u : 0x5410u);
+        if (type == kTypeBF16) fs = __uint_as_float(u << 16), fb = __uint_as_float(u & 0xFFFF0000u);
+        else fs = ElemF16::to_f32(u & 0xFFFFu), fb = ElemF16::to_f32(u >> 16);
+      }
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + i * 256), "f"(fs), "f"(fb) : "memory");
+    }
+  }
   // From ps and pb on, `count` groups of them.  `whole`: 16-bit types, rows of whole chunks
   // (which are then aligned, as every row is).
   __device__ __forceinline__ void load(const char *ps, const char *pb, int type, bool whole, int count) {
@@ -336,11 +286,9 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 
 // The products of up to 16 codes a lane with one plane of x.
 template <int BITS, int G, bool FIRST>
-__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2], const uint16_t *px,
-                                         float (&part)[2][4], float (&ones)[4]) {
+__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2],
+                                         const uint32_t (&x)[Run<BITS, G>::kSub / 2], float (&part)[2][4], float (&ones)[4]) {
   using R = Run<BITS, G>;
-  uint32_t x[R::kSub / 2];
-  pair_x<BITS, G>(px, x);
 #pragma unroll
   for (int tile = 0; tile < 2; ++tile)
     mma_bf16<FIRST>(part[tile], code[2 * tile][0], code[2 * tile + 1][0], code[2 * tile][1], code[2 * tile + 1][1], x[0], x[1]);
@@ -356,19 +304,22 @@ __device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>:
 }
 
 // One chunk of 32 rows: acc[half][2 q + column] += s sum(c x) + b sum(x) over its `count`
-// groups, q = 2 tile + row half; `at` is the chunk's first column.
+// groups, q = 2 tile + row half; `at` is the chunk's first column, `scales` where its scales
+// were spread.  Not unrolled over groups: the warps share an instruction cache that the body
+// must not outgrow.
 template <int BITS, int G, int HALVES>
 __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<HALVES> &c, int at, int count,
-                                        const Scales<Run<BITS, G>::kSteps> &sc, int sb_type, float (&acc)[HALVES][8]) {
+                                        uint32_t scales, float (&acc)[HALVES][8]) {
   using R = Run<BITS, G>;
   const int g = lane / 4, t = lane % 4;
   const uint32_t rows = stage + g * R::kRowBytes, flip = (t * R::kBits / 32 * 4) ^ R::swap(g);
   const uint16_t *px[HALVES];
 #pragma unroll
   for (int half = 0; half < HALVES; ++half) px[half] = c.x[half] + at;
-#pragma unroll
-  for (int step = 0; step < R::kSteps; ++step) {
-    if (step >= count) break;
+  uint32_t sb = scales + g * 8;
+  count = min(count, R::kSteps);
+#pragma unroll 1
+  for (int step = 0; step < count; ++step, sb += 256) {
     float part[HALVES][2][4], ones[HALVES][4];
     uint32_t v[4][R::kWords + 1];
 #pragma unroll
@@ -391,48 +342,37 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
     }
 #pragma unroll
     for (int sub = 0; sub < R::kCodes / R::kSub; ++sub) {
+      uint32_t x[HALVES][R::kSub / 2];  // loaded ahead of the codes' instructions
+#pragma unroll
+      for (int half = 0; half < HALVES; ++half) pair_x<BITS, G>(px[half] + sub * R::kSub, x[half]);
       uint32_t code[4][R::kSub / 2];
 #pragma unroll
       for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, code[q]);
 #pragma unroll
       for (int half = 0; half < HALVES; ++half) {
-        const uint16_t *p = px[half] + step * G + sub * R::kSub;
-        if (sub == 0) multiply<BITS, G, true>(code, p, part[half], ones[half]);
-        else multiply<BITS, G, false>(code, p, part[half], ones[half]);
+        if (sub == 0) multiply<BITS, G, true>(code, x[half], part[half], ones[half]);
+        else multiply<BITS, G, false>(code, x[half], part[half], ones[half]);
 #pragma unroll 1
-        for (int plane = 1; plane < c.planes; ++plane)
-          multiply<BITS, G, false>(code, p + plane * c.plane, part[half], ones[half]);
-      }
-    }
-    float sq[4], bq[4];
-    if (sb_type == kTypeF32) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        sq[q] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.s[step], q, 4));
-        bq[q] = __uint_as_float(__shfl_sync(0xFFFFFFFFu, sc.b[step], q, 4));
-      }
-    } else {
-      const uint32_t both = prmt(sc.s[step / 2], sc.b[step / 2], step & 1 ? 0x7632u : 0x5410u);
-      uint32_t u[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) u[q] = __shfl_sync(0xFFFFFFFFu, both, q, 4);
-      if (sb_type == kTypeBF16) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sq[q] = __uint_as_float(u[q] << 16), bq[q] = __uint_as_float(u[q] & 0xFFFF0000u);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sq[q] = ElemF16::to_f32(u[q] & 0xFFFFu), bq[q] = ElemF16::to_f32(u[q] >> 16);
+        for (int plane = 1; plane < c.planes; ++plane) {
+          pair_x<BITS, G>(px[half] + sub * R::kSub + plane * c.plane, x[half]);
+          multiply<BITS, G, false>(code, x[half], part[half], ones[half]);
+        }
       }
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int half = 0; half < HALVES; ++half) px[half] += G;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float s, b;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(s), "=f"(b) : "r"(sb + q * 64));
 #pragma unroll
       for (int half = 0; half < HALVES; ++half)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float &y = acc[half][2 * q + i];
-          y = fmaf(sq[q], part[half][q / 2][2 * (q % 2) + i], fmaf(bq[q], ones[half][i], y));
+          y = fmaf(s, part[half][q / 2][2 * (q % 2) + i], fmaf(b, ones[half][i], y));
         }
+    }
   }
 }
 
@@ -474,7 +414,7 @@ struct Ring {
   bool dead;         // a wait ran out: nothing more is issued or read
 
   __device__ __forceinline__ void init(unsigned char *stages, uint64_t *barriers, int warp, int lane_) {
-    base = smem_u32(stages) + warp * (R::kDepth * R::kStageBytes);
+    base = smem_u32(stages) + warp * R::kWarpBytes;
     bars = barriers + warp * R::kDepth;
     lane = lane_;
     in = out = flying = 0;
@@ -508,9 +448,7 @@ struct Ring {
   }
   // Waits for the oldest chunk; its stage, or 0 if the wait ran out.
   __device__ __forceinline__ uint32_t wait(bool copied, uint32_t limit, unsigned *err) {
-    if (BITS != 4 && BITS != 8 && copied) {
-      __syncwarp();
-    } else if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity))) {
+    if ((BITS == 4 || BITS == 8 || !copied) && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity))) {
       uint32_t polls = 0;
       do {
         if (++polls >= limit) {
@@ -520,6 +458,7 @@ struct Ring {
         }
       } while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity)));
     }
+    __syncwarp();
     return base + out * R::kStageBytes;
   }
   // The stage may be filled again.
@@ -622,7 +561,7 @@ struct GateUp {
 
   __device__ __forceinline__ float *starts(int w) const {
     static_assert(R::kDepth * R::kStageBytes >= 32 * kMoePass * 4, "a warp's sums fit its ring");
-    return reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(&sh) + sizeof(GateUpShared) + w * (R::kDepth * R::kStageBytes));
+    return reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(&sh) + sizeof(GateUpShared) + w * R::kWarpBytes);
   }
   template <int HALVES>
   __device__ __forceinline__ void run_task() {
@@ -636,14 +575,16 @@ struct GateUp {
       const int token = slots[8 * half + g < count ? 8 * half + g : 0] / a.route.top_k;
       c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
     }
+    const uint32_t spread = ring.base + R::kDepth * R::kStageBytes;
     float acc[HALVES][8] = {};
     const int c0 = chunk, c1 = min(chunks, chunk + left);
     for (; chunk < c1 && !ring.dead; ++chunk) {
-      const Scales<R::kSteps> sc = next;
+      // (the chunk before is read: done() has met the warp)
+      next.spread(spread, lane, a.w.sb_type);
       if (--left > 0) load_scales();
       const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
       if (stage) {
-        consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, sc, a.w.sb_type, acc);
+        consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, spread, acc);
         ring.done();
         advance_load();
       }
@@ -687,14 +628,20 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   s.warp = threadIdx.x / 32, s.lane = threadIdx.x % 32;
   s.ring.init(raw + sizeof(GateUpShared), s.sh.bars, s.warp, s.lane);
   if (threadIdx.x < 2 * kMoeWarps) s.sh.task[threadIdx.x / kMoeWarps][threadIdx.x % kMoeWarps] = -1;
+  // The plan and x's planes are complete.  Kernels launched from here on may read the plan
+  // too, before this one is done.
+  griddep_wait();
   griddep_launch_dependents();
-  make_plan(a.route, a.tokens, a.w.experts, a.err, s.sh.plan);
+  read_plan(a.plan, s.sh.plan, a.tokens * a.route.top_k, false);
   s.tiles = a.w.inner / 16, s.groups = a.w.hidden / G, s.chunks = (a.w.hidden + R::kChunk - 1) / R::kChunk;
-  const int64_t tasks = static_cast<int64_t>(s.sh.plan.units) * s.tiles;
-  const int t0 = static_cast<int>(tasks * blockIdx.x / gridDim.x), t1 = static_cast<int>(tasks * (blockIdx.x + 1) / gridDim.x);
-  const int64_t steps = static_cast<int64_t>(t1 - t0) * s.chunks;
-  const int from = static_cast<int>(steps * s.warp / kMoeWarps);
-  s.left = s.l_left = static_cast<int>(steps * (s.warp + 1) / kMoeWarps) - from;
+  // Tasks t0 .. t1 of the block, an even share; steps from .. of the warp.
+  const int tasks = s.sh.plan.units * s.tiles, grid = gridDim.x, block = blockIdx.x;
+  const int share = tasks / grid, rest = tasks - share * grid;
+  const int t0 = share * block + min(block, rest), t1 = t0 + share + (block < rest);
+  const int steps = (t1 - t0) * s.chunks;
+  auto cut = [&](int w) { return steps / kMoeWarps * w + steps % kMoeWarps * w / kMoeWarps; };
+  const int from = cut(s.warp);
+  s.left = s.l_left = cut(s.warp + 1) - from;
   s.task = t0 + from / s.chunks;
   s.chunk = s.l_chunk = from % s.chunks;
   s.unit = s.l_unit = s.task / s.tiles;
@@ -764,11 +711,11 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   using R = Run<BITS, G>;
   extern __shared__ __align__(1024) unsigned char raw[];
   DownShared &sh = *reinterpret_cast<DownShared *>(raw);
-  float *z = reinterpret_cast<float *>(raw + sizeof(DownShared) + kMoeWarps * R::kDepth * R::kStageBytes);
+  float *z = reinterpret_cast<float *>(raw + sizeof(DownShared) + kMoeWarps * R::kWarpBytes);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   Ring<BITS, G> ring;
   ring.init(raw + sizeof(DownShared), sh.bars, warp, lane);
-  make_plan(a.route, a.tokens, a.w.experts, a.err, sh.plan);
+  read_plan(a.plan, sh.plan, a.tokens * a.route.top_k, true);
   const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * 32;
   const int groups = a.w.inner / G, chunks = (a.w.inner + R::kChunk - 1) / R::kChunk;
   const int total = sh.plan.units * chunks;  // at most 2^22: sizes are at most 2^20
@@ -818,6 +765,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     if (++k == chunks) k = 0, ++u;
   }
 
+  const uint32_t spread = ring.base + R::kDepth * R::kStageBytes;
   int step = step0;
   auto run_unit = [&](auto halves, int unit, int j0) {
     constexpr int HALVES = decltype(halves)::value;
@@ -834,7 +782,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     }
     float acc[HALVES][8] = {};
     for (int j = j0; j < j1 && !ring.dead; ++j) {
-      const Scales<R::kSteps> sc = next;
+      next.spread(spread, lane, a.w.sb_type);
       ++step;
       if (step < step1) {
         const bool same = j + 1 < chunks;
@@ -842,7 +790,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
       }
       const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
       if (stage) {
-        consume<BITS, G, HALVES>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, sc, a.w.sb_type, acc);
+        consume<BITS, G, HALVES>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, spread, acc);
         ring.done();
         load_next(true);
       }
@@ -873,13 +821,12 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     float sum = 0.0f;
 #pragma unroll 4
     for (int k = 0; k < a.route.top_k; ++k) {
-      const int slot = token * a.route.top_k + k, e = sh.plan.slot_expert[slot];
-      if (e < 0) continue;
-      const int place = sh.plan.slot_place[slot], unit = (sh.plan.table[e] >> 16) + place / kMoePass;
+      const int slot = token * a.route.top_k + k, unit = sh.plan.slot_unit[slot], place = sh.plan.slot_place[slot];
+      if (unit < 0) continue;
       const int from = sh.unit_from[unit], to = sh.unit_to[unit];
       float v = remote_f32(z_at + slot * 128, from / kMoeWarps);
       for (int w = from + 1; w <= to; ++w)
-        v += remote_f32(heads_at + ((w % kMoeWarps) * kMoePass + place % kMoePass) * 128, w / kMoeWarps);
+        v += remote_f32(heads_at + ((w % kMoeWarps) * kMoePass + place) * 128, w / kMoeWarps);
       sum = fmaf(sh.plan.slot_weight[slot], v, sum);
     }
     const int64_t at = static_cast<int64_t>(token) * a.w.hidden + row0 + lane;
@@ -903,7 +850,7 @@ cudaError_t weight_map(CUtensorMap *map, const uint32_t *w, int64_t rows, int co
 template <int BITS, int G>
 cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   using R = Run<BITS, G>;
-  const size_t ring = kMoeWarps * R::kDepth * R::kStageBytes;
+  const size_t ring = kMoeWarps * R::kWarpBytes;
   const int slots = a.tokens * a.route.top_k;
   MoeMaps maps = {};
   const int64_t inner_rows = static_cast<int64_t>(a.w.experts) * a.w.inner;
@@ -918,8 +865,17 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
     e = ensure_smem_limit<kernel>(bytes);
     if (e != cudaSuccess) return e;
     const int64_t tasks = static_cast<int64_t>(slots) * (a.w.inner / 16), most = 2 * sm_count();
-    kernel<<<static_cast<unsigned>(tasks < most ? tasks : most), kMoeThreads, bytes, stream>>>(a, maps);
-    e = cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tasks < most ? tasks : most));
+    cfg.blockDim = dim3(kMoeThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, a, maps);
     if (e != cudaSuccess) return e;
   }
   constexpr auto kernel = down_kernel<BITS, G>;

@@ -28,71 +28,84 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The whole warp routes row `row`.  Lane j < top_k returns the row's j-th expert and its
-// weight.  NV = ceil(experts / 32), or more: expert 32 i + lane is entry i of a lane.
-template <int NV>
-__device__ __forceinline__ void route_row(const Routing &r, int experts, int64_t row, int lane,
-                                          int &id, float &weight) {
-  uint32_t key[NV];
+// The whole warp routes rows row .. row + ROWS - 1 (those below `end`), side by side: a
+// choice is two warp reductions long, and rows hide each other's.  Lane j < top_k gets each
+// row's j-th expert and its weight.  NV = ceil(experts / 32), or more: expert 32 i + lane is
+// entry i of a lane.
+template <int NV, int ROWS>
+__device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_t row, int64_t end, int lane,
+                                           int (&id)[ROWS], float (&weight)[ROWS]) {
+  uint32_t key[ROWS][NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = 32 * i + lane;
-    key[i] = e < experts ? logit_key(load_logit(r.logits, r.type, row * experts + e)) : 0u;
-  }
-  float total = 1.0f, largest = 0.0f;
+  for (int k = 0; k < ROWS; ++k)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = 32 * i + lane;
+      key[k][i] = e < experts && row + k < end ? logit_key(load_logit(r.logits, r.type, (row + k) * experts + e)) : 0u;
+    }
+  float total[ROWS], largest[ROWS];
+  uint32_t chosen[ROWS];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) total[k] = 1.0f, largest[k] = 0.0f, chosen[k] = 0, id[k] = 0;
   if (!r.sigmoid) {
-    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) m = max(m, key[i]);
-    largest = key_logit(__reduce_max_sync(0xFFFFFFFFu, m));
-    if (!r.normalize) {  // (the sum over all cancels where the chosen are divided by theirs)
-      float part = 0.0f;
+    for (int k = 0; k < ROWS; ++k) {
+      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const float l = key_logit(key[i]);
-        if (key[i] != 0u && l != -INFINITY) part += l == largest ? 1.0f : __expf(l - largest);
+      for (int i = 0; i < NV; ++i) m = max(m, key[k][i]);
+      largest[k] = key_logit(__reduce_max_sync(0xFFFFFFFFu, m));
+      if (!r.normalize) {  // (the sum over all cancels where the chosen are divided by theirs)
+        float part = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const float l = key_logit(key[k][i]);
+          if (key[k][i] != 0u && l != -INFINITY) part += l == largest[k] ? 1.0f : __expf(l - largest[k]);
+        }
+        total[k] = warp_sum(part);
       }
-      total = warp_sum(part);
     }
   }
-  uint32_t chosen = 0;
-  id = 0;
+#pragma unroll 1
   for (int j = 0; j < r.top_k; ++j) {
-    // the lane's first largest entry, the warp's largest, its lowest expert
-    uint32_t best = 0;
-    int at = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (key[i] > best) best = key[i], at = i;
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * at + lane : 0xFFFFu);
-    if ((e & 31u) == static_cast<uint32_t>(lane)) {
+    for (int k = 0; k < ROWS; ++k) {
+      // the lane's first largest entry, the warp's largest, its lowest expert
+      uint32_t best = 0;
+      int at = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (i == static_cast<int>(e >> 5)) key[i] = 0;
+        if (key[k][i] > best) best = key[k][i], at = i;
+      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
+      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * at + lane : 0xFFFFu);
+      if ((e & 31u) == static_cast<uint32_t>(lane)) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (i == static_cast<int>(e >> 5)) key[k][i] = 0;
+      }
+      if (lane == j) id[k] = static_cast<int>(e), chosen[k] = top;
     }
-    if (lane == j) id = static_cast<int>(e), chosen = top;
   }
-  const float l = key_logit(chosen);
-  float score = 0.0f;
   // Sigmoids that are divided by their sum are taken relative to the largest of them, as
   // exponentials of log sigmoid(l) = min(l, 0) - log(1 + exp(-|l|)): those of logits below
-  // -88 do not fit fp32, but their ratios do.
-  const bool relative = r.sigmoid && r.normalize;
-  // (Few instructions: an expert kernel runs them once a block, each line of them a miss of
-  // the instruction cache.  __expf is off by 2^-21 and 2^-24 of its argument.)
-  float x = l;
-  if (relative) {
-    x = fminf(l, 0.0f) - log1pf(__expf(-fabsf(l)));
-    largest = __shfl_sync(0xFFFFFFFFu, x, 0);
+  // -88 do not fit fp32, but their ratios do.  (Few instructions: an expert kernel runs them
+  // once a block, each line of them a miss of the instruction cache.  __expf is off by 2^-21
+  // and 2^-24 of its argument.)
+  const bool relative = r.sigmoid && r.normalize, alone = r.sigmoid && !r.normalize;
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const float l = key_logit(chosen[k]);
+    float score = 0.0f, x = l;
+    if (relative) {
+      x = fminf(l, 0.0f) - log1pf(__expf(-fabsf(l)));
+      largest[k] = __shfl_sync(0xFFFFFFFFu, x, 0);
+    }
+    if (lane < r.top_k && l != -INFINITY) {
+      score = alone || x != largest[k] ? __expf(alone ? -l : x - largest[k]) : 1.0f;
+      if (alone) score = __fdividef(1.0f, 1.0f + score);
+    }
+    if (r.normalize) total[k] = warp_sum(score);
+    weight[k] = total[k] > 0.0f ? __fdividef(score, total[k]) * r.scale : 0.0f;
   }
-  if (lane < r.top_k && l != -INFINITY) {
-    const bool alone = r.sigmoid && !relative;
-    score = alone || x != largest ? __expf(alone ? -l : x - largest) : 1.0f;
-    if (alone) score = __fdividef(1.0f, 1.0f + score);
-  }
-  if (r.normalize) total = warp_sum(score);
-  weight = total > 0.0f ? __fdividef(score, total) * r.scale : 0.0f;
 }
 
 }  // namespace qmm
