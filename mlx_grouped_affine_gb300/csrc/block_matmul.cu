@@ -1,50 +1,501 @@
-// qmm_block_matmul: product of e4m3 codes, a scale per row and 128 columns on one side and
-// per 128 x 128 block on the other.  One output a thread.
+// qmm_block_matmul: y = A . W^T of e4m3 codes, with fp32 scales per row and 128 columns of A
+// and per 128 x 128 block of W.
+//
+// The scales change every 128 columns, so a sum in the tensor core may be no longer than
+// that: each 128-column step is one accumulator in tensor memory (four tcgen05.mma of
+// kind::f8f6f4, K = 32), which the epilogue warps read, scale and add to fp32 sums in
+// registers while the next step runs into a second accumulator.  Products are exact, sums
+// fp32.
+//
+//   warp 0      loads the codes by TMA (128-byte rows, 128-byte swizzle)
+//   warp 1      owns tensor memory and issues the MMAs (one lane)
+//   the others  epilogue
+//
+// Two kernels.  `tall`: a 128 x 256 tile of y per block, an epilogue thread a row of A and
+// 128 columns of one block column of W, so that a step's factor is one number a thread.
+// `flat`, for few rows of A: W's rows take the MMA's 128 lanes and up to 128 rows of A its
+// columns, so that nothing is padded to 128 rows and W is streamed once; K is split over a
+// cluster, whose partial sums meet in shared memory.
 #include "common.cuh"
-
-#include <cuda_fp8.h>
 
 namespace qmm {
 namespace {
 
-__device__ __forceinline__ float2 widen2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return __half22float2(__half2(h));
+constexpr int kStep = 128;  // columns of a scale: bytes of a tile's row
+
+struct Args {
+  const float *as, *ws;
+  void *y;
+  int y_type;
+  int M, N, steps;  // steps of 128 columns
+  unsigned *err;
+  uint32_t limit;
+};
+
+// ------------------------------------------------------------- PTX glue ----
+
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// Rows of 128 bytes, K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+// fp32 accumulator, A and B e4m3 (format 0), both K-major, M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(int n) {
+  return (1u << 4) | static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(128 >> 4) << 24;
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(add));
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Sixteen columns of this warp's 32 lanes (complete after wait_loads).
+__device__ __forceinline__ void load16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[16]) {
+  // (the registers pass through, so that nothing reads them earlier)
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
-__global__ void __launch_bounds__(256)
-plain_kernel(const uint8_t *__restrict__ a, const float *__restrict__ as, int M,
-             const uint8_t *__restrict__ w, const float *__restrict__ ws, int N, int K, int kb,
-             void *__restrict__ y, int y_type) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 16 + threadIdx.x % 16;
-  const int64_t m = static_cast<int64_t>(blockIdx.y) * 16 + threadIdx.x / 16;
-  if (m >= M || n >= N) return;
-  float sum = 0.0f;
-  for (int b = 0; b < kb; ++b) {
-    float part = 0.0f;
-    for (int k = b * 128; k < min(K, b * 128 + 128); k += 4) {
-      const uint32_t u = *reinterpret_cast<const uint32_t *>(a + m * K + k);
-      const uint32_t v = *reinterpret_cast<const uint32_t *>(w + n * K + k);
-      const float2 u0 = widen2(u & 0xFFFF), u1 = widen2(u >> 16), v0 = widen2(v & 0xFFFF), v1 = widen2(v >> 16);
-      part = fmaf(u0.x, v0.x, part);
-      part = fmaf(u0.y, v0.y, part);
-      part = fmaf(u1.x, v1.x, part);
-      part = fmaf(u1.y, v1.y, part);
+// Two multiply-adds: (x0, x1) += (v0 f0, v1 f1).
+__device__ __forceinline__ void fma2(uint64_t &x, uint32_t v0, uint32_t v1, uint64_t f) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(x) : "r"(v0), "r"(v1), "l"(f));
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(a)) | static_cast<uint64_t>(__float_as_uint(b)) << 32;
+}
+__device__ __forceinline__ float half_of(uint64_t v, int i) {
+  return __uint_as_float(static_cast<uint32_t>(i ? v >> 32 : v));
+}
+
+// Whole-warp bounded wait; false if it ran out or another role gave up.
+__device__ __noinline__ bool wait_slow(uint64_t *b, uint32_t parity, volatile int *abort, unsigned *err, uint32_t limit) {
+  uint32_t polls = 0;
+  while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) {
+    if ((++polls & 255u) == 0 || polls >= limit) {
+      int stop = *abort;
+      if (!stop && polls >= limit) {
+        stop = *abort = 1;
+        atomicOr(err, kErrTimeoutBit);
+      }
+      if (__any_sync(0xFFFFFFFFu, stop)) return false;
     }
-    sum = fmaf(as[m * kb + b] * ws[n / 128 * kb + b], part, sum);
   }
-  const int64_t at = m * N + n;
-  if (y_type == kTypeF32) static_cast<float *>(y)[at] = sum;
-  else static_cast<uint16_t *>(y)[at] = y_type == kTypeBF16 ? ElemBF16::from_f32(sum) : ElemF16::from_f32(sum);
+  return true;
+}
+__device__ __forceinline__ bool wait(uint64_t *b, uint32_t parity, volatile int *abort, const Args &a) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) return true;
+  return wait_slow(b, parity, abort, a.err, a.limit);
+}
+
+template <int STAGES>
+struct Bars {
+  uint64_t full[STAGES], empty[STAGES];  // tiles in shared memory
+  uint64_t ready[2], free[2];            // accumulators
+  uint64_t done;
+  uint32_t tmem;
+  int abort;
+};
+
+template <int STAGES>
+__device__ __forceinline__ void init_bars(Bars<STAGES> &b, uint32_t epilogue_warps) {
+  for (int i = 0; i < STAGES; ++i) mbar_init(&b.full[i], 1), mbar_init(&b.empty[i], 1);
+  for (int i = 0; i < 2; ++i) mbar_init(&b.ready[i], 1), mbar_init(&b.free[i], epilogue_warps);
+  mbar_init(&b.done, 1);
+  b.abort = 0;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void alloc_tmem(uint32_t *to, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "r"(columns));
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void free_tmem(uint32_t at, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+
+// Loads of one block's steps into the ring: rows at y0 of the MMA's A tile, at y1 of its B.
+template <int STAGES, int A_BYTES, int B_BYTES>
+struct Loader {
+  int stage = 0;
+  uint32_t phase = 0, used = 0;  // used: stages loaded at least once
+  __device__ __forceinline__ bool step(Bars<STAGES> &bars, const CUtensorMap *ma, const CUtensorMap *mb, uint32_t smem, int x,
+                                       int y0, int y1, int lane, const Args &a) {
+    if (!wait(&bars.empty[stage], phase ^ 1u, &bars.abort, a)) return false;
+    if (lane == 0) {
+      const uint32_t at = smem + stage * (A_BYTES + B_BYTES);
+      mbar_expect_tx(&bars.full[stage], A_BYTES + B_BYTES);
+      load_tile(at, ma, x, y0, &bars.full[stage]);
+      load_tile(at + A_BYTES, mb, x, y1, &bars.full[stage]);
+    }
+    __syncwarp();
+    used |= 1u << stage;
+    if (++stage == STAGES) stage = 0, phase ^= 1u;
+    return true;
+  }
+  // Stopped early: no copy may land after the block has left (the last one into each stage).
+  __device__ __forceinline__ void drain(Bars<STAGES> &bars, uint32_t limit) {
+    for (int i = 0; i < STAGES; ++i) {
+      if (!(used >> i & 1u)) continue;
+      const uint32_t last = i < stage ? phase : phase ^ 1u;
+      for (uint32_t polls = 0; polls < limit; ++polls)
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars.full[i], last))) break;
+    }
+  }
+};
+
+// The MMAs of one block's steps.
+template <int STAGES, int A_BYTES, int B_BYTES, int COLUMNS>
+struct Multiplier {
+  int stage = 0, acc = 0;
+  uint32_t phase = 0, acc_phase = 0;
+  __device__ __forceinline__ bool step(Bars<STAGES> &bars, uint32_t smem, uint32_t tmem, int lane, const Args &a) {
+    if (!wait(&bars.free[acc], acc_phase ^ 1u, &bars.abort, a) || !wait(&bars.full[stage], phase, &bars.abort, a)) return false;
+    fence_after();
+    if (lane == 0) {
+      const uint32_t at = smem + stage * (A_BYTES + B_BYTES);
+      const uint64_t da = tile_desc(at), db = tile_desc(at + A_BYTES);
+#pragma unroll
+      for (int j = 0; j < kStep / 32; ++j)
+        mma_e4m3(tmem + acc * COLUMNS, da + 2 * j, db + 2 * j, mma_desc(COLUMNS), j ? 1u : 0u);
+      commit(&bars.empty[stage]);
+      commit(&bars.ready[acc]);
+    }
+    __syncwarp();
+    if (++stage == STAGES) stage = 0, phase ^= 1u;
+    acc ^= 1;
+    if (acc == 0) acc_phase ^= 1u;
+    return true;
+  }
+  // Every MMA issued retires before tensor memory is freed.
+  __device__ __forceinline__ void retire(Bars<STAGES> &bars, int lane, uint32_t limit) {
+    if (lane == 0) commit(&bars.done);
+    __syncwarp();
+    for (uint32_t polls = 0; polls < limit; ++polls)
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars.done, 0))) break;
+  }
+};
+
+__device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
+  if (a.y_type == kTypeF32) static_cast<float *>(a.y)[at] = v;
+  else static_cast<uint16_t *>(a.y)[at] = a.y_type == kTypeBF16 ? ElemBF16::from_f32(v) : ElemF16::from_f32(v);
+}
+
+// ----------------------------------------------------------------- tall ----
+
+constexpr int kTallM = 128, kTallN = 256, kTallStages = 4, kTallThreads = 320;
+constexpr int kTallA = kTallM * kStep, kTallB = kTallN * kStep;
+
+__device__ __forceinline__ void store_row(const Args &a, int64_t m, int64_t n, const uint64_t (&sum)[64]) {
+  const int64_t at = m * a.N + n;
+  const int size = a.y_type == kTypeF32 ? 4 : 2;
+  char *to = static_cast<char *>(a.y) + at * size;
+  if (n + 128 <= a.N && reinterpret_cast<uintptr_t>(to) % 16 == 0) {
+    if (a.y_type == kTypeF32) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint64_t u = sum[2 * i], v = sum[2 * i + 1];
+        reinterpret_cast<uint4 *>(to)[i] = make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32),
+                                                      static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
+      }
+    } else {
+      const bool bf16 = a.y_type == kTypeBF16;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float lo = half_of(sum[4 * i + k], 0), hi = half_of(sum[4 * i + k], 1);
+          w[k] = bf16 ? ElemBF16::pack2(lo, hi) : ElemF16::pack2(lo, hi);
+        }
+        reinterpret_cast<uint4 *>(to)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 128; ++i)
+      if (n + i < a.N) store_one(a, at + i, half_of(sum[i / 2], i % 2));
+  }
+}
+
+__global__ void __launch_bounds__(kTallThreads, 1)
+tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  __shared__ Bars<kTallStages> bars;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
+  if (threadIdx.x == 0) init_bars(bars, 8);
+  if (warp == 1) alloc_tmem(&bars.tmem, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars.tmem;
+  const int m_tiles = (a.M + kTallM - 1) / kTallM, n_tiles = (a.N + kTallN - 1) / kTallN;
+  const int64_t tiles = static_cast<int64_t>(m_tiles) * n_tiles;
+
+  if (warp == 0) {
+    Loader<kTallStages, kTallA, kTallB> load;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      const int m0 = static_cast<int>(tile % m_tiles) * kTallM, n0 = static_cast<int>(tile / m_tiles) * kTallN;
+      for (int k = 0; ok && k < a.steps; ++k) ok = load.step(bars, &ma, &mw, smem, k * kStep, m0, n0, lane, a);
+    }
+    if (!ok) load.drain(bars, kDefaultWaitLimit);
+  } else if (warp == 1) {
+    Multiplier<kTallStages, kTallA, kTallB, kTallN> mul;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
+      for (int k = 0; ok && k < a.steps; ++k) ok = mul.step(bars, smem, tmem, lane, a);
+    mul.retire(bars, lane, kDefaultWaitLimit);
+  } else {
+    // Lanes 32 (warp % 4) .. of tensor memory are this warp's; half of the columns each.
+    const int row = 32 * (warp % 4) + lane, half = (warp - 2) / 4;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16) + half * 128;
+    int acc = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      const int64_t m = tile % m_tiles * kTallM + row, n = tile / m_tiles * kTallN + half * 128;
+      const float *as = a.as + (m < a.M ? m : a.M - 1) * a.steps;
+      const float *ws = a.ws + (n < a.N ? n / 128 : 0) * a.steps;
+      uint64_t sum[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) sum[i] = 0;
+      float fa = __ldg(as), fw = __ldg(ws);
+      for (int k = 0; k < a.steps; ++k) {
+        const float f = fa * fw;
+        const uint64_t ff = pair(f, f);
+        if (k + 1 < a.steps) fa = __ldg(as + k + 1), fw = __ldg(ws + k + 1);
+        if (!wait(&bars.ready[acc], phase, &bars.abort, a)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        uint32_t v[2][16];
+        load16(at + acc * kTallN, v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          wait_loads(v[c % 2]);
+          if (c + 1 < 8) load16(at + acc * kTallN + 16 * (c + 1), v[(c + 1) % 2]);
+          if (c == 7) {
+            fence_before();
+            if (lane == 0) mbar_arrive(&bars.free[acc]);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fma2(sum[8 * c + i], v[c % 2][2 * i], v[c % 2][2 * i + 1], ff);
+        }
+        acc ^= 1;
+        if (acc == 0) phase ^= 1u;
+      }
+      if (ok && m < a.M && n < a.N) store_row(a, m, n, sum);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    free_tmem(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------------- flat ----
+
+constexpr int kFlatThreads = 192, kFlatEpilogue = 128;
+template <int T>
+__host__ __device__ constexpr int flat_stages() { return T <= 32 ? 5 : T == 64 ? 4 : 3; }
+template <int T>
+__host__ __device__ constexpr uint32_t flat_columns() { return T == 16 ? 32 : 2 * T; }
+
+__device__ __forceinline__ float remote_f32(uint32_t addr, uint32_t rank) {
+  uint32_t far;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 128 rows of W and T rows of A; the cluster's blocks (blockIdx.x % split) share the steps.
+template <int T>
+__global__ void __launch_bounds__(kFlatThreads, T <= 64 ? 2 : 1)
+flat_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args a,
+            int split) {
+  constexpr int kStages = flat_stages<T>(), kA = 128 * kStep, kB = T * kStep;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  __shared__ Bars<kStages> bars;
+  __shared__ __align__(16) float factors[2][T];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
+  const int rank = blockIdx.x % split, n0 = blockIdx.x / split * 128, m0 = blockIdx.y * T;
+  const int k0 = static_cast<int>(static_cast<int64_t>(a.steps) * rank / split);
+  const int k1 = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / split);
+  if (threadIdx.x == 0) init_bars(bars, kFlatEpilogue / 32);
+  if (warp == 1) alloc_tmem(&bars.tmem, flat_columns<T>());
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = bars.tmem;
+  // Partial sums take the ring's place once every product has read it: [T][128].
+  const uint32_t partial = smem;
+  uint64_t sum[T / 2];
+#pragma unroll
+  for (int i = 0; i < T / 2; ++i) sum[i] = 0;
+  const int row = 32 * (warp % 4) + lane;
+
+  if (warp == 0) {
+    Loader<kStages, kA, kB> load;
+    bool ok = true;
+    for (int k = k0; ok && k < k1; ++k) ok = load.step(bars, &mw, &ma, smem, k * kStep, n0, m0, lane, a);
+    if (!ok) load.drain(bars, kDefaultWaitLimit);
+  } else if (warp == 1) {
+    Multiplier<kStages, kA, kB, T> mul;
+    bool ok = true;
+    for (int k = k0; ok && k < k1; ++k) ok = mul.step(bars, smem, tmem, lane, a);
+    mul.retire(bars, lane, kDefaultWaitLimit);
+  } else {
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16);
+    const float *ws = a.ws + static_cast<int64_t>(n0 / 128) * a.steps;
+    const int column = threadIdx.x - 64;  // of A's rows, whose factor this thread fetches
+    const int64_t m = m0 + column;
+    const float *as = a.as + (m < a.M ? m : a.M - 1) * a.steps;
+    int acc = 0;
+    uint32_t phase = 0;
+    float f = column < T && k0 < k1 ? __ldg(as + k0) * __ldg(ws + k0) : 0.0f;
+    bool ok = true;
+    for (int k = k0; k < k1; ++k) {  // (the barrier is met by every warp, stopped early or not)
+      if (column < T) factors[k % 2][column] = f;
+      if (column < T && k + 1 < k1) f = __ldg(as + k + 1) * __ldg(ws + k + 1);
+      asm volatile("bar.sync 1, %0;" ::"n"(kFlatEpilogue) : "memory");
+      ok = ok && wait(&bars.ready[acc], phase, &bars.abort, a);
+      if (!ok) continue;
+      fence_after();
+#pragma unroll
+      for (int c = 0; c < T / 16; ++c) {
+        uint32_t v[16];
+        load16(at + acc * T + 16 * c, v);
+        wait_loads(v);
+        if (c == T / 16 - 1) {
+          fence_before();
+          if (lane == 0) mbar_arrive(&bars.free[acc]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const ulonglong2 ff = *reinterpret_cast<const ulonglong2 *>(&factors[k % 2][16 * c + 4 * i]);
+          fma2(sum[8 * c + 2 * i], v[4 * i], v[4 * i + 1], ff.x);
+          fma2(sum[8 * c + 2 * i + 1], v[4 * i + 2], v[4 * i + 3], ff.y);
+        }
+      }
+      acc ^= 1;
+      if (acc == 0) phase ^= 1u;
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    free_tmem(tmem, flat_columns<T>());
+  }
+  if (warp >= 2) {
+#pragma unroll
+    for (int c = 0; c < T; ++c)
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(partial + (c * 128 + row) * 4), "f"(half_of(sum[c / 2], c % 2)) : "memory");
+  }
+  cluster_barrier();
+  if (warp >= 2 && n0 + row < a.N) {
+    for (int c = rank; c < T && m0 + c < a.M; c += split) {
+      float v = 0.0f;
+#pragma unroll 4
+      for (int r = 0; r < split; ++r) v += remote_f32(partial + (c * 128 + row) * 4, r);
+      store_one(a, static_cast<int64_t>(m0 + c) * a.N + n0 + row, v);
+    }
+  }
+  cluster_barrier();  // no block leaves while another reads its sums
+}
+
+// --------------------------------------------------------------- launch ----
+
+cudaError_t code_map(CUtensorMap *map, const uint8_t *p, int rows, int cols, int box_rows) {
+  return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, cols, rows, cols, kStep, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int T>
+cudaError_t launch_flat(const uint8_t *pa, const uint8_t *w, int K, const Args &a, cudaStream_t stream) {
+  CUtensorMap ma, mw;
+  cudaError_t e = code_map(&ma, pa, a.M, K, T);
+  if (e == cudaSuccess) e = code_map(&mw, w, a.N, K, 128);
+  if (e != cudaSuccess) return e;
+  constexpr auto kernel = flat_kernel<T>;
+  const size_t bytes = 1024 + static_cast<size_t>(flat_stages<T>()) * (128 + T) * kStep;
+  e = ensure_smem_limit<kernel>(bytes);
+  if (e != cudaSuccess) return e;
+  const int n_tiles = (a.N + 127) / 128, m_tiles = (a.M + T - 1) / T;
+  // K is split until there is a block for every SM, each with a step at least.
+  int split = 1;
+  while (split < 8 && 2 * split <= a.steps && static_cast<int64_t>(n_tiles) * m_tiles * split < sm_count()) split *= 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(n_tiles * split, m_tiles);
+  cfg.blockDim = dim3(kFlatThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, ma, mw, a, split);
 }
 
 }  // namespace
 
-cudaError_t launch_block_matmul(const uint8_t *a, const float *a_scales, int M, const uint8_t *w,
+cudaError_t launch_block_matmul(const uint8_t *pa, const float *a_scales, int M, const uint8_t *w,
                                 const float *w_scales, int N, int K, void *y, int y_type,
                                 cudaStream_t stream) {
-  const dim3 grid((N + 15) / 16, (M + 15) / 16);
-  plain_kernel<<<grid, 256, 0, stream>>>(a, a_scales, M, w, w_scales, N, K, (K + 127) / 128, y, y_type);
+  Args a;
+  a.as = a_scales;
+  a.ws = w_scales;
+  a.y = y;
+  a.y_type = y_type;
+  a.M = M;
+  a.N = N;
+  a.steps = (K + kStep - 1) / kStep;
+  a.err = device_error_word();
+  if (!a.err) return cudaErrorInvalidSymbol;
+  a.limit = wait_limit();
+  if (M <= 16) return launch_flat<16>(pa, w, K, a, stream);
+  if (M <= 32) return launch_flat<32>(pa, w, K, a, stream);
+  if (M <= 64) return launch_flat<64>(pa, w, K, a, stream);
+  const int64_t tiles = static_cast<int64_t>((M + kTallM - 1) / kTallM) * ((N + kTallN - 1) / kTallN);
+  if (tiles < sm_count() / 2) return launch_flat<128>(pa, w, K, a, stream);
+  CUtensorMap ma, mw;
+  cudaError_t e = code_map(&ma, pa, M, K, kTallM);
+  if (e == cudaSuccess) e = code_map(&mw, w, N, K, kTallN);
+  if (e != cudaSuccess) return e;
+  const size_t bytes = 1024 + static_cast<size_t>(kTallStages) * (kTallA + kTallB);
+  e = ensure_smem_limit<tall_kernel>(bytes);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(tiles < sm_count() ? tiles : sm_count());
+  tall_kernel<<<grid, kTallThreads, bytes, stream>>>(ma, mw, a);
   return cudaGetLastError();
 }
 

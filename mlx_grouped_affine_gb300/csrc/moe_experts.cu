@@ -94,9 +94,10 @@ __device__ void make_plan(const Routing r, const int tokens, const int experts, 
       const int e = p.expert[s], n = mine & 0xFFFF, units = mine >> 16, unit = at >> 16;
       p.table[e] = at;
       for (int k = 0; k < units; ++k) {
-        out->unit_expert[unit + k] = static_cast<short>(e);
-        out->unit_first[unit + k] = static_cast<short>((at & 0xFFFF) + k * kMoePass);
-        out->unit_count[unit + k] = static_cast<short>(min(kMoePass, n - k * kMoePass));
+        MoeEntry &u = out->entries[unit + k];
+        u.unit_expert = static_cast<short>(e);
+        u.unit_first = static_cast<short>((at & 0xFFFF) + k * kMoePass);
+        u.unit_count = static_cast<short>(min(kMoePass, n - k * kMoePass));
       }
     }
     if (s / 32 == (slots - 1) / 32 && lane == 31) out->units = (at + mine) >> 16;
@@ -104,10 +105,10 @@ __device__ void make_plan(const Routing r, const int tokens, const int experts, 
   __syncthreads();
   if (s < slots) {
     const int e = p.expert[s], at = e < 0 ? 0 : p.table[e], place = e < 0 ? 0 : p.place[s];
-    if (e >= 0) out->list[(at & 0xFFFF) + place] = static_cast<short>(s);
-    out->slot_unit[s] = static_cast<short>(e < 0 ? -1 : (at >> 16) + place / kMoePass);
-    out->slot_place[s] = static_cast<short>(place % kMoePass);
-    out->slot_weight[s] = p.weight[s];
+    if (e >= 0) out->entries[(at & 0xFFFF) + place].listed = static_cast<short>(s);
+    out->entries[s].slot_unit = static_cast<short>(e < 0 ? -1 : (at >> 16) + place / kMoePass);
+    out->entries[s].slot_place = static_cast<short>(place % kMoePass);
+    out->entries[s].slot_weight = p.weight[s];
   }
 }
 

@@ -55,33 +55,25 @@ struct MoeArgs {
 // Which slots (token * top_k + place) go to which expert (moe_experts.cu works it out).  A
 // unit is an expert with up to kMoePass of its slots; an expert's units follow one another,
 // its slots are in order, and experts come in the order of their first slots.
+// Three tables side by side, an entry of each per slot: units, slots unit by unit, slots.
+struct alignas(16) MoeEntry {
+  short unit_expert, unit_first, unit_count;  // of unit i; first in the second table
+  short listed;                               // the slot at place i
+  short slot_unit, slot_place;                // of slot i; -1: no part in y; its place in the unit
+  float slot_weight;
+};
 struct MoePlan {
-  int units;
-  short unit_expert[kMoeMaxSlots];
-  short unit_first[kMoeMaxSlots];   // in `list`
-  short unit_count[kMoeMaxSlots];
-  short list[kMoeMaxSlots];         // slots, unit by unit
-  short slot_unit[kMoeMaxSlots];    // -1: no part in y
-  short slot_place[kMoeMaxSlots];   // in its unit
-  float slot_weight[kMoeMaxSlots];
+  alignas(16) int units;
+  MoeEntry entries[kMoeMaxSlots];
 };
 
-// The block's copy of what the kernels need of it.  (From L2: a kernel that was launched
-// early may hold nothing older in L1, but this asks for no more than it needs.)
-__device__ __forceinline__ void read_plan(const MoePlan *from, MoePlan &p, int slots, bool slots_too) {
-  for (int i = threadIdx.x; i < slots; i += kMoeThreads) {
-    p.unit_expert[i] = __ldcg(&from->unit_expert[i]);
-    p.unit_first[i] = __ldcg(&from->unit_first[i]);
-    p.unit_count[i] = __ldcg(&from->unit_count[i]);
-    p.list[i] = __ldcg(&from->list[i]);
-    if (slots_too) {
-      p.slot_unit[i] = __ldcg(&from->slot_unit[i]);
-      p.slot_place[i] = __ldcg(&from->slot_place[i]);
-      p.slot_weight[i] = __ldcg(&from->slot_weight[i]);
-    }
-  }
-  if (threadIdx.x == 0) p.units = __ldcg(&from->units);
+// The block's copy.  (From L2: a kernel launched early must not trust its L1.)
+__device__ __forceinline__ int read_plan(const MoePlan *from, MoeEntry *to, int slots) {
+  for (int i = threadIdx.x; i < slots; i += kMoeThreads)
+    reinterpret_cast<uint4 *>(to)[i] = __ldcg(reinterpret_cast<const uint4 *>(&from->entries[i]));
+  const int units = __ldcg(&from->units);
   __syncthreads();
+  return units;
 }
 
 // ------------------------------------------------------------ the codes ----
@@ -379,13 +371,13 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
 // Brings a chunk of x of the unit's slots into L1 ahead of its use: a 4-byte copy of each
 // 32-byte sector to a place that nothing reads.
 template <int CHUNK, bool TOKENS>
-__device__ __forceinline__ void touch_x(uint32_t scratch, const uint16_t *x, int64_t plane, int planes, const short *slots,
+__device__ __forceinline__ void touch_x(uint32_t scratch, const uint16_t *x, int64_t plane, int planes, const MoeEntry *slots,
                                         int count, int top, int width, int chunk, int lane) {
   constexpr int kSectors = CHUNK / 16;
   const int all = count * kSectors;
   for (int p = 0; p < planes; ++p) {
     for (int i = lane; i < all; i += 32) {
-      const int slot = slots[i / kSectors], at = chunk * CHUNK + i % kSectors * 16;
+      const int slot = slots[i / kSectors].listed, at = chunk * CHUNK + i % kSectors * 16;
       const uint16_t *from = x + p * plane + static_cast<int64_t>(TOKENS ? slot / top : slot) * width + at;
       if (at < width)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scratch + 4 * lane), "l"(from) : "memory");
@@ -490,8 +482,7 @@ __device__ __forceinline__ void store_planes(uint16_t *p, int64_t plane, int pla
 
 // -------------------------------------------------------- gate and up ----
 
-struct alignas(1024) GateUpShared {  // the ring follows: swizzled boxes want 1024
-  MoePlan plan;
+struct alignas(1024) GateUpShared {  // the ring follows (swizzled boxes want 1024), then the plan
   alignas(16) float heads[kMoeWarps][32 * kMoePass];  // sums of a warp's first task where it began in an earlier one
   int task[2][kMoeWarps];  // the task that goes on in the next warp, the head's; -1: none
   alignas(16) uint64_t bars[kMoeWarps * 4];
@@ -515,6 +506,8 @@ struct GateUp {
   using R = Run<BITS, G>;
   const MoeArgs &a;
   GateUpShared &sh;
+  MoeEntry *plan;
+  int units;
   Ring<BITS, G> ring;
   Source gate, up;
   const char *scales, *biases;
@@ -532,11 +525,11 @@ struct GateUp {
 
   __device__ __forceinline__ void advance_load() {
     if (l_left <= 0 || ring.dead) return;
-    const int row = sh.plan.unit_expert[l_unit] * a.w.inner + l_tile * 16;
+    const int row = plan[l_unit].unit_expert * a.w.inner + l_tile * 16;
     ring.issue(gate, up, row, row, l_chunk);
     if (l_fresh)
-      touch_x<R::kChunk, true>(smem_u32(sh.unread), a.x, a.x_plane, a.x_planes, &sh.plan.list[sh.plan.unit_first[l_unit]],
-                               sh.plan.unit_count[l_unit], a.route.top_k, a.w.hidden, l_chunk, lane);
+      touch_x<R::kChunk, true>(smem_u32(sh.unread), a.x, a.x_plane, a.x_planes, &plan[plan[l_unit].unit_first],
+                               plan[l_unit].unit_count, a.route.top_k, a.w.hidden, l_chunk, lane);
     --l_left;
     if (++l_chunk == chunks) {
       l_chunk = 0;
@@ -551,11 +544,11 @@ struct GateUp {
     if (++s_chunk == chunks) {
       if (++s_tile == tiles) s_tile = 0, ++s_unit;
       s_chunk = 0;
-      if (s_unit < sh.plan.units) point_scales();
+      if (s_unit < units) point_scales();
     }
   }
   __device__ __forceinline__ void point_scales() {
-    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[s_unit]) * a.w.inner + s_tile * 16 + lane / 4 + 8 * (lane % 2);
+    const int64_t row = static_cast<int64_t>(plan[s_unit].unit_expert) * a.w.inner + s_tile * 16 + lane / 4 + 8 * (lane % 2);
     s_at = (row * groups + s_chunk * R::kSteps) * sb_bytes;
   }
 
@@ -565,14 +558,14 @@ struct GateUp {
   }
   template <int HALVES>
   __device__ __forceinline__ void run_task() {
-    const int g = lane / 4, t = lane % 4, count = sh.plan.unit_count[unit];
-    const short *slots = &sh.plan.list[sh.plan.unit_first[unit]];
+    const int g = lane / 4, t = lane % 4, count = plan[unit].unit_count;
+    const MoeEntry *listed = &plan[plan[unit].unit_first];
     Columns<HALVES> c;
     c.planes = a.x_planes;
     c.plane = a.x_plane;
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) {
-      const int token = slots[8 * half + g < count ? 8 * half + g : 0] / a.route.top_k;
+      const int token = listed[8 * half + g < count ? 8 * half + g : 0].listed / a.route.top_k;
       c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
     }
     const uint32_t spread = ring.base + R::kDepth * R::kStageBytes;
@@ -596,7 +589,7 @@ struct GateUp {
         for (int i = 0; i < 2; ++i) {
           const int place = 8 * half + 2 * t + i;
           if (place < count) {
-            uint16_t *to = a.h + static_cast<int64_t>(slots[place]) * a.w.inner + tile * 16 + g;
+            uint16_t *to = a.h + static_cast<int64_t>(listed[place].listed) * a.w.inner + tile * 16 + g;
             store_planes(to, a.h_plane, a.h_planes, silu_times(acc[half][i], acc[half][4 + i]));
             store_planes(to + 8, a.h_plane, a.h_planes, silu_times(acc[half][2 + i], acc[half][6 + i]));
           }
@@ -624,7 +617,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2)
 gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps maps) {
   using R = Run<BITS, G>;
   extern __shared__ __align__(1024) unsigned char raw[];
-  GateUp<BITS, G> s{a, *reinterpret_cast<GateUpShared *>(raw)};
+  GateUp<BITS, G> s{a, *reinterpret_cast<GateUpShared *>(raw),
+                    reinterpret_cast<MoeEntry *>(raw + sizeof(GateUpShared) + kMoeWarps * R::kWarpBytes + 16)};
   s.warp = threadIdx.x / 32, s.lane = threadIdx.x % 32;
   s.ring.init(raw + sizeof(GateUpShared), s.sh.bars, s.warp, s.lane);
   if (threadIdx.x < 2 * kMoeWarps) s.sh.task[threadIdx.x / kMoeWarps][threadIdx.x % kMoeWarps] = -1;
@@ -632,10 +626,10 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   // too, before this one is done.
   griddep_wait();
   griddep_launch_dependents();
-  read_plan(a.plan, s.sh.plan, a.tokens * a.route.top_k, false);
+  s.units = read_plan(a.plan, s.plan, a.tokens * a.route.top_k);
   s.tiles = a.w.inner / 16, s.groups = a.w.hidden / G, s.chunks = (a.w.hidden + R::kChunk - 1) / R::kChunk;
   // Tasks t0 .. t1 of the block, an even share; steps from .. of the warp.
-  const int tasks = s.sh.plan.units * s.tiles, grid = gridDim.x, block = blockIdx.x;
+  const int tasks = s.units * s.tiles, grid = gridDim.x, block = blockIdx.x;
   const int share = tasks / grid, rest = tasks - share * grid;
   const int t0 = share * block + min(block, rest), t1 = t0 + share + (block < rest);
   const int steps = (t1 - t0) * s.chunks;
@@ -658,7 +652,7 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   s.s_chunk = s.chunk, s.s_unit = s.unit, s.s_tile = s.tile;
   if (s.left > 0) s.point_scales(), s.load_scales();
   while (s.left > 0 && !s.ring.dead) {
-    if (s.sh.plan.unit_count[s.unit] > 8) s.template run_task<2>();
+    if (s.plan[s.unit].unit_count > 8) s.template run_task<2>();
     else s.template run_task<1>();
   }
   s.ring.drain(s.copied, a.wait_limit, a.err);
@@ -669,20 +663,19 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
     const int task = s.sh.task[0][w];
     if (task < 0) continue;
     const int unit = task / s.tiles, tile = task % s.tiles;
-    if (place >= s.sh.plan.unit_count[unit]) continue;
+    if (place >= s.plan[unit].unit_count) continue;
     const int at = r * kMoePass + place, two = 16 * kMoePass;
     float gate = s.starts(w)[at], up = s.starts(w)[at + two];
     for (int v = w + 1; v < kMoeWarps; ++v)
       if (s.sh.task[1][v] == task) gate += s.sh.heads[v][at], up += s.sh.heads[v][at + two];
-    const int slot = s.sh.plan.list[s.sh.plan.unit_first[unit] + place];
+    const int slot = s.plan[s.plan[unit].unit_first + place].listed;
     store_planes(a.h + static_cast<int64_t>(slot) * a.w.inner + tile * 16 + r, a.h_plane, a.h_planes, silu_times(gate, up));
   }
 }
 
 // ---------------------------------------------------------------- down ----
 
-struct alignas(1024) DownShared {  // then the ring, then z: float [slots][32]
-  MoePlan plan;
+struct alignas(1024) DownShared {  // then the ring, the plan, z: float [slots][32]
   alignas(16) float heads[kMoeWarps][kMoePass][32];
   alignas(16) uint64_t bars[kMoeWarps * 4];
   uint32_t unread[32];
@@ -711,21 +704,23 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   using R = Run<BITS, G>;
   extern __shared__ __align__(1024) unsigned char raw[];
   DownShared &sh = *reinterpret_cast<DownShared *>(raw);
-  float *z = reinterpret_cast<float *>(raw + sizeof(DownShared) + kMoeWarps * R::kWarpBytes);
+  const int slots = a.tokens * a.route.top_k;
+  MoeEntry *plan = reinterpret_cast<MoeEntry *>(raw + sizeof(DownShared) + kMoeWarps * R::kWarpBytes);
+  float *z = reinterpret_cast<float *>(plan + slots);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   Ring<BITS, G> ring;
   ring.init(raw + sizeof(DownShared), sh.bars, warp, lane);
-  read_plan(a.plan, sh.plan, a.tokens * a.route.top_k, true);
+  const int units = read_plan(a.plan, plan, slots);
   const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * 32;
   const int groups = a.w.inner / G, chunks = (a.w.inner + R::kChunk - 1) / R::kChunk;
-  const int total = sh.plan.units * chunks;  // at most 2^22: sizes are at most 2^20
+  const int total = units * chunks;  // at most 2^22: sizes are at most 2^20
   // Warps that share the steps, none without any; warp w begins at step total * w / warps.
   const int warps = min(cluster * kMoeWarps, total), self = rank * kMoeWarps + warp;
   const int step0 = self < warps ? total * self / warps : total;
   const int step1 = self < warps ? total * (self + 1) / warps : total;
   // The warps that have a unit's first and last step: step s is in warp w where
   // total * w / warps <= s < total * (w + 1) / warps, so w = ((s + 1) * warps - 1) / total.
-  for (int u = threadIdx.x; u < sh.plan.units; u += kMoeThreads) {
+  for (int u = threadIdx.x; u < units; u += kMoeThreads) {
     sh.unit_from[u] = static_cast<unsigned char>(((u * chunks + 1) * warps - 1) / total);
     sh.unit_to[u] = static_cast<unsigned char>(((u + 1) * chunks * warps - 1) / total);
   }
@@ -736,7 +731,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   const bool whole = a.w.sb_type != kTypeF32 && groups % R::kSteps == 0;
   Scales<R::kSteps> next;
   auto load_scales = [&](int unit, int chunk) {
-    const int64_t row = static_cast<int64_t>(sh.plan.unit_expert[unit]) * a.w.hidden + row0 + g + 8 * t;
+    const int64_t row = static_cast<int64_t>(plan[unit].unit_expert) * a.w.hidden + row0 + g + 8 * t;
     const int64_t at = (row * groups + chunk * R::kSteps) * sb_bytes;
     next.load(scales + at, biases + at, a.w.sb_type, whole, groups - chunk * R::kSteps);
   };
@@ -746,12 +741,12 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   const int first_unit = step0 / chunks, first_chunk = step0 - first_unit * chunks;
   int load_step = step0, load_unit = first_unit, load_chunk = first_chunk;
   auto touch_h = [&](int unit, int chunk) {
-    touch_x<R::kChunk, false>(smem_u32(sh.unread), a.h, a.h_plane, a.h_planes, &sh.plan.list[sh.plan.unit_first[unit]],
-                              sh.plan.unit_count[unit], 1, a.w.inner, chunk, lane);
+    touch_x<R::kChunk, false>(smem_u32(sh.unread), a.h, a.h_plane, a.h_planes, &plan[plan[unit].unit_first],
+                              plan[unit].unit_count, 1, a.w.inner, chunk, lane);
   };
   auto load_next = [&](bool touch) {
     if (load_step >= step1 || ring.dead) return;
-    const int row = sh.plan.unit_expert[load_unit] * a.w.hidden + row0;
+    const int row = plan[load_unit].unit_expert * a.w.hidden + row0;
     ring.issue(down, down, row, row + 16, load_chunk);
     if (touch) touch_h(load_unit, load_chunk);
     ++load_step;
@@ -770,14 +765,14 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   auto run_unit = [&](auto halves, int unit, int j0) {
     constexpr int HALVES = decltype(halves)::value;
     const int j1 = min(chunks, j0 + (step1 - step));
-    const int count = sh.plan.unit_count[unit];
-    const short *slots = &sh.plan.list[sh.plan.unit_first[unit]];
+    const int count = plan[unit].unit_count;
+    const MoeEntry *listed = &plan[plan[unit].unit_first];
     Columns<HALVES> c;
     c.planes = a.h_planes;
     c.plane = a.h_plane;
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) {
-      const int slot = slots[8 * half + g < count ? 8 * half + g : 0];
+      const int slot = listed[8 * half + g < count ? 8 * half + g : 0].listed;
       c.x[half] = a.h + static_cast<int64_t>(slot) * a.w.inner + t * R::kCodes;
     }
     float acc[HALVES][8] = {};
@@ -801,7 +796,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
       for (int i = 0; i < 2; ++i) {
         const int place = half * 8 + 2 * t + i;
         if (place < count) {
-          float *to = j0 == 0 ? z + slots[place] * 32 : sh.heads[warp][place];
+          float *to = j0 == 0 ? z + listed[place].listed * 32 : sh.heads[warp][place];
 #pragma unroll
           for (int q = 0; q < 4; ++q) to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[half][2 * q + i] * kUnscale;
         }
@@ -809,7 +804,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   };
   for (int unit = first_unit; step < step1 && !ring.dead; ++unit) {
     const int j0 = unit == first_unit ? first_chunk : 0;
-    if (sh.plan.unit_count[unit] > 8) run_unit(Int<2>(), unit, j0);
+    if (plan[unit].unit_count > 8) run_unit(Int<2>(), unit, j0);
     else run_unit(Int<1>(), unit, j0);
   }
   ring.drain(copied, a.wait_limit, a.err);
@@ -821,13 +816,13 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     float sum = 0.0f;
 #pragma unroll 4
     for (int k = 0; k < a.route.top_k; ++k) {
-      const int slot = token * a.route.top_k + k, unit = sh.plan.slot_unit[slot], place = sh.plan.slot_place[slot];
+      const int slot = token * a.route.top_k + k, unit = plan[slot].slot_unit, place = plan[slot].slot_place;
       if (unit < 0) continue;
       const int from = sh.unit_from[unit], to = sh.unit_to[unit];
       float v = remote_f32(z_at + slot * 128, from / kMoeWarps);
       for (int w = from + 1; w <= to; ++w)
         v += remote_f32(heads_at + ((w % kMoeWarps) * kMoePass + place) * 128, w / kMoeWarps);
-      sum = fmaf(sh.plan.slot_weight[slot], v, sum);
+      sum = fmaf(plan[slot].slot_weight, v, sum);
     }
     const int64_t at = static_cast<int64_t>(token) * a.w.hidden + row0 + lane;
     if (a.y_type == kTypeF32) static_cast<float *>(a.y)[at] = sum;
@@ -861,7 +856,8 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   {
     constexpr auto kernel = gate_up_kernel<BITS, G>;
-    const size_t bytes = sizeof(GateUpShared) + ring + 16;  // a run's last word may lie past its row
+    // (16 more: a run's last word may lie past its row)
+    const size_t bytes = sizeof(GateUpShared) + ring + 16 + static_cast<size_t>(slots) * sizeof(MoeEntry);
     e = ensure_smem_limit<kernel>(bytes);
     if (e != cudaSuccess) return e;
     const int64_t tasks = static_cast<int64_t>(slots) * (a.w.inner / 16), most = 2 * sm_count();
@@ -879,7 +875,7 @@ cudaError_t launch_moe(const MoeArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   constexpr auto kernel = down_kernel<BITS, G>;
-  const size_t bytes = sizeof(DownShared) + static_cast<size_t>(slots) * 128 + ring;
+  const size_t bytes = sizeof(DownShared) + static_cast<size_t>(slots) * (128 + sizeof(MoeEntry)) + ring;
   e = ensure_smem_limit<kernel>(bytes);
   if (e != cudaSuccess) return e;
   const int tiles = a.w.hidden / 32;
