@@ -482,11 +482,20 @@ cudaError_t launch_block_matmul(const uint8_t *pa, const float *a_scales, int M,
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidSymbol;
   a.limit = wait_limit();
-  if (M <= 16) return launch_flat<16>(pa, w, K, a, stream);
-  if (M <= 32) return launch_flat<32>(pa, w, K, a, stream);
-  if (M <= 64) return launch_flat<64>(pa, w, K, a, stream);
   const int64_t tiles = static_cast<int64_t>((M + kTallM - 1) / kTallM) * ((N + kTallN - 1) / kTallN);
-  if (tiles < sm_count() / 2) return launch_flat<128>(pa, w, K, a, stream);
+  if (M <= 64 || tiles < sm_count() / 2) {
+    // All rows of A at once, so that W is read once, or fewer where that leaves SMs idle (W
+    // then comes from L2 again).
+    const int64_t blocks = static_cast<int64_t>((N + 127) / 128) * (a.steps < 8 ? a.steps : 8);
+    int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    while (rows > 16 && blocks * ((M + rows - 1) / rows) < sm_count()) rows /= 2;
+    switch (rows) {
+      case 16: return launch_flat<16>(pa, w, K, a, stream);
+      case 32: return launch_flat<32>(pa, w, K, a, stream);
+      case 64: return launch_flat<64>(pa, w, K, a, stream);
+      default: return launch_flat<128>(pa, w, K, a, stream);
+    }
+  }
   CUtensorMap ma, mw;
   cudaError_t e = code_map(&ma, pa, M, K, kTallM);
   if (e == cudaSuccess) e = code_map(&mw, w, N, K, kTallN);

@@ -4,8 +4,8 @@
 // scale = max(RN(amax / 448), 2^-126), code = the e4m3 value nearest to x / scale.  The
 // quotient is taken as x * RN(1 / scale): two roundings of 2^-24, so it is within 2^-22 of
 // the exact one and rounds to the same code unless a border between two codes is that near.
-// Those elements (some 2^-17 of them) are compared with the border itself: border * scale
-// has 5 + 24 bits and is exact in 64.  A division an element would cost more than the rest.
+// Those elements (2^-16 of them) are compared with the border itself: border * scale has
+// 5 + 24 bits and is exact in 64.  A division an element would cost more than the rest.
 //
 // Bound by memory: an element is read once and its code written once.  A thread holds 16
 // consecutive elements (columns are a multiple of 16, so none is cut): 8 threads a row of a
@@ -66,48 +66,63 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   return s < kMinScale ? kMinScale : s;  // (a NaN stays)
 }
 
-// Whether q, within 2^-22 of a quotient, may lie on the other side of a border between two
-// codes.  Codes of 2^-6 and more have 3 fraction bits, so a border has fraction bit 4 set and
-// those below clear; smaller codes are multiples of 2^-9, their borders odd ones of 2^-10.
-__device__ __forceinline__ bool near_border(float q) {
-  const uint32_t b = __float_as_uint(q) & 0x7FFFFFFFu;
-  if (b >= 0x3C800000u) return (b & 0xFFFFFu) - 0x7FFF8u <= 16u;
-  const float u = fabsf(q) * 1024.0f, n = rintf(u);
-  return fabsf(u - n) <= 1.9073486328125e-6f * 16.0f && (static_cast<int>(n) & 1);
-}
+// |q| as a number whose codes are 2^-3 of its power of two apart: codes below 2^-6 are
+// multiples of 2^-9, as those in [2^-6, 2^-5) are.  A border between two codes then has
+// fraction bit 4 set and those below clear, whatever its size.
+__device__ __forceinline__ float on_grid(float q) { return fabsf(q) < 0.015625f ? fabsf(q) + 0.015625f : fabsf(q); }
 
-// q moved to the side of its nearest border where x / s is.
-__device__ __noinline__ float settle(float q, float x, float s) {
-  const uint32_t b = __float_as_uint(q) & 0x7FFFFFFFu;
-  const float t = b >= 0x3C800000u ? __uint_as_float((b & 0xFFF00000u) | 0x80000u)
-                                   : rintf(fabsf(q) * 1024.0f) * 9.765625e-4f;
+// Distance of on_grid(q) from the next border, in units of its last place and off by 8.
+__device__ __forceinline__ uint32_t off_border(float q) { return (__float_as_uint(on_grid(q)) - 0x7FFF8u) & 0xFFFFFu; }
+
+// q moved to the side of its border where x / s is.
+__device__ __forceinline__ float settle(float q, float x, float s) {
+  const float up = on_grid(q), border = __uint_as_float((__float_as_uint(up) & 0xFFF00000u) | 0x80000u);
+  const float t = fabsf(q) < 0.015625f ? border - 0.015625f : border;
   const double d = fabs(static_cast<double>(x)) - static_cast<double>(t) * static_cast<double>(s);
   const uint32_t bits = __float_as_uint(t) + (d > 0.0 ? 1u : d < 0.0 ? 0xFFFFFFFFu : 0u);
   return copysignf(__uint_as_float(bits), x);
 }
 
+__device__ __forceinline__ uint32_t code2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The 16 codes again, element by element, for a thread that met a border (one in 4000).
+// Rolled up: nothing here should cost the others instruction cache.
+__device__ __noinline__ uint4 settled_codes(const void *x, int type, int64_t at, float s, float inv) {
+  uint32_t out[4] = {};
+#pragma unroll 1
+  for (int i = 15; i >= 0; --i) {
+    const uint32_t h = type == kTypeF32 ? 0u : static_cast<const uint16_t *>(x)[at + i];
+    const float v = type == kTypeF32    ? static_cast<const float *>(x)[at + i]
+                    : type == kTypeBF16 ? bf16_bits_to_f32(h)
+                                        : ElemF16::to_f32(h);
+    float q = v * inv;
+    if (off_border(q) <= 16u) q = settle(q, v, s);
+    // shift the codes up by one byte and put this one below them
+    out[3] = out[3] << 8 | out[2] >> 24;
+    out[2] = out[2] << 8 | out[1] >> 24;
+    out[1] = out[1] << 8 | out[0] >> 24;
+    out[0] = out[0] << 8 | (code2(q, 0.0f) & 0xFFu);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 template <int T>
-__device__ __forceinline__ uint4 codes_of(const Raw<T> &r, float s) {
+__device__ __forceinline__ uint4 codes_of(const Raw<T> &r, float s, const void *x, int64_t at) {
   const float inv = __frcp_rn(s);
-  uint32_t out[4];
-  float q[16];
-  bool slow = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    q[i] = r.at(i) * inv;
-    slow |= near_border(q[i]);
-  }
-  if (slow) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (near_border(q[i])) q[i] = settle(q[i], r.at(i), s);
-  }
+  uint32_t out[4], nearest = 0xFFFFFu;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * i], q[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * i + 2], q[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
-    out[i] = lo | hi << 16;
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      q[k] = r.at(4 * i + k) * inv;
+      nearest = min(nearest, off_border(q[k]));
+    }
+    out[i] = code2(q[0], q[1]) | code2(q[2], q[3]) << 16;
   }
+  if (nearest <= 16u) return settled_codes(x, T, at, s, inv);
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
@@ -133,7 +148,7 @@ rows_kernel(const void *__restrict__ x, int64_t total, uint32_t col_blocks, uint
 #pragma unroll
   for (int d = 1; d < kLanes; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
   const float s = scale_of(top);
-  if (in) *reinterpret_cast<uint4 *>(codes + at) = codes_of(r, s);
+  if (in) *reinterpret_cast<uint4 *>(codes + at) = codes_of(r, s, x, at);
   if (item < total && lane == 0) scales[item] = s;
 }
 
@@ -166,7 +181,7 @@ square_kernel(const void *__restrict__ x, int64_t rows, uint32_t cols, uint32_t 
 #pragma unroll
   for (int i = 0; i < kParts; ++i) {
     const int64_t row = row0 + i * kStep;
-    if (row < rows && col < cols) *reinterpret_cast<uint4 *>(codes + row * cols + col) = codes_of(r[i], s);
+    if (row < rows && col < cols) *reinterpret_cast<uint4 *>(codes + row * cols + col) = codes_of(r[i], s, x, row * cols + col);
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = s;
 }

@@ -811,19 +811,29 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   asm volatile("cp.async.wait_all;" ::: "memory");
   cluster_barrier();
 
+  // The block's tokens are rank, rank + cluster, ...: their slots' sums, weighted, go to the
+  // block's own z (nobody else reads a slot of its tokens), then the tokens'.
   const uint32_t z_at = smem_u32(z) + lane * 4, heads_at = smem_u32(sh.heads) + lane * 4;
-  for (int token = warp * cluster + rank; token < a.tokens; token += cluster * kMoeWarps) {
-    float sum = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < a.route.top_k; ++k) {
-      const int slot = token * a.route.top_k + k, unit = plan[slot].slot_unit, place = plan[slot].slot_place;
-      if (unit < 0) continue;
+  const int top = a.route.top_k, own = a.tokens > rank ? (a.tokens - rank + cluster - 1) / cluster : 0;
+  for (int i = warp; i < own * top; i += kMoeWarps) {
+    const int slot = (i / top * cluster + rank) * top + i % top;
+    const int unit = plan[slot].slot_unit, place = plan[slot].slot_place;
+    float v = 0.0f;
+    if (unit >= 0) {
       const int from = sh.unit_from[unit], to = sh.unit_to[unit];
-      float v = remote_f32(z_at + slot * 128, from / kMoeWarps);
+      v = remote_f32(z_at + slot * 128, from / kMoeWarps);
+#pragma unroll 4
       for (int w = from + 1; w <= to; ++w)
         v += remote_f32(heads_at + ((w % kMoeWarps) * kMoePass + place) * 128, w / kMoeWarps);
-      sum = fmaf(plan[slot].slot_weight, v, sum);
+      v *= plan[slot].slot_weight;
     }
+    z[slot * 32 + lane] = v;
+  }
+  __syncthreads();
+  for (int i = warp; i < own; i += kMoeWarps) {
+    const int token = i * cluster + rank;
+    float sum = 0.0f;
+    for (int k = 0; k < top; ++k) sum += z[(token * top + k) * 32 + lane];
     const int64_t at = static_cast<int64_t>(token) * a.w.hidden + row0 + lane;
     if (a.y_type == kTypeF32) static_cast<float *>(a.y)[at] = sum;
     else static_cast<uint16_t *>(a.y)[at] = a.y_type == kTypeBF16 ? ElemBF16::from_f32(sum) : ElemF16::from_f32(sum);
