@@ -76,6 +76,25 @@ __device__ __forceinline__ void wait_loads(uint32_t (&r)[16]) {
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
+__device__ __forceinline__ void load32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :: "memory");
+}
+
 // Two multiply-adds: (x0, x1) += (v0 f0, v1 f1).
 __device__ __forceinline__ void fma2(uint64_t &x, uint32_t v0, uint32_t v1, uint64_t f) {
   asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(x) : "r"(v0), "r"(v1), "l"(f));
@@ -87,8 +106,9 @@ __device__ __forceinline__ float half_of(uint64_t v, int i) {
   return __uint_as_float(static_cast<uint32_t>(i ? v >> 32 : v));
 }
 
+// (Inlined: a call would leave the epilogue without the registers that setmaxnreg gives it.)
 // Whole-warp bounded wait; false if it ran out or another role gave up.
-__device__ __noinline__ bool wait_slow(uint64_t *b, uint32_t parity, volatile int *abort, unsigned *err, uint32_t limit) {
+__device__ __forceinline__ bool wait_slow(uint64_t *b, uint32_t parity, volatile int *abort, unsigned *err, uint32_t limit) {
   uint32_t polls = 0;
   while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) {
     if ((++polls & 255u) == 0 || polls >= limit) {
@@ -201,17 +221,23 @@ __device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
 
 // ----------------------------------------------------------------- tall ----
 
-constexpr int kTallM = 128, kTallN = 256, kTallStages = 4, kTallThreads = 320;
+constexpr int kTallM = 128, kTallN = 256, kTallStages = 4;
+// Three warpgroups: one loads and multiplies (two of its warps), two are the epilogue, each
+// thread with 128 sums and two batches of 32 columns on their way in.  (tcgen05.wait::ld waits
+// for every load, so one batch flies while the other is added; batches of 16 made the epilogue
+// the slower side, 1070 cycles a step against the MMAs' 512.)  384 threads start with 168
+// registers; the epilogue takes what the first group gives back: 56 + 2 * 224 = 3 * 168.
+constexpr int kTallEpilogue = 8, kTallColumns = 128, kTallBatch = 32, kTallThreads = 384;
 constexpr int kTallA = kTallM * kStep, kTallB = kTallN * kStep;
 
-__device__ __forceinline__ void store_row(const Args &a, int64_t m, int64_t n, const uint64_t (&sum)[64]) {
+__device__ __forceinline__ void store_row(const Args &a, int64_t m, int64_t n, const uint64_t (&sum)[kTallColumns / 2]) {
   const int64_t at = m * a.N + n;
   const int size = a.y_type == kTypeF32 ? 4 : 2;
   char *to = static_cast<char *>(a.y) + at * size;
-  if (n + 128 <= a.N && reinterpret_cast<uintptr_t>(to) % 16 == 0) {
+  if (n + kTallColumns <= a.N && reinterpret_cast<uintptr_t>(to) % 16 == 0) {
     if (a.y_type == kTypeF32) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < kTallColumns / 4; ++i) {
         const uint64_t u = sum[2 * i], v = sum[2 * i + 1];
         reinterpret_cast<uint4 *>(to)[i] = make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32),
                                                       static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
@@ -219,7 +245,7 @@ __device__ __forceinline__ void store_row(const Args &a, int64_t m, int64_t n, c
     } else {
       const bool bf16 = a.y_type == kTypeBF16;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kTallColumns / 8; ++i) {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -231,7 +257,7 @@ __device__ __forceinline__ void store_row(const Args &a, int64_t m, int64_t n, c
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 128; ++i)
+    for (int i = 0; i < kTallColumns; ++i)
       if (n + i < a.N) store_one(a, at + i, half_of(sum[i / 2], i % 2));
   }
 }
@@ -242,7 +268,11 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   __shared__ Bars<kTallStages> bars;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
-  if (threadIdx.x == 0) init_bars(bars, 8);
+  if (threadIdx.x == 0) {
+    init_bars(bars, kTallEpilogue);
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&ma) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mw) : "memory");
+  }
   if (warp == 1) alloc_tmem(&bars.tmem, 512);
   fence_before();
   __syncthreads();
@@ -251,34 +281,21 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   const int m_tiles = (a.M + kTallM - 1) / kTallM, n_tiles = (a.N + kTallN - 1) / kTallN;
   const int64_t tiles = static_cast<int64_t>(m_tiles) * n_tiles;
 
-  if (warp == 0) {
-    Loader<kTallStages, kTallA, kTallB> load;
-    bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-      const int m0 = static_cast<int>(tile % m_tiles) * kTallM, n0 = static_cast<int>(tile / m_tiles) * kTallN;
-      for (int k = 0; ok && k < a.steps; ++k) ok = load.step(bars, &ma, &mw, smem, k * kStep, m0, n0, lane, a);
-    }
-    if (!ok) load.drain(bars, kDefaultWaitLimit);
-  } else if (warp == 1) {
-    Multiplier<kTallStages, kTallA, kTallB, kTallN> mul;
-    bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
-      for (int k = 0; ok && k < a.steps; ++k) ok = mul.step(bars, smem, tmem, lane, a);
-    mul.retire(bars, lane, kDefaultWaitLimit);
-  } else {
-    // Lanes 32 (warp % 4) .. of tensor memory are this warp's; half of the columns each.
-    const int row = 32 * (warp % 4) + lane, half = (warp - 2) / 4;
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16) + half * 128;
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // Lanes 32 (warp % 4) .. of tensor memory are this warp's, and a part of the columns.
+    const int row = 32 * (warp % 4) + lane, first = (warp - 4) / 4 * kTallColumns;
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16) + first;
     int acc = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-      const int64_t m = tile % m_tiles * kTallM + row, n = tile / m_tiles * kTallN + half * 128;
+      const int64_t m = tile % m_tiles * kTallM + row, n = tile / m_tiles * kTallN + first;
       const float *as = a.as + (m < a.M ? m : a.M - 1) * a.steps;
       const float *ws = a.ws + (n < a.N ? n / 128 : 0) * a.steps;
-      uint64_t sum[64];
+      uint64_t sum[kTallColumns / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) sum[i] = 0;
+      for (int i = 0; i < kTallColumns / 2; ++i) sum[i] = 0;
       float fa = __ldg(as), fw = __ldg(ws);
       for (int k = 0; k < a.steps; ++k) {
         const float f = fa * fw;
@@ -289,23 +306,41 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
           break;
         }
         fence_after();
-        uint32_t v[2][16];
-        load16(at + acc * kTallN, v[0]);
+        uint32_t v[2][kTallBatch];
+        load32(at + acc * kTallN, v[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kTallColumns / kTallBatch; ++c) {
           wait_loads(v[c % 2]);
-          if (c + 1 < 8) load16(at + acc * kTallN + 16 * (c + 1), v[(c + 1) % 2]);
-          if (c == 7) {
+          if (c + 1 < kTallColumns / kTallBatch) load32(at + acc * kTallN + kTallBatch * (c + 1), v[(c + 1) % 2]);
+          if (c + 1 == kTallColumns / kTallBatch) {
             fence_before();
             if (lane == 0) mbar_arrive(&bars.free[acc]);
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) fma2(sum[8 * c + i], v[c % 2][2 * i], v[c % 2][2 * i + 1], ff);
+          for (int i = 0; i < kTallBatch / 2; ++i)
+            fma2(sum[kTallBatch / 2 * c + i], v[c % 2][2 * i], v[c % 2][2 * i + 1], ff);
         }
         acc ^= 1;
         if (acc == 0) phase ^= 1u;
       }
       if (ok && m < a.M && n < a.N) store_row(a, m, n, sum);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      Loader<kTallStages, kTallA, kTallB> load;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        const int m0 = static_cast<int>(tile % m_tiles) * kTallM, n0 = static_cast<int>(tile / m_tiles) * kTallN;
+        for (int k = 0; ok && k < a.steps; ++k) ok = load.step(bars, &ma, &mw, smem, k * kStep, m0, n0, lane, a);
+      }
+      if (!ok) load.drain(bars, kDefaultWaitLimit);
+    } else if (warp == 1) {
+      Multiplier<kTallStages, kTallA, kTallB, kTallN> mul;
+      bool ok = true;
+      for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
+        for (int k = 0; ok && k < a.steps; ++k) ok = mul.step(bars, smem, tmem, lane, a);
+      mul.retire(bars, lane, kDefaultWaitLimit);
     }
   }
   fence_before();
@@ -349,7 +384,11 @@ flat_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   const int rank = blockIdx.x % split, n0 = blockIdx.x / split * 128, m0 = blockIdx.y * T;
   const int k0 = static_cast<int>(static_cast<int64_t>(a.steps) * rank / split);
   const int k1 = static_cast<int>(static_cast<int64_t>(a.steps) * (rank + 1) / split);
-  if (threadIdx.x == 0) init_bars(bars, kFlatEpilogue / 32);
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mw) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&ma) : "memory");
+    init_bars(bars, kFlatEpilogue / 32);
+  }
   if (warp == 1) alloc_tmem(&bars.tmem, flat_columns<T>());
   fence_before();
   __syncthreads();

@@ -4,8 +4,8 @@
 // scale = max(RN(amax / 448), 2^-126), code = the e4m3 value nearest to x / scale.  The
 // quotient is taken as x * RN(1 / scale): two roundings of 2^-24, so it is within 2^-22 of
 // the exact one and rounds to the same code unless a border between two codes is that near.
-// Those elements (2^-16 of them) are compared with the border itself: border * scale has
-// 5 + 24 bits and is exact in 64.  A division an element would cost more than the rest.
+// Those elements (2^-17 of them) are compared with the border itself, border * scale with x
+// in one fused multiply-add.  A division an element would cost more than the rest.
 //
 // Bound by memory: an element is read once and its code written once.  A thread holds 16
 // consecutive elements (columns are a multiple of 16, so none is cut): 8 threads a row of a
@@ -71,15 +71,20 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
 // fraction bit 4 set and those below clear, whatever its size.
 __device__ __forceinline__ float on_grid(float q) { return fabsf(q) < 0.015625f ? fabsf(q) + 0.015625f : fabsf(q); }
 
-// Distance of on_grid(q) from the next border, in units of its last place and off by 8.
-__device__ __forceinline__ uint32_t off_border(float q) { return (__float_as_uint(on_grid(q)) - 0x7FFF8u) & 0xFFFFFu; }
+// At most kNear where on_grid(q) is within 4 units of its last place of a border (it is off
+// by 2.5 at most: two roundings of half a unit of a number up to twice as large, and a third).
+constexpr uint32_t kNear = 8;
+__device__ __forceinline__ uint32_t off_border(float q) { return (__float_as_uint(on_grid(q)) - 0x7FFFCu) & 0xFFFFFu; }
 
 // q moved to the side of its border where x / s is.
 __device__ __forceinline__ float settle(float q, float x, float s) {
   const float up = on_grid(q), border = __uint_as_float((__float_as_uint(up) & 0xFFF00000u) | 0x80000u);
   const float t = fabsf(q) < 0.015625f ? border - 0.015625f : border;
-  const double d = fabs(static_cast<double>(x)) - static_cast<double>(t) * static_cast<double>(s);
-  const uint32_t bits = __float_as_uint(t) + (d > 0.0 ? 1u : d < 0.0 ? 0xFFFFFFFFu : 0u);
+  // t s has 5 + 24 bits: the fused multiply-add gives the difference's sign, after a factor
+  // that keeps small ones from vanishing.
+  const float by = s < 1.0f ? 1099511627776.0f : 1.0f;  // 2^40
+  const float d = fmaf(-t, s * by, fabsf(x) * by);
+  const uint32_t bits = __float_as_uint(t) + (d > 0.0f ? 1u : d < 0.0f ? 0xFFFFFFFFu : 0u);
   return copysignf(__uint_as_float(bits), x);
 }
 
@@ -87,7 +92,7 @@ __device__ __forceinline__ uint32_t code2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The 16 codes again, element by element, for a thread that met a border (one in 4000).
+// The 16 codes again, element by element, for a thread that met a border (one in 7000).
 // Rolled up: nothing here should cost the others instruction cache.
 __device__ __noinline__ uint4 settled_codes(const void *x, int type, int64_t at, float s, float inv) {
   uint32_t out[4] = {};
@@ -98,7 +103,7 @@ __device__ __noinline__ uint4 settled_codes(const void *x, int type, int64_t at,
                     : type == kTypeBF16 ? bf16_bits_to_f32(h)
                                         : ElemF16::to_f32(h);
     float q = v * inv;
-    if (off_border(q) <= 16u) q = settle(q, v, s);
+    if (off_border(q) <= kNear) q = settle(q, v, s);
     // shift the codes up by one byte and put this one below them
     out[3] = out[3] << 8 | out[2] >> 24;
     out[2] = out[2] << 8 | out[1] >> 24;
@@ -122,7 +127,7 @@ __device__ __forceinline__ uint4 codes_of(const Raw<T> &r, float s, const void *
     }
     out[i] = code2(q[0], q[1]) | code2(q[2], q[3]) << 16;
   }
-  if (nearest <= 16u) return settled_codes(x, T, at, s, inv);
+  if (nearest <= kNear) return settled_codes(x, T, at, s, inv);
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
@@ -137,7 +142,8 @@ rows_kernel(const void *__restrict__ x, int64_t total, uint32_t col_blocks, uint
   int64_t at = 0;
   bool in = item < total;
   if (in) {
-    const int64_t row = item / col_blocks;
+    // (a division of 64 bits would cost more than the codes)
+    const int64_t row = total < (int64_t(1) << 31) ? static_cast<uint32_t>(item) / col_blocks : item / col_blocks;
     const uint32_t col = static_cast<uint32_t>(item - row * col_blocks) * 128u + lane * kRun;
     at = row * cols + col;
     in = col < cols;
