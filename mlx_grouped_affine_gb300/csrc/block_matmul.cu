@@ -7,9 +7,13 @@
 // registers while the next step runs into a second accumulator.  Products are exact, sums
 // fp32.
 //
-//   warp 0      loads the codes by TMA (128-byte rows, 128-byte swizzle)
-//   warp 1      owns tensor memory and issues the MMAs (one lane)
+//   warp 0      loads the codes by TMA (128-byte rows, 128-byte swizzle), one lane
+//   warp 1      owns tensor memory and issues the MMAs, one lane
 //   the others  epilogue
+//
+// The issuing lane is the pace: with warp-wide waits, a commit for the ring and another for the
+// epilogue, a step took it 940 cycles, the MMAs 512.  So it waits alone, and one commit a step
+// tells both that the step is done.
 //
 // Two kernels.  `tall`: a 128 x 256 tile of y per block, an epilogue thread a row of A and
 // 128 columns of one block column of W, so that a step's factor is one number a thread.
@@ -127,20 +131,41 @@ __device__ __forceinline__ bool wait(uint64_t *b, uint32_t parity, volatile int 
   return wait_slow(b, parity, abort, a.err, a.limit);
 }
 
+// The same by one thread.
+__device__ __forceinline__ bool wait_alone(uint64_t *b, uint32_t parity, volatile int *abort, const Args &a) {
+  if (mbar_try_wait(b, parity)) return true;
+  uint32_t polls = 0;
+  while (!mbar_try_wait(b, parity)) {
+    if ((++polls & 255u) == 0 || polls >= a.limit) {
+      if (*abort) return false;
+      if (polls >= a.limit) {
+        *abort = 1;
+        atomicOr(a.err, kErrTimeoutBit);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// Step k uses stage k mod STAGES and accumulator k mod 2.  done[k mod STAGES] completes when
+// its MMAs have: the loader may fill the stage again, the epilogue read the accumulator.  (It
+// cannot complete once more before both have seen that: step k + STAGES needs the stage
+// filled, and step k + 2 the accumulator freed.)
 template <int STAGES>
 struct Bars {
-  uint64_t full[STAGES], empty[STAGES];  // tiles in shared memory
-  uint64_t ready[2], free[2];            // accumulators
-  uint64_t done;
+  uint64_t full[STAGES], done[STAGES];
+  uint64_t free[2];  // accumulators
+  uint64_t retired;
   uint32_t tmem;
   int abort;
 };
 
 template <int STAGES>
 __device__ __forceinline__ void init_bars(Bars<STAGES> &b, uint32_t epilogue_warps) {
-  for (int i = 0; i < STAGES; ++i) mbar_init(&b.full[i], 1), mbar_init(&b.empty[i], 1);
-  for (int i = 0; i < 2; ++i) mbar_init(&b.ready[i], 1), mbar_init(&b.free[i], epilogue_warps);
-  mbar_init(&b.done, 1);
+  for (int i = 0; i < STAGES; ++i) mbar_init(&b.full[i], 1), mbar_init(&b.done[i], 1);
+  for (int i = 0; i < 2; ++i) mbar_init(&b.free[i], epilogue_warps);
+  mbar_init(&b.retired, 1);
   b.abort = 0;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -152,21 +177,19 @@ __device__ __forceinline__ void free_tmem(uint32_t at, uint32_t columns) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
 }
 
-// Loads of one block's steps into the ring: rows at y0 of the MMA's A tile, at y1 of its B.
+// Loads of a block's steps into the ring, by one lane: rows at y0 of the MMA's A tile, at y1
+// of its B.
 template <int STAGES, int A_BYTES, int B_BYTES>
 struct Loader {
   int stage = 0;
   uint32_t phase = 0, used = 0;  // used: stages loaded at least once
   __device__ __forceinline__ bool step(Bars<STAGES> &bars, const CUtensorMap *ma, const CUtensorMap *mb, uint32_t smem, int x,
-                                       int y0, int y1, int lane, const Args &a) {
-    if (!wait(&bars.empty[stage], phase ^ 1u, &bars.abort, a)) return false;
-    if (lane == 0) {
-      const uint32_t at = smem + stage * (A_BYTES + B_BYTES);
-      mbar_expect_tx(&bars.full[stage], A_BYTES + B_BYTES);
-      load_tile(at, ma, x, y0, &bars.full[stage]);
-      load_tile(at + A_BYTES, mb, x, y1, &bars.full[stage]);
-    }
-    __syncwarp();
+                                       int y0, int y1, const Args &a) {
+    if (!wait_alone(&bars.done[stage], phase ^ 1u, &bars.abort, a)) return false;
+    const uint32_t at = smem + stage * (A_BYTES + B_BYTES);
+    mbar_expect_tx(&bars.full[stage], A_BYTES + B_BYTES);
+    load_tile(at, ma, x, y0, &bars.full[stage]);
+    load_tile(at + A_BYTES, mb, x, y1, &bars.full[stage]);
     used |= 1u << stage;
     if (++stage == STAGES) stage = 0, phase ^= 1u;
     return true;
@@ -176,41 +199,38 @@ struct Loader {
     for (int i = 0; i < STAGES; ++i) {
       if (!(used >> i & 1u)) continue;
       const uint32_t last = i < stage ? phase : phase ^ 1u;
-      for (uint32_t polls = 0; polls < limit; ++polls)
-        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars.full[i], last))) break;
+      for (uint32_t polls = 0; polls < limit && !mbar_try_wait(&bars.full[i], last); ++polls) {
+      }
     }
   }
 };
 
-// The MMAs of one block's steps.
+// The MMAs of a block's steps, by one lane.
 template <int STAGES, int A_BYTES, int B_BYTES, int COLUMNS>
 struct Multiplier {
   int stage = 0, acc = 0;
   uint32_t phase = 0, acc_phase = 0;
-  __device__ __forceinline__ bool step(Bars<STAGES> &bars, uint32_t smem, uint32_t tmem, int lane, const Args &a) {
-    if (!wait(&bars.free[acc], acc_phase ^ 1u, &bars.abort, a) || !wait(&bars.full[stage], phase, &bars.abort, a)) return false;
+  __device__ __forceinline__ bool step(Bars<STAGES> &bars, uint32_t smem, uint32_t tmem, const Args &a) {
+    if (!wait_alone(&bars.free[acc], acc_phase ^ 1u, &bars.abort, a) ||
+        !wait_alone(&bars.full[stage], phase, &bars.abort, a))
+      return false;
     fence_after();
-    if (lane == 0) {
-      const uint32_t at = smem + stage * (A_BYTES + B_BYTES);
-      const uint64_t da = tile_desc(at), db = tile_desc(at + A_BYTES);
+    const uint32_t at = smem + stage * (A_BYTES + B_BYTES);
+    const uint64_t da = tile_desc(at), db = tile_desc(at + A_BYTES);
 #pragma unroll
-      for (int j = 0; j < kStep / 32; ++j)
-        mma_e4m3(tmem + acc * COLUMNS, da + 2 * j, db + 2 * j, mma_desc(COLUMNS), j ? 1u : 0u);
-      commit(&bars.empty[stage]);
-      commit(&bars.ready[acc]);
-    }
-    __syncwarp();
+    for (int j = 0; j < kStep / 32; ++j)
+      mma_e4m3(tmem + acc * COLUMNS, da + 2 * j, db + 2 * j, mma_desc(COLUMNS), j ? 1u : 0u);
+    commit(&bars.done[stage]);
     if (++stage == STAGES) stage = 0, phase ^= 1u;
     acc ^= 1;
     if (acc == 0) acc_phase ^= 1u;
     return true;
   }
   // Every MMA issued retires before tensor memory is freed.
-  __device__ __forceinline__ void retire(Bars<STAGES> &bars, int lane, uint32_t limit) {
-    if (lane == 0) commit(&bars.done);
-    __syncwarp();
-    for (uint32_t polls = 0; polls < limit; ++polls)
-      if (__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars.done, 0))) break;
+  __device__ __forceinline__ void retire(Bars<STAGES> &bars, uint32_t limit) {
+    commit(&bars.retired);
+    for (uint32_t polls = 0; polls < limit && !mbar_try_wait(&bars.retired, 0); ++polls) {
+    }
   }
 };
 
@@ -286,7 +306,7 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     // Lanes 32 (warp % 4) .. of tensor memory are this warp's, and a part of the columns.
     const int row = 32 * (warp % 4) + lane, first = (warp - 4) / 4 * kTallColumns;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16) + first;
-    int acc = 0;
+    int acc = 0, stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
@@ -301,7 +321,7 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         const float f = fa * fw;
         const uint64_t ff = pair(f, f);
         if (k + 1 < a.steps) fa = __ldg(as + k + 1), fw = __ldg(ws + k + 1);
-        if (!wait(&bars.ready[acc], phase, &bars.abort, a)) {
+        if (!wait(&bars.done[stage], phase, &bars.abort, a)) {
           ok = false;
           break;
         }
@@ -321,26 +341,26 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
             fma2(sum[kTallBatch / 2 * c + i], v[c % 2][2 * i], v[c % 2][2 * i + 1], ff);
         }
         acc ^= 1;
-        if (acc == 0) phase ^= 1u;
+        if (++stage == kTallStages) stage = 0, phase ^= 1u;
       }
       if (ok && m < a.M && n < a.N) store_row(a, m, n, sum);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0) {
+    if (warp == 0 && lane == 0) {
       Loader<kTallStages, kTallA, kTallB> load;
       bool ok = true;
       for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
         const int m0 = static_cast<int>(tile % m_tiles) * kTallM, n0 = static_cast<int>(tile / m_tiles) * kTallN;
-        for (int k = 0; ok && k < a.steps; ++k) ok = load.step(bars, &ma, &mw, smem, k * kStep, m0, n0, lane, a);
+        for (int k = 0; ok && k < a.steps; ++k) ok = load.step(bars, &ma, &mw, smem, k * kStep, m0, n0, a);
       }
       if (!ok) load.drain(bars, kDefaultWaitLimit);
-    } else if (warp == 1) {
+    } else if (warp == 1 && lane == 0) {
       Multiplier<kTallStages, kTallA, kTallB, kTallN> mul;
       bool ok = true;
       for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x)
-        for (int k = 0; ok && k < a.steps; ++k) ok = mul.step(bars, smem, tmem, lane, a);
-      mul.retire(bars, lane, kDefaultWaitLimit);
+        for (int k = 0; ok && k < a.steps; ++k) ok = mul.step(bars, smem, tmem, a);
+      mul.retire(bars, kDefaultWaitLimit);
     }
   }
   fence_before();
@@ -402,22 +422,26 @@ flat_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
   const int row = 32 * (warp % 4) + lane;
 
   if (warp == 0) {
-    Loader<kStages, kA, kB> load;
-    bool ok = true;
-    for (int k = k0; ok && k < k1; ++k) ok = load.step(bars, &mw, &ma, smem, k * kStep, n0, m0, lane, a);
-    if (!ok) load.drain(bars, kDefaultWaitLimit);
+    if (lane == 0) {
+      Loader<kStages, kA, kB> load;
+      bool ok = true;
+      for (int k = k0; ok && k < k1; ++k) ok = load.step(bars, &mw, &ma, smem, k * kStep, n0, m0, a);
+      if (!ok) load.drain(bars, kDefaultWaitLimit);
+    }
   } else if (warp == 1) {
-    Multiplier<kStages, kA, kB, T> mul;
-    bool ok = true;
-    for (int k = k0; ok && k < k1; ++k) ok = mul.step(bars, smem, tmem, lane, a);
-    mul.retire(bars, lane, kDefaultWaitLimit);
+    if (lane == 0) {
+      Multiplier<kStages, kA, kB, T> mul;
+      bool ok = true;
+      for (int k = k0; ok && k < k1; ++k) ok = mul.step(bars, smem, tmem, a);
+      mul.retire(bars, kDefaultWaitLimit);
+    }
   } else {
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16);
     const float *ws = a.ws + static_cast<int64_t>(n0 / 128) * a.steps;
     const int column = threadIdx.x - 64;  // of A's rows, whose factor this thread fetches
     const int64_t m = m0 + column;
     const float *as = a.as + (m < a.M ? m : a.M - 1) * a.steps;
-    int acc = 0;
+    int acc = 0, stage = 0;
     uint32_t phase = 0;
     float f = column < T && k0 < k1 ? __ldg(as + k0) * __ldg(ws + k0) : 0.0f;
     bool ok = true;
@@ -425,7 +449,7 @@ flat_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       if (column < T) factors[k % 2][column] = f;
       if (column < T && k + 1 < k1) f = __ldg(as + k + 1) * __ldg(ws + k + 1);
       asm volatile("bar.sync 1, %0;" ::"n"(kFlatEpilogue) : "memory");
-      ok = ok && wait(&bars.ready[acc], phase, &bars.abort, a);
+      ok = ok && wait(&bars.done[stage], phase, &bars.abort, a);
       if (!ok) continue;
       fence_after();
 #pragma unroll
@@ -445,7 +469,7 @@ flat_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         }
       }
       acc ^= 1;
-      if (acc == 0) phase ^= 1u;
+      if (++stage == kStages) stage = 0, phase ^= 1u;
     }
   }
   fence_before();
