@@ -250,40 +250,59 @@ constexpr int kTallM = 128, kTallN = 256, kTallStages = 4;
 constexpr int kTallEpilogue = 8, kTallColumns = 128, kTallBatch = 32, kTallThreads = 384;
 constexpr int kTallA = kTallM * kStep, kTallB = kTallN * kStep;
 
-__device__ __forceinline__ void store_row(const Args &a, int64_t m, int64_t n, const uint64_t (&sum)[kTallColumns / 2]) {
-  const int64_t at = m * a.N + n;
-  const int size = a.y_type == kTypeF32 ? 4 : 2;
-  char *to = static_cast<char *>(a.y) + at * size;
-  if (n + kTallColumns <= a.N && reinterpret_cast<uintptr_t>(to) % 16 == 0) {
-    if (a.y_type == kTypeF32) {
+// Sums 2 first .. of a row as 128 bytes of y.
+__device__ __forceinline__ void as_output(const uint64_t *sum, int type, uint4 (&out)[8]) {
+  uint32_t w[32];
+  if (type == kTypeF32) {
 #pragma unroll
-      for (int i = 0; i < kTallColumns / 4; ++i) {
-        const uint64_t u = sum[2 * i], v = sum[2 * i + 1];
-        reinterpret_cast<uint4 *>(to)[i] = make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32),
-                                                      static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32));
-      }
-    } else {
-      const bool bf16 = a.y_type == kTypeBF16;
-#pragma unroll
-      for (int i = 0; i < kTallColumns / 8; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float lo = half_of(sum[4 * i + k], 0), hi = half_of(sum[4 * i + k], 1);
-          w[k] = bf16 ? ElemBF16::pack2(lo, hi) : ElemF16::pack2(lo, hi);
-        }
-        reinterpret_cast<uint4 *>(to)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
+    for (int i = 0; i < 16; ++i) w[2 * i] = static_cast<uint32_t>(sum[i]), w[2 * i + 1] = static_cast<uint32_t>(sum[i] >> 32);
   } else {
 #pragma unroll
-    for (int i = 0; i < kTallColumns; ++i)
-      if (n + i < a.N) store_one(a, at + i, half_of(sum[i / 2], i % 2));
+    for (int i = 0; i < 32; ++i) {
+      const float lo = half_of(sum[i], 0), hi = half_of(sum[i], 1);
+      w[i] = type == kTypeBF16 ? ElemBF16::pack2(lo, hi) : ElemF16::pack2(lo, hi);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// A warp's 32 rows of 128 columns to y by TMA, 128 bytes of each row at a time, from 4 KB of
+// its own: the warp goes on while they are written.  (Stored by the threads themselves, each to
+// a row of its own, they held the next tile's steps up by a quarter of the time of a tile.)
+__device__ __forceinline__ void send_rows(const Args &a, const CUtensorMap *my, uint32_t out, int m, int n, int lane,
+                                          const uint64_t (&sum)[kTallColumns / 2]) {
+  auto send = [&](const uint64_t *part, int at) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    uint4 v[8];
+    as_output(part, a.y_type, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // (the 128-byte swizzle of the map)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 128 + ((i ^ (lane & 7)) << 4)), "r"(v[i].x),
+                   "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                   : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0 && n + at < a.N) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(my), "r"(n + at), "r"(m),
+                   "r"(out)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  };
+  if (a.y_type == kTypeF32) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) send(&sum[16 * r], 32 * r);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) send(&sum[32 * r], 64 * r);
   }
 }
 
 __global__ void __launch_bounds__(kTallThreads, 1)
-tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args a) {
+tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw,
+            const __grid_constant__ CUtensorMap my, const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) unsigned char raw[];
   __shared__ Bars<kTallStages> bars;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -308,6 +327,8 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * (warp % 4)) << 16) + first;
     int acc = 0, stage = 0;
     uint32_t phase = 0;
+    const uint32_t out = smem + kTallStages * (kTallA + kTallB) + (warp - 4) * 4096;
+    const bool by_tma = a.N * (a.y_type == kTypeF32 ? 4ll : 2ll) % 16 == 0;  // rows that TMA can address
     bool ok = true;
     for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
       const int64_t m = tile % m_tiles * kTallM + row, n = tile / m_tiles * kTallN + first;
@@ -343,8 +364,16 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         acc ^= 1;
         if (++stage == kTallStages) stage = 0, phase ^= 1u;
       }
-      if (ok && m < a.M && n < a.N) store_row(a, m, n, sum);
+      if (!ok) break;
+      if (by_tma) {
+        if (m - lane < a.M) send_rows(a, &my, out, static_cast<int>(m) - lane, static_cast<int>(n), lane, sum);
+      } else if (m < a.M) {
+#pragma unroll
+        for (int i = 0; i < kTallColumns; ++i)
+          if (n + i < a.N) store_one(a, m * a.N + n + i, half_of(sum[i / 2], i % 2));
+      }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the block's memory goes
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
@@ -563,11 +592,18 @@ cudaError_t launch_block_matmul(const uint8_t *pa, const float *a_scales, int M,
   cudaError_t e = code_map(&ma, pa, M, K, kTallM);
   if (e == cudaSuccess) e = code_map(&mw, w, N, K, kTallN);
   if (e != cudaSuccess) return e;
-  const size_t bytes = 1024 + static_cast<size_t>(kTallStages) * (kTallA + kTallB);
+  // y in boxes of 128 bytes by 32 rows (unused where its rows are no multiple of 16 bytes).
+  CUtensorMap my = {};
+  const uint64_t size = y_type == kTypeF32 ? 4 : 2;
+  if (N * size % 16 == 0)
+    e = encode_map_2d(&my, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, y, N, M, N * size,
+                      static_cast<uint32_t>(128 / size), 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e != cudaSuccess) return e;
+  const size_t bytes = 1024 + static_cast<size_t>(kTallStages) * (kTallA + kTallB) + kTallEpilogue * 4096;
   e = ensure_smem_limit<tall_kernel>(bytes);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(tiles < sm_count() ? tiles : sm_count());
-  tall_kernel<<<grid, kTallThreads, bytes, stream>>>(ma, mw, a);
+  tall_kernel<<<grid, kTallThreads, bytes, stream>>>(ma, mw, my, a);
   return cudaGetLastError();
 }
 
