@@ -80,25 +80,6 @@ __device__ __forceinline__ void wait_loads(uint32_t (&r)[16]) {
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
-__device__ __forceinline__ void load32(uint32_t at, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
-        "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at));
-}
-__device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :: "memory");
-}
-
 // Two multiply-adds: (x0, x1) += (v0 f0, v1 f1).
 __device__ __forceinline__ void fma2(uint64_t &x, uint32_t v0, uint32_t v1, uint64_t f) {
   asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(x) : "r"(v0), "r"(v1), "l"(f));
@@ -243,60 +224,78 @@ __device__ __forceinline__ void store_one(const Args &a, int64_t at, float v) {
 
 constexpr int kTallM = 128, kTallN = 256, kTallStages = 4;
 // Three warpgroups: one loads and multiplies (two of its warps), two are the epilogue, each
-// thread with 128 sums and two batches of 32 columns on their way in.  (tcgen05.wait::ld waits
-// for every load, so one batch flies while the other is added; batches of 16 made the epilogue
-// the slower side, 1070 cycles a step against the MMAs' 512.)  384 threads start with 168
-// registers; the epilogue takes what the first group gives back: 56 + 2 * 224 = 3 * 168.
-constexpr int kTallEpilogue = 8, kTallColumns = 128, kTallBatch = 32, kTallThreads = 384;
+// thread with 128 sums and two batches of 16 columns on their way in (tcgen05.wait::ld waits
+// for every load, so one batch flies while the other is added).  384 threads start with 168
+// registers; the epilogue takes what the first group gives back: 56 + 2 * 224 = 3 * 168.  (A
+// spill there costs half of the rate.)
+constexpr int kTallEpilogue = 8, kTallColumns = 128, kTallBatch = 16, kTallThreads = 384;
 constexpr int kTallA = kTallM * kStep, kTallB = kTallN * kStep;
 
-// Sums 2 first .. of a row as 128 bytes of y.
-__device__ __forceinline__ void as_output(const uint64_t *sum, int type, uint4 (&out)[8]) {
-  uint32_t w[32];
+// Scales of four steps, fetched four steps ahead: a thread's row of A is a line of its own,
+// and a load of 4 bytes a step, 32 lines a warp, held the epilogue up.
+struct Factors {
+  float a[4] = {}, w[4] = {};
+  __device__ __forceinline__ void load(const float *as, const float *ws, int k, int steps) {
+    if (steps % 4 == 0) {  // (then rows are 16-byte aligned)
+      if (k >= steps) return;
+      const float4 u = __ldg(reinterpret_cast<const float4 *>(as + k)), v = __ldg(reinterpret_cast<const float4 *>(ws + k));
+      a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w;
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + i < steps) a[i] = __ldg(as + k + i), w[i] = __ldg(ws + k + i);
+    }
+  }
+};
+
+// 64 bytes of a row of y: 16 sums (fp32) or 32.
+__device__ __forceinline__ void as_output(const uint64_t *sum, int type, uint32_t (&w)[16]) {
   if (type == kTypeF32) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[2 * i] = static_cast<uint32_t>(sum[i]), w[2 * i + 1] = static_cast<uint32_t>(sum[i] >> 32);
+    for (int i = 0; i < 8; ++i) w[2 * i] = static_cast<uint32_t>(sum[i]), w[2 * i + 1] = static_cast<uint32_t>(sum[i] >> 32);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
       const float lo = half_of(sum[i], 0), hi = half_of(sum[i], 1);
       w[i] = type == kTypeBF16 ? ElemBF16::pack2(lo, hi) : ElemF16::pack2(lo, hi);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// A warp's 32 rows of 128 columns to y by TMA, 128 bytes of each row at a time, from 4 KB of
-// its own: the warp goes on while they are written.  (Stored by the threads themselves, each to
-// a row of its own, they held the next tile's steps up by a quarter of the time of a tile.)
+// A warp's 32 rows of 128 columns to y by TMA, 64 bytes of each row at a time, from two
+// buffers of 2 KB of its own: the warp goes on while they are written.  (Stored by the threads
+// themselves, each to a row of its own, they held the next tile's steps up by a quarter of the
+// time of a tile.)
 __device__ __forceinline__ void send_rows(const Args &a, const CUtensorMap *my, uint32_t out, int m, int n, int lane,
                                           const uint64_t (&sum)[kTallColumns / 2]) {
-  auto send = [&](const uint64_t *part, int at) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  auto send = [&](const uint64_t *part, int at, int buffer) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the buffer's last one is read
     __syncwarp();
-    uint4 v[8];
-    as_output(part, a.y_type, v);
+    uint32_t w[16];
+    as_output(part, a.y_type, w);
+    const uint32_t to = out + buffer * 2048 + lane * 64;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // (the 128-byte swizzle of the map)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + lane * 128 + ((i ^ (lane & 7)) << 4)), "r"(v[i].x),
-                   "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+    for (int i = 0; i < 4; ++i)  // (the 64-byte swizzle of the map)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((i ^ (lane >> 1 & 3)) << 4)), "r"(w[4 * i]),
+                   "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
                    : "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
-    if (lane == 0 && n + at < a.N) {
-      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(my), "r"(n + at), "r"(m),
-                   "r"(out)
-                   : "memory");
+    if (lane == 0) {
+      if (n + at < a.N)
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(my), "r"(n + at),
+                     "r"(m), "r"(out + buffer * 2048)
+                     : "memory");
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   };
   if (a.y_type == kTypeF32) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) send(&sum[16 * r], 32 * r);
+    for (int r = 0; r < 8; ++r) send(&sum[8 * r], 16 * r, r % 2);
   } else {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) send(&sum[32 * r], 64 * r);
+    for (int r = 0; r < 4; ++r) send(&sum[16 * r], 32 * r, r % 2);
   }
 }
 
@@ -330,29 +329,41 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
     const uint32_t out = smem + kTallStages * (kTallA + kTallB) + (warp - 4) * 4096;
     const bool by_tma = a.N * (a.y_type == kTypeF32 ? 4ll : 2ll) % 16 == 0;  // rows that TMA can address
     bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+    const float *as, *ws;
+    Factors next;
+    auto begin = [&](int64_t tile) {
       const int64_t m = tile % m_tiles * kTallM + row, n = tile / m_tiles * kTallN + first;
-      const float *as = a.as + (m < a.M ? m : a.M - 1) * a.steps;
-      const float *ws = a.ws + (n < a.N ? n / 128 : 0) * a.steps;
+      as = a.as + (m < a.M ? m : a.M - 1) * a.steps;
+      ws = a.ws + (n < a.N ? n / 128 : 0) * a.steps;
+      next.load(as, ws, 0, a.steps);
+    };
+    begin(blockIdx.x);
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      const int64_t m = tile % m_tiles * kTallM + row, n = tile / m_tiles * kTallN + first;
       uint64_t sum[kTallColumns / 2];
 #pragma unroll
       for (int i = 0; i < kTallColumns / 2; ++i) sum[i] = 0;
-      float fa = __ldg(as), fw = __ldg(ws);
+      float four[4] = {};
       for (int k = 0; k < a.steps; ++k) {
-        const float f = fa * fw;
-        const uint64_t ff = pair(f, f);
-        if (k + 1 < a.steps) fa = __ldg(as + k + 1), fw = __ldg(ws + k + 1);
+        if (k % 4 == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) four[i] = next.a[i] * next.w[i];
+          next.load(as, ws, k + 4, a.steps);
+        }
+        const uint64_t ff = pair(four[0], four[0]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) four[i] = four[i + 1];
         if (!wait(&bars.done[stage], phase, &bars.abort, a)) {
           ok = false;
           break;
         }
         fence_after();
         uint32_t v[2][kTallBatch];
-        load32(at + acc * kTallN, v[0]);
+        load16(at + acc * kTallN, v[0]);
 #pragma unroll
         for (int c = 0; c < kTallColumns / kTallBatch; ++c) {
           wait_loads(v[c % 2]);
-          if (c + 1 < kTallColumns / kTallBatch) load32(at + acc * kTallN + kTallBatch * (c + 1), v[(c + 1) % 2]);
+          if (c + 1 < kTallColumns / kTallBatch) load16(at + acc * kTallN + kTallBatch * (c + 1), v[(c + 1) % 2]);
           if (c + 1 == kTallColumns / kTallBatch) {
             fence_before();
             if (lane == 0) mbar_arrive(&bars.free[acc]);
@@ -365,6 +376,7 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         if (++stage == kTallStages) stage = 0, phase ^= 1u;
       }
       if (!ok) break;
+      if (tile + gridDim.x < tiles) begin(tile + gridDim.x);
       if (by_tma) {
         if (m - lane < a.M) send_rows(a, &my, out, static_cast<int>(m) - lane, static_cast<int>(n), lane, sum);
       } else if (m < a.M) {
@@ -592,12 +604,12 @@ cudaError_t launch_block_matmul(const uint8_t *pa, const float *a_scales, int M,
   cudaError_t e = code_map(&ma, pa, M, K, kTallM);
   if (e == cudaSuccess) e = code_map(&mw, w, N, K, kTallN);
   if (e != cudaSuccess) return e;
-  // y in boxes of 128 bytes by 32 rows (unused where its rows are no multiple of 16 bytes).
+  // y in boxes of 64 bytes by 32 rows (unused where its rows are no multiple of 16 bytes).
   CUtensorMap my = {};
   const uint64_t size = y_type == kTypeF32 ? 4 : 2;
   if (N * size % 16 == 0)
     e = encode_map_2d(&my, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, y, N, M, N * size,
-                      static_cast<uint32_t>(128 / size), 32, CU_TENSOR_MAP_SWIZZLE_128B);
+                      static_cast<uint32_t>(64 / size), 32, CU_TENSOR_MAP_SWIZZLE_64B);
   if (e != cudaSuccess) return e;
   const size_t bytes = 1024 + static_cast<size_t>(kTallStages) * (kTallA + kTallB) + kTallEpilogue * 4096;
   e = ensure_smem_limit<tall_kernel>(bytes);
