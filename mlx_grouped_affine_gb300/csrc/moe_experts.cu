@@ -105,9 +105,12 @@ __device__ void make_plan(const Routing r, const int tokens, const int experts, 
   __syncthreads();
   if (s < slots) {
     const int e = p.expert[s], at = e < 0 ? 0 : p.table[e], place = e < 0 ? 0 : p.place[s];
-    if (e >= 0) out->entries[(at & 0xFFFF) + place].listed = static_cast<short>(s);
-    out->entries[s].slot_unit = static_cast<short>(e < 0 ? -1 : (at >> 16) + place / kMoePass);
-    out->entries[s].slot_place = static_cast<short>(place % kMoePass);
+    if (e >= 0) {
+      out->entries[(at & 0xFFFF) + place].listed = static_cast<short>(s);
+      out->entries[(at & 0xFFFF) + place].token = static_cast<short>(s / r.top_k);
+    }
+    // (unit and place side by side: the unit's first place is a multiple of kMoePass)
+    out->entries[s].slot_unit = static_cast<short>(e < 0 ? -1 : (at >> 16) * kMoePass + place);
     out->entries[s].slot_weight = p.weight[s];
   }
 }
@@ -153,6 +156,7 @@ cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Rout
   a.y_type = y_type;
   a.plan = plan;
   a.wait_limit = wait_limit();
+  a.two_to_127 = kTwoTo127;
   a.x_plane = round128(n);
   a.x_planes = x_type == kTypeBF16 ? 1 : x_type == kTypeF16 ? 2 : 3;
   a.x = x_type == kTypeBF16 ? static_cast<const uint16_t *>(x) : planes;

@@ -49,6 +49,7 @@ struct MoeArgs {
   const MoePlan *plan;
   unsigned *err;
   uint32_t wait_limit;
+  uint32_t two_to_127;  // kTwoTo127
 };
 
 // ------------------------------------------------------------- the plan ----
@@ -58,8 +59,8 @@ struct MoeArgs {
 // Three tables side by side, an entry of each per slot: units, slots unit by unit, slots.
 struct alignas(16) MoeEntry {
   short unit_expert, unit_first, unit_count;  // of unit i; first in the second table
-  short listed;                               // the slot at place i
-  short slot_unit, slot_place;                // of slot i; -1: no part in y; its place in the unit
+  short listed, token;                        // the slot at place i, and its token
+  short slot_unit;                            // of slot i: unit * kMoePass + place in it; -1: no part in y
   float slot_weight;
 };
 struct MoePlan {
@@ -121,10 +122,23 @@ struct Run {
 // Codes as bf16 pairs, each code * 2^-6.  A bf16 pattern P <= 0xFF is worth P * 2^-133, so
 // a code at bit o of a half reads as c * 2^(o - 133), and times 2^(127 - o) it is exact and
 // normal.  sum(x) is taken times 2^-6 too, and the sums times 2^6 at the end.
+// The factors come with the call's arguments: constants would be put into a register again
+// for every product (32 instructions a group).
+constexpr uint32_t kTwoTo127 = 0x7F007F00u;
+template <int BITS>
+struct Factors {
+  static constexpr int kCount = BITS == 8 ? 1 : BITS == 4 ? 2 : BITS == 2 ? 4 : 1;
+  uint32_t v[kCount];  // (2^(127 - o), 2^(127 - o)) for o = 0, BITS, 2 BITS ..
+  __device__ __forceinline__ explicit Factors(uint32_t two_to_127) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) v[i] = two_to_127 - (static_cast<uint32_t>(i * BITS) << 7) * 0x00010001u;
+  }
+};
 constexpr float kUnscale = 64.0f;
 constexpr uint32_t kOnes = 0x3C803C80u;  // 2^-6
 template <int BITS, int G>
-__device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
+__device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, const Factors<BITS> &f,
+                                             uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
   using R = Run<BITS, G>;
   if constexpr (R::kSplit) {
     constexpr int kHalf = 16 / BITS, kPerSub = R::kSub * BITS / 32;
@@ -135,13 +149,13 @@ __device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, uint32_
 #pragma unroll
       for (int j = 0; j < kHalf; ++j) {
         const int o = j * BITS % 8, sh = j * BITS - o;
-        p[i * kHalf + j] = bf16x2_fma((w >> sh) & (kMask << o), ((254u - o) << 7) * 0x00010001u, 0x80008000u);
+        p[i * kHalf + j] = bf16x2_fma((w >> sh) & (kMask << o), f.v[o / BITS], 0x80008000u);
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < R::kSub / 2; ++i)
-      p[i] = bf16x2_fma(pair_at<BITS>(v, sub * R::kSub + 2 * i), (254u << 7) * 0x00010001u, 0x80008000u);
+      p[i] = bf16x2_fma(pair_at<BITS>(v, sub * R::kSub + 2 * i), f.v[0], 0x80008000u);
   }
 }
 
@@ -177,14 +191,16 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, i
       : "memory");
 }
 
-template <int N>
+template <int N, int OFF>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t *v) {
   if constexpr (N == 4)
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(a));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(a), "n"(OFF));
   else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(v[0]), "=r"(v[1]) : "r"(a), "n"(OFF));
   else
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v[0]) : "r"(a));
+    asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(v[0]) : "r"(a), "n"(OFF));
 }
 
 // Scales and biases of a chunk, of the row that this lane stands for: row g + 8 (t % 2) of
@@ -207,19 +223,22 @@ struct Scales {
     }
   }
   // As fp32 pairs (s, b) to `to`, [step][lane's row]: what every lane of the rows reads.
-  __device__ __forceinline__ void spread(uint32_t to, int lane, int type) const {
-    const uint32_t at = to + ((lane % 4) * 8 + lane / 4) * 8;
+  __device__ static __forceinline__ void put(uint32_t at, float fs, float fb) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(fs), "f"(fb) : "memory");
+  }
+  __device__ __forceinline__ void spread(uint32_t at, int type) const {
+    if (type == kTypeBF16) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      float fs, fb;
-      if (type == kTypeF32) {
-        fs = __uint_as_float(s[i]), fb = __uint_as_float(b[i]);
-      } else {
-        const uint32_t u = prmt(s[i / 2], b[i / 2], i & 1 ? 0x7632u : 0x5410u);
-        if (type == kTypeBF16) fs = __uint_as_float(u << 16), fb = __uint_as_float(u & 0xFFFF0000u);
-        else fs = ElemF16::to_f32(u & 0xFFFFu), fb = ElemF16::to_f32(u >> 16);
-      }
-      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + i * 256), "f"(fs), "f"(fb) : "memory");
+      for (int i = 0; i < STEPS; ++i)
+        put(at + i * 256, __uint_as_float(i & 1 ? s[i / 2] & 0xFFFF0000u : s[i / 2] << 16),
+            __uint_as_float(i & 1 ? b[i / 2] & 0xFFFF0000u : b[i / 2] << 16));
+    } else if (type == kTypeF16) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+        put(at + i * 256, ElemF16::to_f32(s[i / 2] >> (16 * (i & 1)) & 0xFFFFu), ElemF16::to_f32(b[i / 2] >> (16 * (i & 1)) & 0xFFFFu));
+    } else {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) put(at + i * 256, __uint_as_float(s[i]), __uint_as_float(b[i]));
     }
   }
   // From ps and pb on, `count` groups of them.  `whole`: 16-bit types, rows of whole chunks
@@ -301,7 +320,7 @@ __device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>:
 // must not outgrow.
 template <int BITS, int G, int HALVES>
 __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<HALVES> &c, int at, int count,
-                                        uint32_t scales, float (&acc)[HALVES][8]) {
+                                        uint32_t scales, const Factors<BITS> &f, float (&acc)[HALVES][8]) {
   using R = Run<BITS, G>;
   const int g = lane / 4, t = lane % 4;
   const uint32_t rows = stage + g * R::kRowBytes, flip = (t * R::kBits / 32 * 4) ^ R::swap(g);
@@ -320,8 +339,10 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
       const uint32_t off = step * (G * BITS / 8) + 4 * i;
       const uint32_t from = rows + (R::kSwizzle == CU_TENSOR_MAP_SWIZZLE_NONE ? off + flip : R::kWhole ? off ^ flip
                                         : ((off + t * R::kBits / 32 * 4) ^ R::swap(g)));
-#pragma unroll
-      for (int q = 0; q < 4; ++q) lds_words<R::kPiece>(from + q * (8 * R::kRowBytes), &v[q][i]);
+      lds_words<R::kPiece, 0>(from, &v[0][i]);
+      lds_words<R::kPiece, 8 * R::kRowBytes>(from, &v[1][i]);
+      lds_words<R::kPiece, 16 * R::kRowBytes>(from, &v[2][i]);
+      lds_words<R::kPiece, 24 * R::kRowBytes>(from, &v[3][i]);
     }
     if constexpr (!R::kWhole) {
       const uint32_t sh = t * R::kBits % 32;
@@ -339,7 +360,7 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
       for (int half = 0; half < HALVES; ++half) pair_x<BITS, G>(px[half] + sub * R::kSub, x[half]);
       uint32_t code[4][R::kSub / 2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, code[q]);
+      for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, f, code[q]);
 #pragma unroll
       for (int half = 0; half < HALVES; ++half) {
         if (sub == 0) multiply<BITS, G, true>(code, x[half], part[half], ones[half]);
@@ -353,10 +374,14 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
     }
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) px[half] += G;
+    uint32_t both[4][2];
+    lds_words<2, 0>(sb, both[0]);
+    lds_words<2, 64>(sb, both[1]);
+    lds_words<2, 128>(sb, both[2]);
+    lds_words<2, 192>(sb, both[3]);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float s, b;
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(s), "=f"(b) : "r"(sb + q * 64));
+      const float s = __uint_as_float(both[q][0]), b = __uint_as_float(both[q][1]);
 #pragma unroll
       for (int half = 0; half < HALVES; ++half)
 #pragma unroll
@@ -372,13 +397,13 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
 // 32-byte sector to a place that nothing reads.
 template <int CHUNK, bool TOKENS>
 __device__ __forceinline__ void touch_x(uint32_t scratch, const uint16_t *x, int64_t plane, int planes, const MoeEntry *slots,
-                                        int count, int top, int width, int chunk, int lane) {
+                                        int count, int width, int chunk, int lane) {
   constexpr int kSectors = CHUNK / 16;
   const int all = count * kSectors;
   for (int p = 0; p < planes; ++p) {
     for (int i = lane; i < all; i += 32) {
-      const int slot = slots[i / kSectors].listed, at = chunk * CHUNK + i % kSectors * 16;
-      const uint16_t *from = x + p * plane + static_cast<int64_t>(TOKENS ? slot / top : slot) * width + at;
+      const int row = TOKENS ? slots[i / kSectors].token : slots[i / kSectors].listed, at = chunk * CHUNK + i % kSectors * 16;
+      const uint16_t *from = x + p * plane + static_cast<int64_t>(row) * width + at;
       if (at < width)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scratch + 4 * lane), "l"(from) : "memory");
     }
@@ -403,7 +428,6 @@ struct Ring {
   int lane, in, out;
   uint32_t parity;   // of the stage to read next
   int flying;        // chunks issued and not yet waited for
-  bool dead;         // a wait ran out: nothing more is issued or read
 
   __device__ __forceinline__ void init(unsigned char *stages, uint64_t *barriers, int warp, int lane_) {
     base = smem_u32(stages) + warp * R::kWarpBytes;
@@ -411,7 +435,6 @@ struct Ring {
     lane = lane_;
     in = out = flying = 0;
     parity = 0;
-    dead = false;
     if (lane == 0) {
       for (int i = 0; i < R::kDepth; ++i) mbar_init(&bars[i], 1);
       asm volatile("fence.mbarrier_init.release.cluster;\n\tfence.proxy.async.shared::cta;" ::: "memory");
@@ -445,7 +468,6 @@ struct Ring {
       do {
         if (++polls >= limit) {
           if (lane == 0) atomicOr(err, kErrTimeoutBit);
-          dead = true;
           return 0;
         }
       } while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&bars[out], parity)));
@@ -515,32 +537,36 @@ struct GateUp {
   int lane, warp, tiles, groups, chunks;
   int first_unit, first_tile;        // the block's first task
   int task, chunk, unit, tile, left;  // what is multiplied next, chunks left to this warp
-  int l_chunk, l_unit, l_tile, l_left;  // what is loaded next
+  int l_chunk, l_unit, l_tile, l_left, l_row;  // what is loaded next
   bool l_fresh;                       // its unit's x is not in L1 yet
   int s_chunk, s_unit, s_tile;        // whose scales are loaded next, and where they are
-  int64_t s_at;
+  const char *s_at, *b_at;
   int sb_bytes;
   bool whole;
   Scales<R::kSteps> next;
+  Factors<BITS> factors{a.two_to_127};
 
   __device__ __forceinline__ void advance_load() {
-    if (l_left <= 0 || ring.dead) return;
-    const int row = plan[l_unit].unit_expert * a.w.inner + l_tile * 16;
-    ring.issue(gate, up, row, row, l_chunk);
+    if (l_left <= 0) return;
+    ring.issue(gate, up, l_row, l_row, l_chunk);
     if (l_fresh)
       touch_x<R::kChunk, true>(smem_u32(sh.unread), a.x, a.x_plane, a.x_planes, &plan[plan[l_unit].unit_first],
-                               plan[l_unit].unit_count, a.route.top_k, a.w.hidden, l_chunk, lane);
+                               plan[l_unit].unit_count, a.w.hidden, l_chunk, lane);
     --l_left;
     if (++l_chunk == chunks) {
       l_chunk = 0;
       l_fresh = false;
-      if (++l_tile == tiles) l_tile = 0, ++l_unit, l_fresh = true;
+      l_row += 16;
+      if (++l_tile == tiles) {
+        l_tile = 0, ++l_unit, l_fresh = true;
+        if (l_left > 0) l_row = plan[l_unit].unit_expert * a.w.inner;
+      }
     }
   }
   // The next chunk's scales, of the row that this lane stands for.
   __device__ __forceinline__ void load_scales() {
-    next.load(scales + s_at, biases + s_at, a.w.sb_type, whole, groups - s_chunk * R::kSteps);
-    s_at += R::kSteps * sb_bytes;
+    next.load(s_at, b_at, a.w.sb_type, whole, groups - s_chunk * R::kSteps);
+    s_at += R::kSteps * sb_bytes, b_at += R::kSteps * sb_bytes;
     if (++s_chunk == chunks) {
       if (++s_tile == tiles) s_tile = 0, ++s_unit;
       s_chunk = 0;
@@ -549,9 +575,9 @@ struct GateUp {
   }
   __device__ __forceinline__ void point_scales() {
     const int64_t row = static_cast<int64_t>(plan[s_unit].unit_expert) * a.w.inner + s_tile * 16 + lane / 4 + 8 * (lane % 2);
-    s_at = (row * groups + s_chunk * R::kSteps) * sb_bytes;
+    const int64_t at = (row * groups + s_chunk * R::kSteps) * sb_bytes;
+    s_at = scales + at, b_at = biases + at;
   }
-
   __device__ __forceinline__ float *starts(int w) const {
     static_assert(R::kDepth * R::kStageBytes >= 32 * kMoePass * 4, "a warp's sums fit its ring");
     return reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(&sh) + sizeof(GateUpShared) + w * R::kWarpBytes);
@@ -565,22 +591,24 @@ struct GateUp {
     c.plane = a.x_plane;
 #pragma unroll
     for (int half = 0; half < HALVES; ++half) {
-      const int token = listed[8 * half + g < count ? 8 * half + g : 0].listed / a.route.top_k;
+      const int token = listed[8 * half + g < count ? 8 * half + g : 0].token;
       c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
     }
-    const uint32_t spread = ring.base + R::kDepth * R::kStageBytes;
+    const uint32_t spread = ring.base + R::kDepth * R::kStageBytes, own_scales = spread + (lane % 4) * 64 + lane / 4 * 8;
     float acc[HALVES][8] = {};
     const int c0 = chunk, c1 = min(chunks, chunk + left);
-    for (; chunk < c1 && !ring.dead; ++chunk) {
+    for (; chunk < c1; ++chunk) {
       // (the chunk before is read: done() has met the warp)
-      next.spread(spread, lane, a.w.sb_type);
+      next.spread(own_scales, a.w.sb_type);
       if (--left > 0) load_scales();
       const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
-      if (stage) {
-        consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, spread, acc);
-        ring.done();
-        advance_load();
+      if (!stage) {
+        left = l_left = 0;
+        return;
       }
+      consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, spread, factors, acc);
+      ring.done();
+      advance_load();
     }
     if (c0 == 0 && c1 == chunks) {
 #pragma unroll
@@ -641,6 +669,7 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   s.unit = s.l_unit = s.task / s.tiles;
   s.tile = s.l_tile = s.task % s.tiles;
   s.l_fresh = true;
+  s.l_row = s.left > 0 ? s.plan[s.unit].unit_expert * a.w.inner + s.tile * 16 : 0;
   s.copied = static_cast<int64_t>(a.w.hidden) * BITS % 128 != 0;
   s.gate = Source{&maps.gate, s.copied ? a.w.w[0] : nullptr, a.w.hidden / 32 * BITS};
   s.up = Source{&maps.up, s.copied ? a.w.w[1] : nullptr, a.w.hidden / 32 * BITS};
@@ -651,7 +680,7 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   s.whole = a.w.sb_type != kTypeF32 && s.groups % R::kSteps == 0;
   s.s_chunk = s.chunk, s.s_unit = s.unit, s.s_tile = s.tile;
   if (s.left > 0) s.point_scales(), s.load_scales();
-  while (s.left > 0 && !s.ring.dead) {
+  while (s.left > 0) {
     if (s.plan[s.unit].unit_count > 8) s.template run_task<2>();
     else s.template run_task<1>();
   }
@@ -730,37 +759,45 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   const int sb_bytes = a.w.sb_type == kTypeF32 ? 4 : 2;
   const bool whole = a.w.sb_type != kTypeF32 && groups % R::kSteps == 0;
   Scales<R::kSteps> next;
-  auto load_scales = [&](int unit, int chunk) {
+  const char *s_at = nullptr, *b_at = nullptr;
+  auto point_scales = [&](int unit, int chunk) {
     const int64_t row = static_cast<int64_t>(plan[unit].unit_expert) * a.w.hidden + row0 + g + 8 * t;
     const int64_t at = (row * groups + chunk * R::kSteps) * sb_bytes;
-    next.load(scales + at, biases + at, a.w.sb_type, whole, groups - chunk * R::kSteps);
+    s_at = scales + at, b_at = biases + at;
   };
-
+  auto load_scales = [&](int chunk) {
+    next.load(s_at, b_at, a.w.sb_type, whole, groups - chunk * R::kSteps);
+    s_at += R::kSteps * sb_bytes, b_at += R::kSteps * sb_bytes;
+  };
   const bool copied = static_cast<int64_t>(a.w.inner) * BITS % 128 != 0;
   const Source down{&maps.down, copied ? a.w.w[2] : nullptr, a.w.inner / 32 * BITS};
   const int first_unit = step0 / chunks, first_chunk = step0 - first_unit * chunks;
   int load_step = step0, load_unit = first_unit, load_chunk = first_chunk;
   auto touch_h = [&](int unit, int chunk) {
     touch_x<R::kChunk, false>(smem_u32(sh.unread), a.h, a.h_plane, a.h_planes, &plan[plan[unit].unit_first],
-                              plan[unit].unit_count, 1, a.w.inner, chunk, lane);
+                              plan[unit].unit_count, a.w.inner, chunk, lane);
   };
+  int load_row = step0 < step1 ? plan[load_unit].unit_expert * a.w.hidden + row0 : 0;
   auto load_next = [&](bool touch) {
-    if (load_step >= step1 || ring.dead) return;
-    const int row = plan[load_unit].unit_expert * a.w.hidden + row0;
-    ring.issue(down, down, row, row + 16, load_chunk);
+    if (load_step >= step1) return;
+    ring.issue(down, down, load_row, load_row + 16, load_chunk);
     if (touch) touch_h(load_unit, load_chunk);
     ++load_step;
-    if (++load_chunk == chunks) load_chunk = 0, ++load_unit;
+    if (++load_chunk == chunks) {
+      load_chunk = 0, ++load_unit;
+      if (load_step < step1) load_row = plan[load_unit].unit_expert * a.w.hidden + row0;
+    }
   };
   for (int i = 0; i < R::kDepth; ++i) load_next(false);
-  if (step0 < step1) load_scales(first_unit, first_chunk);
+  if (step0 < step1) point_scales(first_unit, first_chunk), load_scales(first_chunk);
   griddep_wait();  // h is complete; the weights above do not depend on it
   for (int i = step0, u = first_unit, k = first_chunk; i < load_step; ++i) {
     touch_h(u, k);
     if (++k == chunks) k = 0, ++u;
   }
 
-  const uint32_t spread = ring.base + R::kDepth * R::kStageBytes;
+  const uint32_t spread = ring.base + R::kDepth * R::kStageBytes, own_scales = spread + t * 64 + g * 8;
+  const Factors<BITS> factors(a.two_to_127);
   int step = step0;
   auto run_unit = [&](auto halves, int unit, int j0) {
     constexpr int HALVES = decltype(halves)::value;
@@ -776,19 +813,22 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
       c.x[half] = a.h + static_cast<int64_t>(slot) * a.w.inner + t * R::kCodes;
     }
     float acc[HALVES][8] = {};
-    for (int j = j0; j < j1 && !ring.dead; ++j) {
-      next.spread(spread, lane, a.w.sb_type);
+    for (int j = j0; j < j1; ++j) {
+      next.spread(own_scales, a.w.sb_type);
       ++step;
       if (step < step1) {
         const bool same = j + 1 < chunks;
-        load_scales(same ? unit : unit + 1, same ? j + 1 : 0);
+        if (!same) point_scales(unit + 1, 0);
+        load_scales(same ? j + 1 : 0);
       }
       const uint32_t stage = ring.wait(copied, a.wait_limit, a.err);
-      if (stage) {
-        consume<BITS, G, HALVES>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, spread, acc);
-        ring.done();
-        load_next(true);
+      if (!stage) {
+        step = load_step = step1;
+        return;
       }
+      consume<BITS, G, HALVES>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, spread, factors, acc);
+      ring.done();
+      load_next(true);
     }
 #pragma unroll
     for (int half = 0; half < HALVES; ++half)
@@ -802,7 +842,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
         }
       }
   };
-  for (int unit = first_unit; step < step1 && !ring.dead; ++unit) {
+  for (int unit = first_unit; step < step1; ++unit) {
     const int j0 = unit == first_unit ? first_chunk : 0;
     if (plan[unit].unit_count > 8) run_unit(Int<2>(), unit, j0);
     else run_unit(Int<1>(), unit, j0);
@@ -817,7 +857,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   const int top = a.route.top_k, own = a.tokens > rank ? (a.tokens - rank + cluster - 1) / cluster : 0;
   for (int i = warp; i < own * top; i += kMoeWarps) {
     const int slot = (i / top * cluster + rank) * top + i % top;
-    const int unit = plan[slot].slot_unit, place = plan[slot].slot_place;
+    const int unit = plan[slot].slot_unit >> 4, place = plan[slot].slot_unit & (kMoePass - 1);
     float v = 0.0f;
     if (unit >= 0) {
       const int from = sh.unit_from[unit], to = sh.unit_to[unit];
