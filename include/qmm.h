@@ -644,7 +644,7 @@ qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t tokens, in
  * stands (codes are not rounded, scales and biases applied in fp32), x exact, sums
  * fp32; silu(gate) * up keeps 15 bits or more for 16-bit x_dtype, 24 for fp32; y is
  * rounded once.  Results repeat bit for bit.  Each expert that is asked for is
- * streamed from memory once for every 16 of its slots.
+ * streamed from memory once for every 8 of its slots.
  */
 qmm_status qmm_moe_experts(const void *x, qmm_dtype x_dtype, int64_t tokens, const int32_t *ids,
                            const float *weights, int top_k, const qmm_experts *experts, void *y,

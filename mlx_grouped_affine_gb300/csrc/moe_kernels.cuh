@@ -15,21 +15,17 @@
 // codes come by TMA, a box of 16 rows per tile, into a ring of the warp's own, so that loads
 // in flight cost no registers and need no block barrier.  (Copies by the lanes themselves
 // touch eight rows an instruction and were held up at one cache line a cycle: 2500 cycles
-// for 2048 codes a warp.)  8 slots fill the MMA's columns; 16 slots of an expert are taken
-// per pass over its weights.
+// for 2048 codes a warp.)  8 slots fill the MMA's columns, and so many of an expert are taken
+// per pass over its weights.  (16 a pass halve the passes of experts with more than 8 slots, but
+// their registers cost all others: 48 tokens of 4 of 32 experts in fp32 76 us against 56.)
 #pragma once
 #include "common.cuh"
 
 namespace qmm {
 
 constexpr int kMoeThreads = 256, kMoeWarps = kMoeThreads / 32;
-constexpr int kMoePass = 16;      // slots of an expert per pass over its weights
+constexpr int kMoePass = 8;       // slots of an expert per pass over its weights
 constexpr int kMoeMaxCluster = 8;
-
-template <int N>
-struct Int {
-  static constexpr int value = N;
-};
 
 struct MoePlan;
 
@@ -49,7 +45,7 @@ struct MoeArgs {
   const MoePlan *plan;
   unsigned *err;
   uint32_t wait_limit;
-  uint32_t two_to_127;  // kTwoTo127
+  unsigned char *x_large, *h_large;  // of a token, of a slot: a finite value of 2^26 or more in its row
 };
 
 // ------------------------------------------------------------- the plan ----
@@ -119,26 +115,25 @@ struct Run {
   }
 };
 
-// Codes as bf16 pairs, each code * 2^-6.  A bf16 pattern P <= 0xFF is worth P * 2^-133, so
-// a code at bit o of a half reads as c * 2^(o - 133), and times 2^(127 - o) it is exact and
-// normal.  sum(x) is taken times 2^-6 too, and the sums times 2^6 at the end.
-// The factors come with the call's arguments: constants would be put into a register again
-// for every product (32 instructions a group).
-constexpr uint32_t kTwoTo127 = 0x7F007F00u;
-template <int BITS>
-struct Factors {
-  static constexpr int kCount = BITS == 8 ? 1 : BITS == 4 ? 2 : BITS == 2 ? 4 : 1;
-  uint32_t v[kCount];  // (2^(127 - o), 2^(127 - o)) for o = 0, BITS, 2 BITS ..
-  __device__ __forceinline__ explicit Factors(uint32_t two_to_127) {
-#pragma unroll
-    for (int i = 0; i < kCount; ++i) v[i] = two_to_127 - (static_cast<uint32_t>(i * BITS) << 7) * 0x00010001u;
-  }
-};
-constexpr float kUnscale = 64.0f;
-constexpr uint32_t kOnes = 0x3C803C80u;  // 2^-6
+// Codes as bf16 pairs, as they are: a bf16 pattern P <= 0xFF is worth P * 2^-133, so a code at
+// bit o of an otherwise clear half reads as c * 2^(o - 133), exactly, and the tensor cores take
+// such small numbers at their worth.  x makes up for it: it is taken times 2^(100 - o), a power
+// of two, which keeps products with x of 2^-93 and more out of fp32's smallest numbers and
+// x below 2^27 inside bf16.  Where a slot's row has a value of 2^26 or more, x stays as it is
+// and the codes are taken times 2^(127 - o), to c * 2^-6.  (The tensor cores' sums are times
+// 2^-33 or 2^-6 then, and sum(x) is taken the same way, with ones for codes.)  Multiplying the
+// few x instead of the many codes saves a quarter of a group's instructions.
 template <int BITS, int G>
-__device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, const Factors<BITS> &f,
-                                             uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
+struct Offsets {  // of the pair i of a run's codes
+  static constexpr int kHalf = BITS == 2 || BITS == 4 || BITS == 8 ? 16 / BITS : 1;
+  __device__ static constexpr int at(int i) { return Run<BITS, G>::kSplit ? i % kHalf * BITS % 8 : 0; }
+};
+constexpr float kUnscaleSmall = 8589934592.0f, kUnscaleLarge = 64.0f;  // 2^33, 2^6
+__device__ __forceinline__ uint32_t twice_bf16(int exponent) { return static_cast<uint32_t>(exponent + 127) << 7 | static_cast<uint32_t>(exponent + 127) << 23; }
+__device__ __forceinline__ uint32_t bf16x2_times(uint32_t a, uint32_t b) { return bf16x2_fma(a, b, 0x80008000u); }
+
+template <int BITS, int G>
+__device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, bool large, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
   using R = Run<BITS, G>;
   if constexpr (R::kSplit) {
     constexpr int kHalf = 16 / BITS, kPerSub = R::kSub * BITS / 32;
@@ -149,19 +144,22 @@ __device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, const F
 #pragma unroll
       for (int j = 0; j < kHalf; ++j) {
         const int o = j * BITS % 8, sh = j * BITS - o;
-        p[i * kHalf + j] = bf16x2_fma((w >> sh) & (kMask << o), f.v[o / BITS], 0x80008000u);
+        p[i * kHalf + j] = (w >> sh) & (kMask << o);
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < R::kSub / 2; ++i)
-      p[i] = bf16x2_fma(pair_at<BITS>(v, sub * R::kSub + 2 * i), f.v[0], 0x80008000u);
+    for (int i = 0; i < R::kSub / 2; ++i) p[i] = pair_at<BITS>(v, sub * R::kSub + 2 * i);
+  }
+  if (large) {
+#pragma unroll
+    for (int i = 0; i < R::kSub / 2; ++i) p[i] = bf16x2_times(p[i], twice_bf16(127 - Offsets<BITS, G>::at(i)));
   }
 }
 
 // x of those codes, in the same pairs.
 template <int BITS, int G>
-__device__ __forceinline__ void pair_x(const uint16_t *x, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
+__device__ __forceinline__ void pair_x(const uint16_t *x, bool large, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
   using R = Run<BITS, G>;
   uint32_t n[R::kSub / 2];
 #pragma unroll
@@ -179,6 +177,10 @@ __device__ __forceinline__ void pair_x(const uint16_t *x, uint32_t (&p)[Run<BITS
   } else {
 #pragma unroll
     for (int i = 0; i < R::kSub / 2; ++i) p[i] = n[i];
+  }
+  if (!large) {
+#pragma unroll
+    for (int i = 0; i < R::kSub / 2; ++i) p[i] = bf16x2_times(p[i], twice_bf16(100 - Offsets<BITS, G>::at(i)));
   }
 }
 
@@ -268,11 +270,11 @@ struct Scales {
   }
 };
 
-// The MMA's columns: rows of x (or h) of up to 8 HALVES slots, lane 4 g + t reading column
-// g.  Columns without a slot repeat the first: nothing looks at their sums.
-template <int HALVES>
+// The MMA's columns: rows of x (or h) of up to 8 slots, lane 4 g + t reading column g.
+// Columns without a slot repeat the first: nothing looks at their sums.
 struct Columns {
-  const uint16_t *x[HALVES];  // this lane's column of each half of the pass, at its run
+  const uint16_t *x;  // this lane's column, at its run
+  bool large;         // a row of the pass has a value of 2^26 or more
   int planes;
   int64_t plane;
 };
@@ -295,43 +297,47 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The products of up to 16 codes a lane with one plane of x.
+// The products of up to 16 codes a lane with one plane of x.  A one is a code of 1 at its
+// pair's bit, or 2^-6.
 template <int BITS, int G, bool FIRST>
-__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2],
+__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2], bool large,
                                          const uint32_t (&x)[Run<BITS, G>::kSub / 2], float (&part)[2][4], float (&ones)[4]) {
   using R = Run<BITS, G>;
 #pragma unroll
-  for (int tile = 0; tile < 2; ++tile)
-    mma_bf16<FIRST>(part[tile], code[2 * tile][0], code[2 * tile + 1][0], code[2 * tile][1], code[2 * tile + 1][1], x[0], x[1]);
-  mma_bf16<FIRST>(ones, kOnes, kOnes, kOnes, kOnes, x[0], x[1]);
+  for (int m = 0; m < R::kSub / 4; ++m) {
+    const uint32_t one0 = large ? 0x3C803C80u : 0x00010001u << Offsets<BITS, G>::at(2 * m);
+    const uint32_t one1 = large ? 0x3C803C80u : 0x00010001u << Offsets<BITS, G>::at(2 * m + 1);
+    if (FIRST && m == 0) {
 #pragma unroll
-  for (int m = 1; m < R::kSub / 4; ++m) {
+      for (int tile = 0; tile < 2; ++tile)
+        mma_bf16<true>(part[tile], code[2 * tile][0], code[2 * tile + 1][0], code[2 * tile][1], code[2 * tile + 1][1], x[0], x[1]);
+      mma_bf16<true>(ones, one0, one0, one1, one1, x[0], x[1]);
+    } else {
 #pragma unroll
-    for (int tile = 0; tile < 2; ++tile)
-      mma_bf16<false>(part[tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
-                      code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
-    mma_bf16<false>(ones, kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
+      for (int tile = 0; tile < 2; ++tile)
+        mma_bf16<false>(part[tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
+                        code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
+      mma_bf16<false>(ones, one0, one0, one1, one1, x[2 * m], x[2 * m + 1]);
+    }
   }
 }
 
-// One chunk of 32 rows: acc[half][2 q + column] += s sum(c x) + b sum(x) over its `count`
+// One chunk of 32 rows: acc[2 q + column] += s sum(c x) + b sum(x) over its `count`
 // groups, q = 2 tile + row half; `at` is the chunk's first column, `scales` where its scales
 // were spread.  Not unrolled over groups: the warps share an instruction cache that the body
 // must not outgrow.
-template <int BITS, int G, int HALVES>
-__device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<HALVES> &c, int at, int count,
-                                        uint32_t scales, const Factors<BITS> &f, float (&acc)[HALVES][8]) {
+template <int BITS, int G>
+__device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns &c, int at, int count,
+                                        uint32_t scales, float (&acc)[8]) {
   using R = Run<BITS, G>;
   const int g = lane / 4, t = lane % 4;
   const uint32_t rows = stage + g * R::kRowBytes, flip = (t * R::kBits / 32 * 4) ^ R::swap(g);
-  const uint16_t *px[HALVES];
-#pragma unroll
-  for (int half = 0; half < HALVES; ++half) px[half] = c.x[half] + at;
+  const uint16_t *px = c.x + at;
   uint32_t sb = scales + g * 8;
   count = min(count, R::kSteps);
 #pragma unroll 1
   for (int step = 0; step < count; ++step, sb += 256) {
-    float part[HALVES][2][4], ones[HALVES][4];
+    float part[2][4], ones[4];
     uint32_t v[4][R::kWords + 1];
 #pragma unroll
     for (int i = 0; i < R::kWords; i += R::kPiece) {
@@ -355,25 +361,20 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
     }
 #pragma unroll
     for (int sub = 0; sub < R::kCodes / R::kSub; ++sub) {
-      uint32_t x[HALVES][R::kSub / 2];  // loaded ahead of the codes' instructions
-#pragma unroll
-      for (int half = 0; half < HALVES; ++half) pair_x<BITS, G>(px[half] + sub * R::kSub, x[half]);
+      uint32_t x[R::kSub / 2];  // loaded ahead of the codes' instructions
+      pair_x<BITS, G>(px + sub * R::kSub, c.large, x);
       uint32_t code[4][R::kSub / 2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, f, code[q]);
-#pragma unroll
-      for (int half = 0; half < HALVES; ++half) {
-        if (sub == 0) multiply<BITS, G, true>(code, x[half], part[half], ones[half]);
-        else multiply<BITS, G, false>(code, x[half], part[half], ones[half]);
+      for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, c.large, code[q]);
+      if (sub == 0) multiply<BITS, G, true>(code, c.large, x, part, ones);
+      else multiply<BITS, G, false>(code, c.large, x, part, ones);
 #pragma unroll 1
-        for (int plane = 1; plane < c.planes; ++plane) {
-          pair_x<BITS, G>(px[half] + sub * R::kSub + plane * c.plane, x[half]);
-          multiply<BITS, G, false>(code, x[half], part[half], ones[half]);
-        }
+      for (int plane = 1; plane < c.planes; ++plane) {
+        pair_x<BITS, G>(px + sub * R::kSub + plane * c.plane, c.large, x);
+        multiply<BITS, G, false>(code, c.large, x, part, ones);
       }
     }
-#pragma unroll
-    for (int half = 0; half < HALVES; ++half) px[half] += G;
+    px += G;
     uint32_t both[4][2];
     lds_words<2, 0>(sb, both[0]);
     lds_words<2, 64>(sb, both[1]);
@@ -383,12 +384,7 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns<
     for (int q = 0; q < 4; ++q) {
       const float s = __uint_as_float(both[q][0]), b = __uint_as_float(both[q][1]);
 #pragma unroll
-      for (int half = 0; half < HALVES; ++half)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float &y = acc[half][2 * q + i];
-          y = fmaf(s, part[half][q / 2][2 * (q % 2) + i], fmaf(b, ones[half][i], y));
-        }
+      for (int i = 0; i < 2; ++i) acc[2 * q + i] = fmaf(s, part[q / 2][2 * (q % 2) + i], fmaf(b, ones[i], acc[2 * q + i]));
     }
   }
 }
@@ -491,6 +487,9 @@ struct Ring {
   }
 };
 
+// Whether v is a finite number too large for the codes as they are.
+__device__ __forceinline__ bool is_large(float v) { return fabsf(v) >= 67108864.0f && fabsf(v) < INFINITY; }
+
 // The bf16 planes of v: its leading bits cut off 8 at a time (three hold all 24).  What is
 // not finite stays in the first.
 __device__ __forceinline__ void store_planes(uint16_t *p, int64_t plane, int planes, float v) {
@@ -515,7 +514,6 @@ struct MoeMaps {
 };
 
 __device__ __forceinline__ float silu_times(float gate, float up) {
-  gate *= kUnscale, up *= kUnscale;
   return __fdividef(gate, 1.0f + expf(-gate)) * up;
 }
 
@@ -544,7 +542,6 @@ struct GateUp {
   int sb_bytes;
   bool whole;
   Scales<R::kSteps> next;
-  Factors<BITS> factors{a.two_to_127};
 
   __device__ __forceinline__ void advance_load() {
     if (l_left <= 0) return;
@@ -582,20 +579,17 @@ struct GateUp {
     static_assert(R::kDepth * R::kStageBytes >= 32 * kMoePass * 4, "a warp's sums fit its ring");
     return reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(&sh) + sizeof(GateUpShared) + w * R::kWarpBytes);
   }
-  template <int HALVES>
   __device__ __forceinline__ void run_task() {
     const int g = lane / 4, t = lane % 4, count = plan[unit].unit_count;
     const MoeEntry *listed = &plan[plan[unit].unit_first];
-    Columns<HALVES> c;
+    Columns c;
     c.planes = a.x_planes;
     c.plane = a.x_plane;
-#pragma unroll
-    for (int half = 0; half < HALVES; ++half) {
-      const int token = listed[8 * half + g < count ? 8 * half + g : 0].token;
-      c.x[half] = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
-    }
+    const int token = listed[g < count ? g : 0].token;
+    c.large = __any_sync(0xFFFFFFFFu, a.x_large[token]);
+    c.x = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
     const uint32_t spread = ring.base + R::kDepth * R::kStageBytes, own_scales = spread + (lane % 4) * 64 + lane / 4 * 8;
-    float acc[HALVES][8] = {};
+    float acc[8] = {};
     const int c0 = chunk, c1 = min(chunks, chunk + left);
     for (; chunk < c1; ++chunk) {
       // (the chunk before is read: done() has met the warp)
@@ -606,33 +600,34 @@ struct GateUp {
         left = l_left = 0;
         return;
       }
-      consume<BITS, G, HALVES>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, spread, factors, acc);
+      consume<BITS, G>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, spread, acc);
       ring.done();
       advance_load();
     }
+    const float unscale = c.large ? kUnscaleLarge : kUnscaleSmall;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] *= unscale;
     if (c0 == 0 && c1 == chunks) {
 #pragma unroll
-      for (int half = 0; half < HALVES; ++half)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int place = 8 * half + 2 * t + i;
-          if (place < count) {
-            uint16_t *to = a.h + static_cast<int64_t>(listed[place].listed) * a.w.inner + tile * 16 + g;
-            store_planes(to, a.h_plane, a.h_planes, silu_times(acc[half][i], acc[half][4 + i]));
-            store_planes(to + 8, a.h_plane, a.h_planes, silu_times(acc[half][2 + i], acc[half][6 + i]));
-          }
+      for (int i = 0; i < 2; ++i) {
+        const int place = 2 * t + i;
+        if (place < count) {
+          const int slot = listed[place].listed;
+          uint16_t *to = a.h + static_cast<int64_t>(slot) * a.w.inner + tile * 16 + g;
+          const float h0 = silu_times(acc[i], acc[4 + i]), h1 = silu_times(acc[2 + i], acc[6 + i]);
+          store_planes(to, a.h_plane, a.h_planes, h0);
+          store_planes(to + 8, a.h_plane, a.h_planes, h1);
+          if (is_large(h0) || is_large(h1)) a.h_large[slot] = 1;
         }
+      }
     } else {
       const int kind = c0 == 0 ? 0 : 1;
       if (lane == 0) sh.task[kind][warp] = task;
       // a task that goes on is the warp's last: its ring is free
       float *to = kind ? sh.heads[warp] : starts(warp);
 #pragma unroll
-      for (int half = 0; half < HALVES; ++half)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<float2 *>(to + ((q / 2) * 16 + (q % 2) * 8 + g) * kMoePass + half * 8 + 2 * t) =
-              make_float2(acc[half][2 * q], acc[half][2 * q + 1]);
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float2 *>(to + ((q / 2) * 16 + (q % 2) * 8 + g) * kMoePass + 2 * t) = make_float2(acc[2 * q], acc[2 * q + 1]);
     }
     chunk = 0;
     ++task;
@@ -681,8 +676,7 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   s.s_chunk = s.chunk, s.s_unit = s.unit, s.s_tile = s.tile;
   if (s.left > 0) s.point_scales(), s.load_scales();
   while (s.left > 0) {
-    if (s.plan[s.unit].unit_count > 8) s.template run_task<2>();
-    else s.template run_task<1>();
+    s.run_task();
   }
   s.ring.drain(s.copied, a.wait_limit, a.err);
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -698,7 +692,9 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
     for (int v = w + 1; v < kMoeWarps; ++v)
       if (s.sh.task[1][v] == task) gate += s.sh.heads[v][at], up += s.sh.heads[v][at + two];
     const int slot = s.plan[s.plan[unit].unit_first + place].listed;
-    store_planes(a.h + static_cast<int64_t>(slot) * a.w.inner + tile * 16 + r, a.h_plane, a.h_planes, silu_times(gate, up));
+    const float h = silu_times(gate, up);
+    store_planes(a.h + static_cast<int64_t>(slot) * a.w.inner + tile * 16 + r, a.h_plane, a.h_planes, h);
+    if (is_large(h)) a.h_large[slot] = 1;
   }
 }
 
@@ -797,22 +793,18 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   }
 
   const uint32_t spread = ring.base + R::kDepth * R::kStageBytes, own_scales = spread + t * 64 + g * 8;
-  const Factors<BITS> factors(a.two_to_127);
   int step = step0;
-  auto run_unit = [&](auto halves, int unit, int j0) {
-    constexpr int HALVES = decltype(halves)::value;
+  auto run_unit = [&](int unit, int j0) {
     const int j1 = min(chunks, j0 + (step1 - step));
     const int count = plan[unit].unit_count;
     const MoeEntry *listed = &plan[plan[unit].unit_first];
-    Columns<HALVES> c;
+    Columns c;
     c.planes = a.h_planes;
     c.plane = a.h_plane;
-#pragma unroll
-    for (int half = 0; half < HALVES; ++half) {
-      const int slot = listed[8 * half + g < count ? 8 * half + g : 0].listed;
-      c.x[half] = a.h + static_cast<int64_t>(slot) * a.w.inner + t * R::kCodes;
-    }
-    float acc[HALVES][8] = {};
+    const int own_slot = listed[g < count ? g : 0].listed;
+    c.large = __any_sync(0xFFFFFFFFu, __ldcg(&a.h_large[own_slot]));
+    c.x = a.h + static_cast<int64_t>(own_slot) * a.w.inner + t * R::kCodes;
+    float acc[8] = {};
     for (int j = j0; j < j1; ++j) {
       next.spread(own_scales, a.w.sb_type);
       ++step;
@@ -826,26 +818,24 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
         step = load_step = step1;
         return;
       }
-      consume<BITS, G, HALVES>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, spread, factors, acc);
+      consume<BITS, G>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, spread, acc);
       ring.done();
       load_next(true);
     }
 #pragma unroll
-    for (int half = 0; half < HALVES; ++half)
+    for (int i = 0; i < 2; ++i) {
+      const int place = 2 * t + i;
+      if (place < count) {
+        float *to = j0 == 0 ? z + listed[place].listed * 32 : sh.heads[warp][place];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int place = half * 8 + 2 * t + i;
-        if (place < count) {
-          float *to = j0 == 0 ? z + listed[place].listed * 32 : sh.heads[warp][place];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[half][2 * q + i] * kUnscale;
-        }
+        for (int q = 0; q < 4; ++q)
+          to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[2 * q + i] * (c.large ? kUnscaleLarge : kUnscaleSmall);
       }
+    }
   };
   for (int unit = first_unit; step < step1; ++unit) {
     const int j0 = unit == first_unit ? first_chunk : 0;
-    if (plan[unit].unit_count > 8) run_unit(Int<2>(), unit, j0);
-    else run_unit(Int<1>(), unit, j0);
+    run_unit(unit, j0);
   }
   ring.drain(copied, a.wait_limit, a.err);
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -857,7 +847,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   const int top = a.route.top_k, own = a.tokens > rank ? (a.tokens - rank + cluster - 1) / cluster : 0;
   for (int i = warp; i < own * top; i += kMoeWarps) {
     const int slot = (i / top * cluster + rank) * top + i % top;
-    const int unit = plan[slot].slot_unit >> 4, place = plan[slot].slot_unit & (kMoePass - 1);
+    const int at = plan[slot].slot_unit, unit = at >> 3, place = at & 7;
     float v = 0.0f;
     if (unit >= 0) {
       const int from = sh.unit_from[unit], to = sh.unit_to[unit];
