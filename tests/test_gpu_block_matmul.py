@@ -130,3 +130,32 @@ def test_quantize_then_multiply():
     # the smallest codes are 2^-9 apart: half of that, of each scale, beside half a step
     low = (sa.max() * 2.0 ** -10) * v.double().abs().sum(1) + (sw.max() * 2.0 ** -10) * x.double().abs().sum(1)[:, None]
     assert ((y.double() - full).abs() <= size * (2.0 ** -3 + 2.0 ** -8 + 2.0 ** -8) + 2 * low).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 1024, 4096), (100, 640, 4096), (1024, 12800, 1024)])
+def test_a_wait_that_runs_out_is_reported(m, n, k):
+    """One poll a wait and operands that come from memory: loads and products in flight
+    retire, the status is reported, and the next call is right."""
+    a, sa, w, sw = [t.cuda() for t in operands(m, n, k, 8)]
+    y = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    qmm.qmm_get_device_error()
+    seen = []
+    before = qmm.qmm_set_wait_limit(1)
+    try:
+        for _ in range(10):
+            flush.zero_()
+            qmm.qmm_block_matmul(a, sa, m, w, sw, n, k, y, qmm.QMM_BF16)
+            seen.append(qmm.qmm_get_device_error())
+    finally:
+        qmm.qmm_set_wait_limit(before)
+    assert set(seen) <= {qmm.QMM_OK, qmm.QMM_ERR_TIMEOUT} and qmm.QMM_ERR_TIMEOUT in seen
+    check(m, n, k, "bf16")
+
+
+@pytest.mark.parametrize("m,n,k,kind", [(3000, 4104, 256, "bf16"), (3000, 4100, 384, "f32"), (3001, 4099, 128, "f16"),
+                                        (129, 16640, 272, "f32"), (1300, 8200, 144, "bf16")])
+def test_tiles_at_the_edges_of_y(m, n, k, kind):
+    """Rows of y that TMA can address and rows that it cannot, last tiles of a few rows and
+    columns, steps that are and are not a multiple of four."""
+    check(m, n, k, kind)

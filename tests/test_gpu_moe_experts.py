@@ -124,6 +124,36 @@ def test_large_and_small_values():
     check(layer, x, ids, weights * 1e-9, "f32")
 
 
+@pytest.mark.parametrize("bits", [1, 2, 3, 4, 6, 8])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_rows_with_values_from_two_to_26(bits, kind):
+    """Tokens below and above the size at which codes are scaled instead of x, in the same
+    expert and alone; and silu(gate) * up that crosses it though x does not."""
+    layer = Layer(3, 192, 128, bits, 64, "f32", bits)
+    x = tokens(24, 192, kind).float()
+    x[3] *= 2.0 ** 26
+    x[9] *= 2.0 ** 40
+    x[10, 5] = 2.0 ** 26
+    x[11, 5] = 2.0 ** 26 * (1 - 2.0 ** -8)
+    x[17] *= 3e4
+    x[18] *= 2.0 ** -80
+    x = x.to(TYPES[kind][0])
+    ids = torch.tensor([[t % 3, (t + 1) % 3] for t in range(24)], dtype=torch.int32, device="cuda")
+    weights = torch.rand(24, 2, device="cuda") + 0.1
+    check(layer, x, ids, weights, "f32")
+    for t in (3, 9, 11, 17):
+        check(layer, x[t:t + 1].clone(), ids[t:t + 1].clone(), weights[t:t + 1].clone(), "f32")
+
+
+@pytest.mark.parametrize("counts", [(7, 8, 9), (16, 17, 1), (24, 8, 25)])
+def test_passes_over_an_expert(counts):
+    """Experts with about a whole number of passes of 8 slots."""
+    layer = Layer(3, 256, 192, 4, 64, "bf16", 5)
+    ids = torch.tensor([e for e, n in enumerate(counts) for _ in range(n)], dtype=torch.int32, device="cuda")[:, None]
+    weights = torch.rand(sum(counts), 1, device="cuda") + 0.1
+    check(layer, tokens(sum(counts), 256, "bf16"), ids, weights, "f32")
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("sigmoid,normalize", [(False, True), (True, False)])
 @pytest.mark.parametrize("t,experts,top", [(1, 8, 2), (16, 40, 6), (7, 300, 4), (64, 16, 8), (2, 1024, 32)])
