@@ -366,12 +366,23 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns 
       uint32_t code[4][R::kSub / 2];
 #pragma unroll
       for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, c.large, code[q]);
-      if (sub == 0) multiply<BITS, G, true>(code, c.large, x, part, ones);
-      else multiply<BITS, G, false>(code, c.large, x, part, ones);
+      if (c.planes < 3) {
+        if (sub == 0) multiply<BITS, G, true>(code, c.large, x, part, ones);
+        else multiply<BITS, G, false>(code, c.large, x, part, ones);
+        if (c.planes == 2) {
+          pair_x<BITS, G>(px + sub * R::kSub + c.plane, c.large, x);
+          multiply<BITS, G, false>(code, c.large, x, part, ones);
+        }
+      } else {
+        // fp32: the smallest part of x first, the tensor cores cut what they add to a large sum.
+        if (sub == 0)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[0][i] = part[1][i] = ones[i] = 0.0f;
 #pragma unroll 1
-      for (int plane = 1; plane < c.planes; ++plane) {
-        pair_x<BITS, G>(px + sub * R::kSub + plane * c.plane, c.large, x);
-        multiply<BITS, G, false>(code, c.large, x, part, ones);
+        for (int plane = 2; plane >= 0; --plane) {
+          pair_x<BITS, G>(px + sub * R::kSub + plane * c.plane, c.large, x);
+          multiply<BITS, G, false>(code, c.large, x, part, ones);
+        }
       }
     }
     px += G;
