@@ -587,7 +587,8 @@ qmm_status qmm_block_matmul(const uint8_t *a, const float *a_scales, int64_t M, 
 /* ------------------------------------------------ mixture of experts ----
  * The feed-forward of a layer with routed experts, for the few tokens of a decode
  * step: qmm_moe_layer from the router's logits, or qmm_moe_route and qmm_moe_experts
- * (any routing).  Many tokens (a prompt) go through qmm_moe_route and qmm_gather_qmm.
+ * (any routing); three launches, the later ones overlapping the earlier.  Many tokens (a
+ * prompt) go through qmm_moe_route and qmm_gather_qmm.
  * (nuvec_core quantized.rs, `gather_qmm`, is one product of such a layer.) */
 
 /* How a logit becomes a weight. */
@@ -642,7 +643,8 @@ qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t tokens, in
  * holds.  An id outside [0, experts) has none either and is reported by
  * qmm_get_device_error as QMM_ERR_INDEX.  Each weight is scale * code + bias as it
  * stands (codes are not rounded, scales and biases applied in fp32), x exact, sums
- * fp32; silu(gate) * up keeps 15 bits or more for 16-bit x_dtype, 24 for fp32; y is
+ * fp32 (for 16-bit x_dtype a group's sums may lose bits below 2^-17 of its largest
+ * terms); silu(gate) * up keeps 15 bits or more for 16-bit x_dtype, 24 for fp32; y is
  * rounded once.  Results repeat bit for bit.  Each expert that is asked for is
  * streamed from memory once for every 8 of its slots.
  */

@@ -20,6 +20,10 @@
 // `flat`, for few rows of A: W's rows take the MMA's 128 lanes and up to 128 rows of A its
 // columns, so that nothing is padded to 128 rows and W is streamed once; K is split over a
 // cluster, whose partial sums meet in shared memory.
+//
+// Measured: 2048 x 14336 x 4096 in 94.4 us, 2549 TFLOP/s, bound by the 48 KB a step and SM that
+// come from L2 (products alone 62 us, with loads 89) and by the stores; 1 x 4096 x 4096 in 6.2
+// us, of which the 16.8 MB are 2.5: launch, first tiles, cluster barrier and join.
 #include "common.cuh"
 
 namespace qmm {

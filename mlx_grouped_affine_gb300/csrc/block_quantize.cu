@@ -10,7 +10,9 @@
 // Bound by memory: an element is read once and its code written once.  A thread holds 16
 // consecutive elements (columns are a multiple of 16, so none is cut): 8 threads a row of a
 // block, whose largest magnitude is joined by shuffles (and through shared memory over the
-// 128 rows of a square block, whose elements wait in registers meanwhile).
+// 128 rows of a square block, whose elements wait in registers meanwhile).  [11008, 4096] fp32
+// in square blocks 41.9 us, 5.4 TB/s, 0.79 of the copy rate; 16 x 4096 bf16 by rows 3.4 us, the
+// launch and one chain of load, shuffles and codes.
 #include "common.cuh"
 
 #include <cuda_fp8.h>
