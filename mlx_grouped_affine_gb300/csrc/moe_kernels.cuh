@@ -105,7 +105,7 @@ struct Run {
   static constexpr int kSteps = kChunk / G;
   static constexpr int kRowBytes = kChunk * BITS / 8;
   static constexpr int kStageBytes = 2 * 16 * kRowBytes;
-  static constexpr int kDepth = kStageBytes >= 3072 ? 2 : 4;
+  static constexpr int kDepth = kStageBytes > 2560 ? 2 : 4;
   // A warp's part of the ring: its stages, then a chunk's scales as every lane reads them.
   static constexpr int kWarpBytes = kDepth * kStageBytes + (kSteps * 256 + 1023) / 1024 * 1024;
   static constexpr CUtensorMapSwizzle kSwizzle = kRowBytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B

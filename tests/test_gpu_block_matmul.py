@@ -12,6 +12,7 @@ def run(a, sa, w, sw, kind, guard=64):
     dt, k = TYPES[kind]
     m, n = a.shape[0], w.shape[0]
     y = torch.full((m * n + guard,), -3.0, dtype=dt, device="cuda")
+    qmm.qmm_get_device_error()  # (other tests may have left theirs)
     qmm.qmm_block_matmul(a.cuda(), sa.cuda(), m, w.cuda(), sw.cuda(), n, a.shape[1], y, k)
     torch.cuda.synchronize()
     assert qmm.qmm_get_device_error() == qmm.QMM_OK
