@@ -621,7 +621,8 @@ typedef struct {
  *
  * A logit of -infinity (a masked expert) has score 0, a NaN counts as -infinity; in a
  * row that has nothing else every weight is 0.  Logits of +infinity share a softmax
- * equally.  fp32 throughout.  Outputs overlap neither the logits nor each other.
+ * equally.  Normalized sigmoids keep their ratios where they themselves vanish in fp32
+ * (a row of the type's lowest values is shared equally).  fp32 throughout.  Outputs overlap neither the logits nor each other.
  */
 qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t tokens, int64_t experts,
                          int top_k, qmm_scoring scoring, int normalize, float scale,

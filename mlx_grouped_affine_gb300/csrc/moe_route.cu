@@ -1,7 +1,8 @@
 // qmm_moe_route: top experts and weights, one warp a token.  A lane keeps every 32nd logit
 // as an ordered integer in a register; each choice is the warp's largest of them and, of
-// equal ones, the lowest expert (two warp reductions).  8192 tokens over 256 experts, top 8, in
-// 8.3 us: bound by integer instructions (724 a token, the ALUs 76 % busy); 16 over 128 in 2.6 us.
+// equal ones, the lowest expert: two warp reductions, one for 16-bit logits, which share a word
+// with their expert.  8192 tokens over 256 experts, top 8, bf16, in 6.5 us (8.3 with two
+// reductions), bound by integer instructions; 16 over 128 in 2.4 us, the launch and eight choices.
 #include "moe_route.cuh"
 
 namespace qmm {
@@ -9,7 +10,7 @@ namespace {
 
 constexpr int kWarps = 8;
 
-template <int NV>
+template <int NV, bool PACKED>
 __global__ void __launch_bounds__(32 * kWarps)
 route_kernel(const __grid_constant__ Routing r, int64_t tokens, int experts, int *__restrict__ ids,
              float *__restrict__ weights) {
@@ -18,7 +19,7 @@ route_kernel(const __grid_constant__ Routing r, int64_t tokens, int experts, int
   if (row >= tokens) return;
   int id[1];
   float weight[1];
-  route_rows<NV, 1>(r, experts, row, tokens, lane, id, weight);
+  route_rows<NV, 1, PACKED>(r, experts, row, tokens, lane, id, weight);
   if (lane < r.top_k) {
     ids[row * r.top_k + lane] = id[0];
     weights[row * r.top_k + lane] = weight[0];
@@ -29,7 +30,8 @@ template <int NV>
 cudaError_t launch(const Routing &r, int64_t tokens, int experts, int *ids, float *weights,
                    cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((tokens + kWarps - 1) / kWarps);
-  route_kernel<NV><<<grid, 32 * kWarps, 0, stream>>>(r, tokens, experts, ids, weights);
+  if (r.type == kTypeF32) route_kernel<NV, false><<<grid, 32 * kWarps, 0, stream>>>(r, tokens, experts, ids, weights);
+  else route_kernel<NV, true><<<grid, 32 * kWarps, 0, stream>>>(r, tokens, experts, ids, weights);
   return cudaGetLastError();
 }
 

@@ -21,6 +21,20 @@ __device__ __forceinline__ float load_logit(const void *p, int type, int64_t at)
   return type == kTypeBF16 ? bf16_bits_to_f32(h) : ElemF16::to_f32(h);
 }
 
+// 16-bit logits leave room for the expert in the same word, below the ordered pattern and
+// counted down: one comparison then settles equal logits too.
+__device__ __forceinline__ uint32_t packed_key(const void *p, int type, int64_t at, int expert) {
+  const uint32_t h = static_cast<const uint16_t *>(p)[at], infinity = type == kTypeBF16 ? 0x7F80u : 0x7C00u;
+  const uint32_t v = (h & 0x7FFFu) > infinity ? infinity | 0x8000u : h == 0x8000u ? 0u : h;  // NaN; -0
+  return (v ^ (v & 0x8000u ? 0xFFFFu : 0x8000u)) << 16 | (0xFFFFu - static_cast<uint32_t>(expert));
+}
+template <bool PACKED>
+__device__ __forceinline__ float logit_of(uint32_t key, int type) {
+  if constexpr (!PACKED) return key_logit(key);
+  const uint32_t o = key >> 16, h = o & 0x8000u ? o ^ 0x8000u : ~o & 0xFFFFu;
+  return type == kTypeBF16 ? bf16_bits_to_f32(h) : ElemF16::to_f32(h);
+}
+
 // Sum over the warp, in an order that does not depend on anything.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -29,10 +43,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // The whole warp routes rows row .. row + ROWS - 1 (those below `end`), side by side: a
-// choice is two warp reductions long, and rows hide each other's.  Lane j < top_k gets each
+// choice is two warp reductions long (one where keys are PACKED), and rows hide each other's.  Lane j < top_k gets each
 // row's j-th expert and its weight.  NV = ceil(experts / 32), or more: expert 32 i + lane is
 // entry i of a lane.
-template <int NV, int ROWS>
+template <int NV, int ROWS, bool PACKED = false>
 __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_t row, int64_t end, int lane,
                                            int (&id)[ROWS], float (&weight)[ROWS]) {
   uint32_t key[ROWS][NV];
@@ -41,7 +55,10 @@ __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = 32 * i + lane;
-      key[k][i] = e < experts && row + k < end ? logit_key(load_logit(r.logits, r.type, (row + k) * experts + e)) : 0u;
+      const int64_t at = (row + k) * experts + e;
+      key[k][i] = e >= experts || row + k >= end ? 0u
+                  : PACKED                        ? packed_key(r.logits, r.type, at, e)
+                                                  : logit_key(load_logit(r.logits, r.type, at));
     }
   float total[ROWS], largest[ROWS];
   uint32_t chosen[ROWS];
@@ -53,12 +70,12 @@ __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) m = max(m, key[k][i]);
-      largest[k] = key_logit(__reduce_max_sync(0xFFFFFFFFu, m));
+      largest[k] = logit_of<PACKED>(__reduce_max_sync(0xFFFFFFFFu, m), r.type);
       if (!r.normalize) {  // (the sum over all cancels where the chosen are divided by theirs)
         float part = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const float l = key_logit(key[k][i]);
+          const float l = logit_of<PACKED>(key[k][i], r.type);
           if (key[k][i] != 0u && l != -INFINITY) part += l == largest[k] ? 1.0f : __expf(l - largest[k]);
         }
         total[k] = warp_sum(part);
@@ -70,17 +87,26 @@ __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
       // the lane's first largest entry, the warp's largest, its lowest expert
-      uint32_t best = 0;
-      int at = 0;
+      uint32_t best = 0, top, e;
+      if constexpr (PACKED) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (key[k][i] > best) best = key[k][i], at = i;
-      const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-      const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * at + lane : 0xFFFFu);
-      if ((e & 31u) == static_cast<uint32_t>(lane)) {
+        for (int i = 0; i < NV; ++i) best = max(best, key[k][i]);
+        top = __reduce_max_sync(0xFFFFFFFFu, best);
+        e = 0xFFFFu - (top & 0xFFFFu);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[k][i] = key[k][i] == top ? 0u : key[k][i];
+      } else {
+        int at = 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (i == static_cast<int>(e >> 5)) key[k][i] = 0;
+          if (key[k][i] > best) best = key[k][i], at = i;
+        top = __reduce_max_sync(0xFFFFFFFFu, best);
+        e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * at + lane : 0xFFFFu);
+        if ((e & 31u) == static_cast<uint32_t>(lane)) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (i == static_cast<int>(e >> 5)) key[k][i] = 0;
+        }
       }
       if (lane == j) id[k] = static_cast<int>(e), chosen[k] = top;
     }
@@ -93,7 +119,7 @@ __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_
   const bool relative = r.sigmoid && r.normalize, alone = r.sigmoid && !r.normalize;
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
-    const float l = key_logit(chosen[k]);
+    const float l = lane < r.top_k ? logit_of<PACKED>(chosen[k], r.type) : -INFINITY;
     float score = 0.0f, x = l;
     if (relative) {
       x = fminf(l, 0.0f) - log1pf(__expf(-fabsf(l)));

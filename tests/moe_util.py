@@ -92,6 +92,12 @@ def routed(logits, top, sigmoid, normalize, scale):
         score = torch.where(total > 0, score / total, 0.0)
     w = score.gather(1, ids.long())
     if normalize:
+        if sigmoid:
+            # sigmoids below 2^-1074 vanish even in 64 bits, their ratios do not: exponentials of
+            # log sigmoid(l) = -log(1 + exp(-l)) relative to the largest
+            chosen = l.gather(1, ids.long())
+            log = torch.nn.functional.logsigmoid(chosen)
+            w = torch.where(chosen == -math.inf, 0.0, torch.exp(log - log[:, :1]))
         total = w.sum(1, keepdim=True)
         w = torch.where(total > 0, w / total, 0.0)
     return ids, w * scale

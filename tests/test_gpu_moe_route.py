@@ -69,6 +69,26 @@ def test_masks_ties_and_values_that_are_not_finite(sigmoid, normalize):
     assert weights.isfinite().all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("normalize", [False, True])
+def test_masks_and_ties_of_16_bit_logits(kind, sigmoid, normalize):
+    inf, nan = math.inf, math.nan
+    g = torch.Generator().manual_seed(3)
+    x = (torch.randn(12, 300, generator=g) * 4).round() / 4        # many equal logits
+    x[0], x[1] = -inf, nan
+    x[2, 6:] = -inf
+    x[2, :5] = -nan
+    x[3, ::2], x[3, 1::2] = -0.0, 0.0
+    x[4, [299, 7]] = inf
+    x[5] = torch.finfo(TYPES[kind][0]).min
+    x[6] = torch.finfo(TYPES[kind][0]).tiny
+    x[6, 200] = -torch.finfo(TYPES[kind][0]).tiny
+    x[7] = -torch.linspace(0, 60000, 300)
+    ids, weights = check(x.to(TYPES[kind][0]), 9, sigmoid, normalize)
+    assert (weights[:2] == 0).all() and torch.equal(ids[3], torch.arange(9, dtype=torch.int32))
+
+
 def test_many_tokens_and_bf16_ties():
     g = torch.Generator().manual_seed(2)
     logits = torch.randn(5000, 128, generator=g).to(torch.bfloat16)
