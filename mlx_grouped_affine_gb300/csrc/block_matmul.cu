@@ -179,12 +179,15 @@ struct Loader {
     if (++stage == STAGES) stage = 0, phase ^= 1u;
     return true;
   }
-  // Stopped early: no copy may land after the block has left (the last one into each stage).
-  __device__ __forceinline__ void drain(Bars<STAGES> &bars, uint32_t limit) {
+  // No copy may land after the block has left, or after its sums have taken the ring's place:
+  // waits for the last one into each stage.  Whoever stopped early: where every step fits the
+  // ring the loader itself never waits, and another role's wait is the one that runs out.
+  // (Otherwise these copies have landed long since: a poll a stage.)
+  __device__ __forceinline__ void drain(Bars<STAGES> &bars) {
     for (int i = 0; i < STAGES; ++i) {
       if (!(used >> i & 1u)) continue;
       const uint32_t last = i < stage ? phase : phase ^ 1u;
-      for (uint32_t polls = 0; polls < limit && !mbar_try_wait(&bars.full[i], last); ++polls) {
+      for (uint32_t polls = 0; polls < kDefaultWaitLimit && !mbar_try_wait(&bars.full[i], last); ++polls) {
       }
     }
   }
@@ -399,7 +402,7 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
         const int m0 = static_cast<int>(tile % m_tiles) * kTallM, n0 = static_cast<int>(tile / m_tiles) * kTallN;
         for (int k = 0; ok && k < a.steps; ++k) ok = load.step(bars, &ma, &mw, smem, k * kStep, m0, n0, a);
       }
-      if (!ok) load.drain(bars, kDefaultWaitLimit);
+      load.drain(bars);
     } else if (warp == 1 && lane == 0) {
       Multiplier<kTallStages, kTallA, kTallB, kTallN> mul;
       bool ok = true;
@@ -471,7 +474,7 @@ flat_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
       Loader<kStages, kA, kB> load;
       bool ok = true;
       for (int k = k0; ok && k < k1; ++k) ok = load.step(bars, &mw, &ma, smem, k * kStep, n0, m0, a);
-      if (!ok) load.drain(bars, kDefaultWaitLimit);
+      load.drain(bars);
     }
   } else if (warp == 1) {
     if (lane == 0) {

@@ -1,0 +1,52 @@
+"""A kernel whose wait runs out leaves only when its own copies have landed, whichever of its
+roles stopped.  Sizes at which every load fits its ring, so that the loading role has no wait
+that could run out, behind a flushed L2, each followed at once (nothing waits in between) by a
+call that uses the shared memory again and must be right."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+from mlx_grouped_affine_gb300 import qmm  # noqa: E402
+from block_util import bound, operands, product  # noqa: E402
+
+TRIES = 10
+
+
+@pytest.fixture(scope="module")
+def flush():
+    return torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+
+
+def stopped_then_right(flush, call, right):
+    """Runs call() with one poll a wait, then right() with the default; the statuses seen."""
+    qmm.qmm_get_device_error()
+    seen = []
+    for _ in range(TRIES):
+        flush.zero_()
+        before = qmm.qmm_set_wait_limit(1)
+        try:
+            call()
+        finally:
+            qmm.qmm_set_wait_limit(before)
+        right()
+        seen.append(qmm.qmm_get_device_error())
+    assert set(seen) <= {qmm.QMM_OK, qmm.QMM_ERR_TIMEOUT}
+    return seen
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 1024, 4096),      # few rows: 4 steps a block, 5 stages
+                                   (100, 640, 2048),     # 128 rows: 2 steps, 3 stages
+                                   (1024, 12800, 256)])  # tiles of many rows: 2 steps a tile, 4 stages
+def test_block_product(flush, m, n, k):
+    a, sa, w, sw = [t.cuda() for t in operands(m, n, k, 8)]
+    y = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    again = torch.empty_like(y)
+
+    def call(out):
+        qmm.qmm_block_matmul(a, sa, m, w, sw, n, k, out, qmm.QMM_BF16)
+
+    seen = stopped_then_right(flush, lambda: call(y), lambda: call(again))
+    assert qmm.QMM_ERR_TIMEOUT in seen
+    want, terms = product(a, sa, w, sw)
+    assert ((again.double() - want).abs() <= bound((want, terms), k, y.dtype)).all()
