@@ -487,7 +487,7 @@ __device__ void w_tma_role(const CUtensorMap *wmap, const CUtensorMap *smap,
   volatile int *abort = &bars->abort;
   int ps = 0, ss = 0;
   uint32_t pph = 0, sph = 0;
-  // Parity of the last load issued into each slot, for the drain after a stop.
+  // Parity of the last load issued into each slot, for the drain at the end.
   int pend_p[SP], pend_s[SS];
 #pragma unroll
   for (int i = 0; i < SP; ++i) pend_p[i] = -1;
@@ -524,20 +524,19 @@ __device__ void w_tma_role(const CUtensorMap *wmap, const CUtensorMap *smap,
       if (++ps == SP) { ps = 0; pph ^= 1u; }
     }
   }
-  if (!ok) {
-    // Stopped early: wait (bounded) for the copies still in flight.
+  // No copy outlives the role, whichever role stopped early: where every load fits the ring,
+  // this one has no wait that could run out.  (Otherwise they have landed: a poll a slot.)
 #pragma unroll
-    for (int i = 0; i < SP; ++i) {
-      if (pend_p[i] < 0) continue;
-      for (uint32_t spin = 0; spin < kSpinLimit; ++spin)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->full_p[i], pend_p[i]))) break;
-    }
+  for (int i = 0; i < SP; ++i) {
+    if (pend_p[i] < 0) continue;
+    for (uint32_t spin = 0; spin < kSpinLimit; ++spin)
+      if (__all_sync(0xffffffffu, mbar_try_wait(&bars->full_p[i], pend_p[i]))) break;
+  }
 #pragma unroll
-    for (int i = 0; i < SS; ++i) {
-      if (pend_s[i] < 0) continue;
-      for (uint32_t spin = 0; spin < kSpinLimit; ++spin)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->full_s[i], pend_s[i]))) break;
-    }
+  for (int i = 0; i < SS; ++i) {
+    if (pend_s[i] < 0) continue;
+    for (uint32_t spin = 0; spin < kSpinLimit; ++spin)
+      if (__all_sync(0xffffffffu, mbar_try_wait(&bars->full_s[i], pend_s[i]))) break;
   }
 }
 
@@ -625,8 +624,7 @@ __device__ void tma_role(const CUtensorMap *tmap, const GemmArgs &a, uint8_t *sA
   volatile int *abort = &bars->abort;
   int s = 0;
   uint32_t ph = 0;
-  // Parity of the last load issued into each stage that has not been seen to
-  // land, so that a role that stops early can wait for its copies.
+  // Parity of the last load issued into each stage, for the drain at the end.
   int pending[SA];
   for (int i = 0; i < SA; ++i) pending[i] = -1;
   bool ok = true;
@@ -644,13 +642,11 @@ __device__ void tma_role(const CUtensorMap *tmap, const GemmArgs &a, uint8_t *sA
       if (++s == SA) { s = 0; ph ^= 1u; }
     }
   }
-  if (!ok) {
-    // Stopped early: wait (bounded) for the copies still in flight.
-    for (int i = 0; i < SA; ++i) {
-      if (pending[i] < 0) continue;
-      for (uint32_t spin = 0; spin < kSpinLimit; ++spin)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->full_a[i], pending[i]))) break;
-    }
+  // No copy outlives the role, whichever role stopped early (as in w_tma_role).
+  for (int i = 0; i < SA; ++i) {
+    if (pending[i] < 0) continue;
+    for (uint32_t spin = 0; spin < kSpinLimit; ++spin)
+      if (__all_sync(0xffffffffu, mbar_try_wait(&bars->full_a[i], pending[i]))) break;
   }
 }
 

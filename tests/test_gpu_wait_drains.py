@@ -4,11 +4,14 @@ that could run out, behind a flushed L2, each followed at once (nothing waits in
 call that uses the shared memory again and must be right."""
 import pytest
 
+import oracle
+
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
-from mlx_grouped_affine_gb300 import qmm  # noqa: E402
+from mlx_grouped_affine_gb300 import qmm, synth  # noqa: E402
 from block_util import bound, operands, product  # noqa: E402
+from gpu_util import assert_within_tolerance, dev, empty_out, weight  # noqa: E402
 
 TRIES = 10
 
@@ -50,3 +53,24 @@ def test_block_product(flush, m, n, k):
     assert qmm.QMM_ERR_TIMEOUT in seen
     want, terms = product(a, sa, w, sw)
     assert ((again.double() - want).abs() <= bound((want, terms), k, y.dtype)).all()
+
+
+@pytest.mark.parametrize("bits", [4, 6])
+@pytest.mark.parametrize("m,n,k,sure", [(256, 14336, 128, False),   # two steps: x and W fit their rings
+                                        (256, 14336, 256, True),    # four: W does
+                                        (1024, 14336, 128, True)])  # three tiles a block, two steps each
+def test_quantized_product(flush, m, n, k, bits, sure):
+    """(One poll may stay suspended until a first load has come; where more than that is waited
+    for, waits ran out in every call.)"""
+    w = synth.quant_weight(820 + m, n, k, bits, 64)
+    x = synth.x_bf16(821 + m, m, k)
+    px, parts = dev(x), weight(w)
+    y, again = (empty_out((m, n), qmm.QMM_BF16) for _ in range(2))
+
+    def call(out):
+        qmm.qmm_quantized_matmul(px, m, *parts, n, k, 1, 64, bits, out, qmm.QMM_BF16)
+
+    seen = stopped_then_right(flush, lambda: call(y), lambda: call(again))
+    assert not sure or qmm.QMM_ERR_TIMEOUT in seen
+    ref, absy = oracle.qmm(x, m, w.packed, w.scales, w.biases, n, k, True, 64, bits)
+    assert_within_tolerance(again, ref, absy, "after a wait that ran out")
