@@ -401,18 +401,17 @@ __device__ void key_role(const AttnArgs &a, Cursor c, const CUtensorMap *qmap, c
     }
     if (ok) piece_done(a, c, p);
   }
-  // No copy outlives the warp's part.  Stopped early, the barriers of the steps
-  // under way may lack other warps' arrivals: their waits are short.
+  // No copy outlives the warp's part, whichever role stopped early: where every load fits the
+  // ring, this one's only waits are met.  Stopped early, the barriers of the steps under way may
+  // lack other warps' arrivals: the waits are short.
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if (!ok) {
-    if (q_count) {
-      for (uint32_t x = 0; x < kDrainPolls; ++x)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->q_full, (q_count - 1) & 1))) break;
-    }
-    for (uint32_t n = steps > X::SLOTS ? steps - X::SLOTS : 0; n < steps; ++n) {
-      for (uint32_t x = 0; x < kDrainPolls; ++x)
-        if (__all_sync(0xffffffffu, mbar_try_wait(&bars->kv_full[n % kSteps], (n / kSteps) & 1))) break;
-    }
+  if (q_count) {
+    for (uint32_t x = 0; x < kDrainPolls; ++x)
+      if (__all_sync(0xffffffffu, mbar_try_wait(&bars->q_full, (q_count - 1) & 1))) break;
+  }
+  for (uint32_t n = steps > X::SLOTS ? steps - X::SLOTS : 0; n < steps; ++n) {
+    for (uint32_t x = 0; x < kDrainPolls; ++x)
+      if (__all_sync(0xffffffffu, mbar_try_wait(&bars->kv_full[n % kSteps], (n / kSteps) & 1))) break;
   }
 }
 

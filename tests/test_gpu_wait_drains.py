@@ -12,6 +12,7 @@ torch = pytest.importorskip("torch")
 from mlx_grouped_affine_gb300 import qmm, synth  # noqa: E402
 from block_util import bound, operands, product  # noqa: E402
 from gpu_util import assert_within_tolerance, dev, empty_out, weight  # noqa: E402
+from paged_util import Pool, attend, check, queries  # noqa: E402
 
 TRIES = 10
 
@@ -74,3 +75,16 @@ def test_quantized_product(flush, m, n, k, bits, sure):
     assert not sure or qmm.QMM_ERR_TIMEOUT in seen
     ref, absy = oracle.qmm(x, m, w.packed, w.scales, w.biases, n, k, True, 64, bits)
     assert_within_tolerance(again, ref, absy, "after a wait that ran out")
+
+
+@pytest.mark.parametrize("dtype,dim,page", [("bf16", 128, 16), ("f16", 64, 24), ("bf16", 128, 7)])
+def test_prompt_of_one_tile(flush, dtype, dim, page):
+    """Keys of one tile: queries, K and V fit the ring (pages of 7 are copied by the lanes)."""
+    pool = Pool([100], page, 2, dim, dtype)
+    q = queries(pool, 100, 8)
+    got = []
+    seen = stopped_then_right(flush, lambda: attend(pool, q, [100], 8, 0.1),
+                              lambda: got.append(attend(pool, q, [100], 8, 0.1)))
+    assert qmm.QMM_ERR_TIMEOUT in seen
+    for g in got:
+        check(pool, q, [100], 8, 0.1, got=g)
