@@ -492,10 +492,11 @@ struct Ring {
     if (out == 0) parity ^= 1;
     --flying;
   }
-  // No copy may land after the block has left.
-  __device__ __forceinline__ void drain(bool copied, uint32_t limit, unsigned *err) {
+  // No copy may land after the block has left (flying: a wait has run out).  Not with the
+  // caller's limit, which may be one poll.
+  __device__ __forceinline__ void drain(bool copied, unsigned *err) {
     while (flying > 0) {
-      wait(copied, limit, err);
+      wait(copied, kDefaultWaitLimit, err);
       done();
     }
   }
@@ -692,7 +693,7 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
   while (s.left > 0) {
     s.run_task();
   }
-  s.ring.drain(s.copied, a.wait_limit, a.err);
+  s.ring.drain(s.copied, a.err);
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
   const int r = threadIdx.x % 16, place = threadIdx.x / 16;
@@ -851,7 +852,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     const int j0 = unit == first_unit ? first_chunk : 0;
     run_unit(unit, j0);
   }
-  ring.drain(copied, a.wait_limit, a.err);
+  ring.drain(copied, a.err);
   asm volatile("cp.async.wait_all;" ::: "memory");
   cluster_barrier();
 

@@ -10,6 +10,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 from mlx_grouped_affine_gb300 import qmm, synth  # noqa: E402
+import moe_util  # noqa: E402
 from block_util import bound, operands, product  # noqa: E402
 from gpu_util import assert_within_tolerance, dev, empty_out, weight  # noqa: E402
 from paged_util import Pool, attend, check, queries  # noqa: E402
@@ -88,3 +89,45 @@ def test_prompt_of_one_tile(flush, dtype, dim, page):
     assert qmm.QMM_ERR_TIMEOUT in seen
     for g in got:
         check(pool, q, [100], 8, 0.1, got=g)
+
+
+class FarLayer(moe_util.Layer):
+    """Experts made on the GPU, whole memory's random words."""
+
+    def __init__(self, experts, hidden, inner, bits, group):
+        self.experts, self.hidden, self.inner, self.bits, self.group = experts, hidden, inner, bits, group
+        g = torch.Generator(device="cuda").manual_seed(bits)
+
+        def part(rows, cols):
+            words = torch.empty(experts, rows, cols * bits // 32, dtype=torch.int32, device="cuda")
+            for e in range(experts):
+                words[e].random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+            s = torch.empty(experts, rows, cols // group, dtype=torch.bfloat16, device="cuda").uniform_(0.002, 0.02, generator=g)
+            return words, s.mul_(8 / 2 ** (bits - 1)), s * -2 ** (bits - 1)
+
+        self.parts = [part(inner, hidden), part(inner, hidden), part(hidden, inner)]
+        self.handle = qmm.Experts(*self.parts, qmm.QMM_BF16, experts, hidden, inner, group, bits)
+
+
+@pytest.mark.parametrize("experts,hidden,inner,bits,group", [
+    (1024, 2048, 4096, 8, 64),  # experts spread over 8.6 GB each of gate, up and down
+    (1024, 992, 2080, 6, 32),   # rows of gate and up that the lanes copy
+])
+def test_expert_layer(flush, experts, hidden, inner, bits, group):
+    """Weights far apart in memory: a chunk takes longer than a poll may stay suspended.  (Waits
+    of the first case ran out in every call measured; in the second, and with weights of less than a
+    few GB, none was seen to.  It depends on memory alone, so the status may be either.)"""
+    t, top = 64, 8
+    layer = FarLayer(experts, hidden, inner, bits, group)
+    ids, weights = moe_util.random_ids(t, top, experts, 3)
+    x = torch.randn(t, hidden, generator=torch.Generator().manual_seed(t)).bfloat16().cuda()
+    y, again = (torch.empty(t, hidden, device="cuda") for _ in range(2))
+    ws, n = moe_util.workspace(t, top, hidden, inner)
+
+    def call(to):
+        qmm.qmm_moe_experts(x, qmm.QMM_BF16, t, ids, weights, top, layer.handle, to, qmm.QMM_F32, ws, n)
+
+    print(stopped_then_right(flush, lambda: call(y), lambda: call(again)))
+    few = [0, 31, 63]
+    want, far = moe_util.reference(layer, x[few], ids[few], weights[few], again.dtype)
+    assert ((again[few].double() - want).abs() <= far).all()
