@@ -719,7 +719,10 @@ gemv_t_tma_kernel(const __grid_constant__ CUtensorMap wmap, GemvArgs a, TmaLayou
         load_x(c, xv);
       }
       uint32_t spins = 0;
-      while (!mbar_try_wait(&bars[c], 0)) {
+      // By the whole warp: lanes that gave up alone would leave the others to products and
+      // votes without them.  (0.3 % of the decode benchmark's rate; going on with what is
+      // there, without a vote, 0.6 %.)
+      while (!__all_sync(0xffffffffu, mbar_try_wait(&bars[c], 0))) {
         if (++spins >= a.spin_limit) {
           if (lane == 0) atomicOr(err, kErrTimeoutBit);
           ok = false;
