@@ -644,10 +644,12 @@ qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t tokens, in
  * holds.  An id outside [0, experts) has none either and is reported by
  * qmm_get_device_error as QMM_ERR_INDEX.  Each weight is scale * code + bias as it
  * stands (codes are not rounded, scales and biases applied in fp32), x exact, sums
- * fp32 (for 16-bit x_dtype a group's sums may lose bits below 2^-17 of its largest
- * terms); silu(gate) * up keeps 15 bits or more for 16-bit x_dtype, 24 for fp32; y is
- * rounded once.  Results repeat bit for bit.  Each expert that is asked for is
- * streamed from memory once for every 8 of its slots.
+ * fp32 (values of x, or of silu(gate) * up, below 2^-110 may lose bits); silu(gate) * up
+ * keeps 15 bits or more for 16-bit x_dtype, 24 for fp32; y is rounded once.  An infinity
+ * in a token's x may come out as NaN.  Results repeat bit for bit, whatever the other
+ * tokens of the call hold; with other ids (other experts, more tokens) sums are cut in
+ * other places, and last bits may differ.  Each expert that is asked for is streamed from
+ * memory once for every 8 of its slots.
  */
 qmm_status qmm_moe_experts(const void *x, qmm_dtype x_dtype, int64_t tokens, const int32_t *ids,
                            const float *weights, int top_k, const qmm_experts *experts, void *y,

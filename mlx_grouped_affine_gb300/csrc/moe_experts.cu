@@ -115,42 +115,27 @@ __device__ void make_plan(const Routing r, const int tokens, const int experts, 
   }
 }
 
-// Block 0: the plan, and every slot's mark cleared.  Block 1 + t: token t's row of x, looked
-// over for large values and, where it is not bf16, cut into planes.  fp32 rows are marked as
-// large whatever they hold: the tensor cores line products up by the exponents of their
-// factors, and a code as it is, an unnormalised number, then costs the sum some of its last
-// bits (2.4e-6 of the outputs' norm in fp32 against 1.9e-6; 16-bit types round far above).
+// Block 0: the plan.  Block 1 + t (where x is not bf16): token t's row of x, cut into planes.
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const __grid_constant__ Routing r, int tokens, int experts, unsigned *err, MoePlan *plan,
-            const void *__restrict__ x, int x_type, int hidden, uint16_t *__restrict__ planes, int64_t plane, int count,
-            unsigned char *__restrict__ x_large, unsigned char *__restrict__ h_large) {
+            const void *__restrict__ x, int x_type, int hidden, uint16_t *__restrict__ planes, int64_t plane, int count) {
   __shared__ PlanShared shared;
   griddep_launch_dependents();
   if (blockIdx.x == 0) {
-    if (threadIdx.x < kMoeMaxSlots) h_large[threadIdx.x] = x_type == kTypeF32;
     make_plan(r, tokens, experts, err, shared, plan);
     return;
   }
-  const int token = blockIdx.x - 1;
-  const int64_t row = static_cast<int64_t>(token) * hidden;
-  bool large = x_type == kTypeF32;
-  for (int i = threadIdx.x; i < hidden; i += kPlanThreads) {
-    const float v = load_logit(x, x_type, row + i);
-    large |= is_large(v);
-    if (x_type != kTypeBF16) store_planes(planes + row + i, plane, count, v);
-  }
-  large = __syncthreads_or(large);
-  if (threadIdx.x == 0) x_large[token] = large;
+  const int64_t row = static_cast<int64_t>(blockIdx.x - 1) * hidden;
+  for (int i = threadIdx.x; i < hidden; i += kPlanThreads)
+    store_planes(planes + row + i, plane, count, load_logit(x, x_type, row + i));
 }
 
 int64_t round128(int64_t n) { return (n + 127) / 128 * 128; }
-constexpr int64_t kMarks = 128 + kMoeMaxSlots;  // of tokens, of slots
-static_assert(kMoeMaxTokens <= 128 && kMarks % 128 == 0, "marks are whole lines");
 
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner) {
-  return static_cast<size_t>(kWorkspaceAlign + round128(sizeof(MoePlan)) + kMarks + 2 * 3 * round128(tokens * hidden) +
+  return static_cast<size_t>(kWorkspaceAlign + round128(sizeof(MoePlan)) + 2 * 3 * round128(tokens * hidden) +
                              2 * 3 * round128(tokens * top_k * inner));
 }
 
@@ -162,9 +147,7 @@ cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Rout
   if (!a.err) return cudaErrorInvalidSymbol;
   const Workspace ws = aligned_workspace(workspace, workspace_bytes);
   MoePlan *plan = reinterpret_cast<MoePlan *>(ws.base);
-  a.x_large = reinterpret_cast<unsigned char *>(ws.base + round128(sizeof(MoePlan)));
-  a.h_large = a.x_large + 128;
-  uint16_t *planes = reinterpret_cast<uint16_t *>(a.x_large + kMarks);
+  uint16_t *planes = reinterpret_cast<uint16_t *>(ws.base + round128(sizeof(MoePlan)));
   const int64_t n = static_cast<int64_t>(tokens) * w.hidden;
   a.route = r;
   a.w = w;
@@ -173,14 +156,15 @@ cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Rout
   a.y_type = y_type;
   a.plan = plan;
   a.wait_limit = wait_limit();
+  a.code_scale = kCodeScale;
   a.x_plane = round128(n);
   a.x_planes = x_type == kTypeBF16 ? 1 : x_type == kTypeF16 ? 2 : 3;
   a.x = x_type == kTypeBF16 ? static_cast<const uint16_t *>(x) : planes;
   a.h = planes + 3 * a.x_plane;
   a.h_plane = round128(static_cast<int64_t>(tokens) * r.top_k * w.inner);
   a.h_planes = x_type == kTypeF32 ? 3 : 2;
-  plan_kernel<<<1 + tokens, kPlanThreads, 0, stream>>>(r, tokens, w.experts, a.err, plan, x, x_type, w.hidden, planes, a.x_plane,
-                                                       a.x_planes, a.x_large, a.h_large);
+  plan_kernel<<<a.x == planes ? 1 + tokens : 1, kPlanThreads, 0, stream>>>(r, tokens, w.experts, a.err, plan, x, x_type, w.hidden,
+                                                                           planes, a.x_plane, a.x_planes);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   switch (w.bits) {

@@ -48,7 +48,7 @@ struct MoeArgs {
   const MoePlan *plan;
   unsigned *err;
   uint32_t wait_limit;
-  unsigned char *x_large, *h_large;  // of a token, of a slot: a finite value of 2^26 or more in its row
+  uint32_t code_scale;  // kCodeScale
 };
 
 // ------------------------------------------------------------- the plan ----
@@ -118,25 +118,32 @@ struct Run {
   }
 };
 
-// Codes as bf16 pairs, as they are: a bf16 pattern P <= 0xFF is worth P * 2^-133, so a code at
-// bit o of an otherwise clear half reads as c * 2^(o - 133), exactly, and the tensor cores take
-// such small numbers at their worth.  x makes up for it: it is taken times 2^(100 - o), a power
-// of two, which keeps products with x of 2^-93 and more out of fp32's smallest numbers and
-// x below 2^27 inside bf16.  Where a slot's row has a value of 2^26 or more, x stays as it is
-// and the codes are taken times 2^(127 - o), to c * 2^-6.  (The tensor cores' sums are times
-// 2^-33 or 2^-6 then, and sum(x) is taken the same way, with ones for codes.)  Multiplying the
-// few x instead of the many codes saves a quarter of a group's instructions.
-template <int BITS, int G>
-struct Offsets {  // of the pair i of a run's codes
-  static constexpr int kHalf = BITS == 2 || BITS == 4 || BITS == 8 ? 16 / BITS : 1;
-  __device__ static constexpr int at(int i) { return Run<BITS, G>::kSplit ? i % kHalf * BITS % 8 : 0; }
+// Codes as bf16 pairs, each code * 2^-15.  A bf16 pattern P <= 0xFF is worth P * 2^-133, so a
+// code at bit o of an otherwise clear half reads as c * 2^(o - 133), and times 2^(118 - o) it is
+// exact and normal; sum(x) is taken times 2^-15 too, and the sums times 2^15 at the end.  Not
+// multiplied as it stands, with the powers of two in x: the tensor cores line products up by
+// their factors' exponents, and an unnormalised code costs the sum up to 7 of its last bits
+// (1e-5 of the outputs' norm; the few x instead of the many codes saved 5 % of the time).
+// 2^-15, so that 128 codes of 8 bits do not take a sum beyond its x: x as large as fp32 holds
+// goes in, and sums keep all their bits down to x of 2^-110.
+// The factors come with the call's arguments: constants would be put into a register again
+// for every product (32 instructions a group).
+constexpr uint32_t kCodeScale = 0x7A807A80u;  // 2^118, twice
+constexpr uint32_t kOnes = 0x38003800u;       // 2^-15, twice
+constexpr float kUnscale = 32768.0f;
+template <int BITS>
+struct Factors {
+  static constexpr int kCount = BITS == 8 ? 1 : BITS == 4 ? 2 : BITS == 2 ? 4 : 1;
+  uint32_t v[kCount];  // (2^(118 - o), 2^(118 - o)) for o = 0, BITS, 2 BITS ..
+  __device__ __forceinline__ explicit Factors(uint32_t code_scale) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) v[i] = code_scale - (static_cast<uint32_t>(i * BITS) << 7) * 0x00010001u;
+  }
 };
-constexpr float kUnscaleSmall = 8589934592.0f, kUnscaleLarge = 64.0f;  // 2^33, 2^6
-__device__ __forceinline__ uint32_t twice_bf16(int exponent) { return static_cast<uint32_t>(exponent + 127) << 7 | static_cast<uint32_t>(exponent + 127) << 23; }
-__device__ __forceinline__ uint32_t bf16x2_times(uint32_t a, uint32_t b) { return bf16x2_fma(a, b, 0x80008000u); }
 
 template <int BITS, int G>
-__device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, bool large, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
+__device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, const Factors<BITS> &f,
+                                             uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
   using R = Run<BITS, G>;
   if constexpr (R::kSplit) {
     constexpr int kHalf = 16 / BITS, kPerSub = R::kSub * BITS / 32;
@@ -147,22 +154,19 @@ __device__ __forceinline__ void spread_codes(const uint32_t *v, int sub, bool la
 #pragma unroll
       for (int j = 0; j < kHalf; ++j) {
         const int o = j * BITS % 8, sh = j * BITS - o;
-        p[i * kHalf + j] = (w >> sh) & (kMask << o);
+        p[i * kHalf + j] = bf16x2_fma((w >> sh) & (kMask << o), f.v[o / BITS], 0x80008000u);
       }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < R::kSub / 2; ++i) p[i] = pair_at<BITS>(v, sub * R::kSub + 2 * i);
-  }
-  if (large) {
-#pragma unroll
-    for (int i = 0; i < R::kSub / 2; ++i) p[i] = bf16x2_times(p[i], twice_bf16(127 - Offsets<BITS, G>::at(i)));
+    for (int i = 0; i < R::kSub / 2; ++i)
+      p[i] = bf16x2_fma(pair_at<BITS>(v, sub * R::kSub + 2 * i), f.v[0], 0x80008000u);
   }
 }
 
 // x of those codes, in the same pairs.
 template <int BITS, int G>
-__device__ __forceinline__ void pair_x(const uint16_t *x, bool large, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
+__device__ __forceinline__ void pair_x(const uint16_t *x, uint32_t (&p)[Run<BITS, G>::kSub / 2]) {
   using R = Run<BITS, G>;
   uint32_t n[R::kSub / 2];
 #pragma unroll
@@ -180,10 +184,6 @@ __device__ __forceinline__ void pair_x(const uint16_t *x, bool large, uint32_t (
   } else {
 #pragma unroll
     for (int i = 0; i < R::kSub / 2; ++i) p[i] = n[i];
-  }
-  if (!large) {
-#pragma unroll
-    for (int i = 0; i < R::kSub / 2; ++i) p[i] = bf16x2_times(p[i], twice_bf16(100 - Offsets<BITS, G>::at(i)));
   }
 }
 
@@ -277,7 +277,6 @@ struct Scales {
 // Columns without a slot repeat the first: nothing looks at their sums.
 struct Columns {
   const uint16_t *x;  // this lane's column, at its run
-  bool large;         // a row of the pass has a value of 2^26 or more
   int planes;
   int64_t plane;
 };
@@ -300,27 +299,24 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The products of up to 16 codes a lane with one plane of x.  A one is a code of 1 at its
-// pair's bit, or 2^-6.
+// The products of up to 16 codes a lane with one plane of x.
 template <int BITS, int G, bool FIRST>
-__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2], bool large,
+__device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>::kSub / 2],
                                          const uint32_t (&x)[Run<BITS, G>::kSub / 2], float (&part)[2][4], float (&ones)[4]) {
   using R = Run<BITS, G>;
 #pragma unroll
   for (int m = 0; m < R::kSub / 4; ++m) {
-    const uint32_t one0 = large ? 0x3C803C80u : 0x00010001u << Offsets<BITS, G>::at(2 * m);
-    const uint32_t one1 = large ? 0x3C803C80u : 0x00010001u << Offsets<BITS, G>::at(2 * m + 1);
     if (FIRST && m == 0) {
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
         mma_bf16<true>(part[tile], code[2 * tile][0], code[2 * tile + 1][0], code[2 * tile][1], code[2 * tile + 1][1], x[0], x[1]);
-      mma_bf16<true>(ones, one0, one0, one1, one1, x[0], x[1]);
+      mma_bf16<true>(ones, kOnes, kOnes, kOnes, kOnes, x[0], x[1]);
     } else {
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
         mma_bf16<false>(part[tile], code[2 * tile][2 * m], code[2 * tile + 1][2 * m], code[2 * tile][2 * m + 1],
                         code[2 * tile + 1][2 * m + 1], x[2 * m], x[2 * m + 1]);
-      mma_bf16<false>(ones, one0, one0, one1, one1, x[2 * m], x[2 * m + 1]);
+      mma_bf16<false>(ones, kOnes, kOnes, kOnes, kOnes, x[2 * m], x[2 * m + 1]);
     }
   }
 }
@@ -331,7 +327,7 @@ __device__ __forceinline__ void multiply(const uint32_t (&code)[4][Run<BITS, G>:
 // must not outgrow.
 template <int BITS, int G>
 __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns &c, int at, int count,
-                                        uint32_t scales, float (&acc)[8]) {
+                                        uint32_t scales, const Factors<BITS> &f, float (&acc)[8]) {
   using R = Run<BITS, G>;
   const int g = lane / 4, t = lane % 4;
   const uint32_t rows = stage + g * R::kRowBytes, flip = (t * R::kBits / 32 * 4) ^ R::swap(g);
@@ -365,16 +361,16 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns 
 #pragma unroll
     for (int sub = 0; sub < R::kCodes / R::kSub; ++sub) {
       uint32_t x[R::kSub / 2];  // loaded ahead of the codes' instructions
-      pair_x<BITS, G>(px + sub * R::kSub, c.large, x);
+      pair_x<BITS, G>(px + sub * R::kSub, x);
       uint32_t code[4][R::kSub / 2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, c.large, code[q]);
+      for (int q = 0; q < 4; ++q) spread_codes<BITS, G>(v[q], sub, f, code[q]);
       if (c.planes < 3) {
-        if (sub == 0) multiply<BITS, G, true>(code, c.large, x, part, ones);
-        else multiply<BITS, G, false>(code, c.large, x, part, ones);
+        if (sub == 0) multiply<BITS, G, true>(code, x, part, ones);
+        else multiply<BITS, G, false>(code, x, part, ones);
         if (c.planes == 2) {
-          pair_x<BITS, G>(px + sub * R::kSub + c.plane, c.large, x);
-          multiply<BITS, G, false>(code, c.large, x, part, ones);
+          pair_x<BITS, G>(px + sub * R::kSub + c.plane, x);
+          multiply<BITS, G, false>(code, x, part, ones);
         }
       } else {
         // fp32: the smallest part of x first, the tensor cores cut what they add to a large sum.
@@ -383,8 +379,8 @@ __device__ __forceinline__ void consume(uint32_t stage, int lane, const Columns 
           for (int i = 0; i < 4; ++i) part[0][i] = part[1][i] = ones[i] = 0.0f;
 #pragma unroll 1
         for (int plane = 2; plane >= 0; --plane) {
-          pair_x<BITS, G>(px + sub * R::kSub + plane * c.plane, c.large, x);
-          multiply<BITS, G, false>(code, c.large, x, part, ones);
+          pair_x<BITS, G>(px + sub * R::kSub + plane * c.plane, x);
+          multiply<BITS, G, false>(code, x, part, ones);
         }
       }
     }
@@ -502,9 +498,6 @@ struct Ring {
   }
 };
 
-// Whether v is a finite number too large for the codes as they are.
-__device__ __forceinline__ bool is_large(float v) { return fabsf(v) >= 67108864.0f && fabsf(v) < INFINITY; }
-
 // The bf16 planes of v: its leading bits cut off 8 at a time (three hold all 24).  What is
 // not finite stays in the first.
 __device__ __forceinline__ void store_planes(uint16_t *p, int64_t plane, int planes, float v) {
@@ -557,6 +550,7 @@ struct GateUp {
   int sb_bytes;
   bool whole;
   Scales<R::kSteps> next;
+  Factors<BITS> factors{a.code_scale};
 
   __device__ __forceinline__ void advance_load() {
     if (l_left <= 0) return;
@@ -601,7 +595,6 @@ struct GateUp {
     c.planes = a.x_planes;
     c.plane = a.x_plane;
     const int token = listed[g < count ? g : 0].token;
-    c.large = __any_sync(0xFFFFFFFFu, a.x_large[token]);
     c.x = a.x + static_cast<int64_t>(token) * a.w.hidden + t * R::kCodes;
     const uint32_t spread = ring.base + R::kDepth * R::kStageBytes, own_scales = spread + (lane % 4) * 64 + lane / 4 * 8;
     float acc[8] = {};
@@ -615,13 +608,12 @@ struct GateUp {
         left = l_left = 0;
         return;
       }
-      consume<BITS, G>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, spread, acc);
+      consume<BITS, G>(stage, lane, c, chunk * R::kChunk, groups - chunk * R::kSteps, spread, factors, acc);
       ring.done();
       advance_load();
     }
-    const float unscale = c.large ? kUnscaleLarge : kUnscaleSmall;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] *= unscale;
+    for (int i = 0; i < 8; ++i) acc[i] *= kUnscale;
     if (c0 == 0 && c1 == chunks) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -632,7 +624,6 @@ struct GateUp {
           const float h0 = silu_times(acc[i], acc[4 + i]), h1 = silu_times(acc[2 + i], acc[6 + i]);
           store_planes(to, a.h_plane, a.h_planes, h0);
           store_planes(to + 8, a.h_plane, a.h_planes, h1);
-          if (is_large(h0) || is_large(h1)) a.h_large[slot] = 1;
         }
       }
     } else {
@@ -709,7 +700,6 @@ gate_up_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMap
     const int slot = s.plan[s.plan[unit].unit_first + place].listed;
     const float h = silu_times(gate, up);
     store_planes(a.h + static_cast<int64_t>(slot) * a.w.inner + tile * 16 + r, a.h_plane, a.h_planes, h);
-    if (is_large(h)) a.h_large[slot] = 1;
   }
 }
 
@@ -808,6 +798,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
   }
 
   const uint32_t spread = ring.base + R::kDepth * R::kStageBytes, own_scales = spread + t * 64 + g * 8;
+  const Factors<BITS> factors(a.code_scale);
   int step = step0;
   auto run_unit = [&](int unit, int j0) {
     const int j1 = min(chunks, j0 + (step1 - step));
@@ -817,7 +808,6 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
     c.planes = a.h_planes;
     c.plane = a.h_plane;
     const int own_slot = listed[g < count ? g : 0].listed;
-    c.large = __any_sync(0xFFFFFFFFu, __ldcg(&a.h_large[own_slot]));
     c.x = a.h + static_cast<int64_t>(own_slot) * a.w.inner + t * R::kCodes;
     float acc[8] = {};
     for (int j = j0; j < j1; ++j) {
@@ -833,7 +823,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
         step = load_step = step1;
         return;
       }
-      consume<BITS, G>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, spread, acc);
+      consume<BITS, G>(stage, lane, c, j * R::kChunk, groups - j * R::kSteps, spread, factors, acc);
       ring.done();
       load_next(true);
     }
@@ -844,7 +834,7 @@ down_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ MoeMaps m
         float *to = j0 == 0 ? z + listed[place].listed * 32 : sh.heads[warp][place];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[2 * q + i] * (c.large ? kUnscaleLarge : kUnscaleSmall);
+          to[(q / 2) * 16 + (q % 2) * 8 + g] = acc[2 * q + i] * kUnscale;
       }
     }
   };
