@@ -645,8 +645,8 @@ qmm_status qmm_moe_route(const void *logits, qmm_dtype dtype, int64_t tokens, in
  * qmm_get_device_error as QMM_ERR_INDEX.  Each weight is scale * code + bias as it
  * stands (codes are not rounded, scales and biases applied in fp32), x exact, sums
  * fp32 (values of x, or of silu(gate) * up, below 2^-110 may lose bits); silu(gate) * up
- * keeps 15 bits or more for 16-bit x_dtype, 24 for fp32; y is rounded once.  An infinity
- * in a token's x may come out as NaN.  Results repeat bit for bit, whatever the other
+ * goes on in fp32, or to 2^-18 of itself where y has 16 bits; y is rounded once.  An
+ * infinity in a token's x may come out as NaN.  Results repeat bit for bit, whatever the other
  * tokens of the call hold; with other ids (other experts, more tokens) sums are cut in
  * other places, and last bits may differ.  Each expert that is asked for is streamed from
  * memory once for every 8 of its slots.

@@ -162,7 +162,9 @@ cudaError_t launch_moe_experts(const void *x, int x_type, int tokens, const Rout
   a.x = x_type == kTypeBF16 ? static_cast<const uint16_t *>(x) : planes;
   a.h = planes + 3 * a.x_plane;
   a.h_plane = round128(static_cast<int64_t>(tokens) * r.top_k * w.inner);
-  a.h_planes = x_type == kTypeF32 ? 3 : 2;
+  // Two planes hold silu(gate) * up to 2^-18, well below y's own rounding where it has 16 bits
+  // (2^-9 and 2^-12); the third costs down half as many products again.
+  a.h_planes = y_type == kTypeF32 ? 3 : 2;
   plan_kernel<<<a.x == planes ? 1 + tokens : 1, kPlanThreads, 0, stream>>>(r, tokens, w.experts, a.err, plan, x, x_type, w.hidden,
                                                                            planes, a.x_plane, a.x_planes);
   const cudaError_t e = cudaGetLastError();

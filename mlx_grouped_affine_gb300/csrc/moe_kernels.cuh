@@ -498,14 +498,15 @@ struct Ring {
   }
 };
 
-// The bf16 planes of v: its leading bits cut off 8 at a time (three hold all 24).  What is
-// not finite stays in the first.
+// The bf16 planes of v: the nearest bf16 number, then that of what is left of it, exactly (two
+// hold v to 2^-18 of itself, three all of its 24 bits).  What is not finite stays in the first;
+// what would round to infinity is cut there instead.
 __device__ __forceinline__ void store_planes(uint16_t *p, int64_t plane, int planes, float v) {
   for (int i = 0; i < planes; ++i) {
-    const uint32_t cut = __float_as_uint(v) & 0xFFFF0000u;
-    p[i * plane] = static_cast<uint16_t>(cut >> 16);
-    const bool more = (cut & 0x7F800000u) != 0x7F800000u;
-    v = more ? v - __uint_as_float(cut) : 0.0f;
+    uint32_t near = static_cast<uint32_t>(f32_to_bf16_bits(v)) << 16;
+    if ((near & 0x7F800000u) == 0x7F800000u && fabsf(v) < INFINITY) near = __float_as_uint(v) & 0xFFFF0000u;
+    p[i * plane] = static_cast<uint16_t>(near >> 16);
+    v = (near & 0x7F800000u) != 0x7F800000u ? v - __uint_as_float(near) : 0.0f;
   }
 }
 

@@ -72,6 +72,31 @@ def test_fp32_keeps_24_bits(bits, group):
     assert torch.equal(y.cpu(), x[:, at[back]])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("bits", [2, 4, 5, 8])
+def test_sums_of_24_bits(bits, kind):
+    """A sum of codes times x with one large term among small ones, below 2^24: nothing of it
+    may be lost.  (A code taken as an unnormalised number loses the small ones.)"""
+    hidden, inner, t, group = 128, 64, 8, 64
+    top = 2 ** bits - 1
+    g = torch.Generator().manual_seed(bits)
+    codes = torch.randint(0, min(top, 2) + 1, (inner, hidden), generator=g)
+    codes[:, 0] = 0
+    codes[:, 1 + torch.randint(0, 63, (1,), generator=g)] = top
+    large = codes[0].argmax().item()
+    x = torch.randint(-3, 4, (t, hidden), generator=g).float() * 2 + 1
+    x[:, 0] = 1.0
+    # the large term near, and all of them below, 2^23; fp16 ends at 65504
+    x[:, large] = min(2 ** 23 // (top + 1), 2 ** 15) if kind == "f16" else 2 ** 23 // (top + 1)
+    layer = Codes(codes, pick(inner, hidden, torch.zeros(inner, dtype=torch.long)),
+                  pick(hidden, inner, torch.arange(hidden) % inner), bits, group)
+    x = x.to(TYPES[kind][0])
+    want = x.double() @ codes.double().T
+    assert (want >= 20).all() and (want < 2 ** 24).all()
+    y = one_expert(layer, x.cuda())
+    assert torch.equal(y.cpu().double(), want[:, torch.arange(hidden) % inner])
+
+
 @pytest.mark.parametrize("part,power,kind", [(p, n, k) for p in "xh" for n in (-80, -40, 60, 100) for k in ("bf16", "f32")] +
                          [("x", -100, "bf16")])  # (below 2^-110 parts of x or h leave bf16)
 @pytest.mark.parametrize("bits", [4, 8])
@@ -120,3 +145,18 @@ def test_a_token_does_not_depend_on_the_values_of_others(kind):
     z = run(layer, x, ids, weights, "f32")
     keep = [t for t in range(16) if t not in (5, 11)]
     assert torch.equal(y[keep], z[keep])
+
+
+@pytest.mark.parametrize("x,sb", [("bf16", "bf16"), ("f16", "f16"), ("f32", "bf16")])
+@pytest.mark.parametrize("bits", [2, 4, 8])
+def test_outputs_in_fp32_are_near(x, sb, bits):
+    """Relative to the norm of y: each of the three products in a row may lose 8 units of 2^-23
+    of its norm (a group's few sums, a fused multiply-add a group), its inputs kept whole."""
+    layer = Layer(8, 1024, 768, bits, 64, sb, bits)
+    ids, weights = random_ids(12, 3, 8, 5)
+    v = torch.randn(12, 1024, generator=torch.Generator().manual_seed(5)).to(TYPES[x][0]).cuda()
+    y = run(layer, v, ids, weights, "f32").double()
+    want, _ = reference(layer, v, ids, weights, torch.float32)
+    off = ((y - want).norm() / want.norm()).item()
+    print("off by %.2e" % off)
+    assert off <= 3 * 8 * 2.0 ** -23
