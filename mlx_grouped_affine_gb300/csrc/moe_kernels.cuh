@@ -522,8 +522,12 @@ struct MoeMaps {
   CUtensorMap gate, up, down;
 };
 
+// gate / (1 + exp(-gate)) * up, by exp(-|gate|) so that the divisor is in [1, 2]: exp(-gate)
+// itself leaves fp32, and __fdividef's range, below -87, where the product with up need not
+// have vanished.
 __device__ __forceinline__ float silu_times(float gate, float up) {
-  return __fdividef(gate, 1.0f + expf(-gate)) * up;
+  const float e = expf(-fabsf(gate));
+  return __fdividef(gate >= 0.0f ? gate : gate * e, 1.0f + e) * up;
 }
 
 // h = silu(gate x) * (up x).  A task is a unit and 16 rows of gate and of up.  A block has
