@@ -76,7 +76,7 @@ __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const float l = logit_of<PACKED>(key[k][i], r.type);
-          if (key[k][i] != 0u && l != -INFINITY) part += l == largest[k] ? 1.0f : __expf(l - largest[k]);
+          if (key[k][i] != 0u && l != -INFINITY) part += l == largest[k] ? 1.0f : expf(l - largest[k]);
         }
         total[k] = warp_sum(part);
       }
@@ -111,26 +111,25 @@ __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_
       if (lane == j) id[k] = static_cast<int>(e), chosen[k] = top;
     }
   }
-  // Sigmoids that are divided by their sum are taken relative to the largest of them, as
-  // exponentials of log sigmoid(l) = min(l, 0) - log(1 + exp(-|l|)): those of logits below
-  // -88 do not fit fp32, but their ratios do.  (Few instructions: an expert kernel runs them
-  // once a block, each line of them a miss of the instruction cache.  __expf is off by 2^-21
-  // and 2^-24 of its argument.)
-  const bool relative = r.sigmoid && r.normalize, alone = r.sigmoid && !r.normalize;
+  // softmax: exp(l - largest).  sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)); where all of a row's
+  // are divided by their sum and lie below exp(-64), exp(l - largest): they may not fit fp32,
+  // but their ratios do.  (With __expf, off by 2^-24 of its argument, weights of logits spread
+  // by 10 are three times as far off, for 0.5 us of 8192 tokens over 256 experts.)
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
     const float l = lane < r.top_k ? logit_of<PACKED>(chosen[k], r.type) : -INFINITY;
-    float score = 0.0f, x = l;
-    if (relative) {
-      x = fminf(l, 0.0f) - log1pf(__expf(-fabsf(l)));
-      largest[k] = __shfl_sync(0xFFFFFFFFu, x, 0);
+    if (r.sigmoid) {
+      const float first = __shfl_sync(0xFFFFFFFFu, l, 0);
+      largest[k] = r.normalize && first < -64.0f ? first : 0.0f;
     }
+    float score = 0.0f;
     if (lane < r.top_k && l != -INFINITY) {
-      score = alone || x != largest[k] ? __expf(alone ? -l : x - largest[k]) : 1.0f;
-      if (alone) score = __fdividef(1.0f, 1.0f + score);
+      const float x = r.sigmoid && l >= 0.0f ? 0.0f : l == largest[k] ? 0.0f : l - largest[k];
+      score = expf(x);
+      if (r.sigmoid) score /= 1.0f + expf(-fabsf(l));
     }
     if (r.normalize) total[k] = warp_sum(score);
-    weight[k] = total[k] > 0.0f ? __fdividef(score, total[k]) * r.scale : 0.0f;
+    weight[k] = total[k] > 0.0f ? score / total[k] * r.scale : 0.0f;
   }
 }
 
