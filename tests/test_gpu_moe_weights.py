@@ -5,7 +5,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 from mlx_grouped_affine_gb300 import qmm  # noqa: E402
-from moe_util import TYPES  # noqa: E402
+from moe_util import TYPES, routed  # noqa: E402
 
 
 def scores(logits, sigmoid):
@@ -38,3 +38,18 @@ def test_rms_of_relative_errors(normalize, sigmoid, spread, kind):
     if normalize:
         plain = plain / plain.sum(1, keepdim=True)
     assert off(weights) <= 1.25 * off(plain)
+
+
+def test_logits_of_more_than_two_to_31():
+    """8 400 000 tokens over 256 experts: the first rows, those about element 2^31, the last."""
+    tokens, experts, top = 8400000, 256, 8
+    logits = torch.empty(tokens, experts, dtype=torch.bfloat16, device="cuda")
+    logits.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    ids = torch.empty(tokens, top, dtype=torch.int32, device="cuda")
+    weights = torch.empty(tokens, top, device="cuda")
+    qmm.qmm_moe_route(logits, qmm.QMM_BF16, tokens, experts, top, qmm.QMM_SCORE_SOFTMAX, True, 1.0, ids, weights)
+    for first in (0, 2 ** 31 // experts - 32, tokens - 64):
+        rows = slice(first, first + 64)
+        want_ids, want = routed(logits[rows].cpu(), top, False, True, 1.0)
+        assert torch.equal(ids[rows].cpu(), want_ids)
+        assert ((weights[rows].cpu().double() - want).abs() <= 2.0 ** -18 * want).all()
