@@ -111,21 +111,22 @@ __device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_
       if (lane == j) id[k] = static_cast<int>(e), chosen[k] = top;
     }
   }
-  // softmax: exp(l - largest).  sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)); where all of a row's
-  // are divided by their sum and lie below exp(-64), exp(l - largest): they may not fit fp32,
-  // but their ratios do.  (With __expf, off by 2^-24 of its argument, weights of logits spread
-  // by 10 are three times as far off, for 0.5 us of 8192 tokens over 256 experts.)
+  // softmax: exp(l - largest).  sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)), and where they are
+  // divided by their sum, exp(min(l, 0) - min(largest, 0)) in its place: those of logits below
+  // -88 do not fit fp32, but their ratios do.  (With __expf, off by 2^-24 of its argument,
+  // weights of logits spread by 10 are three times as far off, for 0.5 us of 8192 tokens over
+  // 256 experts.)
 #pragma unroll
   for (int k = 0; k < ROWS; ++k) {
     const float l = lane < r.top_k ? logit_of<PACKED>(chosen[k], r.type) : -INFINITY;
     if (r.sigmoid) {
       const float first = __shfl_sync(0xFFFFFFFFu, l, 0);
-      largest[k] = r.normalize && first < -64.0f ? first : 0.0f;
+      largest[k] = r.normalize ? fminf(first, 0.0f) : 0.0f;
     }
     float score = 0.0f;
     if (lane < r.top_k && l != -INFINITY) {
-      const float x = r.sigmoid && l >= 0.0f ? 0.0f : l == largest[k] ? 0.0f : l - largest[k];
-      score = expf(x);
+      const float x = r.sigmoid ? fminf(l, 0.0f) : l;
+      score = x == largest[k] ? 1.0f : expf(x - largest[k]);
       if (r.sigmoid) score /= 1.0f + expf(-fabsf(l));
     }
     if (r.normalize) total[k] = warp_sum(score);

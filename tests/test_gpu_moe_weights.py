@@ -53,3 +53,19 @@ def test_logits_of_more_than_two_to_31():
         want_ids, want = routed(logits[rows].cpu(), top, False, True, 1.0)
         assert torch.equal(ids[rows].cpu(), want_ids)
         assert ((weights[rows].cpu().double() - want).abs() <= 2.0 ** -18 * want).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("first", [30.0, -0.5, -10.0, -60.0, -64.5, -100.0, -3000.0])
+def test_normalized_sigmoids_keep_their_ratios(first, kind):
+    """Logits 0 to 80 below the largest: every weight to a few roundings (2^-24 of the
+    difference, 16 more), and what lies below 2^-126."""
+    dt, k = TYPES[kind]
+    logits = (first - torch.linspace(0, 80, 32))[None].to(dt)
+    ids = torch.empty(1, 32, dtype=torch.int32, device="cuda")
+    weights = torch.empty(1, 32, device="cuda")
+    qmm.qmm_moe_route(logits.cuda(), k, 1, 32, 32, qmm.QMM_SCORE_SIGMOID, True, 1.0, ids, weights)
+    want_ids, want = routed(logits, 32, True, True, 1.0)
+    assert torch.equal(ids.cpu(), want_ids)
+    far = want * (100 + 16) * 2.0 ** -24 + 2.0 ** -126
+    assert ((weights.cpu().double() - want).abs() <= far).all()
