@@ -18,8 +18,8 @@
 // Two kernels.  `tall`: a 128 x 256 tile of y per block, an epilogue thread a row of A and
 // 128 columns of one block column of W, so that a step's factor is one number a thread.
 // `flat`, for few rows of A: W's rows take the MMA's 128 lanes and up to 128 rows of A its
-// columns, so that nothing is padded to 128 rows and W is streamed once; K is split over a
-// cluster, whose partial sums meet in shared memory.
+// columns, so that nothing is padded to 128 rows; W is streamed once for each tile of A's rows.
+// K is split over a cluster, whose partial sums meet in shared memory.
 //
 // Measured: 2048 x 14336 x 4096 in 94.4 us, 2549 TFLOP/s, bound by the 48 KB a step and SM that
 // come from L2 (products alone 62 us, with loads 89) and by the stores; 1 x 4096 x 4096 in 6.2
@@ -42,12 +42,6 @@ struct Args {
 
 // ------------------------------------------------------------- PTX glue ----
 
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
@@ -95,8 +89,8 @@ __device__ __forceinline__ float half_of(uint64_t v, int i) {
   return __uint_as_float(static_cast<uint32_t>(i ? v >> 32 : v));
 }
 
-// (Inlined: a call would leave the epilogue without the registers that setmaxnreg gives it.)
-// Whole-warp bounded wait; false if it ran out or another role gave up.
+// Whole-warp bounded wait; false if it ran out or another role gave up.  (Inlined: a call would
+// leave the epilogue without the registers that setmaxnreg gives it.)
 __device__ __forceinline__ bool wait_slow(uint64_t *b, uint32_t parity, volatile int *abort, unsigned *err, uint32_t limit) {
   uint32_t polls = 0;
   while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity))) {
@@ -173,8 +167,8 @@ struct Loader {
     if (!wait_alone(&bars.done[stage], phase ^ 1u, &bars.abort, a)) return false;
     const uint32_t at = smem + stage * (A_BYTES + B_BYTES);
     mbar_expect_tx(&bars.full[stage], A_BYTES + B_BYTES);
-    load_tile(at, ma, x, y0, &bars.full[stage]);
-    load_tile(at + A_BYTES, mb, x, y1, &bars.full[stage]);
+    tma_load_2d(at, ma, x, y0, &bars.full[stage]);
+    tma_load_2d(at + A_BYTES, mb, x, y1, &bars.full[stage]);
     used |= 1u << stage;
     if (++stage == STAGES) stage = 0, phase ^= 1u;
     return true;
@@ -426,17 +420,6 @@ template <int T>
 __host__ __device__ constexpr int flat_stages() { return T <= 32 ? 5 : T == 64 ? 4 : 3; }
 template <int T>
 __host__ __device__ constexpr uint32_t flat_columns() { return T == 16 ? 32 : 2 * T; }
-
-__device__ __forceinline__ float remote_f32(uint32_t addr, uint32_t rank) {
-  uint32_t far;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // 128 rows of W and T rows of A; the cluster's blocks (blockIdx.x % split) share the steps.
 template <int T>

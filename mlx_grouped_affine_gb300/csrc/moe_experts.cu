@@ -27,12 +27,12 @@ template <int NV>
 __device__ __noinline__ void route_tokens(const Routing r, int tokens, int experts, PlanShared &p) {
   const int lane = threadIdx.x % 32;
   for (int t = threadIdx.x / 32; t < tokens; t += kPlanWarps) {
-    int id[1];
-    float weight[1];
-    route_rows<NV, 1>(r, experts, t, tokens, lane, id, weight);
+    int id;
+    float weight;
+    route_row<NV>(r, experts, t, lane, id, weight);
     if (lane < r.top_k) {
-      p.expert[t * r.top_k + lane] = static_cast<short>(weight[0] == 0.0f ? -1 : id[0]);
-      p.weight[t * r.top_k + lane] = weight[0];
+      p.expert[t * r.top_k + lane] = static_cast<short>(weight == 0.0f ? -1 : id);
+      p.weight[t * r.top_k + lane] = weight;
     }
   }
 }

@@ -189,13 +189,6 @@ __device__ __forceinline__ void pair_x(const uint16_t *x, uint32_t (&p)[Run<BITS
 
 // ------------------------------------------------------------- the ring ----
 
-__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-      : "memory");
-}
-
 template <int N, int OFF>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t *v) {
   if constexpr (N == 4)
@@ -461,8 +454,8 @@ struct Ring {
       }
     } else if (lane == 0) {
       mbar_expect_tx(&bars[in], R::kStageBytes);
-      load_box(st, s0.map, chunk * kRowWords, y0, &bars[in]);
-      load_box(st + R::kStageBytes / 2, s1.map, chunk * kRowWords, y1, &bars[in]);
+      tma_load_2d(st, s0.map, chunk * kRowWords, y0, &bars[in]);
+      tma_load_2d(st + R::kStageBytes / 2, s1.map, chunk * kRowWords, y1, &bars[in]);
     }
     in = in + 1 == R::kDepth ? 0 : in + 1;
     ++flying;
@@ -546,7 +539,6 @@ struct GateUp {
   const char *scales, *biases;
   bool copied;
   int lane, warp, tiles, groups, chunks;
-  int first_unit, first_tile;        // the block's first task
   int task, chunk, unit, tile, left;  // what is multiplied next, chunks left to this warp
   int l_chunk, l_unit, l_tile, l_left, l_row;  // what is loaded next
   bool l_fresh;                       // its unit's x is not in L1 yet
@@ -716,17 +708,6 @@ struct alignas(1024) DownShared {  // then the ring, the plan, z: float [slots][
   uint32_t unread[32];
   unsigned char unit_from[kMoeMaxSlots], unit_to[kMoeMaxSlots];
 };
-
-__device__ __forceinline__ float remote_f32(uint32_t addr, uint32_t rank) {
-  uint32_t far;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(far) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // y = sum over a token's slots of weight * (down h).  A cluster takes 32 rows of every
 // unit: the steps (unit, chunk), in order, are cut evenly over the cluster's warps, so a

@@ -17,12 +17,12 @@ route_kernel(const __grid_constant__ Routing r, int64_t tokens, int experts, int
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   if (row >= tokens) return;
-  int id[1];
-  float weight[1];
-  route_rows<NV, 1, PACKED>(r, experts, row, tokens, lane, id, weight);
+  int id;
+  float weight;
+  route_row<NV, PACKED>(r, experts, row, lane, id, weight);
   if (lane < r.top_k) {
-    ids[row * r.top_k + lane] = id[0];
-    weights[row * r.top_k + lane] = weight[0];
+    ids[row * r.top_k + lane] = id;
+    weights[row * r.top_k + lane] = weight;
   }
 }
 

@@ -1,5 +1,5 @@
 // Routing of a token by one warp: its top experts and their weights, from its logits.
-// Shared by qmm_moe_route and by the expert kernels, which route for themselves.
+// Shared by qmm_moe_route and by the plan of qmm_moe_layer.
 #pragma once
 #include "common.cuh"
 
@@ -42,96 +42,79 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The whole warp routes rows row .. row + ROWS - 1 (those below `end`), side by side: a
-// choice is two warp reductions long (one where keys are PACKED), and rows hide each other's.  Lane j < top_k gets each
-// row's j-th expert and its weight.  NV = ceil(experts / 32), or more: expert 32 i + lane is
-// entry i of a lane.
-template <int NV, int ROWS, bool PACKED = false>
-__device__ __forceinline__ void route_rows(const Routing &r, int experts, int64_t row, int64_t end, int lane,
-                                           int (&id)[ROWS], float (&weight)[ROWS]) {
-  uint32_t key[ROWS][NV];
+// The whole warp routes row `row`: lane j < top_k gets its j-th expert and that one's weight.
+// NV = ceil(experts / 32), or more: expert 32 i + lane is entry i of a lane.
+template <int NV, bool PACKED = false>
+__device__ __forceinline__ void route_row(const Routing &r, int experts, int64_t row, int lane, int &id, float &weight) {
+  uint32_t key[NV];
 #pragma unroll
-  for (int k = 0; k < ROWS; ++k)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = 32 * i + lane;
-      const int64_t at = (row + k) * experts + e;
-      key[k][i] = e >= experts || row + k >= end ? 0u
-                  : PACKED                        ? packed_key(r.logits, r.type, at, e)
-                                                  : logit_key(load_logit(r.logits, r.type, at));
-    }
-  float total[ROWS], largest[ROWS];
-  uint32_t chosen[ROWS];
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) total[k] = 1.0f, largest[k] = 0.0f, chosen[k] = 0, id[k] = 0;
+  for (int i = 0; i < NV; ++i) {
+    const int e = 32 * i + lane;
+    const int64_t at = row * experts + e;
+    key[i] = e >= experts ? 0u : PACKED ? packed_key(r.logits, r.type, at, e) : logit_key(load_logit(r.logits, r.type, at));
+  }
+  float total = 1.0f, largest = 0.0f;
+  uint32_t chosen = 0;
+  id = 0;
   if (!r.sigmoid) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      uint32_t m = 0;
+    for (int i = 0; i < NV; ++i) m = max(m, key[i]);
+    largest = logit_of<PACKED>(__reduce_max_sync(0xFFFFFFFFu, m), r.type);
+    if (!r.normalize) {  // (the sum over all cancels where the chosen are divided by theirs)
+      float part = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) m = max(m, key[k][i]);
-      largest[k] = logit_of<PACKED>(__reduce_max_sync(0xFFFFFFFFu, m), r.type);
-      if (!r.normalize) {  // (the sum over all cancels where the chosen are divided by theirs)
-        float part = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const float l = logit_of<PACKED>(key[k][i], r.type);
-          if (key[k][i] != 0u && l != -INFINITY) part += l == largest[k] ? 1.0f : expf(l - largest[k]);
-        }
-        total[k] = warp_sum(part);
+      for (int i = 0; i < NV; ++i) {
+        const float l = logit_of<PACKED>(key[i], r.type);
+        if (key[i] != 0u && l != -INFINITY) part += l == largest ? 1.0f : expf(l - largest);
       }
+      total = warp_sum(part);
     }
   }
 #pragma unroll 1
   for (int j = 0; j < r.top_k; ++j) {
+    // the lane's first largest entry, the warp's largest, its lowest expert
+    uint32_t best = 0, top, e;
+    if constexpr (PACKED) {
 #pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-      // the lane's first largest entry, the warp's largest, its lowest expert
-      uint32_t best = 0, top, e;
-      if constexpr (PACKED) {
+      for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+      top = __reduce_max_sync(0xFFFFFFFFu, best);
+      e = 0xFFFFu - (top & 0xFFFFu);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) best = max(best, key[k][i]);
-        top = __reduce_max_sync(0xFFFFFFFFu, best);
-        e = 0xFFFFu - (top & 0xFFFFu);
+      for (int i = 0; i < NV; ++i) key[i] = key[i] == top ? 0u : key[i];
+    } else {
+      int at = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) key[k][i] = key[k][i] == top ? 0u : key[k][i];
-      } else {
-        int at = 0;
+      for (int i = 0; i < NV; ++i)
+        if (key[i] > best) best = key[i], at = i;
+      top = __reduce_max_sync(0xFFFFFFFFu, best);
+      e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * at + lane : 0xFFFFu);
+      if ((e & 31u) == static_cast<uint32_t>(lane)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (key[k][i] > best) best = key[k][i], at = i;
-        top = __reduce_max_sync(0xFFFFFFFFu, best);
-        e = __reduce_min_sync(0xFFFFFFFFu, best == top ? 32u * at + lane : 0xFFFFu);
-        if ((e & 31u) == static_cast<uint32_t>(lane)) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (i == static_cast<int>(e >> 5)) key[k][i] = 0;
-        }
+          if (i == static_cast<int>(e >> 5)) key[i] = 0;
       }
-      if (lane == j) id[k] = static_cast<int>(e), chosen[k] = top;
     }
+    if (lane == j) id = static_cast<int>(e), chosen = top;
   }
   // softmax: exp(l - largest).  sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)), and where they are
   // divided by their sum, exp(min(l, 0) - min(largest, 0)) in its place: those of logits below
   // -88 do not fit fp32, but their ratios do.  (With __expf, off by 2^-24 of its argument,
   // weights of logits spread by 10 are three times as far off, for 0.5 us of 8192 tokens over
   // 256 experts.)
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    const float l = lane < r.top_k ? logit_of<PACKED>(chosen[k], r.type) : -INFINITY;
-    if (r.sigmoid) {
-      const float first = __shfl_sync(0xFFFFFFFFu, l, 0);
-      largest[k] = r.normalize ? fminf(first, 0.0f) : 0.0f;
-    }
-    float score = 0.0f;
-    if (lane < r.top_k && l != -INFINITY) {
-      const float x = r.sigmoid ? fminf(l, 0.0f) : l;
-      score = x == largest[k] ? 1.0f : expf(x - largest[k]);
-      if (r.sigmoid) score /= 1.0f + expf(-fabsf(l));
-    }
-    if (r.normalize) total[k] = warp_sum(score);
-    weight[k] = total[k] > 0.0f ? score / total[k] * r.scale : 0.0f;
+  const float l = lane < r.top_k ? logit_of<PACKED>(chosen, r.type) : -INFINITY;
+  if (r.sigmoid) {
+    const float first = __shfl_sync(0xFFFFFFFFu, l, 0);
+    largest = r.normalize ? fminf(first, 0.0f) : 0.0f;
   }
+  float score = 0.0f;
+  if (lane < r.top_k && l != -INFINITY) {
+    const float x = r.sigmoid ? fminf(l, 0.0f) : l;
+    score = x == largest ? 1.0f : expf(x - largest);
+    if (r.sigmoid) score /= 1.0f + expf(-fabsf(l));
+  }
+  if (r.normalize) total = warp_sum(score);
+  weight = total > 0.0f ? score / total * r.scale : 0.0f;
 }
 
 }  // namespace qmm
