@@ -17,7 +17,7 @@
 //
 // Two kernels.  `tall`: a 128 x 256 tile of y per block, an epilogue thread a row of A and
 // 128 columns of one block column of W, so that a step's factor is one number a thread.
-// `flat`, for few rows of A: W's rows take the MMA's 128 lanes and up to 128 rows of A its
+// `flat`, for few rows of A: W's rows take the MMA's 128 lanes and up to 64 rows of A its
 // columns, so that nothing is padded to 128 rows; W is streamed once for each tile of A's rows.
 // K is split over a cluster, whose partial sums meet in shared memory.
 //
@@ -417,13 +417,13 @@ tall_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUte
 
 constexpr int kFlatThreads = 192, kFlatEpilogue = 128;
 template <int T>
-__host__ __device__ constexpr int flat_stages() { return T <= 32 ? 5 : T == 64 ? 4 : 3; }
+__host__ __device__ constexpr int flat_stages() { return T <= 32 ? 5 : 4; }
 template <int T>
 __host__ __device__ constexpr uint32_t flat_columns() { return T == 16 ? 32 : 2 * T; }
 
 // 128 rows of W and T rows of A; the cluster's blocks (blockIdx.x % split) share the steps.
 template <int T>
-__global__ void __launch_bounds__(kFlatThreads, T <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(kFlatThreads, 2)
 flat_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args a,
             int split) {
   constexpr int kStages = flat_stages<T>(), kA = 128 * kStep, kB = T * kStep;
@@ -532,8 +532,42 @@ cudaError_t code_map(CUtensorMap *map, const uint8_t *p, int rows, int cols, int
   return encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, cols, rows, cols, kStep, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Rows of A and blocks that share the steps in `flat`; no split: the call goes to `tall`.
+//
+// Two blocks fit an SM; more blocks than that are a second round, which costs more than a split
+// gains (384 blocks of an eighth of the steps 28 us, 192 of a half 20.5).  So rows are halved while
+// four-fold splits still fit (eight-fold from 64 steps on: 128 x 1024 x 14336 12 us against 15.5),
+// and then K is split for as long as blocks fit.  The cluster's blocks
+// add up the rows of their tile in turns, 0.22 us a row, which few steps do not pay for: `tall`
+// takes 3 us and 0.4 a step whatever its rows.  Measured, us (`flat` as chosen here / `tall`; K is
+// 32 steps but where it is given):
+//   M            16           32           64           128          256
+//   N 1024       6.2 / 16.6   6.5 / 16.6   7.3 / 16.7   8.6 / 17.1   9.9 / 17.2
+//   N 4096       8.5 / 17.0   9.0 / 17.1  10.4 / 17.2  13.2 / 17.6  21.1 / 17.7 (32 rows a block)
+//   N 14336     16.2 / 18.7  18.5 / 18.5  23.2 / 18.7  29.7 / 19.3
+//   N 128256    97.0 / 97.7   108 / 92
+//   K 256, N 4096    5.7 / 4.5 (8 rows), M = 1: 3.9 / 4.5
+//   K 512, N 4096    4.7 / 5.4   5.4 / 5.4   6.5 / 5.5 (8 rows)   8.8 / 6.2 (16)
+//   K 1024, N 4096   6.4 / 7.5   6.4 / 7.6   7.5 / 7.8 (8 rows)   9.8 / 8.2 (16)
+//   K 2048, N 14336  11.9 / 11.9 (8 rows)   14.2 / 11.9 (16)
+//   K 8192, N 4096  11.2 / 29.7  12.2 / 29.7  13.9 / 29.7  17.2 / 30.1
+struct FlatShape {
+  int rows, split;
+};
+FlatShape flat_shape(int M, int N, int steps) {
+  const int64_t n_tiles = (N + 127) / 128, room = 2 * sm_count();
+  auto blocks = [&](int rows) { return n_tiles * ((M + rows - 1) / rows); };
+  int rows = M <= 16 ? 16 : M <= 32 ? 32 : 64, split = 1;
+  const int ways = steps < 4 ? steps : steps < 64 ? 4 : 8;
+  while (rows > 16 && blocks(rows / 2) * ways <= room) rows /= 2;
+  while (split < 8 && 2 * split <= steps && 2 * split * blocks(rows) <= room) split *= 2;
+  const int joined = ((M < rows ? M : rows) + split - 1) / split;
+  const int pays = steps < 8 ? 4 : steps < 32 ? steps / 2 : 16;
+  return {rows, joined <= pays ? split : 0};
+}
+
 template <int T>
-cudaError_t launch_flat(const uint8_t *pa, const uint8_t *w, int K, const Args &a, cudaStream_t stream) {
+cudaError_t launch_flat(const uint8_t *pa, const uint8_t *w, int K, const Args &a, int split, cudaStream_t stream) {
   CUtensorMap ma, mw;
   cudaError_t e = code_map(&ma, pa, a.M, K, T);
   if (e == cudaSuccess) e = code_map(&mw, w, a.N, K, 128);
@@ -543,9 +577,6 @@ cudaError_t launch_flat(const uint8_t *pa, const uint8_t *w, int K, const Args &
   e = ensure_smem_limit<kernel>(bytes);
   if (e != cudaSuccess) return e;
   const int n_tiles = (a.N + 127) / 128, m_tiles = (a.M + T - 1) / T;
-  // K is split until there is a block for every SM, each with a step at least.
-  int split = 1;
-  while (split < 8 && 2 * split <= a.steps && static_cast<int64_t>(n_tiles) * m_tiles * split < sm_count()) split *= 2;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = split;
@@ -576,18 +607,12 @@ cudaError_t launch_block_matmul(const uint8_t *pa, const float *a_scales, int M,
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidSymbol;
   a.limit = wait_limit();
-  const int64_t tiles = static_cast<int64_t>((M + kTallM - 1) / kTallM) * ((N + kTallN - 1) / kTallN);
-  if (M <= 64 || tiles < sm_count() / 2) {
-    // All rows of A at once, so that W is read once, or fewer where that leaves SMs idle (W
-    // then comes from L2 again).
-    const int64_t blocks = static_cast<int64_t>((N + 127) / 128) * (a.steps < 8 ? a.steps : 8);
-    int rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    while (rows > 16 && blocks * ((M + rows - 1) / rows) < sm_count()) rows /= 2;
-    switch (rows) {
-      case 16: return launch_flat<16>(pa, w, K, a, stream);
-      case 32: return launch_flat<32>(pa, w, K, a, stream);
-      case 64: return launch_flat<64>(pa, w, K, a, stream);
-      default: return launch_flat<128>(pa, w, K, a, stream);
+  const FlatShape flat = flat_shape(M, N, a.steps);
+  if (flat.split > 0) {
+    switch (flat.rows) {
+      case 16: return launch_flat<16>(pa, w, K, a, flat.split, stream);
+      case 32: return launch_flat<32>(pa, w, K, a, flat.split, stream);
+      default: return launch_flat<64>(pa, w, K, a, flat.split, stream);
     }
   }
   CUtensorMap ma, mw;
@@ -604,6 +629,7 @@ cudaError_t launch_block_matmul(const uint8_t *pa, const float *a_scales, int M,
   const size_t bytes = 1024 + static_cast<size_t>(kTallStages) * (kTallA + kTallB) + kTallEpilogue * 4096;
   e = ensure_smem_limit<tall_kernel>(bytes);
   if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((M + kTallM - 1) / kTallM) * ((N + kTallN - 1) / kTallN);
   const unsigned grid = static_cast<unsigned>(tiles < sm_count() ? tiles : sm_count());
   tall_kernel<<<grid, kTallThreads, bytes, stream>>>(ma, mw, my, a);
   return cudaGetLastError();

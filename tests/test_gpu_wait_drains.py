@@ -41,7 +41,7 @@ def stopped_then_right(flush, call, right):
 
 
 @pytest.mark.parametrize("m,n,k", [(4, 1024, 4096),      # few rows: 4 steps a block, 5 stages
-                                   (100, 640, 2048),     # 128 rows: 2 steps, 3 stages
+                                   (100, 640, 2048),     # 7 tiles of them: 2 steps a block
                                    (1024, 12800, 256)])  # tiles of many rows: 2 steps a tile, 4 stages
 def test_block_product(flush, m, n, k):
     a, sa, w, sw = [t.cuda() for t in operands(m, n, k, 8)]
