@@ -536,14 +536,14 @@ cudaError_t code_map(CUtensorMap *map, const uint8_t *p, int rows, int cols, int
 //
 // Two blocks fit an SM; more blocks than that are a second round, which costs more than a split
 // gains (384 blocks of an eighth of the steps 28 us, 192 of a half 20.5).  So rows are halved while
-// four-fold splits still fit (eight-fold from 64 steps on: 128 x 1024 x 14336 12 us against 15.5),
-// and then K is split for as long as blocks fit.  The cluster's blocks
+// four-fold splits still fit (eight-fold from 32 steps on: 128 x 1024 x 14336 12 us against 15.5,
+// 77 x 1021 x 4208 7.7 against 8.7), and then K is split for as long as blocks fit.  The cluster's blocks
 // add up the rows of their tile in turns, 0.22 us a row, which few steps do not pay for: `tall`
 // takes 3 us and 0.4 a step whatever its rows.  Measured, us (`flat` as chosen here / `tall`; K is
 // 32 steps but where it is given):
 //   M            16           32           64           128          256
-//   N 1024       6.2 / 16.6   6.5 / 16.6   7.3 / 16.7   8.6 / 17.1   9.9 / 17.2
-//   N 4096       8.5 / 17.0   9.0 / 17.1  10.4 / 17.2  13.2 / 17.6  21.1 / 17.7 (32 rows a block)
+//   N 1024       6.2 / 16.6   6.5 / 16.6   7.3 / 16.7   8.2 / 17.1  10.3 / 17.2
+//   N 4096       8.5 / 17.0   9.5 / 17.1  11.4 / 17.2  13.2 / 17.6  21.1 / 17.7 (32 rows a block)
 //   N 14336     16.2 / 18.7  18.5 / 18.5  23.2 / 18.7  29.7 / 19.3
 //   N 128256    97.0 / 97.7   108 / 92
 //   K 256, N 4096    5.7 / 4.5 (8 rows), M = 1: 3.9 / 4.5
@@ -558,7 +558,7 @@ FlatShape flat_shape(int M, int N, int steps) {
   const int64_t n_tiles = (N + 127) / 128, room = 2 * sm_count();
   auto blocks = [&](int rows) { return n_tiles * ((M + rows - 1) / rows); };
   int rows = M <= 16 ? 16 : M <= 32 ? 32 : 64, split = 1;
-  const int ways = steps < 4 ? steps : steps < 64 ? 4 : 8;
+  const int ways = steps < 4 ? steps : steps < 32 ? 4 : 8;
   while (rows > 16 && blocks(rows / 2) * ways <= room) rows /= 2;
   while (split < 8 && 2 * split <= steps && 2 * split * blocks(rows) <= room) split *= 2;
   const int joined = ((M < rows ? M : rows) + split - 1) / split;
