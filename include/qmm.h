@@ -578,7 +578,8 @@ qmm_status qmm_block_quantize(const void *x, qmm_dtype x_dtype, int64_t rows, in
  *
  * y[m, n] = sum over blocks b of a_scales[m, b] w_scales[n / 128, b] times the sum
  * over the block's columns of a[m, k] w[n, k]: products exact, sums fp32, y rounded
- * once.  Results repeat bit for bit.  K > 0 and a multiple of 16; M, N, K below 2^31.
+ * once.  The two scales are multiplied first, in fp32: where their product leaves its
+ * range, the block's part is 0, or infinite, or (of a sum that is 0) NaN.  Results repeat bit for bit.  K > 0 and a multiple of 16; M, N, K below 2^31.
  */
 qmm_status qmm_block_matmul(const uint8_t *a, const float *a_scales, int64_t M, const uint8_t *w,
                             const float *w_scales, int64_t N, int64_t K, void *y,
@@ -618,6 +619,10 @@ typedef struct {
  *   ids        int32 [tokens, top_k]: largest logits first, of equal ones (+0 and -0
  *              are equal) the lowest index first
  *   weights    fp32 [tokens, top_k]
+ *
+ * Experts are chosen by their logits alone.  (Routers that choose by the score plus a
+ * bias of each expert, or within groups of experts, make ids and weights themselves and
+ * call qmm_moe_experts.)
  *
  * A logit of -infinity (a masked expert) has score 0, a NaN counts as -infinity; in a
  * row that has nothing else every weight is 0.  Logits of +infinity share a softmax
