@@ -21,9 +21,9 @@
 // columns, so that nothing is padded to 128 rows; W is streamed once for each tile of A's rows.
 // K is split over a cluster, whose partial sums meet in shared memory.
 //
-// Measured: 2048 x 14336 x 4096 in 94.4 us, 2549 TFLOP/s, bound by the 48 KB a step and SM that
+// Measured: 2048 x 14336 x 4096 in 92.5 us, 2600 TFLOP/s, bound by the 48 KB a step and SM that
 // come from L2 (products alone 62 us, with loads 89) and by the stores; 1 x 4096 x 4096 in 6.2
-// us, of which the 16.8 MB are 2.5: launch, first tiles, cluster barrier and join.
+// us (three weights in turn), of which the 16.8 MB are 2.5: launch, first tiles, cluster barrier and join.
 #include "common.cuh"
 
 namespace qmm {

@@ -9,11 +9,11 @@
 // (fp16) or three (fp32) bf16 planes that hold it exactly, one product each.
 //
 // The weights that the routing asks for are streamed once; everything else (x, h, scales'
-// sectors) stays in L1 or L2.  Bound by instructions and their latency: 187 per 64 columns of
-// 32 rows (40 spread 4-bit codes, 12 are products, 16 apply scales), at half of the issue slots
-// with the 16 warps an SM that registers allow.  16 tokens of 8 of 64 experts, 2048 x 1024 at 4
-// bits, 82.2 us (gate and up 46, down 39), 0.36 of HBM; 16 tokens of 2 of 8, 4096 x 14336, 268.6
-// us, 0.43.  A warp works on its own: 32 weight rows (two 16-row tiles of
+// sectors) stays in L1 or L2.  Bound by instructions and their latency: 211 per 64 columns of
+// 32 rows (72 spread 4-bit codes and scale them, 12 are products, 16 apply scales), at half of the
+// issue slots with the 16 warps an SM that registers allow.  16 tokens of 8 of 64 experts, 2048 x
+// 1024 at 4 bits, 84.2 us (gate and up 46, down 43), 0.35 of HBM; 16 tokens of 2 of 8, 4096 x
+// 14336, 269 us, 0.43.  A warp works on its own: 32 weight rows (two 16-row tiles of
 // the MMA, sharing the x operand) and a range of chunks of 128 or 256 columns.  A chunk's
 // codes come by TMA, a box of 16 rows per tile, into a ring of the warp's own, so that loads
 // in flight cost no registers and need no block barrier.  (Copies by the lanes themselves

@@ -1,8 +1,10 @@
 // qmm_moe_route: top experts and weights, one warp a token.  A lane keeps every 32nd logit
 // as an ordered integer in a register; each choice is the warp's largest of them and, of
 // equal ones, the lowest expert: two warp reductions, one for 16-bit logits, which share a word
-// with their expert.  8192 tokens over 256 experts, top 8, bf16, in 6.5 us (8.3 with two
-// reductions), bound by integer instructions; 16 over 128 in 2.4 us, the launch and eight choices.
+// with their expert.  8192 tokens over 256 experts, top 8, bf16, in 6.9 us (two more with two
+// reductions; fp32 8.4), bound by integer instructions: every choice looks at all of a lane's
+// entries again (fp32 over 1024 experts 23.8 us).  16 over 128 in 2.8 us, the launch and eight
+// choices.
 #include "moe_route.cuh"
 
 namespace qmm {
